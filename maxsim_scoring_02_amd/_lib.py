@@ -20,11 +20,16 @@ import torch
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "liblik.so")
 HEADER_PATH = os.path.join(os.path.dirname(PKG), "include", "lik.h")
+ROWS_HEADER_PATH = os.path.join(os.path.dirname(PKG), "include", "lik_rows.h")
 
 LIK_OK, LIK_ERR_INVALID_ARG, LIK_ERR_UNSUPPORTED, LIK_ERR_HIP = 0, 1, 2, 3
 LIK_F16, LIK_BF16, LIK_F32, LIK_F32_BF16X3 = 0, 1, 2, 3
 (LIK_OP_FWD, LIK_OP_BWD, LIK_OP_PAIRWISE_FWD, LIK_OP_PAIRWISE_BWD,
  LIK_OP_KD_FWD, LIK_OP_KD_BWD) = range(6)
+
+(LIK_ROWS_LOGPROB_FWD, LIK_ROWS_LOGPROB_BWD, LIK_ROWS_DISTILL, LIK_ROWS_POLICY,
+ LIK_ROWS_PREFERENCE) = range(5)
+LIK_PREF_SIGMOID, LIK_PREF_HINGE, LIK_PREF_SQUARE = range(3)
 
 DTYPE_CODE = {torch.float16: LIK_F16, torch.bfloat16: LIK_BF16, torch.float32: LIK_F32}
 
@@ -34,6 +39,7 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _I = ctypes.c_int
+_F = ctypes.c_float
 
 _FWD_ALLPAIRS = [_P, _P, _I, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]
 _BWD_ALLPAIRS = [_P, _P, _I, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
@@ -58,6 +64,19 @@ SIGNATURES = {
     "lik_ce_rows": ([_P, _I64, _I64, _P, ctypes.c_float, _P, _P, _P, _P], _I),
 }
 
+# include/lik_rows.h
+_ROWS = [_P, _I, _I64, _I64, _I64]                 # logits, dtype, R, C, ld
+ROWS_SIGNATURES = {
+    "lik_rows_workspace_bytes": ([_I, _I64, _I64, _I64, _I], _SZ),
+    "lik_logprob_rows_fwd": (_ROWS + [_P, _F, _P, _P, _P, _SZ, _P], _I),
+    "lik_logprob_rows_bwd": (_ROWS + [_P, _F, _P, _P, _P, _I64, _P], _I),
+    "lik_distill_rows": (_ROWS + [_P, _P, _I64, _P, _F, _P, _P, _P, _P, _I64, _P, _SZ, _P], _I),
+    "lik_policy_rows": (_ROWS + [_P, _P, _P, _P, _F, _F, _F, _F, _P, _P, _P, _P, _P, _I64, _P,
+                                 _SZ, _P], _I),
+    "lik_preference_rows": (_ROWS + [_P, _P, _I64, _P, _P, _I64, _P, _I, _F, _F, _F, _I, _F, _P,
+                                     _P, _P, _P, _P, _I64, _P, _SZ, _P], _I),
+}
+
 
 class LikError(RuntimeError):
     def __init__(self, status: int, detail: str):
@@ -65,9 +84,9 @@ class LikError(RuntimeError):
         self.status = status
 
 
-def header_functions() -> list:
-    """Names of the functions declared in include/lik.h."""
-    with open(HEADER_PATH) as f:
+def header_functions(path: str = HEADER_PATH) -> list:
+    """Names of the functions declared in include/lik.h (or another header)."""
+    with open(path) as f:
         text = f.read()
     return sorted(set(re.findall(r"^[a-z0-9_ ]+?\**\s*\b(lik_[a-z_]+)\s*\(", text, re.M)))
 
@@ -80,7 +99,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(
                 f"{LIB_PATH} is not built; run `python -m maxsim_scoring_02_amd.build`")
         l = ctypes.CDLL(LIB_PATH)
-        for name, (args, res) in SIGNATURES.items():
+        for name, (args, res) in {**SIGNATURES, **ROWS_SIGNATURES}.items():
             fn = getattr(l, name)
             fn.argtypes = args
             fn.restype = res
@@ -336,6 +355,184 @@ def lik_ce_rows(scores, labels=None, scale=1.0, want_grad=True) -> Tuple:
     _check(lib().lik_ce_rows(_ptr(S), R, C, _ptr(lab), float(scale), _ptr(row_loss), _ptr(loss),
                              _ptr(grad), _stream()))
     return loss, row_loss, grad
+
+
+# ---------------------------------------------------------------------------
+# losses over rows of logits (include/lik_rows.h)
+# ---------------------------------------------------------------------------
+
+def _row_stride(x: torch.Tensor, name: str) -> int:
+    """Row stride in elements of a 2-D tensor with dense columns."""
+    R, C = x.shape
+    if C > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name} must have dense columns (stride 1)")
+    if R > 1 and x.stride(0) < C:
+        raise ValueError(f"{name} rows must not overlap")
+    return x.stride(0) if R > 1 else C
+
+
+def _rows(logits: torch.Tensor) -> Tuple:
+    """(dtype code, R, C, row stride) of logits [R, C]."""
+    if logits.dim() != 2 or logits.dtype not in DTYPE_CODE:
+        raise ValueError("logits must be a 2-D float16, bfloat16 or float32 tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a GPU tensor")
+    R, C = logits.shape
+    return DTYPE_CODE[logits.dtype], R, C, _row_stride(logits, "logits")
+
+
+def _row_arg(x, shape, name: str, device, dtype=torch.float32):
+    """A dense argument of this shape on the logits' device, or None.  Integer
+    arguments may be int32 or int64 (values past int32 count as out of range)."""
+    if x is None:
+        return None
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(x.shape)}")
+    if x.device != device:
+        raise ValueError(f"{name} must be on the logits' device")
+    if dtype == torch.int32 and x.dtype == torch.int64:
+        x = x.clamp(-1, 2 ** 31 - 1).to(torch.int32)
+    if x.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {x.dtype}")
+    return x.contiguous()
+
+
+def _row_grad(logits: torch.Tensor, want: bool, out: Optional[torch.Tensor]) -> Tuple:
+    """(gradient tensor or None, its row stride)."""
+    if not want:
+        if out is not None:
+            raise ValueError("grad_out given without want_grad")
+        return None, 0
+    if out is None:
+        out = torch.empty(tuple(logits.shape), dtype=logits.dtype, device=logits.device)
+    elif (out.shape != logits.shape or out.dtype != logits.dtype or
+          out.device != logits.device):
+        raise ValueError("grad_out must have the logits' shape, type and device")
+    return out, _row_stride(out, "grad_out")
+
+
+def _row_outs(R: int, device, *shapes) -> list:
+    """float32 outputs; a call without rows writes none of them, so they are 0 then."""
+    make = torch.empty if R else torch.zeros
+    return [make(s, dtype=torch.float32, device=device) for s in shapes]
+
+
+def _rows_workspace(op: int, R: int, C: int, S: int, dt: int, device) -> Tuple:
+    n = lib().lik_rows_workspace_bytes(op, R, C, S, dt)
+    return _workspace(n, device), n
+
+
+def lik_logprob_rows_fwd(logits, targets, scale=1.0) -> Tuple:
+    """Log-probabilities of the columns `targets` [R] of softmax(scale * logits
+    [R, C]): (logp [R], lse [R]) float32.  Rows with a negative target are not
+    read; both are 0 there."""
+    dt, R, C, ld = _rows(logits)
+    dev = logits.device
+    t = _row_arg(targets, (R,), "targets", dev, torch.int32)
+    with torch.cuda.device(dev):
+        logp, lse = _row_outs(R, dev, (R,), (R,))
+        ws, wsb = _rows_workspace(LIK_ROWS_LOGPROB_FWD, R, C, 0, dt, dev)
+        _check(lib().lik_logprob_rows_fwd(_ptr(logits), dt, R, C, ld, _ptr(t), float(scale),
+                                          _ptr(logp), _ptr(lse), _ptr(ws), wsb, _stream()))
+    return logp, lse
+
+
+def lik_logprob_rows_bwd(logits, targets, lse, grad_logp, scale=1.0, grad_out=None):
+    """Gradient [R, C] of sum(grad_logp * logp) in the logits' type; lse [R]
+    from the forward with the same scale."""
+    dt, R, C, ld = _rows(logits)
+    dev = logits.device
+    t = _row_arg(targets, (R,), "targets", dev, torch.int32)
+    lse = _row_arg(lse, (R,), "lse", dev)
+    g = _row_arg(grad_logp, (R,), "grad_logp", dev)
+    grad, gld = _row_grad(logits, True, grad_out)
+    with torch.cuda.device(dev):
+        _check(lib().lik_logprob_rows_bwd(_ptr(logits), dt, R, C, ld, _ptr(t), float(scale),
+                                          _ptr(lse), _ptr(g), _ptr(grad), gld, _stream()))
+    return grad
+
+
+def lik_distill_rows(logits, teacher_idx, teacher_logits, teacher_lse=None, scale=1.0,
+                     row_weight=None, want_grad=True, grad_out=None) -> Tuple:
+    """KL divergence from a teacher known by its top logits: teacher_idx [R, K]
+    columns (negative = absent), teacher_logits [R, K] float32.  Without
+    teacher_lse the teacher is renormalised over its list; with it [R] (the
+    log-sum-exp of scale * its logits over all columns) the mass it leaves to
+    the other columns is matched too.  row_weight [R], None = 1 / R.  Returns
+    (loss [1], row_loss [R], grad [R, C] in the logits' type or None)."""
+    dt, R, C, ld = _rows(logits)
+    dev = logits.device
+    if teacher_idx.dim() != 2:
+        raise ValueError("teacher_idx must be [R, K]")
+    K = teacher_idx.shape[1]
+    idx = _row_arg(teacher_idx, (R, K), "teacher_idx", dev, torch.int32)
+    val = _row_arg(teacher_logits, (R, K), "teacher_logits", dev)
+    tl = _row_arg(teacher_lse, (R,), "teacher_lse", dev)
+    w = _row_arg(row_weight, (R,), "row_weight", dev)
+    grad, gld = _row_grad(logits, want_grad, grad_out)
+    with torch.cuda.device(dev):
+        row_loss, loss = _row_outs(R, dev, (R,), (1,))
+        ws, wsb = _rows_workspace(LIK_ROWS_DISTILL, R, C, 0, dt, dev)
+        _check(lib().lik_distill_rows(_ptr(logits), dt, R, C, ld, _ptr(idx), _ptr(val), K,
+                                      _ptr(tl), float(scale), _ptr(w), _ptr(row_loss),
+                                      _ptr(loss), _ptr(grad), gld, _ptr(ws), wsb, _stream()))
+    return loss, row_loss, grad
+
+
+def lik_policy_rows(logits, targets, old_logp, advantage, ref_logp=None, scale=1.0, clip_low=0.2,
+                    clip_high=0.2, kl_coef=0.0, row_weight=None, want_grad=True,
+                    grad_out=None) -> Tuple:
+    """Clipped policy loss on the columns `targets` [R], with a KL term against
+    ref_logp [R] if given.  row_weight [R], None = 1 / R.  Returns (loss [1],
+    row_loss [R], logp [R], grad [R, C] in the logits' type or None)."""
+    dt, R, C, ld = _rows(logits)
+    dev = logits.device
+    t = _row_arg(targets, (R,), "targets", dev, torch.int32)
+    old = _row_arg(old_logp, (R,), "old_logp", dev)
+    adv = _row_arg(advantage, (R,), "advantage", dev)
+    ref = _row_arg(ref_logp, (R,), "ref_logp", dev)
+    w = _row_arg(row_weight, (R,), "row_weight", dev)
+    grad, gld = _row_grad(logits, want_grad, grad_out)
+    with torch.cuda.device(dev):
+        row_loss, logp, loss = _row_outs(R, dev, (R,), (R,), (1,))
+        ws, wsb = _rows_workspace(LIK_ROWS_POLICY, R, C, 0, dt, dev)
+        _check(lib().lik_policy_rows(_ptr(logits), dt, R, C, ld, _ptr(t), _ptr(old), _ptr(adv),
+                                     _ptr(ref), float(scale), float(clip_low), float(clip_high),
+                                     float(kl_coef), _ptr(w), _ptr(row_loss), _ptr(logp),
+                                     _ptr(loss), _ptr(grad), gld, _ptr(ws), wsb, _stream()))
+    return loss, row_loss, logp, grad
+
+
+def lik_preference_rows(logits, targets, seq_offsets, chosen, rejected, ref_logp=None,
+                        kind=LIK_PREF_SIGMOID, beta=0.1, margin=0.0, smoothing=0.0,
+                        mean_logp=False, scale=1.0, pair_weight=None, want_grad=True,
+                        grad_out=None) -> Tuple:
+    """Preference loss on paired log ratios: sequence s is the rows
+    seq_offsets[s] .. seq_offsets[s + 1] - 1, pair p sets sequence chosen[p]
+    against rejected[p]; ref_logp [S] or None.  pair_weight [P], None = 1 / P.
+    Returns (loss [1], pair_loss [P], seq_logp [S], grad [R, C] in the logits'
+    type or None)."""
+    dt, R, C, ld = _rows(logits)
+    dev = logits.device
+    if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 1 or chosen.dim() != 1:
+        raise ValueError("seq_offsets must be [S + 1], chosen and rejected [P]")
+    S, P = seq_offsets.shape[0] - 1, chosen.shape[0]
+    t = _row_arg(targets, (R,), "targets", dev, torch.int32)
+    off = _row_arg(seq_offsets, (S + 1,), "seq_offsets", dev, torch.int32)
+    c = _row_arg(chosen, (P,), "chosen", dev, torch.int32)
+    r = _row_arg(rejected, (P,), "rejected", dev, torch.int32)
+    ref = _row_arg(ref_logp, (S,), "ref_logp", dev)
+    w = _row_arg(pair_weight, (P,), "pair_weight", dev)
+    grad, gld = _row_grad(logits, want_grad, grad_out)
+    with torch.cuda.device(dev):
+        pair_loss, seq, loss = _row_outs(R, dev, (P,), (S,), (1,))
+        ws, wsb = _rows_workspace(LIK_ROWS_PREFERENCE, R, C, S, dt, dev)
+        _check(lib().lik_preference_rows(
+            _ptr(logits), dt, R, C, ld, _ptr(t), _ptr(off), S, _ptr(c), _ptr(r), P, _ptr(ref),
+            int(kind), float(beta), float(margin), float(smoothing), int(bool(mean_logp)),
+            float(scale), _ptr(w), _ptr(pair_loss), _ptr(seq), _ptr(loss), _ptr(grad), gld,
+            _ptr(ws), wsb, _stream()))
+    return loss, pair_loss, seq, grad
 
 
 FORWARD = {"allpairs": lik_maxsim_fwd, "pairwise": lik_maxsim_pairwise_fwd,

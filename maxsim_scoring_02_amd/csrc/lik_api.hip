@@ -14,6 +14,7 @@
 #include <mutex>
 
 #include "lik.h"
+#include "lik_host.h"
 #include "lik_kernels.h"
 #include "lik_plan.h"
 
@@ -29,6 +30,12 @@ namespace {
 
 thread_local char g_last_error[512] = "";
 thread_local hipEvent_t g_prof_start = nullptr, g_prof_stop = nullptr;
+constexpr int64_t kMaxElems = int64_t(1) << 56;
+std::atomic<int> g_dev_ok[64];   // 0 unknown, 1 gfx950, 2 other
+
+}  // namespace
+
+namespace lik {
 
 lik_status fail(lik_status s, const char* fmt, ...) {
   va_list ap;
@@ -43,9 +50,6 @@ lik_status ok() {
   return LIK_OK;
 }
 
-constexpr int64_t kMaxElems = int64_t(1) << 56;
-
-// a*b*c... without overflow, or -1
 int64_t mul_ok(std::initializer_list<int64_t> xs) {
   int64_t r = 1;
   for (int64_t x : xs) {
@@ -55,12 +59,6 @@ int64_t mul_ok(std::initializer_list<int64_t> xs) {
   }
   return r;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-
-std::atomic<int> g_dev_ok[64];   // 0 unknown, 1 gfx950, 2 other
 
 lik_status check_device() {
   int dev = 0;
@@ -79,6 +77,17 @@ lik_status check_device() {
   if (!good) return fail(LIK_ERR_UNSUPPORTED, "device %d is %s, not gfx950", dev, prop.gcnArchName);
   return LIK_OK;
 }
+
+}  // namespace lik
+
+namespace {
+
+using lik::aligned16;
+using lik::aligned4;
+using lik::check_device;
+using lik::fail;
+using lik::mul_ok;
+using lik::ok;
 
 // Common checks.  `D_rows` = number of document token rows, `pairs` = score count.
 struct Shapes {

@@ -23,6 +23,9 @@ Modules:
   pins ``maxsim`` independently of numpy's matmul.
 * ``loss``    float64 row cross-entropy over a score matrix (the loss head
   the colpali pull request puts on the scores), with its gradient.
+* ``rows``    float64 losses over rows of logits (log-probabilities,
+  distillation from top logits, clipped policy loss, preference loss), with
+  their gradients.
 
 Every function here is pinned by the ``-m "not gpu"`` tests (brute force,
 closed forms, finite differences, invariants, integer-exact inputs); none is
@@ -45,4 +48,11 @@ from .maxsim import (  # noqa: F401
     scores_as_float32,
 )
 from .loss import ce_rows  # noqa: F401
+from .rows import (  # noqa: F401
+    logprob_rows,
+    logprob_rows_bwd,
+    distill_rows,
+    policy_rows,
+    preference_rows,
+)
 from . import brute  # noqa: F401

@@ -1,0 +1,710 @@
+"""GPU parity of the row losses (log-probabilities, distillation, policy and
+preference loss) against the float64 oracle, through the binding.  Bounds: see
+rows_bounds.py."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from maxsim_scoring_02_amd import _lib
+from maxsim_scoring_02_amd import workloads as wl
+from parity import gpu_forward, say, to_gpu
+from rows_bounds import U, grad_bound, logp_bound, rounded, row_bounds
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+LOWEST = torch.finfo(F32).min
+
+
+def on_gpu(z, dtype, pad=0, shift=0):
+    """z on the GPU in rows of stride C + pad, `shift` elements into a buffer
+    whose other elements are NaN; and the values it holds there."""
+    R, C = z.shape
+    buf = torch.full((shift + R * (C + pad) + 8,), float("nan"), dtype=dtype)
+    view = buf[shift:shift + R * (C + pad)].view(R, C + pad)[:, :C]
+    view.copy_(torch.from_numpy(np.ascontiguousarray(z)))
+    held = view.double().numpy().copy()
+    dev = buf.cuda()[shift:shift + R * (C + pad)].view(R, C + pad)[:, :C]
+    return dev, held
+
+
+def gpu_out(R, C, dtype, pad, shift):
+    """A strided gradient buffer filled with 7, and its [R, C] view."""
+    buf = torch.full((shift + R * (C + pad) + 8,), 7.0, dtype=dtype, device="cuda")
+    return buf, buf[shift:shift + R * (C + pad)].view(R, C + pad)[:, :C]
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32).cuda()
+
+
+def f32(x):
+    return None if x is None else torch.as_tensor(np.asarray(x), dtype=torch.float32).cuda()
+
+
+def host(x):
+    return x.double().cpu().numpy()
+
+
+def within(x, y, tol, what):
+    x, y, tol = np.asarray(x), np.asarray(y), np.broadcast_to(np.asarray(tol), np.shape(y))
+    assert np.array_equal(np.isnan(x), np.isnan(y)), f"{what}: NaN in other places"
+    fine = ~np.isnan(y)
+    same = x[fine] == y[fine]                 # infinities
+    with np.errstate(invalid="ignore"):
+        off = np.where(same, 0.0, np.abs(x[fine] - y[fine]) - tol[fine])
+    assert not np.any(~(off <= 0)), f"{what}: {np.nanmax(off):.3e} beyond its bound"
+
+
+def draw(R, C, seed, spread=3.0):
+    rng = np.random.default_rng(seed)
+    z = (rng.standard_normal((R, C)) * spread).astype(np.float32)
+    t = rng.integers(0, C, size=R)
+    z[np.arange(R), t] += 4
+    if R > 2:
+        t[R // 2] = -1
+    return rng, z, t
+
+
+# sizes around the widths kernels step in, one column, one row, long rows
+SIZES = [(1, 1), (3, 2), (5, 17), (4, 64), (9, 255), (6, 1000), (3, 4097), (130, 520), (2, 33001),
+         (3, 70000), (1, 140001)]
+TYPES = [F16, BF16, F32]
+
+
+def check_logprob(z, held, t, scale):
+    logp, lse = _lib.lik_logprob_rows_fwd(z, i32(t), scale)
+    rl, rs = oracle.logprob_rows(held, t, scale)
+    q, logq, q_rel, ln_z = row_bounds(held, scale)
+    x_t = np.where(np.isfinite(rl), -rl, 0)
+    within(host(logp), rl, logp_bound(rl, ln_z, x_t), "logp")
+    within(host(lse), rs, ln_z + 2 * U * np.abs(rs), "lse")
+    return logp, lse
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("R,C", SIZES)
+def test_logprob(R, C, dtype):
+    say(f"[rows] logprob {R} x {C} {dtype}")
+    rng, z, t = draw(R, C, R + C)
+    scale = [1.0, 0.6, 1.7][C % 3]
+    pad, shift = [(0, 0), (3, 1), (8, 8)][R % 3]
+    dev, held = on_gpu(z, dtype, pad, shift)
+    check_logprob(dev, held, t, scale)
+    # backward of a given upstream gradient
+    g = rng.standard_normal(R).astype(np.float32)
+    if R > 3:
+        g[0] = 0.0
+    rs = oracle.logprob_rows(held, t, scale)[1].astype(np.float32)
+    buf, out = gpu_out(R, C, dtype, 5, 1)
+    grad = _lib.lik_logprob_rows_bwd(dev, i32(t), f32(rs), f32(g), scale, grad_out=out)
+    ref = oracle.logprob_rows_bwd(held, t, g, scale)
+    q, logq, _, _ = row_bounds(held, scale)
+    q_rel = U * (np.abs(rs)[:, None] + 4 * np.minimum(np.abs(logq), 200.0) + 6)
+    live = (t >= 0) & (g != 0)
+    onehot = np.zeros_like(q)
+    onehot[np.arange(R), np.maximum(t, 0)] = live
+    k = np.where(live, g * scale, 0.0)
+    within(host(grad), ref, grad_bound(k, 2 * U * np.abs(k), onehot, q, q_rel, dtype), "grad")
+    # what lies between the rows stays as it was
+    written = torch.zeros_like(buf, dtype=torch.bool)
+    written[1:1 + R * (C + 5)].view(R, C + 5)[:, :C] = True
+    assert torch.all(buf[~written] == 7)
+
+
+def distill_case(R, C, K, rest, dtype, scale, seed, weight=None, idx=None, val=None, lse=None,
+                 z=None, pad=0, shift=0):
+    rng, zz, _ = draw(R, C, seed)
+    z = zz if z is None else z
+    dev, held = on_gpu(z, dtype, pad, shift)
+    if idx is None:
+        idx = np.stack([rng.permutation(C)[:K] if K <= C else rng.integers(0, C, K)
+                        for _ in range(R)]).reshape(R, K).astype(np.int32)
+        idx[rng.random((R, K)) < 0.1] = -1
+    if val is None:
+        val = (np.take_along_axis(held, np.maximum(idx, 0), 1) +
+               rng.standard_normal((R, K))).astype(np.float32)
+    if rest and lse is None:
+        with np.errstate(divide="ignore"):
+            lse = np.log(np.where(idx >= 0, np.exp(scale * val.astype(np.float64)), 0).sum(1))
+        lse = (np.where(np.isfinite(lse), lse, 0.0) + rng.uniform(0.01, 1.0, R)).astype(np.float32)
+    out = gpu_out(R, C, dtype, pad, shift)[1]
+    loss, rows, grad = _lib.lik_distill_rows(dev, i32(idx), f32(val), f32(lse), scale,
+                                             f32(weight), grad_out=out)
+    rl, rr, rg = oracle.distill_rows(held, idx, val, lse, scale, weight)
+    # bounds
+    q, logq, q_rel, ln_z = row_bounds(held, scale)
+    w = np.full(R, 1.0 / R) if weight is None else np.asarray(weight, dtype=np.float64)
+    tol_l, tol_g = np.zeros(R), np.zeros((R, C))
+    for r in range(R):
+        if w[r] == 0 or np.any(idx[r] >= C):
+            continue
+        on = [k for k in range(K) if idx[r, k] >= 0 and val[r, k] > -np.inf]
+        if lse is None and not on:
+            continue
+        a = scale * val[r].astype(np.float64)
+        lt = lse[r] if lse is not None else np.logaddexp.reduce(a[on])
+        e_p = U * (2 * np.abs(a - lt) + 2 * abs(lt) + 16 + K / 32)
+        p = np.exp(a - lt)
+        p_col, e_col, mass, e_mass = np.zeros(C), np.zeros(C), 0.0, 2 * U
+        for k in on:
+            gap = abs(a[k] - lt - logq[r, idx[r, k]])
+            tol_l[r] += p[k] * (e_p[k] * (gap + 2) + ln_z[r] + U * (4 * gap + 8))
+            p_col[idx[r, k]] += p[k]
+            e_col[idx[r, k]] += p[k] * (e_p[k] + 2 * U)
+            mass += p[k]
+            e_mass += p[k] * e_p[k]
+        listed = np.zeros(C, dtype=bool)
+        listed[idx[r][idx[r] >= 0]] = True
+        p_rest = max(0.0, 1 - mass) if lse is not None and not listed.all() else 0.0
+        tol_g[r] = (mass + p_rest) * q[r] * (q_rel[r] + 4 * U) + q[r] * e_mass + e_col
+        if lse is not None and not listed.all():
+            q_rest = q[r][~listed].sum()
+            gap = abs(np.log(max(p_rest, e_mass)) - np.log(q_rest))
+            share = (q[r] * q_rel[r])[~listed].sum() / q_rest + 2 * ln_z[r]
+            tol_l[r] += e_mass * (gap + 1) + p_rest * (share + U * (2 * gap + 8))
+            tol_g[r] += np.where(listed, 0.0, q[r] / q_rest * (
+                p_rest * (q_rel[r] + share + 4 * U) + e_mass))
+        tol_g[r] *= abs(w[r]) * scale
+    tol_g += 4 * U * np.abs(rg)
+    within(host(rows), rr, tol_l + 2 * U * np.abs(rr), "row_loss")
+    within(host(loss)[0], rl, (np.abs(w) * tol_l).sum() + 3 * U * np.sum(np.abs(w * rr)), "loss")
+    within(host(grad), rg, rounded(rg, tol_g, dtype), "grad")
+    none = _lib.lik_distill_rows(dev, i32(idx), f32(val), f32(lse), scale, f32(weight),
+                                 want_grad=False)
+    assert none[2] is None
+    within(host(none[1]), rr, tol_l + 2 * U * np.abs(rr), "row_loss without gradient")
+    within(host(none[0])[0], rl, (np.abs(w) * tol_l).sum() + 3 * U * np.sum(np.abs(w * rr)),
+           "loss without gradient")
+    return loss, rows, grad
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("R,C", SIZES)
+@pytest.mark.parametrize("rest", [False, True])
+def test_distill(R, C, dtype, rest):
+    K = [1, 5, 32, 100][(R + C) % 4]
+    K = min(K, C)
+    say(f"[rows] distill {R} x {C} K {K} rest {rest} {dtype}")
+    rng = np.random.default_rng(R * C)
+    weight = None if R % 2 else rng.uniform(0.5, 2, R).astype(np.float32)
+    if weight is not None and R > 3:
+        weight[1] = 0.0
+    pad, shift = [(0, 0), (3, 1), (8, 8)][(R + 1) % 3]
+    distill_case(R, C, K, rest, dtype, [1.0, 0.5, 2.0][C % 3], 7 * R + C, weight, pad=pad,
+                 shift=shift)
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("R,C,K", [(3, 40, 1024), (2, 5000, 1024), (3, 9, 0), (200, 30, 30)])
+def test_distill_list_lengths(R, C, K, rest):
+    # 1024 entries over 40 columns: every column many times; none; all columns
+    say(f"[rows] distill lists {R} x {C} K {K} rest {rest}")
+    distill_case(R, C, K, rest, F32, 1.0, 31)
+
+
+def test_distill_odd_lists():
+    say("[rows] distill odd lists")
+    C = 12
+    idx = np.array([[-1, -1, -1, -1],      # no entry
+                    [3, 3, -1, 3],         # one column three times
+                    [5, 7, 5, 2],
+                    [0, 1, 2, 3],
+                    [4, 12, 1, 0],         # a column out of range
+                    [4, 2, 1, 0]], dtype=np.int32)
+    val = np.random.default_rng(3).standard_normal((6, 4)).astype(np.float32)
+    val[3] = -np.inf                       # entries without mass
+    val[2, 1] = -np.inf
+    for lse in (None, np.full(6, 2.5, dtype=np.float32)):
+        loss, rows, grad = distill_case(6, C, 4, lse is not None, F32, 1.0, 5, idx=idx, val=val,
+                                        lse=lse)
+        assert torch.isnan(loss[0]) and torch.isnan(rows[4]) and torch.isnan(grad[4]).all()
+        assert torch.isfinite(grad[[0, 1, 2, 3, 5]]).all()
+    # a student that rules out what the teacher wants
+    z = np.zeros((1, 4), dtype=np.float32)
+    z[0, 1] = -np.inf
+    loss, _, grad = _lib.lik_distill_rows(f32(z), i32([[1, 2]]), f32([[0.0, 0.0]]))
+    assert torch.isinf(loss[0]) and loss[0] > 0
+    assert torch.allclose(grad.cpu(), torch.tensor([[1 / 3, -0.5, 1 / 3 - 0.5, 1 / 3]]))
+
+
+def policy_case(z, t, dtype, scale, seed, weight=None, kl=0.1, low=0.2, high=0.3, pad=0, shift=0,
+                use_ref=True):
+    R, C = z.shape
+    rng = np.random.default_rng(seed)
+    dev, held = on_gpu(z, dtype, pad, shift)
+    with np.errstate(invalid="ignore"):
+        logp = oracle.logprob_rows(held, t, scale)[0]
+    drift = 0.4 * rng.standard_normal(R)
+    for border in (np.log(1 - low) if low < 1 else -9, np.log1p(high)):
+        drift = np.where(np.abs(drift - border) < 1e-3, border + 2e-3, drift)
+    old = np.where(np.isfinite(logp), logp - drift, 0.0).astype(np.float32)
+    adv = rng.standard_normal(R).astype(np.float32)
+    if R > 4:
+        adv[1] = 0.0
+    ref = (np.where(np.isfinite(logp), logp, 0.0) + 0.5 * rng.standard_normal(R)).astype(np.float32)
+    ref = ref if use_ref else None
+    out = gpu_out(R, C, dtype, pad, shift)[1]
+    args = (dev, i32(t), f32(old), f32(adv), f32(ref), scale, low, high, kl, f32(weight))
+    loss, rows, lp, grad = _lib.lik_policy_rows(*args, grad_out=out)
+    with np.errstate(invalid="ignore"):
+        rl, rr, rlp, rg, slope = oracle.policy_rows(held, t, old, adv, ref, scale,
+                                                    np.float32(low), np.float32(high),
+                                                    np.float32(kl), weight)
+    w = np.full(R, 1.0 / R) if weight is None else np.asarray(weight, dtype=np.float64)
+    with np.errstate(invalid="ignore"):
+        q, logq, q_rel, ln_z = row_bounds(held, scale)
+    lp_tol = logp_bound(rlp, ln_z, np.abs(rlp))
+    within(host(lp), rlp, lp_tol, "logp")
+    rho_a = np.exp(rlp - old) * np.abs(adv)
+    d = ref - rlp if use_ref else np.zeros(R)
+    s_tol = rho_a * (lp_tol + U * (2 * np.abs(rlp - old) + 8))
+    s_tol = s_tol + abs(kl) * np.exp(d) * (lp_tol + U * (2 * np.abs(d) + 8)) * use_ref
+    l_tol = s_tol + 4 * U * (np.abs(adv) * 2 + np.abs(rr))
+    on = (t >= 0) & (w != 0)
+    within(host(rows), rr, np.where(on, l_tol, 0.0), "row_loss")
+    within(host(loss)[0], rl, np.nansum(np.abs(w) * l_tol * on) + 2 * U * np.nansum(np.abs(w * rr)),
+           "loss")
+    onehot = np.zeros_like(q)
+    onehot[np.arange(R), np.clip(t, 0, C - 1)] = on
+    k = np.where(on, w * slope * scale, 0.0)
+    k_tol = np.where(on, np.abs(w) * scale * s_tol, 0.0) + 4 * U * np.abs(k)
+    tol = grad_bound(k, k_tol, onehot, np.where(on[:, None], q, 0.0), q_rel, dtype)
+    within(host(grad), rg, tol, "grad")
+    none = _lib.lik_policy_rows(*args, want_grad=False)
+    assert none[3] is None
+    within(host(none[1]), rr, np.where(on, l_tol, 0.0), "row_loss without gradient")
+    return loss, rows, lp, grad
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("R,C", SIZES)
+def test_policy(R, C, dtype):
+    say(f"[rows] policy {R} x {C} {dtype}")
+    rng, z, t = draw(R, C, 3 * R + C)
+    weight = None if C % 2 else rng.uniform(0.5, 2, R).astype(np.float32)
+    if weight is not None and R > 3:
+        weight[1] = 0.0
+    pad, shift = [(0, 0), (3, 1), (8, 8)][(R + 2) % 3]
+    policy_case(z, t, dtype, [1.0, 0.5, 2.0][C % 3], R, weight, kl=[0.0, 0.2][R % 2], pad=pad,
+                shift=shift, use_ref=R % 2 == 1)
+
+
+def test_policy_clips_and_borders():
+    say("[rows] policy borders")
+    rng, z, t = draw(40, 50, 17)
+    policy_case(z, t, F32, 1.0, 3, low=0.0, high=float("inf"), kl=0.0, use_ref=False)
+    policy_case(z, t, F32, 1.0, 4, low=1.0, high=0.0, kl=-0.3)
+    # two columns, so logp = -ln 2 exactly as float32 sees it on both sides: a
+    # row on the border keeps its gradient
+    zz = f32(np.zeros((2, 2)))
+    lp = _lib.lik_logprob_rows_fwd(zz, i32([0, 1]))[0]
+    _, rows, _, grad = _lib.lik_policy_rows(zz, i32([0, 1]), lp, f32([2.0, -2.0]), clip_low=0.0,
+                                            clip_high=0.0)
+    assert torch.allclose(rows.cpu(), torch.tensor([-2.0, 2.0]))
+    assert torch.allclose(grad.abs().cpu(), torch.full((2, 2), 0.5), rtol=1e-5)
+
+
+def test_targets_and_weights_leave_rows_out():
+    """Rows left out are not read: NaN there reaches nothing."""
+    say("[rows] rows left out")
+    rng, z, t = draw(9, 700, 5)
+    t[:] = rng.integers(0, 700, 9)
+    t[[0, 4]] = [-1, -100]
+    w = np.ones(9, dtype=np.float32)
+    w[[2, 8]] = 0.0
+    clean = policy_case(z, t, F32, 1.0, 1, w)
+    z2 = z.copy()
+    z2[[0, 4, 2, 8]] = np.nan
+    dirty, held = on_gpu(z2, F32)
+    old, adv = f32(np.zeros(9)), f32(np.ones(9))
+    loss, rows, lp, grad = _lib.lik_policy_rows(dirty, i32(t), old, adv, row_weight=f32(w))
+    assert torch.isfinite(loss).all() and torch.isfinite(grad).all()
+    for r in (0, 2, 4, 8):
+        assert rows[r] == 0 and lp[r] == 0 and torch.all(grad[r] == 0)
+        assert torch.all(clean[3][r] == 0)
+    w2 = np.ones(9, dtype=np.float32)
+    w2[[0, 2, 4, 8]] = 0.0
+    loss, rows, grad = _lib.lik_distill_rows(dirty, i32(np.tile([1, 2], (9, 1))),
+                                             f32(np.zeros((9, 2))), row_weight=f32(w2))
+    assert torch.isfinite(loss).all() and torch.isfinite(grad).all()
+    lp, lse = _lib.lik_logprob_rows_fwd(dirty, i32(np.where(w2 == 0, -1, t)))
+    assert torch.isfinite(lp).all() and lp[0] == 0 and lse[0] == 0
+
+
+def test_target_out_of_range_is_nan_in_its_row_only():
+    say("[rows] target out of range")
+    rng, z, t = draw(5, 33, 6)
+    t[:] = [1, 33, 5, 2 ** 31 - 1, 7]
+    dev, _ = on_gpu(z, BF16)
+    lp, lse = _lib.lik_logprob_rows_fwd(dev, i32(t))
+    bad = np.array([False, True, False, True, False])
+    assert np.array_equal(np.isnan(host(lp)), bad) and torch.isfinite(lse).all()
+    one = f32(np.ones(5))
+    grad = _lib.lik_logprob_rows_bwd(dev, i32(t), lse, one)
+    assert np.array_equal(np.isnan(host(grad)).all(1), bad)
+    assert np.array_equal(np.isnan(host(grad)).any(1), bad)
+    loss, rows, _, grad = _lib.lik_policy_rows(dev, i32(t), f32(np.zeros(5)), one)
+    assert torch.isnan(loss[0]) and np.array_equal(np.isnan(host(rows)), bad)
+    assert np.array_equal(np.isnan(host(grad)).all(1), bad)
+    assert np.array_equal(np.isnan(host(grad)).any(1), bad)
+
+
+@pytest.mark.parametrize("C", [37, 3000, 80000])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_masked_columns(C, dtype):
+    """-inf and the type's lowest value beside real logits: probability 0; a row
+    all of the lowest value is uniform; a row all of -inf is NaN, alone."""
+    say(f"[rows] masked columns {C} {dtype}")
+    rng, z, t = draw(6, C, 8)
+    t[:] = rng.integers(C // 2, C, 6)
+    low = float(torch.finfo(dtype).min)
+    z[0, :C // 2] = -np.inf
+    z[1, :C // 2] = low
+    z[2] = low
+    z[3] = -np.inf
+    z[4, ::2] = low
+    z[4, 1::2] = -np.inf
+    t[4] = 2 * (C // 4)
+    z[5, :] = -np.inf
+    z[5, t[5]] = 3.0
+    dev, held = on_gpu(z, dtype)
+    lp, lse = _lib.lik_logprob_rows_fwd(dev, i32(t))
+    n_low = (C + 1) // 2
+    with np.errstate(invalid="ignore"):
+        want = oracle.logprob_rows(held, t)[0]
+    assert np.isnan(want[3]) and torch.isnan(lp[3])
+    assert abs(want[2] + np.log(C)) < 1e-9 and abs(want[4] + np.log(n_low)) < 1e-9
+    keep = [0, 1, 2, 4, 5]
+    within(host(lp)[keep], want[keep], 1e-5, "logp")     # |logp| < 32: U (3 * 32 + C / 64 + 24)
+    _, rows, lp2, grad = _lib.lik_policy_rows(dev, i32(t), lp, f32(np.ones(6)), clip_high=1.0)
+    g = host(grad)
+    assert np.all(g[0, :C // 2] == 0) and np.all(g[1, :C // 2] == 0)
+    assert np.isnan(g[3]).all() and np.isfinite(g[keep]).all()
+    assert np.all(g[4, 1::2] == 0) and np.all(g[5][np.arange(C) != t[5]] == 0)
+    # k - (k / Z) e with e = Z: the quotient and the product are rounded, and k
+    assert abs(host(rows)[5] + 1) < 1e-6 and abs(g[5, t[5]]) <= 3 * U / 6
+    if dtype != F16:                       # 1 / (6 C) is below float16's steps
+        off = np.abs(np.delete(g[2], t[2]) * 6 * C - 1)
+        assert off.max() < torch.finfo(dtype).eps + 1e-5
+    idx = np.stack([t, t - 1], 1)
+    loss, rows, grad = _lib.lik_distill_rows(dev, i32(idx), f32(np.zeros((6, 2))))
+    assert np.array_equal(np.isnan(host(rows)), np.arange(6) == 3)
+    assert np.isinf(host(rows)[5]) and np.isfinite(host(grad)[keep]).all()
+
+
+def test_infinite_and_nan_logits_stay_in_their_row():
+    say("[rows] nan and inf logits")
+    rng, z, t = draw(4, 900, 9)
+    t[:] = [3, 4, 5, 6]
+    z[1, 700] = np.nan
+    z[2, 100] = np.inf
+    dev, _ = on_gpu(z, F32)
+    lp, _ = _lib.lik_logprob_rows_fwd(dev, i32(t))
+    assert np.array_equal(np.isnan(host(lp)), [False, True, True, False])
+    _, rows, _, grad = _lib.lik_policy_rows(dev, i32(t), f32(np.zeros(4)), f32(np.ones(4)))
+    assert np.array_equal(np.isnan(host(grad)).any(1), [False, True, True, False])
+    _, rows, grad = _lib.lik_distill_rows(dev, i32(np.tile([1, 2], (4, 1))), f32(np.zeros((4, 2))),
+                                          f32(np.full(4, 1.0)))
+    assert np.array_equal(np.isnan(host(rows)), [False, True, True, False])
+
+
+def pref_case(R, C, S, P, dtype, scale, seed, kind, mean, offsets=None, weight=None, margin=0.0,
+              smoothing=0.0, pad=0, shift=0, use_ref=True, beta=None, chosen=None, rejected=None):
+    rng, z, t = draw(R, C, seed)
+    t[rng.random(R) < 0.1] = -1
+    dev, held = on_gpu(z, dtype, pad, shift)
+    if offsets is None:
+        end = R - R // 10
+        offsets = np.concatenate([[0], np.sort(rng.integers(0, end + 1, S - 1)), [end]])
+    if chosen is None:
+        chosen, rejected = rng.integers(0, S, P), rng.integers(0, S, P)
+    beta = beta if beta is not None else (0.7 if mean else 0.2)
+    seq = oracle.preference_rows(held, t, offsets, [], [], mean=mean, scale=scale)[2]
+    ref = (seq + rng.standard_normal(S) / beta).astype(np.float32) if use_ref else None
+    if kind == _lib.LIK_PREF_HINGE:        # off the hinge
+        off = seq if ref is None else seq - ref
+        ok = (chosen >= 0) & (chosen < S) & (rejected >= 0) & (rejected < S)
+        h = beta * (off[chosen % S] - off[rejected % S]) - margin
+        chosen = np.where(ok & (np.abs(h - 1) < 1e-3), rejected, chosen)
+    out = gpu_out(R, C, dtype, pad, shift)[1]
+    args = (dev, i32(t), i32(offsets), i32(chosen), i32(rejected), f32(ref), kind, beta, margin,
+            smoothing, mean, scale, f32(weight))
+    loss, pairs, sl, grad = _lib.lik_preference_rows(*args, grad_out=out)
+    b32 = float(np.float32(beta))
+    rl, rp, rs, rg, d_row = oracle.preference_rows(
+        held, t, offsets, chosen, rejected, ref, kind, b32, float(np.float32(margin)),
+        float(np.float32(smoothing)), mean, scale, weight)
+    q, logq, q_rel, ln_z = row_bounds(held, scale)
+    logp = oracle.logprob_rows(held, t, scale)[0]
+    row_tol = np.where(t >= 0, logp_bound(logp, ln_z, np.abs(logp)), 0.0)
+    s_tol, n = np.zeros(S), np.ones(S)
+    for s in range(S):
+        a, b = offsets[s], offsets[s + 1]
+        n[s] = max(1, (t[a:b] >= 0).sum()) if mean else 1
+        s_tol[s] = row_tol[a:b].sum() / n[s]
+    within(host(sl), rs, s_tol + U * np.abs(rs), "seq_logp")
+    w = (np.full(P, 1.0 / max(P, 1)) if weight is None else np.asarray(weight, dtype=np.float64))
+    p_tol, c_tol = np.zeros(P), np.zeros(S)
+    for i in range(P):
+        c, r = chosen[i], rejected[i]
+        if not (0 <= c < S and 0 <= r < S):
+            continue
+        d_tol = s_tol[c] + s_tol[r]
+        steep = np.sqrt(rp[i]) * 2 if kind == _lib.LIK_PREF_SQUARE else b32
+        bend = 2.0 if kind == _lib.LIK_PREF_SQUARE else b32 * b32 / 4 * (kind == 0)
+        p_tol[i] = steep * d_tol + d_tol ** 2 + U * np.abs(rp[i]) + 1e-30
+        if w[i] != 0 and c != r:
+            for s in (c, r):
+                c_tol[s] += abs(w[i]) * bend * d_tol
+    within(host(pairs), rp, p_tol, "pair_loss")
+    on = (w != 0) if P else np.zeros(0, bool)
+    within(host(loss)[0], rl, np.sum((np.abs(w) * p_tol)[on]) + U * abs(rl) +
+           4 * U * np.sum(np.abs(w * rp)[on]), "loss")
+    k = d_row * scale
+    k_tol = 3 * U * np.abs(k)
+    for s in range(S):
+        a, b = offsets[s], offsets[s + 1]
+        k_tol[a:b] += np.where(t[a:b] >= 0, c_tol[s] / n[s] * scale, 0.0)
+    onehot = np.zeros_like(q)
+    onehot[np.arange(R), np.maximum(t, 0)] = d_row != 0
+    within(host(grad), rg, grad_bound(k, k_tol, onehot, q, q_rel, dtype), "grad")
+    none = _lib.lik_preference_rows(*args, want_grad=False)
+    assert none[3] is None and torch.equal(none[1], pairs) | torch.isnan(pairs).any()
+    return loss, pairs, sl, grad
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("R,C,S,P", [(2, 1, 2, 1), (6, 2, 3, 4), (40, 17, 8, 8), (120, 300, 16, 15),
+                                     (33, 4097, 2, 1), (64, 1000, 64, 300), (12, 70000, 4, 2),
+                                     (5, 140001, 2, 3)])
+def test_preference(R, C, S, P, dtype):
+    say(f"[rows] preference {R} x {C} S {S} P {P} {dtype}")
+    kind = (R + C) % 3
+    rng = np.random.default_rng(R)
+    weight = None if R % 2 else rng.uniform(0.5, 2, P).astype(np.float32)
+    if weight is not None and P > 3:
+        weight[1] = 0.0
+    pad, shift = [(0, 0), (3, 1), (8, 8)][S % 3]
+    pref_case(R, C, S, P, dtype, [1.0, 0.5, 2.0][C % 3], R + C, kind, S % 2 == 0, weight=weight,
+              pad=pad, shift=shift, use_ref=P != 4)
+
+
+@pytest.mark.parametrize("kind,margin,smoothing", [(0, 0.5, 0.0), (0, 0.0, 0.2), (0, -0.3, 0.5),
+                                                   (1, 0.4, 0.0), (2, 0.0, 0.0)])
+@pytest.mark.parametrize("mean", [False, True])
+def test_preference_kinds(kind, margin, smoothing, mean):
+    say(f"[rows] preference kind {kind} margin {margin} smoothing {smoothing} mean {mean}")
+    pref_case(90, 130, 9, 12, F32, 1.0, 77, kind, mean, margin=margin, smoothing=smoothing)
+
+
+def test_preference_odd_sequences_and_pairs():
+    say("[rows] preference odd sequences")
+    # rows before the first and behind the last sequence, empty sequences; the
+    # same pair twice, a sequence against itself, numbers out of range
+    off = np.array([2, 2, 6, 6, 11, 14])
+    c, r = np.array([1, 1, 3, 5, -1, 0, 4]), np.array([3, 3, 3, 1, 2, 2, 1])
+    w = np.array([1, 1, 1, 0.0, 0.0, 2, 1], dtype=np.float32)
+    loss, pairs, seq, grad = pref_case(20, 60, 5, 7, F32, 1.0, 78, 0, False, off, w, chosen=c,
+                                       rejected=r)
+    assert torch.isnan(pairs[3]) and torch.isnan(pairs[4]) and torch.isfinite(loss[0])
+    assert torch.all(grad[:2] == 0) and torch.all(grad[14:] == 0)
+    # with weight, a pair out of range makes the loss NaN and no gradient
+    loss, _, _, grad2 = pref_case(20, 60, 5, 7, F32, 1.0, 78, 0, False, off,
+                                  np.ones(7, dtype=np.float32), chosen=c, rejected=r)
+    assert torch.isnan(loss[0]) and torch.isfinite(grad2).all()
+    # no pairs, no sequences
+    loss, _, _, grad = pref_case(20, 60, 5, 0, F32, 1.0, 78, 0, False, off,
+                                 chosen=np.zeros(0, int), rejected=np.zeros(0, int))
+    assert loss[0] == 0 and torch.all(grad == 0)
+    z = f32(np.random.default_rng(0).standard_normal((3, 8)))
+    loss, pairs, seq, grad = _lib.lik_preference_rows(z, i32([1, 2, 3]), i32([0]), i32([0]), i32([0]))
+    assert torch.isnan(pairs).all() and seq.numel() == 0 and torch.all(grad == 0)
+
+
+def test_preference_reads_only_rows_of_sequences():
+    say("[rows] preference reads")
+    rng, z, t = draw(12, 200, 12)
+    t[:] = 5
+    z[:2] = np.nan
+    z[10:] = np.nan
+    z[4] = np.nan
+    t[4] = -1
+    dev, _ = on_gpu(z, F32)
+    out = _lib.lik_preference_rows(dev, i32(t), i32([2, 6, 10]), i32([0]), i32([1]))
+    assert all(torch.isfinite(x).all() for x in out)
+    # NaN inside a sequence: its pair and the rows of that pair's sequences
+    z[7, 9] = np.nan
+    dev, _ = on_gpu(z, F32)
+    loss, pairs, seq, grad = _lib.lik_preference_rows(dev, i32(t), i32([2, 6, 8, 10]), i32([0]),
+                                                      i32([1]))
+    assert torch.isnan(loss).all() and torch.isnan(seq[1]) and torch.isfinite(seq[[0, 2]]).all()
+    assert torch.all(grad[8:10] == 0)
+
+
+@pytest.mark.parametrize("op", ["logprob", "distill", "policy", "preference"])
+@pytest.mark.parametrize("R,C,dtype", [(7, 100, F32), (40, 9001, BF16), (3, 131072, BF16)])
+def test_gradient_against_differences(op, R, C, dtype):
+    """The GPU gradient along a direction against differences of the GPU loss
+    in float32 logits: rounding of the two losses over the step, and h^2 / 6 of
+    a third derivative of a log-softmax along a direction of entries at most a
+    (below (2 a)^3 each row), for slopes of order one."""
+    if dtype != F32:
+        dtype = F32 if C < 10000 else BF16
+    rng, z, t = draw(R, C, 21)
+    t[t < 0] = 0
+    v = rng.choice([-1.0, 1.0], size=(R, C)).astype(np.float32)
+    h = 2.0 ** -5
+    # entries that both types hold exactly with the step on top
+    z = np.round(z * 16) / 16
+    old = oracle.logprob_rows(z, t)[0] - 0.1
+    K = 4
+    idx = rng.integers(0, C, size=(R, K))
+    val = rng.standard_normal((R, K))
+    S = 2
+    off = [0, R // 2, R]
+    w = np.ones(R)
+
+    def run(x, grad):
+        x = torch.from_numpy(x).to(F32).cuda()
+        if op == "logprob":
+            lp, lse = _lib.lik_logprob_rows_fwd(x, i32(t))
+            g = _lib.lik_logprob_rows_bwd(x, i32(t), lse, f32(w)) if grad else None
+            return host(lp).sum(), g
+        if op == "distill":
+            l, rows, g = _lib.lik_distill_rows(x, i32(idx), f32(val), f32(np.full(R, 3.0)),
+                                               row_weight=f32(w), want_grad=grad)
+            return host(rows).sum(), g
+        if op == "policy":
+            l, rows, _, g = _lib.lik_policy_rows(x, i32(t), f32(old), f32(w), clip_high=9.0,
+                                                 clip_low=1.0, row_weight=f32(w), want_grad=grad)
+            return host(rows).sum(), g
+        l, pairs, _, g = _lib.lik_preference_rows(x, i32(t), i32(off), i32([0]), i32([1]),
+                                                  beta=0.5, want_grad=grad)
+        return host(pairs).sum(), g
+
+    _, g = run(z, True)
+    along = float(np.sum(host(g) * v))
+    up, down = run(z + h * v, False)[0], run(z - h * v, False)[0]
+    size = R * (np.abs(z).max() + np.log(C) + 1)
+    tol = 2 * (20 + C / 64) * U * size / (2 * h) + h * h / 6 * R * 8 * 4
+    assert abs((up - down) / (2 * h) - along) <= tol, (along, (up - down) / (2 * h), tol)
+
+
+def test_bitwise_reproducible_and_on_another_stream():
+    say("[rows] reproducible")
+    rng, z, t = draw(300, 2500, 30)
+    dev, _ = on_gpu(z, BF16)
+    idx = rng.integers(0, 2500, size=(300, 40))
+    idx[:, 5] = idx[:, 3]                     # the same column twice
+    val = rng.standard_normal((300, 40))
+    off = np.arange(0, 301, 10)
+    c, r = rng.integers(0, 30, 50), rng.integers(0, 30, 50)
+
+    def everything():
+        lp, lse = _lib.lik_logprob_rows_fwd(dev, i32(t))
+        return [lp, lse, _lib.lik_logprob_rows_bwd(dev, i32(t), lse, lp),
+                *_lib.lik_distill_rows(dev, i32(idx), f32(val), f32(np.full(300, 5.0))),
+                *_lib.lik_policy_rows(dev, i32(t), lp, lp, lse),
+                *_lib.lik_preference_rows(dev, i32(t), i32(off), i32(c), i32(r))]
+
+    a = everything()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        b = everything()
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_captured_and_replayed():
+    """Every operator in one captured graph, replayed on new inputs with eager
+    work of the same calls between the replays."""
+    say("[rows] graph")
+    rng, z, t = draw(64, 3001, 40)
+    zs = [torch.from_numpy(z).cuda().to(BF16), torch.from_numpy(z[::-1].copy()).cuda().to(BF16)]
+    tt = i32(np.maximum(t, 0))
+    idx, val = i32(rng.integers(0, 3001, size=(64, 20))), f32(rng.standard_normal((64, 20)))
+    off, c, r = i32(np.arange(0, 65, 8)), i32([0, 2, 4]), i32([1, 3, 5])
+    old, adv = f32(-5 * np.ones(64)), f32(rng.standard_normal(64))
+    z_in = zs[0].clone()
+
+    def everything():
+        lp, lse = _lib.lik_logprob_rows_fwd(z_in, tt)
+        return [lp, lse, _lib.lik_logprob_rows_bwd(z_in, tt, lse, adv),
+                *_lib.lik_distill_rows(z_in, idx, val),
+                *_lib.lik_policy_rows(z_in, tt, old, adv, lp),
+                *_lib.lik_preference_rows(z_in, tt, off, c, r)]
+
+    everything()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = everything()
+    for k in (0, 1, 0, 1):
+        z_in.copy_(zs[k])
+        want = [x.clone() for x in everything()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(outs, want))
+
+
+def test_together_with_maxsim_scores():
+    """A distillation step on kd scores and a policy step on all-pairs scores:
+    MaxSim forward, the loss on its scores, MaxSim backward, against the oracle
+    chain; the log-probabilities of the first feed the second and the pairs."""
+    say("[rows] with maxsim")
+    w = wl.kd_candidates(B=6, N=5, Ld=300)
+    Q, D, qm, dm = to_gpu(w)
+    s, a = _lib.lik_maxsim_kd_fwd(Q, D, qm, dm)
+    rng = np.random.default_rng(5)
+    idx = np.stack([rng.permutation(5)[:3] for _ in range(6)])
+    val = (rng.standard_normal((6, 3)) * 2).astype(np.float32)
+    loss, rows, g = _lib.lik_distill_rows(s, i32(idx), f32(val), scale=0.5)
+    gQ, gD = _lib.lik_maxsim_kd_bwd(Q, D, g, a, qm, dm)
+    Qn, Dn, qmn, dmn = w.numpy_inputs()
+    ref = oracle.maxsim_kd(Qn, Dn, qmn, dmn)
+    rl, rr, rg = oracle.distill_rows(ref.scores, idx, val, scale=0.5)
+    assert abs(float(loss[0]) - rl) <= 1e-4
+    merged = oracle.admissible_argmax(ref, a.cpu().numpy(), Qn, Dn, dmn, "kd")
+    rQ, rD = oracle.maxsim_kd_bwd(Qn, Dn, rg, merged, qmn, dmn)
+    for x, y in ((host(gQ), rQ), (host(gD), rD)):
+        assert np.all(np.abs(x - y) <= 1e-3 * np.abs(y) + 1e-5 * np.abs(y).max())
+
+    w = wl.inbatch_pages(B=20)
+    Q, D, qm, dm = to_gpu(w)
+    s, a = _lib.lik_maxsim_fwd(Q, D, qm, dm)
+    t = rng.integers(0, 20, 20)
+    old, _ = _lib.lik_logprob_rows_fwd(s, i32(t))
+    adv = rng.standard_normal(20).astype(np.float32)
+    loss, rows, lp, g = _lib.lik_policy_rows(s, i32(t), old, f32(adv), old - 0.1, kl_coef=0.1)
+    assert torch.equal(lp, old)               # the same arithmetic on the same scores
+    gQ, gD = _lib.lik_maxsim_bwd(Q, D, g, a, qm, dm)
+    off, c, r = np.arange(0, 21, 4), [0, 1], [2, 3]
+    ploss, _, seq, pg = _lib.lik_preference_rows(s, i32(t), i32(off), i32(c), i32(r))
+    within(host(seq), host(old).reshape(5, 4).sum(1), 8 * U * 40, "sequences of rows")
+    Qn, Dn, qmn, dmn = w.numpy_inputs()
+    ref = oracle.maxsim_allpairs(Qn, Dn, qmn, dmn)
+    rlp = oracle.logprob_rows(ref.scores, t)[0]
+    rl, _, _, rg, _ = oracle.policy_rows(ref.scores, t, rlp, adv, rlp - np.float32(0.1), kl=0.1)
+    assert abs(float(loss[0]) - rl) <= 1e-4
+    merged = oracle.admissible_argmax(ref, a.cpu().numpy(), Qn, Dn, dmn, "allpairs")
+    rQ, rD = oracle.maxsim_allpairs_bwd(Qn, Dn, rg, merged, qmn, dmn)
+    for x, y in ((host(gQ), rQ), (host(gD), rD)):
+        assert np.all(np.abs(x - y) <= 1e-3 * np.abs(y) + 1e-5 * np.abs(y).max())
+    rl, _, _, rg, _ = oracle.preference_rows(ref.scores, t, off, c, r)
+    assert abs(float(ploss[0]) - rl) <= 1e-4
+
+
+def test_no_rows():
+    z = torch.empty((0, 9), device="cuda")
+    e, i = torch.empty(0, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda")
+    assert _lib.lik_logprob_rows_fwd(z, i)[0].numel() == 0
+    assert _lib.lik_policy_rows(z, i, e, e)[0].item() == 0
+    assert _lib.lik_distill_rows(z, i.view(0, 1), e.view(0, 1))[0].item() == 0
+    out = _lib.lik_preference_rows(z, i, i32([0, 0]), i32([0]), i32([0]))
+    assert out[0].item() == 0 and out[3].shape == (0, 9)

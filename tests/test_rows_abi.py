@@ -1,0 +1,205 @@
+"""Host-side checks of the row losses' C ABI (include/lik_rows.h) and of their
+binding: exports, refusals with their status, and calls without rows.  No GPU
+is needed: every call fails a check or has nothing to do."""
+
+import ctypes
+
+import pytest
+import torch
+
+from maxsim_scoring_02_amd import _lib
+from maxsim_scoring_02_amd._lib import (LIK_BF16, LIK_ERR_INVALID_ARG, LIK_ERR_UNSUPPORTED,
+                                        LIK_F16, LIK_F32, LIK_OK)
+
+P = ctypes.c_void_p
+A, B = P(0x100000), P(0x900000)      # never dereferenced; far enough apart not to overlap
+MIS = P(0x100002)
+
+
+@pytest.fixture(scope="module")
+def L():
+    return _lib.lib()
+
+
+def test_exports_every_declared_function(L):
+    names = _lib.header_functions(_lib.ROWS_HEADER_PATH)
+    assert set(names) == set(_lib.ROWS_SIGNATURES)
+    for n in names:
+        assert hasattr(L, n)
+
+
+BASE = dict(logits=A, dtype=LIK_F32, R=4, C=8, ld=8)
+ARGS = {
+    "lik_logprob_rows_fwd": dict(BASE, targets=B, scale=1.0, logp=B, lse=B, ws=B, wsb=1 << 30,
+                                 stream=None),
+    "lik_logprob_rows_bwd": dict(BASE, targets=B, scale=1.0, lse=B, grad_logp=B, grad=B, grad_ld=8,
+                                 stream=None),
+    "lik_distill_rows": dict(BASE, idx=B, val=B, K=3, teacher_lse=None, scale=1.0, weight=None,
+                             row_loss=B, loss=B, grad=B, grad_ld=8, ws=B, wsb=1 << 30, stream=None),
+    "lik_policy_rows": dict(BASE, targets=B, old=B, adv=B, ref=None, scale=1.0, low=0.2, high=0.2,
+                            kl=0.0, weight=None, row_loss=B, logp=B, loss=B, grad=B, grad_ld=8,
+                            ws=B, wsb=1 << 30, stream=None),
+    "lik_preference_rows": dict(BASE, targets=B, offsets=B, S=2, chosen=B, rejected=B, P=1,
+                                ref=None, kind=0, beta=0.1, margin=0.0, smoothing=0.0, mean=0,
+                                scale=1.0, weight=None, pair_loss=B, seq_logp=B, loss=B, grad=B,
+                                grad_ld=8, ws=B, wsb=1 << 30, stream=None),
+}
+
+
+def call(L, name, **kw):
+    a = dict(ARGS[name])
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return getattr(L, name)(*a.values())
+
+
+@pytest.mark.parametrize("name", sorted(ARGS))
+@pytest.mark.parametrize("kw,msg", [
+    (dict(logits=None), "logits is NULL"),
+    (dict(logits=MIS), "aligned"),
+    (dict(dtype=3), "dtype"),
+    (dict(dtype=-1), "dtype"),
+    (dict(R=-1), "negative"),
+    (dict(C=-1), "negative"),
+    (dict(C=0, ld=0), "no columns"),
+    (dict(ld=7), "ld 7"),
+    (dict(R=1 << 40, ld=1 << 30), "overflows"),
+    (dict(scale=0.0), "scale"),
+    (dict(scale=-1.0), "scale"),
+    (dict(scale=float("nan")), "scale"),
+    (dict(scale=float("inf")), "scale"),
+])
+def test_common_refusals(L, name, kw, msg):
+    assert call(L, name, **kw) == LIK_ERR_INVALID_ARG
+    assert msg in L.lik_last_error().decode()
+
+
+@pytest.mark.parametrize("name", sorted(n for n in ARGS if "grad" in ARGS[n]))
+def test_gradient_refusals(L, name):
+    for kw, msg in ((dict(grad_ld=7), "grad_ld 7"), (dict(grad=MIS), "aligned"),
+                    (dict(grad=A), "overlaps"), (dict(grad=P(A.value + 64)), "overlaps"),
+                    (dict(grad=P(A.value - 64)), "overlaps")):
+        assert call(L, name, **kw) == LIK_ERR_INVALID_ARG
+        assert msg in L.lik_last_error().decode()
+    # 16-bit logits may start at any even address
+    assert call(L, name, dtype=LIK_F16, logits=MIS, scale=0.0) == LIK_ERR_INVALID_ARG
+    assert "scale" in L.lik_last_error().decode()
+
+
+@pytest.mark.parametrize("name,fields", [
+    ("lik_logprob_rows_fwd", ["targets", "logp", "lse"]),
+    ("lik_logprob_rows_bwd", ["targets", "lse", "grad_logp", "grad"]),
+    ("lik_distill_rows", ["idx", "val", "row_loss", "loss"]),
+    ("lik_policy_rows", ["targets", "old", "adv", "row_loss", "logp", "loss"]),
+    ("lik_preference_rows", ["targets", "offsets", "chosen", "rejected", "pair_loss", "seq_logp",
+                             "loss"]),
+])
+def test_required_pointers(L, name, fields):
+    for f in fields:
+        assert call(L, name, **{f: None}) == LIK_ERR_INVALID_ARG
+        assert "NULL" in L.lik_last_error().decode()
+        if f != "grad":
+            assert call(L, name, **{f: MIS}) == LIK_ERR_INVALID_ARG
+            assert "aligned" in L.lik_last_error().decode()
+
+
+@pytest.mark.parametrize("name,kw,status,msg", [
+    ("lik_distill_rows", dict(K=-1), LIK_ERR_INVALID_ARG, "negative K"),
+    ("lik_distill_rows", dict(K=1025), LIK_ERR_UNSUPPORTED, "K <= 1024"),
+    ("lik_distill_rows", dict(C=(1 << 20) + 1, ld=(1 << 20) + 1, grad=None), LIK_ERR_UNSUPPORTED,
+     "C <= 1048576"),
+    ("lik_distill_rows", dict(weight=MIS), LIK_ERR_INVALID_ARG, "aligned"),
+    ("lik_distill_rows", dict(teacher_lse=MIS), LIK_ERR_INVALID_ARG, "aligned"),
+    ("lik_policy_rows", dict(low=-0.1), LIK_ERR_INVALID_ARG, "clip_low"),
+    ("lik_policy_rows", dict(low=1.5), LIK_ERR_INVALID_ARG, "clip_low"),
+    ("lik_policy_rows", dict(high=-0.1), LIK_ERR_INVALID_ARG, "clip_high"),
+    ("lik_policy_rows", dict(high=float("nan")), LIK_ERR_INVALID_ARG, "clip_high"),
+    ("lik_policy_rows", dict(kl=float("inf")), LIK_ERR_INVALID_ARG, "kl_coef"),
+    ("lik_policy_rows", dict(ref=MIS), LIK_ERR_INVALID_ARG, "aligned"),
+    ("lik_preference_rows", dict(S=-1), LIK_ERR_INVALID_ARG, "negative"),
+    ("lik_preference_rows", dict(P=-1), LIK_ERR_INVALID_ARG, "negative"),
+    ("lik_preference_rows", dict(kind=3), LIK_ERR_INVALID_ARG, "kind"),
+    ("lik_preference_rows", dict(beta=0.0), LIK_ERR_INVALID_ARG, "beta"),
+    ("lik_preference_rows", dict(beta=float("inf")), LIK_ERR_INVALID_ARG, "beta"),
+    ("lik_preference_rows", dict(margin=float("nan")), LIK_ERR_INVALID_ARG, "margin"),
+    ("lik_preference_rows", dict(smoothing=0.6), LIK_ERR_INVALID_ARG, "smoothing"),
+    ("lik_preference_rows", dict(kind=1, smoothing=0.1), LIK_ERR_INVALID_ARG, "smoothing"),
+    ("lik_preference_rows", dict(kind=2, margin=0.1), LIK_ERR_INVALID_ARG, "margin"),
+])
+def test_refusals_of_each_operator(L, name, kw, status, msg):
+    assert call(L, name, **kw) == status
+    assert msg in L.lik_last_error().decode()
+
+
+def test_workspace_is_checked(L):
+    need = L.lik_rows_workspace_bytes(_lib.LIK_ROWS_PREFERENCE, 4, 8, 2, LIK_F32)
+    assert 0 < need < 1 << 30
+    for kw in (dict(wsb=need - 1), dict(ws=None)):
+        assert call(L, "lik_preference_rows", **kw) == LIK_ERR_INVALID_ARG
+        assert "workspace too small" in L.lik_last_error().decode()
+    assert call(L, "lik_preference_rows", ws=P(B.value + 4)) == LIK_ERR_INVALID_ARG
+    big = ctypes.c_size_t(-1).value
+    w = L.lik_rows_workspace_bytes
+    assert w(_lib.LIK_ROWS_PREFERENCE, -1, 8, 2, LIK_F32) == big
+    assert w(_lib.LIK_ROWS_PREFERENCE, 4, 8, -2, LIK_F32) == big
+    assert w(_lib.LIK_ROWS_POLICY, 4, 8, 0, 9) == big and w(9, 4, 8, 0, LIK_F32) == big
+    assert w(_lib.LIK_ROWS_POLICY, 1 << 40, 1 << 40, 0, LIK_F32) == big
+    for op in range(5):
+        assert w(op, 0, 8, 0, LIK_BF16) == 0
+
+
+@pytest.mark.parametrize("name", sorted(ARGS))
+def test_calls_without_rows_do_nothing(L, name):
+    kw = {k: None for k, v in ARGS[name].items() if isinstance(v, P)}
+    assert call(L, name, R=0, **kw) == LIK_OK
+
+
+def test_a_sound_call_reaches_the_device_check(L):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present; the pointers are not real")
+    for name in ARGS:
+        assert call(L, name) == LIK_ERR_UNSUPPORTED
+        assert "device" in L.lik_last_error().decode()
+
+
+def test_binding_refuses_before_the_library(monkeypatch):
+    def no_library():
+        raise AssertionError("the library was reached")
+
+    monkeypatch.setattr(_lib, "lib", no_library)
+    z, t, f = torch.zeros(3, 5), torch.zeros(3, dtype=torch.int32), torch.zeros(3)
+    calls = [lambda x: _lib.lik_logprob_rows_fwd(x, t), lambda x: _lib.lik_logprob_rows_bwd(x, t, f, f),
+             lambda x: _lib.lik_distill_rows(x, t[:, None], f[:, None]),
+             lambda x: _lib.lik_policy_rows(x, t, f, f),
+             lambda x: _lib.lik_preference_rows(x, t, t[:2], t[:1], t[:1])]
+    for c in calls:
+        with pytest.raises(ValueError, match="GPU"):
+            c(z)
+        with pytest.raises(ValueError, match="2-D"):
+            c(z[0])
+        with pytest.raises(ValueError, match="float16"):
+            c(z.double())
+
+
+def test_binding_checks_shapes_strides_and_types():
+    z = torch.zeros(4, 6)
+    assert _lib._row_stride(z, "x") == 6 and _lib._row_stride(z[:, :5], "x") == 6
+    assert _lib._row_stride(z[:1, :5], "x") == 5 and _lib._row_stride(z[:, 2:3], "x") == 6
+    with pytest.raises(ValueError, match="dense"):
+        _lib._row_stride(z.T, "x")
+    with pytest.raises(ValueError, match="overlap"):
+        _lib._row_stride(z[:1].expand(4, 6), "x")
+    dev = z.device
+    with pytest.raises(ValueError, match="shape"):
+        _lib._row_arg(torch.zeros(3), (4,), "w", dev)
+    with pytest.raises(ValueError, match="float32"):
+        _lib._row_arg(torch.zeros(4, dtype=torch.float64), (4,), "w", dev)
+    with pytest.raises(ValueError, match="int32"):
+        _lib._row_arg(torch.zeros(4), (4,), "t", dev, torch.int32)
+    t = _lib._row_arg(torch.tensor([2 ** 31 + 7, -100, 5, -2 ** 40]), (4,), "t", dev, torch.int32)
+    assert t.tolist() == [2 ** 31 - 1, -1, 5, -1]
+    for out in (torch.zeros(4, 5), torch.zeros(4, 6, dtype=torch.float16)):
+        with pytest.raises(ValueError, match="grad_out"):
+            _lib._row_grad(z, True, out)
+    with pytest.raises(ValueError, match="want_grad"):
+        _lib._row_grad(z, False, z)
