@@ -17,15 +17,12 @@ using lik::ok;
 
 constexpr int64_t kMaxRows = INT32_MAX;
 
-int64_t elem_bytes(lik_dtype t) {
-  return t == LIK_F32 ? 4 : (t == LIK_F16 || t == LIK_BF16 ? 2 : 0);
-}
 
 // What every operator checks: sizes, type, scale, logits and gradient.
 // `done` is set when there is nothing to do.
 lik_status check_rows(const lik::Rows& a, bool need_grad, bool* done) {
   *done = false;
-  const int64_t size = elem_bytes(a.dtype);
+  const int64_t size = lik::elem_bytes_of(a.dtype);
   if (!size) return fail(LIK_ERR_INVALID_ARG, "unknown dtype %d for logits", (int)a.dtype);
   if (a.R < 0 || a.C < 0)
     return fail(LIK_ERR_INVALID_ARG, "negative size (R %lld, C %lld)", (long long)a.R,
@@ -104,18 +101,21 @@ extern "C" {
 
 size_t lik_rows_workspace_bytes(lik_rows_op op, int64_t R, int64_t C, int64_t n_seqs,
                                 lik_dtype dtype) {
-  const int64_t size = elem_bytes(dtype);
+  const int64_t size = lik::elem_bytes_of(dtype);
   if (!size || R < 0 || C < 0 || mul_ok({R, C, size}) < 0 || mul_ok({R, 64}) < 0) return SIZE_MAX;
+  if (R > kMaxRows || C > kMaxRows) return SIZE_MAX;
   switch (op) {
-    case LIK_ROWS_LOGPROB_FWD:
     case LIK_ROWS_LOGPROB_BWD:
+      return 0;
+    case LIK_ROWS_LOGPROB_FWD:
+      return R == 0 || C == 0 ? 0 : lik::parts_layout(R, C, dtype).bytes;
     case LIK_ROWS_DISTILL:
     case LIK_ROWS_POLICY:
-      return 0;
+      return R == 0 || C == 0 || lik::rows_held(R, C, dtype) ? 0
+                                                             : lik::parts_layout(R, C, dtype).bytes;
     case LIK_ROWS_PREFERENCE:
       if (n_seqs < 0 || mul_ok({n_seqs, 64}) < 0) return SIZE_MAX;
-      if (R == 0 || C == 0) return 0;
-      return lik::pref_layout(R, n_seqs).bytes;
+      return R == 0 || C == 0 ? 0 : lik::pref_layout(R, C, n_seqs, dtype).bytes;
   }
   return SIZE_MAX;
 }
@@ -133,7 +133,8 @@ lik_status lik_logprob_rows_fwd(const void* logits, lik_dtype dtype, int64_t R, 
   LIK_TRY(need4(lse, "lse"));
   LIK_TRY(check_workspace(LIK_ROWS_LOGPROB_FWD, a, 0, workspace, workspace_bytes));
   LIK_TRY(check_device());
-  return launched(lik::run_logprob_fwd(a, targets, logp, lse, static_cast<hipStream_t>(stream)));
+  return launched(lik::run_logprob_fwd(a, targets, logp, lse, static_cast<char*>(workspace),
+                                       static_cast<hipStream_t>(stream)));
 }
 
 lik_status lik_logprob_rows_bwd(const void* logits, lik_dtype dtype, int64_t R, int64_t C,
@@ -180,7 +181,8 @@ lik_status lik_distill_rows(const void* logits, lik_dtype dtype, int64_t R, int6
   LIK_TRY(check_workspace(LIK_ROWS_DISTILL, a, 0, workspace, workspace_bytes));
   LIK_TRY(check_device());
   return launched(lik::run_distill(a, teacher_idx, teacher_val, K, teacher_lse, row_weight,
-                                   row_loss, loss, static_cast<hipStream_t>(stream)));
+                                   row_loss, loss, static_cast<char*>(workspace),
+                                   static_cast<hipStream_t>(stream)));
 }
 
 lik_status lik_policy_rows(const void* logits, lik_dtype dtype, int64_t R, int64_t C, int64_t ld,
@@ -209,6 +211,7 @@ lik_status lik_policy_rows(const void* logits, lik_dtype dtype, int64_t R, int64
   LIK_TRY(check_device());
   return launched(lik::run_policy(a, targets, old_logp, advantage, ref_logp, clip_low, clip_high,
                                   kl_coef, row_weight, row_loss, logp, loss,
+                                  static_cast<char*>(workspace),
                                   static_cast<hipStream_t>(stream)));
 }
 

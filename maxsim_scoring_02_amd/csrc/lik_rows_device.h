@@ -1,7 +1,7 @@
-// Device-side building blocks of the row losses: softmax statistics of a row
-// of logits and the reductions they need.
+// Device-side building blocks of the row losses: 16-byte pieces of a row,
+// softmax statistics and their merges, reductions over a wave.
 //
-// A row's exponentials are taken in base 2 relative to the row's maximum m:
+// A row's exponentials are taken in base 2 relative to a maximum m:
 //
 //   e_c = 2^(z_c c - A),  c = scale log2(e),  A = fl(m c),  Z = sum_c e_c,
 //
@@ -10,6 +10,10 @@
 // q_c = e_c / Z, and the log-sum-exp takes it out again:
 //
 //   lse = scale m + ln2 (log2 Z - (mc - A)),  mc - A exact by one fma.
+//
+// Every wave takes its own maximum first and its exponentials relative to it,
+// so that a row needs one meeting of its waves, where the pairs (m, Z) are
+// merged.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -19,24 +23,116 @@ namespace lik {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr double kLn2 = 0.69314718055994530942;
+constexpr float kInf = __builtin_inff();
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// ---------------------------------------------------------------------------
+// reductions over a wave: every lane gets the result, formed in one fixed tree
+// ---------------------------------------------------------------------------
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_word(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, true);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __uint_as_float(dpp_word<CTRL>(__float_as_uint(x)));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double x) {
+  const uint64_t u = (uint64_t)__double_as_longlong(x);
+  const uint64_t lo = dpp_word<CTRL>((uint32_t)u), hi = dpp_word<CTRL>((uint32_t)(u >> 32));
+  return __longlong_as_double((long long)(hi << 32 | lo));
+}
+
+// Both halves of x exchanged over 16 (or 32) lanes: a + b of the two results
+// is x plus its partner's.
+template <bool Wide>
+__device__ __forceinline__ void swap_word(uint32_t x, uint32_t* a, uint32_t* b) {
+  const auto r = Wide ? __builtin_amdgcn_permlane32_swap(x, x, false, false)
+                      : __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  *a = r[0];
+  *b = r[1];
+}
+template <bool Wide>
+__device__ __forceinline__ void swap_half(float x, float* a, float* b) {
+  uint32_t p, q;
+  swap_word<Wide>(__float_as_uint(x), &p, &q);
+  *a = __uint_as_float(p);
+  *b = __uint_as_float(q);
+}
+template <bool Wide>
+__device__ __forceinline__ void swap_half(double x, double* a, double* b) {
+  const uint64_t u = (uint64_t)__double_as_longlong(x);
+  uint32_t p0, q0, p1, q1;
+  swap_word<Wide>((uint32_t)u, &p0, &q0);
+  swap_word<Wide>((uint32_t)(u >> 32), &p1, &q1);
+  *a = __longlong_as_double((long long)((uint64_t)p1 << 32 | p0));
+  *b = __longlong_as_double((long long)((uint64_t)q1 << 32 | q0));
+}
+
+struct MaxF {
+  __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct SumF {
+  template <typename V>
+  __device__ V operator()(V a, V b) const { return a + b; }
+};
+
+// Every step's operands are the same two values in both partners, so all lanes
+// hold the same bits at the end.
+template <typename V, typename F>
+__device__ __forceinline__ V wave_reduce(V v, F f) {
+  v = f(v, dpp<0xB1>(v));     // quad_perm 1,0,3,2
+  v = f(v, dpp<0x4E>(v));     // quad_perm 2,3,0,1
+  v = f(v, dpp<0x141>(v));    // row_half_mirror: the other quad of eight
+  v = f(v, dpp<0x140>(v));    // row_mirror: the other half of sixteen
+  V a, b;
+  swap_half<false>(v, &a, &b);
+  v = f(a, b);
+  swap_half<true>(v, &a, &b);
+  return f(a, b);
+}
+__device__ __forceinline__ float wave_max(float v) { return wave_reduce(v, MaxF()); }
+__device__ __forceinline__ float wave_sum(float v) { return wave_reduce(v, SumF()); }
+__device__ __forceinline__ double wave_sum(double v) { return wave_reduce(v, SumF()); }
+
+// The wave's number in its workgroup, in a scalar register.
+__device__ __forceinline__ int wave_id() {
+  return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+}
+
+// Threads that share LDS meet: one wave, or the workgroup.
+template <int GT>
+__device__ __forceinline__ void group_sync() {
+  if constexpr (GT == 64) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  } else {
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// softmax statistics
+// ---------------------------------------------------------------------------
 
 // A row's softmax: e_c = exp2(fma(z_c, c, -A)), q_c = e_c / Z.
 struct RowSoft {
   float m, c, A, Z;
 };
 
-// c and A from a row's maximum.  Where m * c overflows float32 (a row of the
-// type's lowest values), logits that differ at all differ by more than any
-// exponent, so the power of two that brings m next to 2^64 serves as c: equal
-// logits still give 1 and smaller ones 0.  An infinite m gives NaN throughout.
+// c and A from a maximum.  Where m * c overflows float32 (a row of the type's
+// lowest values), logits that differ at all differ by more than any exponent,
+// so the power of two that brings m next to 2^64 serves as c: equal logits
+// still give 1 and smaller ones 0.  An infinite m gives NaN throughout.
 __device__ __forceinline__ RowSoft row_ref(float m, float scale) {
   RowSoft r;
   r.m = m;
   r.c = scale * kLog2e;
   r.A = m * r.c;
-  if (!(fabsf(r.A) < 1e38f) && fabsf(m) < __builtin_inff()) {
+  if (!(fabsf(r.A) < 1e38f) && fabsf(m) < kInf) {
     r.c = ldexpf(1.0f, 64 - ilogbf(m));
     r.A = m * r.c;
   }
@@ -46,6 +142,23 @@ __device__ __forceinline__ RowSoft row_ref(float m, float scale) {
 
 __device__ __forceinline__ float row_exp(const RowSoft& r, float z) {
   return exp2_fast(fmaf(z, r.c, -r.A));
+}
+
+// The reference of one part of a row (a wave, a piece).  A part without a
+// finite logit has none: its exponentials of -inf are 0 there.
+__device__ __forceinline__ RowSoft part_ref(float m, float scale) {
+  RowSoft r = row_ref(m, scale);
+  if (m == -kInf) r.A = 0.0f;
+  return r;
+}
+
+// What a part's sum counts for in a row with the maximum s.m: 1 where the
+// maxima are the same, nothing beside a maximum so large that only equal
+// logits count.
+__device__ __forceinline__ float part_factor(const RowSoft& s, float m, float scale) {
+  const float c = scale * kLog2e;
+  if (m == s.m) return 1.0f;
+  return s.c == c ? exp2_fast(m * c - s.A) : 0.0f;
 }
 
 // ln(Z 2^-(mc - A)), the log-sum-exp relative to the maximum.  The logarithm
@@ -66,51 +179,282 @@ __device__ __forceinline__ double row_logp(const RowSoft& r, float z, float scal
   return (double)scale * ((double)z - (double)r.m) - ln_sum;
 }
 
-// Reductions over a workgroup of NT threads; every thread gets the result.
-// `tmp` holds NT / 64 values and is free again after the call.
-template <int NT, typename V, typename F>
-__device__ __forceinline__ V block_reduce(V v, V* tmp, F f) {
-#pragma unroll
-  for (int k = 32; k >= 1; k >>= 1) v = f(v, __shfl_xor(v, k));
-  if constexpr (NT > 64) {
-    if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = tmp[0];
-#pragma unroll
-    for (int i = 1; i < NT / 64; ++i) v = f(v, tmp[i]);
-    __syncthreads();
-  }
-  return v;
+// The parts (m, Z) of a row as one softmax, by one wave.  A row all of -inf has
+// none: NaN.
+__device__ __forceinline__ RowSoft merge_parts(const float2* __restrict__ parts, int n, float scale) {
+  const int lane = threadIdx.x & 63;
+  float m = -kInf;
+  for (int i = lane; i < n; i += 64) m = fmaxf(m, parts[i].x);
+  RowSoft s = row_ref(wave_max(m), scale);
+  float Z = 0.0f;
+  for (int i = lane; i < n; i += 64) Z += parts[i].y * part_factor(s, parts[i].x, scale);
+  s.Z = s.m == -kInf ? __builtin_nanf("") : wave_sum(Z);
+  return s;
 }
 
-struct MaxF {
-  __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
-};
-struct SumF {
-  template <typename V>
-  __device__ V operator()(V a, V b) const { return a + b; }
-};
+// ---------------------------------------------------------------------------
+// 16-byte pieces of a row
+// ---------------------------------------------------------------------------
 
-// The softmax of a row in two passes over it.  `listed` (or null) is a bitmap
-// of columns left out of Z; the maximum is over all columns.
-template <int NT, typename T>
-__device__ RowSoft row_softmax(const T* __restrict__ row, int64_t C, float scale,
-                               const uint32_t* listed, float* tmp) {
-  float m = -__builtin_inff();
-  for (int64_t c = threadIdx.x; c < C; c += NT) m = fmaxf(m, (float)row[c]);
-  m = block_reduce<NT>(m, tmp, MaxF());
-  RowSoft r = row_ref(m, scale);
-  float z = 0.0f;
-  for (int64_t c = threadIdx.x; c < C; c += NT) {
-    const float e = row_exp(r, (float)row[c]);
-    if (!listed || !(listed[c >> 5] >> (c & 31) & 1)) z += e;
-  }
-  r.Z = block_reduce<NT>(z, tmp, SumF());
+typedef uint32_t piece __attribute__((ext_vector_type(4)));
+// rows start at any element, so pieces are loaded and stored at any alignment
+typedef uint32_t piece_u2 __attribute__((ext_vector_type(4), aligned(2)));
+
+template <typename T> struct PieceOf { static constexpr int N = 16 / sizeof(T); };
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
   return r;
 }
 
+template <typename T>
+__device__ __forceinline__ void unpack(piece p, float* f) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(p[i]);
+  } else if constexpr (__is_same(T, __bf16)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(p[i] << 16);
+      f[2 * i + 1] = __uint_as_float(p[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = (float)__builtin_bit_cast(_Float16, (uint16_t)p[i]);
+      f[2 * i + 1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(p[i] >> 16));
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ piece pack(const float* f) {
+  if constexpr (sizeof(T) == 4) {
+    return piece{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                 __float_as_uint(f[3])};
+  } else {
+    typedef T pair __attribute__((ext_vector_type(2)));
+    piece p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[i] = __builtin_bit_cast(uint32_t, pair{(T)f[2 * i], (T)f[2 * i + 1]});
+    return p;
+  }
+}
+
+// -inf in every element
+template <typename T>
+__device__ __forceinline__ piece no_logits() {
+  const uint32_t w = sizeof(T) == 4 ? 0xff800000u : (__is_same(T, __bf16) ? 0xff80ff80u : 0xfc00fc00u);
+  return piece{w, w, w, w};
+}
+
+// Once: nothing reads the row again, so it need not stay in the caches.
+template <bool Once, typename T>
+__device__ __forceinline__ piece load_piece(const T* p) {
+  const piece_u2* q = reinterpret_cast<const piece_u2*>(p);
+  if constexpr (Once) return __builtin_nontemporal_load(q);
+  return *q;
+}
+template <typename T>
+__device__ __forceinline__ void store_piece(T* p, piece v) {
+  *reinterpret_cast<piece_u2*>(p) = v;
+}
+
+template <typename T>
+__device__ __forceinline__ float piece_max(piece p, float m) {
+  float f[PieceOf<T>::N];
+  unpack<T>(p, f);
+#pragma unroll
+  for (int i = 0; i < PieceOf<T>::N; i += 2) m = max3(m, f[i], f[i + 1]);
+  return m;
+}
+
+// Sum of the piece's exponentials; bit i of `out` leaves element i out.
+template <typename T>
+__device__ __forceinline__ float piece_sum(piece p, const RowSoft& s, uint32_t out) {
+  float f[PieceOf<T>::N];
+  unpack<T>(p, f);
+#pragma unroll
+  for (int i = 0; i < PieceOf<T>::N; ++i) f[i] = row_exp(s, f[i]);
+  if (out) {
+#pragma unroll
+    for (int i = 0; i < PieceOf<T>::N; ++i)
+      if (out >> i & 1) f[i] = 0.0f;
+  }
+  float a = f[0], b = f[1];
+#pragma unroll
+  for (int i = 2; i < PieceOf<T>::N; i += 2) {
+    a += f[i];
+    b += f[i + 1];
+  }
+  return a + b;
+}
+
+// k * e for every element
+template <typename T>
+__device__ __forceinline__ piece piece_grad(piece p, const RowSoft& s, float k) {
+  float f[PieceOf<T>::N];
+  unpack<T>(p, f);
+#pragma unroll
+  for (int i = 0; i < PieceOf<T>::N; ++i) f[i] = k * row_exp(s, f[i]);
+  return pack<T>(f);
+}
+
+// Waits for this wave's loads (and stores): vmcnt(0) alone.
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }
+
+// `C` columns from `row` as 16-byte pieces, dealt to GT threads in turn, the
+// first NV of every thread held in registers; the columns behind the last
+// whole piece, one to a thread, in `last`.  No column is touched twice.
+template <typename T, int GT, int NV, bool Once = true>
+struct HeldRow {
+  static constexpr int N = PieceOf<T>::N;
+  static constexpr int64_t kColumns = (int64_t)GT * NV * N;
+  piece d[NV];
+  float last;
+  int tid, pieces, tail;
+
+  __device__ __forceinline__ void load(const T* __restrict__ row, int C, int t) {
+    tid = t;
+    pieces = C / N;
+    tail = C - pieces * N;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      d[i] = no_logits<T>();
+      if (i * GT < pieces && i * GT + tid < pieces) d[i] = load_piece<Once>(row + (i * GT + tid) * N);
+    }
+    last = -kInf;
+    if (tid < tail) last = (float)row[pieces * N + tid];
+  }
+  __device__ __forceinline__ float max() const {
+    float m = last;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (i * GT < pieces) m = piece_max<T>(d[i], m);
+    return m;
+  }
+  // `listed`: a bit per column that is left out of the sum, or null
+  __device__ __forceinline__ float sum(const RowSoft& s, const uint32_t* listed) const {
+    float z = row_exp(s, last);
+    if (listed && tid < tail) {
+      const int c = pieces * N + tid;
+      if (listed[c >> 5] >> (c & 31) & 1) z = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (i * GT < pieces) {
+        uint32_t out = 0;
+        if (listed && i * GT + tid < pieces) {
+          const int c = (i * GT + tid) * N;
+          out = listed[c >> 5] >> (c & 31) & ((1u << N) - 1);
+        }
+        z += piece_sum<T>(d[i], s, out);
+      }
+    }
+    return z;
+  }
+  // g = k e.  The pieces are all here by now; said once, before the stores, it
+  // keeps the compiler from waiting for every store before the next piece.
+  __device__ __forceinline__ void store_grad(T* __restrict__ g, const RowSoft& s, float k) const {
+    wait_loads();
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (i * GT < pieces && i * GT + tid < pieces)
+        store_piece(g + (i * GT + tid) * N, piece_grad<T>(d[i], s, k));
+    if (tid < tail) g[pieces * N + tid] = (T)(k * row_exp(s, last));
+  }
+  // whether this thread holds column c
+  __device__ __forceinline__ bool holds(int c) const {
+    const int p = c / N;
+    return p < pieces ? p % GT == tid : c - pieces * N == tid;
+  }
+};
+
+// Zeros, NaN or any constant over a row.
+template <typename T, int GT>
+__device__ __forceinline__ void fill_row(T* __restrict__ g, int C, int tid, float v) {
+  constexpr int N = PieceOf<T>::N;
+  float f[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = v;
+  const piece p = pack<T>(f);
+  const int pieces = C / N;
+  for (int i = tid; i < pieces; i += GT) store_piece(g + (int64_t)i * N, p);
+  if (tid < C - pieces * N) g[(int64_t)pieces * N + tid] = (T)v;
+}
+
+// The softmax of a group's columns: each wave's (m, Z), merged in LDS.  `tmp`
+// holds two floats per wave.  With Part the columns are one part of a row, and
+// one without a finite logit has Z = 0.
+template <int GT, bool Part = false, typename Held>
+__device__ __forceinline__ RowSoft held_softmax(const Held& h, float scale, const uint32_t* listed,
+                                                float* tmp) {
+  const RowSoft w = part_ref(wave_max(h.max()), scale);
+  const float Z = wave_sum(h.sum(w, listed));
+  RowSoft s;
+  if constexpr (GT == 64) {
+    s = row_ref(w.m, scale);
+    s.Z = Z;
+  } else {
+    constexpr int W = GT / 64;
+    const int lane = threadIdx.x & 63;
+    if (lane == 0) {
+      tmp[2 * wave_id()] = w.m;
+      tmp[2 * wave_id() + 1] = Z;
+    }
+    group_sync<GT>();
+    const float m = lane < W ? tmp[2 * lane] : -kInf, z = lane < W ? tmp[2 * lane + 1] : 0.0f;
+    s = row_ref(wave_max(m), scale);
+    s.Z = wave_sum(z * part_factor(s, m, scale));
+  }
+  if (!Part && s.m == -kInf) s.Z = __builtin_nanf("");
+  return s;
+}
+
+// ---------------------------------------------------------------------------
+// grids
+// ---------------------------------------------------------------------------
+
+// A grid of n workgroups; linear_block() numbers them, those >= n are idle.
+inline dim3 linear_grid(int64_t n) {
+  const int64_t x = n < (1 << 20) ? n : (1 << 20);
+  return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
+}
+__device__ __forceinline__ int64_t linear_block() {
+  return (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+}
+
+// One group of GT threads a row: workgroups of 256 threads at least.
+template <int GT>
+constexpr int group_threads() { return GT == 64 ? 256 : GT; }
+template <int GT>
+inline dim3 group_grid(int64_t R) { return linear_grid(GT == 64 ? (R + 3) / 4 : R); }
+template <int GT>
+__device__ __forceinline__ int64_t group_row() {
+  return GT == 64 ? linear_block() * 4 + wave_id() : linear_block();
+}
+template <int GT>
+__device__ __forceinline__ int group_tid() { return GT == 64 ? threadIdx.x & 63 : threadIdx.x; }
+
+// The part of a row that a workgroup of 256 threads takes in a grid of R * n.
+struct PartAt {
+  int64_t r;
+  int p, lo, cols;
+};
+__device__ __forceinline__ PartAt part_at(int cols, int n, int C) {
+  PartAt x;
+  const int64_t b = linear_block();
+  x.r = b / n;
+  x.p = (int)(b - x.r * n);
+  x.lo = x.p * cols;
+  x.cols = C - x.lo < cols ? C - x.lo : cols;
+  return x;
+}
+
 // Policy loss of one row and its slope dl/dlogp.  x = logp - old, away =
-// ref - logp (used with kl != 0 only).
+// ref - logp (used with with_kl only).
 __device__ __forceinline__ void policy_loss(float x, float adv, float low, float high, bool with_kl,
                                             float away, float kl, float* loss, float* slope) {
   const float rho = expf(x);

@@ -1,6 +1,12 @@
 // Row losses whose gradient needs nothing beyond its own row: distillation
 // from a teacher's top logits, and the clipped policy loss.
+//
+// Held rows (HeldRow): a group of threads loads its row once into registers,
+// takes the statistics and writes the gradient from there, so the logits are
+// read once and the gradient written once, which is all the traffic there is.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "lik_rows_device.h"
 #include "lik_rows_kernels.h"
@@ -8,14 +14,6 @@
 namespace lik {
 
 namespace {
-
-constexpr int kNT = 256;
-constexpr int64_t kMaxGrid = int64_t(1) << 20;
-
-template <int NT, typename T>
-__device__ void fill_row(T* __restrict__ g, int64_t C, float v) {
-  for (int64_t c = threadIdx.x; c < C; c += NT) g[c] = (T)v;
-}
 
 // loss = sum_r w_r l_r, rows of weight 0 left out
 __global__ __launch_bounds__(256) void weighted_sum_kernel(const float* __restrict__ l,
@@ -27,208 +25,478 @@ __global__ __launch_bounds__(256) void weighted_sum_kernel(const float* __restri
     const float k = w ? w[r] : 1.0f;
     if (k != 0.0f) acc += (double)k * (double)l[r];
   }
-  acc = block_reduce<256>(acc, tmp, SumF());
-  if (threadIdx.x == 0) *loss = (float)(w ? acc : acc / (double)R);
-}
-
-template <typename T>
-__global__ __launch_bounds__(kNT) void policy_rows_kernel(
-    const T* __restrict__ z, int64_t R, int64_t C, int64_t ld, float scale,
-    const int32_t* __restrict__ targets, const float* __restrict__ old_logp,
-    const float* __restrict__ adv, const float* __restrict__ ref, float low, float high, float kl,
-    const float* __restrict__ weight, float* __restrict__ row_loss, float* __restrict__ logp,
-    T* __restrict__ grad, int64_t gld) {
-  __shared__ float tmp[kNT / 64];
-  for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
-    const int64_t t = targets[r];
-    const float w = weight ? weight[r] : 1.0f / (float)R;
-    T* g = grad ? grad + r * gld : nullptr;
-    if (t < 0 || w == 0.0f) {
-      if (threadIdx.x == 0) row_loss[r] = logp[r] = 0.0f;
-      if (g) fill_row<kNT>(g, C, 0.0f);
-      continue;
-    }
-    const T* row = z + r * ld;
-    const RowSoft s = row_softmax<kNT>(row, C, scale, nullptr, tmp);
-    const float zt = t < C ? (float)row[t] : __builtin_nanf("");
-    const double lp = row_logp(s, zt, scale, row_ln_sum(s));
-    float l, slope;
-    policy_loss((float)(lp - (double)old_logp[r]), adv[r], low, high, ref != nullptr,
-                ref ? (float)((double)ref[r] - lp) : 0.0f, kl, &l, &slope);
-    if (threadIdx.x == 0) {
-      row_loss[r] = l;
-      logp[r] = (float)lp;
-    }
-    if (g) {
-      const float k = w * slope * scale;
-      const float kz = -k / s.Z;
-      for (int64_t c = threadIdx.x; c < C; c += kNT) {
-        const float e = row_exp(s, (float)row[c]);
-        g[c] = (T)(c == t ? fmaf(kz, e, k) : kz * e);
-      }
-    }
+  acc = wave_sum(acc);
+  if ((threadIdx.x & 63) == 0) tmp[wave_id()] = acc;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    acc = (tmp[0] + tmp[1]) + (tmp[2] + tmp[3]);
+    *loss = (float)(w ? acc : acc / (double)R);
   }
 }
 
-// What the teacher's list says of a row, held in LDS while the row is done.
-struct TeacherList {
-  int32_t col[kDistillMaxK];    // column, or -1
-  int32_t lead[kDistillMaxK];   // 1: first entry of its column
-  float p[kDistillMaxK];        // teacher probability
-  float zs[kDistillMaxK];       // the student's logit there
+template <typename T>
+struct PolicyArgs {
+  const T* z;
+  int64_t R, ld;
+  int C;
+  float scale;
+  const int32_t* targets;
+  const float *old_logp, *adv, *ref;
+  float low, high, kl;
+  const float* weight;
+  float *row_loss, *logp;
+  T* grad;
+  int64_t gld;
 };
 
+// What a row's loss needs beside its softmax, loaded ahead of it.
+struct PolicyRow {
+  float zt, old, adv, ref, w;
+};
 template <typename T>
-__global__ __launch_bounds__(kNT) void distill_rows_kernel(
-    const T* __restrict__ z, int64_t R, int64_t C, int64_t ld, float scale,
-    const int32_t* __restrict__ idx, const float* __restrict__ val, int K,
-    const float* __restrict__ t_lse, const float* __restrict__ weight,
-    float* __restrict__ row_loss, T* __restrict__ grad, int64_t gld) {
-  __shared__ TeacherList L;
-  __shared__ float tmp[kNT / 64];
-  __shared__ double tmpd[kNT / 64];
-  __shared__ int flags;                     // 1: a column >= C, 2: a column twice, 4: an entry with mass
-  extern __shared__ uint32_t listed[];      // bitmap of the listed columns
+__device__ __forceinline__ PolicyRow policy_row(const PolicyArgs<T>& a, int64_t r, int t, float w) {
+  const float zt = t < a.C ? (float)a.z[r * a.ld + t] : __builtin_nanf("");
+  return PolicyRow{zt, a.old_logp[r], a.adv[r], a.ref ? a.ref[r] : 0.0f, w};
+}
+// Writes the row's loss and log-probability from one thread and returns the
+// slope of w l along logp, times scale.
+template <typename T>
+__device__ __forceinline__ float policy_finish(const PolicyArgs<T>& a, int64_t r,
+                                               const PolicyRow& x, const RowSoft& s, bool write) {
+  const double lp = row_logp(s, x.zt, a.scale, row_ln_sum(s));
+  float l, slope;
+  policy_loss((float)(lp - (double)x.old), x.adv, a.low, a.high, a.ref != nullptr,
+              (float)((double)x.ref - lp), a.kl, &l, &slope);
+  if (write) {
+    a.row_loss[r] = l;
+    a.logp[r] = (float)lp;
+  }
+  return x.w * slope * a.scale;
+}
+
+template <typename T, int GT, int NV>
+__global__ __launch_bounds__(group_threads<GT>()) __attribute__((amdgpu_waves_per_eu(4)))
+void policy_held_kernel(const PolicyArgs<T> a) {
+  __shared__ float tmp[2 * (GT / 64)];
+  const int64_t r = group_row<GT>();
+  if (r >= a.R) return;
+  const int tid = group_tid<GT>();
+  const int t = a.targets[r];
+  const float w = a.weight ? a.weight[r] : 1.0f / (float)a.R;
+  T* g = a.grad ? a.grad + r * a.gld : nullptr;
+  if (t < 0 || w == 0.0f) {
+    if (tid == 0) a.row_loss[r] = a.logp[r] = 0.0f;
+    if (g) fill_row<T, GT>(g, a.C, tid, 0.0f);
+    return;
+  }
+  HeldRow<T, GT, NV> h;
+  h.load(a.z + r * a.ld, a.C, tid);
+  const PolicyRow x = policy_row(a, r, t, w);
+  const RowSoft s = held_softmax<GT>(h, a.scale, nullptr, tmp);
+  const float k = policy_finish(a, r, x, s, tid == 0);
+  if (g) {
+    const float kz = -k / s.Z;
+    h.store_grad(g, s, kz);
+    // the same thread stored the column just before
+    if (t < a.C && h.holds(t)) g[t] = (T)fmaf(kz, row_exp(s, x.zt), k);
+  }
+}
+
+// Rows in parts, the second look: loss (part 0) and gradient.
+template <typename T>
+__global__ __launch_bounds__(256) void policy_parts_kernel(const PolicyArgs<T> a, Parts parts,
+                                                           const float2* __restrict__ mz) {
+  const PartAt at = part_at(parts.cols, parts.n, a.C);
+  if (at.r >= a.R) return;
+  const int64_t r = at.r;
   const int tid = threadIdx.x;
-  const int words = (int)((C + 31) / 32);
-  for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
-    const float w = weight ? weight[r] : 1.0f / (float)R;
-    T* g = grad ? grad + r * gld : nullptr;
-    if (w == 0.0f) {
-      if (tid == 0) row_loss[r] = 0.0f;
-      if (g) fill_row<kNT>(g, C, 0.0f);
-      continue;
-    }
-    const T* row = z + r * ld;
-    __syncthreads();
-    for (int i = tid; i < words; i += kNT) listed[i] = 0;
-    if (tid == 0) flags = 0;
-    __syncthreads();
-    float tmax = -__builtin_inff();
-    for (int k = tid; k < K; k += kNT) {
-      const int32_t j = idx[r * K + k];
-      const float t = val[r * K + k];
-      int32_t col = j < 0 ? -1 : j;
-      if (j >= C) {
-        col = -1;
-        atomicOr(&flags, 1);
-      }
-      L.col[k] = col;
-      L.lead[k] = col >= 0;
-      L.p[k] = t;
-      L.zs[k] = 0.0f;
-      if (col >= 0) {
-        L.zs[k] = (float)row[col];
-        const uint32_t bit = 1u << (col & 31);
-        if (atomicOr(&listed[col >> 5], bit) & bit) atomicOr(&flags, 2);
-        tmax = fmaxf(tmax, t);
-        if (!(t == -__builtin_inff())) atomicOr(&flags, 4);
-      }
-    }
-    __syncthreads();
-    if (flags & 2) {
-      // a column twice: its first entry stands for it
-      for (int k = tid; k < K; k += kNT) {
-        int lead = L.col[k] >= 0;
-        for (int i = 0; i < k; ++i) lead &= L.col[i] != L.col[k];
-        L.lead[k] = lead;
-      }
-      __syncthreads();
-    }
-    if (!t_lse && !(flags & 5)) {
-      if (tid == 0) row_loss[r] = 0.0f;
-      if (g) fill_row<kNT>(g, C, 0.0f);
-      continue;
-    }
-    // teacher probabilities
-    double lt;
-    if (t_lse) {
-      lt = (double)t_lse[r];
-    } else {
-      tmax = block_reduce<kNT>(tmax, tmp, MaxF());
-      float sum = 0.0f;
-      for (int k = tid; k < K; k += kNT)
-        if (L.col[k] >= 0) sum += expf(scale * (L.p[k] - tmax));
-      sum = block_reduce<kNT>(sum, tmp, SumF());
-      lt = (double)scale * (double)tmax + (double)logf(sum);
-    }
-    double mass = 0.0;
-    for (int k = tid; k < K; k += kNT) {
-      float p = 0.0f;
-      if (L.col[k] >= 0 && L.p[k] != -__builtin_inff())
-        p = expf((float)((double)scale * (double)L.p[k] - lt));
-      if (L.col[k] >= 0) mass += (double)p;
-    }
-    mass = block_reduce<kNT>(mass, tmpd, SumF());
-    // the student's: listed columns apart from the rest
-    RowSoft s = row_softmax<kNT>(row, C, scale, listed, tmp);
-    const float rest = s.Z;
-    double top = 0.0, terms = 0.0, leads = 0.0;
-    for (int k = tid; k < K; k += kNT) {
-      if (L.col[k] < 0) continue;
-      if (L.lead[k]) {
-        top += (double)row_exp(s, L.zs[k]);
-        leads += 1.0;
-      }
-      const double lp = (double)scale * (double)L.p[k] - lt;
-      const float p = L.p[k] == -__builtin_inff() ? 0.0f : expf((float)lp);
-      if (p != 0.0f) terms += (double)p * (lp - (double)scale * ((double)L.zs[k] - (double)s.m));
-      L.p[k] = p;
-    }
-    top = block_reduce<kNT>(top, tmpd, SumF());
-    terms = block_reduce<kNT>(terms, tmpd, SumF());
-    leads = block_reduce<kNT>(leads, tmpd, SumF());
-    s.Z = (float)((double)rest + top);
-    const double ln_sum = row_ln_sum(s);
-    double l = terms + mass * ln_sum;
-    float p_rest = 0.0f;
-    if (t_lse && leads < (double)C) {
-      p_rest = (float)fmax(0.0, 1.0 - mass);
-      if (mass != mass) p_rest = __builtin_nanf("");
-      if (p_rest != 0.0f)
-        l += (double)p_rest * ((double)logf(p_rest) - (double)logf(rest / s.Z));
-    }
-    const float nan = flags & 1 ? __builtin_nanf("") : 0.0f;
-    if (tid == 0) row_loss[r] = (float)l + nan;
-    if (g) {
-      const float k = w * scale + nan;
-      const float M = (float)(mass + (double)p_rest);
-      const float others = rest > 0.0f ? k * (M / s.Z - p_rest / rest) : (rest == 0.0f ? nan : rest);
-      const float on = k * (M / s.Z);
-      for (int64_t c = tid; c < C; c += kNT)
-        if (!(listed[c >> 5] >> (c & 31) & 1)) g[c] = (T)(others * row_exp(s, (float)row[c]));
-      __syncthreads();
-      for (int i = tid; i < K; i += kNT) {
-        if (!L.lead[i]) continue;
-        float p = L.p[i];
-        if (flags & 2)
-          for (int j = i + 1; j < K; ++j)
-            if (L.col[j] == L.col[i]) p += L.p[j];
-        g[L.col[i]] = (T)(on * row_exp(s, L.zs[i]) - k * p);
-      }
+  const int t = a.targets[r];
+  const float w = a.weight ? a.weight[r] : 1.0f / (float)a.R;
+  T* g = a.grad ? a.grad + r * a.gld + at.lo : nullptr;
+  if (!g && at.p != 0) return;
+  if (t < 0 || w == 0.0f) {
+    if (at.p == 0 && tid == 0) a.row_loss[r] = a.logp[r] = 0.0f;
+    if (g) fill_row<T, 256>(g, at.cols, tid, 0.0f);
+    return;
+  }
+  HeldRow<T, 256, kPartPieces> h;
+  if (g) h.load(a.z + r * a.ld + at.lo, at.cols, tid);
+  const PolicyRow x = policy_row(a, r, t, w);
+  const RowSoft s = merge_parts(mz + r * parts.n, parts.n, a.scale);
+  const float k = policy_finish(a, r, x, s, at.p == 0 && tid == 0);
+  if (g) {
+    const float kz = -k / s.Z;
+    h.store_grad(g, s, kz);
+    const int c = t - at.lo;
+    if (c >= 0 && c < at.cols && h.holds(c)) g[c] = (T)fmaf(kz, row_exp(s, x.zt), k);
+  }
+}
+
+template <typename T>
+struct DistillArgs {
+  const T* z;
+  int64_t R, ld;
+  int C, K;
+  float scale;
+  const int32_t* idx;
+  const float* val;
+  const float* t_lse;
+  const float* weight;
+  float* row_loss;
+  T* grad;
+  int64_t gld;
+};
+
+// The teacher's list of one row in LDS, and a bitmap of its columns.
+struct TeacherList {
+  int32_t* col;        // column, -1 absent, | kAgain behind the column's first entry
+  float* t;            // teacher logit
+  float* zs;           // the student's logit there
+  int* flags;          // 1: a column >= C, 2: a column twice, 4: an entry with mass
+  uint32_t* listed;
+};
+constexpr int32_t kAgain = 1 << 24;
+static_assert(kDistillMaxC < kAgain, "a column and its mark share a word");
+
+__host__ __device__ inline size_t teacher_bytes(int C, int K) {
+  return ((size_t)K * 12 + 4 + ((size_t)C + 31) / 32 * 4 + 15) / 16 * 16;
+}
+__device__ __forceinline__ TeacherList teacher_at(char* p, int K) {
+  TeacherList L;
+  L.col = (int32_t*)p;
+  L.t = (float*)p + K;
+  L.zs = (float*)p + 2 * K;
+  L.flags = (int*)p + 3 * K;
+  L.listed = (uint32_t*)p + 3 * K + 1;
+  return L;
+}
+__device__ __forceinline__ int entry_col(int32_t c) { return c < 0 ? -1 : c & (kAgain - 1); }
+
+// One entry of the list into LDS.
+template <typename T>
+__device__ __forceinline__ void teacher_entry(const DistillArgs<T>& a, const TeacherList& L,
+                                              const T* row, int k, int32_t j, float t) {
+  const bool in = j >= 0 && j < a.C;
+  int flags = j >= a.C ? 1 : 0;
+  if (in) {
+    const uint32_t bit = 1u << (j & 31);
+    if (atomicOr(&L.listed[j >> 5], bit) & bit) flags |= 2;
+    if (t != -kInf) flags |= 4;
+  }
+  L.col[k] = in ? j : -1;
+  L.t[k] = t;
+  L.zs[k] = in ? (float)row[j] : 0.0f;
+  if (flags) atomicOr(L.flags, flags);
+}
+
+// The list's second look, where a column is listed twice: its first entry
+// stands for it.  Which thread marked the bitmap first does not matter.
+template <int GT>
+__device__ __forceinline__ void teacher_first(const TeacherList& L, int K, int tid) {
+  for (int k = tid; k < K; k += GT) {
+    const int32_t c = L.col[k];
+    bool first = true;
+    for (int i = 0; i < k; ++i) first &= entry_col(L.col[i]) != c;
+    if (!first && c >= 0) L.col[k] = c | kAgain;
+  }
+  group_sync<GT>();
+}
+
+// A thread's first entry, loaded ahead of the row.
+template <typename T>
+__device__ __forceinline__ void teacher_ahead(const DistillArgs<T>& a, int64_t r, int tid,
+                                              int32_t* j, float* t) {
+  *j = -1;
+  *t = 0.0f;
+  if (tid < a.K) {
+    *j = a.idx[r * a.K + tid];
+    *t = a.val[r * a.K + tid];
+  }
+}
+
+// The whole list and the bitmap into LDS.
+template <typename T, int GT>
+__device__ __forceinline__ void teacher_fill(const DistillArgs<T>& a, const TeacherList& L,
+                                             int64_t r, const T* row, int tid, int32_t j0,
+                                             float t0) {
+  const int words = (a.C + 31) / 32;
+  for (int i = tid; i < words; i += GT) L.listed[i] = 0;
+  if (tid == 0) *L.flags = 0;
+  group_sync<GT>();
+  if (tid < a.K) teacher_entry(a, L, row, tid, j0, t0);
+  for (int k = tid + GT; k < a.K; k += GT)
+    teacher_entry(a, L, row, k, a.idx[r * a.K + k], a.val[r * a.K + k]);
+  group_sync<GT>();
+  if (*L.flags & 2) teacher_first<GT>(L, a.K, tid);
+}
+
+// log of the teacher's normaliser, from the list where none was given.  Every
+// wave goes over the whole list, so that no further meeting is needed.
+__device__ __forceinline__ double teacher_ln(const TeacherList& L, int K, float scale, int lane) {
+  float m = -kInf;
+  for (int k = lane; k < K; k += 64)
+    if (L.col[k] >= 0) m = fmaxf(m, L.t[k]);
+  m = wave_max(m);
+  float sum = 0.0f;
+  for (int k = lane; k < K; k += 64)
+    if (L.col[k] >= 0) sum += expf(scale * (L.t[k] - m));
+  return (double)scale * (double)m + (double)logf(wave_sum(sum));
+}
+
+// What the list adds up to against the student's softmax.
+struct TeacherSums {
+  double mass = 0.0;       // teacher probability of the list
+  double terms = 0.0;      // sum p (log p - scale (z - m))
+  double top = 0.0;        // student exponentials of the listed columns
+  double columns = 0.0;    // how many those are
+};
+__device__ __forceinline__ float teacher_p(float t, float scale, double lt) {
+  return t == -kInf ? 0.0f : expf((float)((double)scale * (double)t - lt));
+}
+__device__ __forceinline__ TeacherSums teacher_sums(const TeacherList& L, int K, float scale,
+                                                    double lt, const RowSoft& s, int lane) {
+  TeacherSums x;
+  for (int k = lane; k < K; k += 64) {
+    const int32_t c = L.col[k];
+    if (c < 0) continue;
+    const float z = L.zs[k], t = L.t[k];
+    const float p = teacher_p(t, scale, lt);
+    x.mass += (double)p;
+    if (p != 0.0f)
+      x.terms += (double)p * ((double)scale * ((double)t - (double)z + (double)s.m) - lt);
+    if (!(c & kAgain)) {
+      x.top += (double)row_exp(s, z);
+      x.columns += 1.0;
     }
   }
+  x.mass = wave_sum(x.mass);
+  x.terms = wave_sum(x.terms);
+  x.top = wave_sum(x.top);
+  x.columns = wave_sum(x.columns);
+  return x;
+}
+
+// Loss of a row and the factors of its gradient:
+//   listed columns  on * e - k p,   others  off * e   (k = w scale)
+struct DistillRow {
+  float loss, on, off;
+};
+// s.Z: all columns without the rest's term, else the columns not listed (and
+// the whole sum on return).
+__device__ __forceinline__ DistillRow distill_row(const TeacherSums& x, double lt, bool with_rest,
+                                                  int C, float k, RowSoft* s) {
+  const float rest = s->Z;
+  if (with_rest) s->Z = (float)((double)rest + x.top);
+  const double ln_sum = row_ln_sum(*s);
+  double l = x.terms + x.mass * ln_sum;
+  DistillRow d;
+  float M = (float)x.mass, cut = 0.0f;
+  if (with_rest && x.columns < (double)C) {
+    const float p = x.mass != x.mass ? __builtin_nanf("") : (float)fmax(0.0, 1.0 - x.mass);
+    if (p != 0.0f) l += (double)p * ((double)logf(p) - (double)logf(rest / s->Z));
+    M = (float)(x.mass + (double)p);
+    cut = rest == 0.0f ? M / s->Z : p / rest;    // nothing left to write to: e = 0 there
+  }
+  d.loss = (float)l;
+  d.on = k * (M / s->Z);
+  d.off = k * (M / s->Z - cut);
+  return d;
+}
+
+// The gradient on the listed columns, over what the row's pass wrote there.
+template <typename T, int GT>
+__device__ __forceinline__ void teacher_grad(const TeacherList& L, int K, float scale, double lt,
+                                             const RowSoft& s, float on, float k, int flags,
+                                             T* __restrict__ g, int lo, int hi, int tid) {
+  for (int i = tid; i < K; i += GT) {
+    const int32_t c = L.col[i];
+    if (c < lo || c >= hi) continue;             // absent, not the first, or elsewhere
+    double p = (double)teacher_p(L.t[i], scale, lt);
+    if (flags & 2)
+      for (int j = i + 1; j < K; ++j)
+        if (entry_col(L.col[j]) == c) p += (double)teacher_p(L.t[j], scale, lt);
+    g[c] = (T)(on * row_exp(s, L.zs[i]) - k * (float)p);
+  }
+}
+
+template <typename T, int GT, int NV>
+__global__ __launch_bounds__(group_threads<GT>()) __attribute__((amdgpu_waves_per_eu(4)))
+void distill_held_kernel(const DistillArgs<T> a) {
+  __shared__ float tmp[2 * (GT / 64)];
+  extern __shared__ char lists[];
+  const int64_t r = group_row<GT>();
+  if (r >= a.R) return;
+  const int tid = group_tid<GT>();
+  const int lane = threadIdx.x & 63;
+  const float w = a.weight ? a.weight[r] : 1.0f / (float)a.R;
+  T* g = a.grad ? a.grad + r * a.gld : nullptr;
+  if (w == 0.0f) {
+    if (tid == 0) a.row_loss[r] = 0.0f;
+    if (g) fill_row<T, GT>(g, a.C, tid, 0.0f);
+    return;
+  }
+  const T* row = a.z + r * a.ld;
+  const TeacherList L =
+      teacher_at(lists + (GT == 64 ? wave_id() * teacher_bytes(a.C, a.K) : 0), a.K);
+  // the list's loads go first: what waits for them does not wait for the row
+  int32_t j0;
+  float t0;
+  teacher_ahead(a, r, tid, &j0, &t0);
+  HeldRow<T, GT, NV> h;
+  h.load(row, a.C, tid);
+  teacher_fill<T, GT>(a, L, r, row, tid, j0, t0);
+  const int flags = *L.flags;
+  const bool with_rest = a.t_lse != nullptr;
+  if (!with_rest && !(flags & 5)) {
+    // no entry with mass
+    if (tid == 0) a.row_loss[r] = 0.0f;
+    if (g) fill_row<T, GT>(g, a.C, tid, 0.0f);
+    return;
+  }
+  RowSoft s = held_softmax<GT>(h, a.scale, with_rest ? L.listed : nullptr, tmp);
+  const double lt = with_rest ? (double)a.t_lse[r] : teacher_ln(L, a.K, a.scale, lane);
+  const TeacherSums x = teacher_sums(L, a.K, a.scale, lt, s, lane);
+  const float k = w * a.scale + (flags & 1 ? __builtin_nanf("") : 0.0f);
+  const DistillRow d = distill_row(x, lt, with_rest, a.C, k, &s);
+  if (tid == 0) a.row_loss[r] = flags & 1 ? __builtin_nanf("") : d.loss;
+  if (g) {
+    h.store_grad(g, s, d.off);
+    group_sync<GT>();
+    teacher_grad<T, GT>(L, a.K, a.scale, lt, s, d.on, k, flags, g, 0, a.C, tid);
+  }
+}
+
+// Rows in parts, the first look: each part's (m, Z), listed columns left out of
+// Z where the rest has a term of its own.
+template <typename T>
+__global__ __launch_bounds__(256) void distill_stats_kernel(const DistillArgs<T> a, Parts parts,
+                                                            float2* __restrict__ mz) {
+  __shared__ float tmp[8];
+  __shared__ uint32_t listed[256 * kPartPieces * PieceOf<T>::N / 32];
+  const PartAt at = part_at(parts.cols, parts.n, a.C);
+  if (at.r >= a.R) return;
+  const int64_t r = at.r;
+  const int tid = threadIdx.x;
+  if (a.weight && a.weight[r] == 0.0f) return;
+  HeldRow<T, 256, kPartPieces, false> h;
+  h.load(a.z + r * a.ld + at.lo, at.cols, tid);
+  const bool with_rest = a.t_lse != nullptr;
+  if (with_rest) {
+    for (int i = tid; i < (at.cols + 31) / 32; i += 256) listed[i] = 0;
+    __syncthreads();
+    for (int k = tid; k < a.K; k += 256) {
+      const int64_t c = (int64_t)a.idx[r * a.K + k] - at.lo;
+      if (c >= 0 && c < at.cols) atomicOr(&listed[c >> 5], 1u << (c & 31));
+    }
+    __syncthreads();
+  }
+  const RowSoft s = held_softmax<256, true>(h, a.scale, with_rest ? listed : nullptr, tmp);
+  if (tid == 0) mz[r * parts.n + at.p] = make_float2(s.m, s.Z);
+}
+
+// The second look: loss (part 0) and gradient.
+template <typename T>
+__global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T> a, Parts parts,
+                                                            const float2* __restrict__ mz) {
+  extern __shared__ char lists[];
+  const PartAt at = part_at(parts.cols, parts.n, a.C);
+  if (at.r >= a.R) return;
+  const int64_t r = at.r;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const float w = a.weight ? a.weight[r] : 1.0f / (float)a.R;
+  const bool first = at.p == 0 && tid == 0;
+  T* g = a.grad ? a.grad + r * a.gld : nullptr;
+  if (!g && at.p != 0) return;
+  if (w == 0.0f) {
+    if (first) a.row_loss[r] = 0.0f;
+    if (g) fill_row<T, 256>(g + at.lo, at.cols, tid, 0.0f);
+    return;
+  }
+  const T* row = a.z + r * a.ld;
+  const TeacherList L = teacher_at(lists, a.K);
+  int32_t j0;
+  float t0;
+  teacher_ahead(a, r, tid, &j0, &t0);
+  HeldRow<T, 256, kPartPieces> h;
+  if (g) h.load(row + at.lo, at.cols, tid);
+  teacher_fill<T, 256>(a, L, r, row, tid, j0, t0);
+  const int flags = *L.flags;
+  const bool with_rest = a.t_lse != nullptr;
+  if (!with_rest && !(flags & 5)) {
+    if (first) a.row_loss[r] = 0.0f;
+    if (g) fill_row<T, 256>(g + at.lo, at.cols, tid, 0.0f);
+    return;
+  }
+  RowSoft s = merge_parts(mz + r * parts.n, parts.n, a.scale);
+  const double lt = with_rest ? (double)a.t_lse[r] : teacher_ln(L, a.K, a.scale, lane);
+  const TeacherSums x = teacher_sums(L, a.K, a.scale, lt, s, lane);
+  const float k = w * a.scale + (flags & 1 ? __builtin_nanf("") : 0.0f);
+  const DistillRow d = distill_row(x, lt, with_rest, a.C, k, &s);
+  if (first) a.row_loss[r] = flags & 1 ? __builtin_nanf("") : d.loss;
+  if (g) {
+    h.store_grad(g + at.lo, s, d.off);
+    __syncthreads();
+    teacher_grad<T, 256>(L, a.K, a.scale, lt, s, d.on, k, flags, g, at.lo, at.lo + at.cols, tid);
+  }
+}
+
+// Calls f with the group size and pieces per thread that hold C columns.
+template <typename T, typename F>
+hipError_t held_dispatch(int64_t C, F f) {
+#define LIK_HELD(GT, NV) \
+  if (C <= HeldRow<T, GT, NV>::kColumns) return f(std::integral_constant<int, GT>(), std::integral_constant<int, NV>());
+  LIK_HELD(64, 4)
+  LIK_HELD(64, 16)
+  LIK_HELD(256, 16)
+  LIK_HELD(512, 16)
+  LIK_HELD(1024, 16)
+#undef LIK_HELD
+  return hipErrorInvalidValue;
 }
 
 template <typename T>
 hipError_t policy_t(const Rows& a, const int32_t* targets, const float* old_logp, const float* adv,
                     const float* ref, float low, float high, float kl, const float* weight,
-                    float* row_loss, float* logp, hipStream_t s) {
-  const unsigned grid = (unsigned)(a.R < kMaxGrid ? a.R : kMaxGrid);
-  hipLaunchKernelGGL(policy_rows_kernel<T>, dim3(grid), dim3(kNT), 0, s, (const T*)a.z, a.R, a.C,
-                     a.ld, a.scale, targets, old_logp, adv, ref, low, high, kl, weight, row_loss,
-                     logp, (T*)a.grad, a.grad_ld);
+                    float* row_loss, float* logp, char* ws, hipStream_t s) {
+  const PolicyArgs<T> p{(const T*)a.z, a.R, a.ld, (int)a.C, a.scale, targets, old_logp, adv, ref,
+                        low, high, kl, weight, row_loss, logp, (T*)a.grad, a.grad_ld};
+  if (rows_held(a.R, a.C, a.dtype))
+    return held_dispatch<T>(a.C, [&](auto gt, auto nv) {
+      constexpr int GT = decltype(gt)::value, NV = decltype(nv)::value;
+      hipLaunchKernelGGL((policy_held_kernel<T, GT, NV>), group_grid<GT>(a.R),
+                         dim3(group_threads<GT>()), 0, s, p);
+      return hipGetLastError();
+    });
+  Parts parts = plan_parts(a.R, a.C, sizeof(T));
+  float2* mz = (float2*)ws;
+  hipError_t e = run_parts(a, parts, targets, weight, nullptr, 0, mz, s);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(policy_parts_kernel<T>, linear_grid(a.R * parts.n), dim3(256), 0, s, p, parts,
+                     mz);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t distill_t(const Rows& a, const int32_t* idx, const float* val, int64_t K,
-                     const float* t_lse, const float* weight, float* row_loss, hipStream_t s) {
-  const unsigned grid = (unsigned)(a.R < kMaxGrid ? a.R : kMaxGrid);
-  const size_t lds = (size_t)((a.C + 31) / 32) * 4;
-  hipLaunchKernelGGL(distill_rows_kernel<T>, dim3(grid), dim3(kNT), lds, s, (const T*)a.z, a.R,
-                     a.C, a.ld, a.scale, idx, val, (int)K, t_lse, weight, row_loss, (T*)a.grad,
-                     a.grad_ld);
+                     const float* t_lse, const float* weight, float* row_loss, char* ws,
+                     hipStream_t s) {
+  const DistillArgs<T> p{(const T*)a.z, a.R, a.ld, (int)a.C, (int)K, a.scale, idx, val, t_lse,
+                         weight, row_loss, (T*)a.grad, a.grad_ld};
+  const size_t lds = teacher_bytes((int)a.C, (int)K);
+  if (rows_held(a.R, a.C, a.dtype))
+    return held_dispatch<T>(a.C, [&](auto gt, auto nv) {
+      constexpr int GT = decltype(gt)::value, NV = decltype(nv)::value;
+      hipLaunchKernelGGL((distill_held_kernel<T, GT, NV>), group_grid<GT>(a.R),
+                         dim3(group_threads<GT>()), lds * (GT == 64 ? 4 : 1), s, p);
+      return hipGetLastError();
+    });
+  Parts parts = plan_parts(a.R, a.C, sizeof(T));
+  float2* mz = (float2*)ws;
+  const dim3 grid = linear_grid(a.R * parts.n);
+  hipLaunchKernelGGL(distill_stats_kernel<T>, grid, dim3(256), 0, s, p, parts, mz);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(distill_parts_kernel<T>, grid, dim3(256), lds, s, p, parts, mz);
   return hipGetLastError();
 }
 
@@ -239,30 +507,35 @@ hipError_t weighted_sum(const float* l, const float* w, int64_t R, float* loss, 
 
 }  // namespace
 
+bool rows_held(int64_t R, int64_t C, lik_dtype dtype) {
+  const int64_t bytes = C * elem_bytes_of(dtype);
+  return bytes <= 16384 * 16 && (R >= 256 || bytes <= 16384);
+}
+
 hipError_t run_policy(const Rows& a, const int32_t* targets, const float* old_logp,
                       const float* adv, const float* ref, float low, float high, float kl,
                       const float* weight, float* row_loss, float* logp, float* loss,
-                      hipStream_t s) {
+                      char* ws, hipStream_t s) {
   hipError_t e;
   if (a.dtype == LIK_F16)
-    e = policy_t<_Float16>(a, targets, old_logp, adv, ref, low, high, kl, weight, row_loss, logp, s);
+    e = policy_t<_Float16>(a, targets, old_logp, adv, ref, low, high, kl, weight, row_loss, logp, ws, s);
   else if (a.dtype == LIK_BF16)
-    e = policy_t<__bf16>(a, targets, old_logp, adv, ref, low, high, kl, weight, row_loss, logp, s);
+    e = policy_t<__bf16>(a, targets, old_logp, adv, ref, low, high, kl, weight, row_loss, logp, ws, s);
   else
-    e = policy_t<float>(a, targets, old_logp, adv, ref, low, high, kl, weight, row_loss, logp, s);
+    e = policy_t<float>(a, targets, old_logp, adv, ref, low, high, kl, weight, row_loss, logp, ws, s);
   return e != hipSuccess ? e : weighted_sum(row_loss, weight, a.R, loss, s);
 }
 
 hipError_t run_distill(const Rows& a, const int32_t* idx, const float* val, int64_t K,
                        const float* t_lse, const float* weight, float* row_loss, float* loss,
-                       hipStream_t s) {
+                       char* ws, hipStream_t s) {
   hipError_t e;
   if (a.dtype == LIK_F16)
-    e = distill_t<_Float16>(a, idx, val, K, t_lse, weight, row_loss, s);
+    e = distill_t<_Float16>(a, idx, val, K, t_lse, weight, row_loss, ws, s);
   else if (a.dtype == LIK_BF16)
-    e = distill_t<__bf16>(a, idx, val, K, t_lse, weight, row_loss, s);
+    e = distill_t<__bf16>(a, idx, val, K, t_lse, weight, row_loss, ws, s);
   else
-    e = distill_t<float>(a, idx, val, K, t_lse, weight, row_loss, s);
+    e = distill_t<float>(a, idx, val, K, t_lse, weight, row_loss, ws, s);
   return e != hipSuccess ? e : weighted_sum(row_loss, weight, a.R, loss, s);
 }
 

@@ -9,78 +9,91 @@ namespace lik {
 
 namespace {
 
-constexpr int kNT = 256;
-constexpr int64_t kMaxGrid = int64_t(1) << 20;
-
-unsigned grid_of(int64_t n) { return (unsigned)(n < kMaxGrid ? n : kMaxGrid); }
-
-template <typename T>
-__global__ __launch_bounds__(kNT) void logprob_fwd_kernel(
-    const T* __restrict__ z, int64_t R, int64_t C, int64_t ld, float scale,
-    const int32_t* __restrict__ targets, float* __restrict__ logp, float* __restrict__ lse) {
-  __shared__ float tmp[kNT / 64];
-  for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
-    const int64_t t = targets[r];
-    float lp = 0.0f, l = 0.0f;
-    if (t >= 0) {
-      const T* row = z + r * ld;
-      const RowSoft s = row_softmax<kNT>(row, C, scale, nullptr, tmp);
-      const double ln_sum = row_ln_sum(s);
-      lp = t < C ? (float)row_logp(s, (float)row[t], scale, ln_sum) : __builtin_nanf("");
-      l = (float)((double)scale * (double)s.m + ln_sum);
-    }
-    if (threadIdx.x == 0) {
-      logp[r] = lp;
-      lse[r] = l;
-    }
-  }
+// Whether a row has to be read, for the rows' statistics.
+__device__ __forceinline__ bool row_counts(int64_t r, const int32_t* targets, const float* weight,
+                                           const int32_t* offsets, int64_t S) {
+  if (targets && targets[r] < 0) return false;
+  if (weight && weight[r] == 0.0f) return false;
+  return !offsets || (r >= offsets[0] && r < offsets[S]);
 }
 
 template <typename T>
-__global__ __launch_bounds__(kNT) void logprob_bwd_kernel(
-    const T* __restrict__ z, int64_t R, int64_t C, int64_t ld, float scale,
+__global__ __launch_bounds__(256) void parts_kernel(const T* __restrict__ z, int64_t R, int C,
+                                                    int64_t ld, float scale, Parts parts,
+                                                    const int32_t* __restrict__ targets,
+                                                    const float* __restrict__ weight,
+                                                    const int32_t* __restrict__ offsets, int64_t S,
+                                                    float2* __restrict__ out) {
+  __shared__ float tmp[8];
+  const PartAt at = part_at(parts.cols, parts.n, C);
+  if (at.r >= R || !row_counts(at.r, targets, weight, offsets, S)) return;
+  HeldRow<T, 256, kPartPieces, false> h;
+  h.load(z + at.r * ld + at.lo, at.cols, threadIdx.x);
+  const RowSoft s = held_softmax<256, true>(h, scale, nullptr, tmp);
+  if (threadIdx.x == 0) out[at.r * parts.n + at.p] = make_float2(s.m, s.Z);
+}
+
+// One wave a row: log-probability and log-sum-exp from the row's parts.
+template <typename T>
+__global__ __launch_bounds__(256) void logprob_finish_kernel(
+    const T* __restrict__ z, int64_t R, int C, int64_t ld, float scale,
+    const int32_t* __restrict__ targets, const float2* __restrict__ mz, int n,
+    float* __restrict__ logp, float* __restrict__ lse) {
+  const int64_t r = group_row<64>();
+  if (r >= R) return;
+  const int t = targets[r];
+  float lp = 0.0f, l = 0.0f;
+  if (t >= 0) {
+    const float zt = t < C ? (float)z[r * ld + t] : __builtin_nanf("");
+    const RowSoft s = merge_parts(mz + r * n, n, scale);
+    const double ln_sum = row_ln_sum(s);
+    lp = (float)row_logp(s, zt, scale, ln_sum);
+    l = (float)((double)scale * (double)s.m + ln_sum);
+  }
+  if ((threadIdx.x & 63) == 0) {
+    logp[r] = lp;
+    lse[r] = l;
+  }
+}
+
+// A part of a row: k ([c == t] - exp(y - lse)).
+template <typename T>
+__global__ __launch_bounds__(256) void logprob_bwd_kernel(
+    const T* __restrict__ z, int64_t R, int C, int64_t ld, float scale, Parts parts,
     const int32_t* __restrict__ targets, const float* __restrict__ lse,
     const float* __restrict__ dlogp, T* __restrict__ grad, int64_t gld) {
-  for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
-    const int64_t t = targets[r];
-    const float d = dlogp[r];
-    T* g = grad + r * gld;
-    if (t < 0 || d == 0.0f) {
-      for (int64_t c = threadIdx.x; c < C; c += kNT) g[c] = (T)0.0f;
-      continue;
-    }
-    const T* row = z + r * ld;
-    const float k = t < C ? d * scale : __builtin_nanf("");
-    const float l = lse[r];
-    for (int64_t c = threadIdx.x; c < C; c += kNT) {
-      const float q = exp2_fast(fmaf((float)row[c], scale, -l) * kLog2e);
-      g[c] = (T)(c == t ? k - k * q : -k * q);
+  constexpr int N = PieceOf<T>::N;
+  const PartAt at = part_at(parts.cols, parts.n, C);
+  if (at.r >= R) return;
+  const int64_t r = at.r;
+  const int tid = threadIdx.x, t = targets[r];
+  const float d = dlogp[r];
+  T* g = grad + r * gld + at.lo;
+  if (t < 0 || d == 0.0f) {
+    fill_row<T, 256>(g, at.cols, tid, 0.0f);
+    return;
+  }
+  const T* row = z + r * ld + at.lo;
+  const float k = t < C ? d * scale : __builtin_nanf("");
+  const float l = lse[r];
+  HeldRow<T, 256, kPartPieces> h;
+  h.load(row, at.cols, tid);
+  wait_loads();
+  // y - lse is rounded once, relative to itself, before it is scaled
+  auto prob = [&](float x) { return exp2_fast(fmaf(x, scale, -l) * kLog2e); };
+#pragma unroll
+  for (int i = 0; i < kPartPieces; ++i) {
+    if (i * 256 < h.pieces && i * 256 + tid < h.pieces) {
+      float f[N];
+      unpack<T>(h.d[i], f);
+#pragma unroll
+      for (int j = 0; j < N; ++j) f[j] = -k * prob(f[j]);
+      store_piece(g + (i * 256 + tid) * N, pack<T>(f));
     }
   }
-}
-
-// Rows' softmax statistics and log-probabilities, of rows inside a sequence.
-template <typename T>
-__global__ __launch_bounds__(kNT) void pref_rows_kernel(
-    const T* __restrict__ z, int64_t R, int64_t C, int64_t ld, float scale,
-    const int32_t* __restrict__ targets, const int32_t* __restrict__ offsets, int64_t S,
-    float4* __restrict__ soft, double* __restrict__ logp, float* __restrict__ coef) {
-  __shared__ float tmp[kNT / 64];
-  for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
-    const int64_t t = targets[r];
-    double lp = 0.0;
-    RowSoft s{0, 0, 0, 1};
-    if (t >= 0 && r >= offsets[0] && r < offsets[S]) {
-      const T* row = z + r * ld;
-      s = row_softmax<kNT>(row, C, scale, nullptr, tmp);
-      lp = t < C ? row_logp(s, (float)row[t], scale, row_ln_sum(s)) : __builtin_nan("");
-    }
-    if (threadIdx.x == 0) {
-      soft[r] = make_float4(s.m, s.c, s.A, s.Z);
-      logp[r] = lp;
-      coef[r] = 0.0f;
-    }
-  }
+  if (tid < h.tail) g[h.pieces * N + tid] = (T)(-k * prob(h.last));
+  const int c = t - at.lo;
+  if (c >= 0 && c < at.cols && h.holds(c)) g[c] = (T)fmaf(-k, prob((float)row[c]), k);
 }
 
 // The rows of a sequence, kept inside [0, R) whatever the offsets say.
@@ -91,34 +104,39 @@ __device__ __forceinline__ void seq_range(const int32_t* offsets, int64_t s, int
   *b = y > R ? R : y;
 }
 
-template <typename V>
-__device__ __forceinline__ V wave_sum(V v) {
-#pragma unroll
-  for (int k = 32; k >= 1; k >>= 1) v += __shfl_xor(v, k);
-  return v;
-}
-
-// One wave per sequence: L_s.
-__global__ __launch_bounds__(64) void pref_seq_kernel(PrefArgs p, int64_t R,
-                                                      const double* __restrict__ logp,
+// One wave per sequence: a lane per row merges the row's parts and keeps its
+// softmax; then L_s.
+template <typename T>
+__global__ __launch_bounds__(64) void pref_seq_kernel(PrefArgs p, const T* __restrict__ z,
+                                                      int64_t R, int C, int64_t ld, float scale,
+                                                      const float2* __restrict__ mz, int n,
+                                                      float4* __restrict__ soft,
                                                       double* __restrict__ seq) {
-  for (int64_t s = blockIdx.x; s < p.S; s += gridDim.x) {
-    int64_t a, b;
-    seq_range(p.offsets, s, R, &a, &b);
-    double sum = 0.0, n = 0.0;
-    for (int64_t r = a + threadIdx.x; r < b; r += 64) {
-      sum += logp[r];
-      n += p.targets[r] >= 0 ? 1.0 : 0.0;
-    }
-    sum = wave_sum(sum);
-    if (p.mean) {
-      n = wave_sum(n);
-      if (n > 0.0) sum /= n;
-    }
-    if (threadIdx.x == 0) {
-      seq[s] = sum;
-      p.seq_logp[s] = (float)sum;
-    }
+  const int64_t s = linear_block();
+  if (s >= p.S) return;
+  int64_t a, b;
+  seq_range(p.offsets, s, R, &a, &b);
+  double sum = 0.0, count = 0.0;
+  for (int64_t r = a + threadIdx.x; r < b; r += 64) {
+    const int t = p.targets[r];
+    if (t < 0) continue;
+    const float zt = t < C ? (float)z[r * ld + t] : __builtin_nanf("");
+    const float2* part = mz + r * n;
+    float m = -kInf;
+    for (int i = 0; i < n; ++i) m = fmaxf(m, part[i].x);
+    RowSoft f = row_ref(m, scale);
+    for (int i = 0; i < n; ++i) f.Z += part[i].y * part_factor(f, part[i].x, scale);
+    if (m == -kInf) f.Z = __builtin_nanf("");
+    soft[r] = make_float4(f.m, f.c, f.A, f.Z);
+    sum += row_logp(f, zt, scale, row_ln_sum(f));
+    count += 1.0;
+  }
+  sum = wave_sum(sum);
+  count = wave_sum(count);
+  if (p.mean && count > 0.0) sum /= count;
+  if (threadIdx.x == 0) {
+    seq[s] = sum;
+    p.seq_logp[s] = (float)sum;
   }
 }
 
@@ -158,6 +176,16 @@ __device__ __forceinline__ double pair_weight(const PrefArgs& p, int64_t i) {
   return p.weight ? (double)p.weight[i] : 1.0 / (double)p.P;
 }
 
+// Sum over 256 threads, in every thread.
+__device__ __forceinline__ double block_sum(double v, double* tmp) {
+  v = wave_sum(v);
+  if ((threadIdx.x & 63) == 0) tmp[wave_id()] = v;
+  __syncthreads();
+  v = (tmp[0] + tmp[1]) + (tmp[2] + tmp[3]);
+  __syncthreads();
+  return v;
+}
+
 // Block 0: the pairs' losses and their sum.  Block 1 + s, one sequence: dl/dL_s
 // from every pair it is in, in the pairs' order by lane, onto its rows.
 __global__ __launch_bounds__(256) void pref_pairs_kernel(PrefArgs p, int64_t R,
@@ -165,117 +193,137 @@ __global__ __launch_bounds__(256) void pref_pairs_kernel(PrefArgs p, int64_t R,
                                                          float* __restrict__ coef) {
   __shared__ double tmp[4];
   const int tid = threadIdx.x;
-  for (int64_t s = (int64_t)blockIdx.x - 1; s < p.S; s += gridDim.x) {
-    if (s < 0) {
-      double acc = 0.0;
-      for (int64_t i = tid; i < p.P; i += 256) {
-        double l, g;
-        pair_loss(p, seq, i, &l, &g);
-        const double w = pair_weight(p, i);
-        p.pair_loss[i] = (float)l;
-        if (w != 0.0) acc += w * l;
-      }
-      acc = block_reduce<256>(acc, tmp, SumF());
-      if (tid == 0) *p.loss = (float)acc;
-      continue;
-    }
-    int64_t a, b;
-    seq_range(p.offsets, s, R, &a, &b);
+  const int64_t s = linear_block() - 1;
+  if (s >= p.S) return;
+  if (s < 0) {
     double acc = 0.0;
     for (int64_t i = tid; i < p.P; i += 256) {
-      const bool c = p.chosen[i] == s, j = p.rejected[i] == s;
-      if (c == j) continue;              // in neither place, or in both
       double l, g;
       pair_loss(p, seq, i, &l, &g);
       const double w = pair_weight(p, i);
-      if (w != 0.0) acc += c ? w * g : -w * g;
+      p.pair_loss[i] = (float)l;
+      if (w != 0.0) acc += w * l;
     }
-    acc = block_reduce<256>(acc, tmp, SumF());
-    if (p.mean) {
-      double n = 0.0;
-      for (int64_t r = a + tid; r < b; r += 256) n += p.targets[r] >= 0 ? 1.0 : 0.0;
-      n = block_reduce<256>(n, tmp, SumF());
-      if (n > 0.0) acc /= n;
-    }
-    for (int64_t r = a + tid; r < b; r += 256) coef[r] = p.targets[r] >= 0 ? (float)acc : 0.0f;
+    acc = block_sum(acc, tmp);
+    if (tid == 0) *p.loss = (float)acc;
+    return;
   }
+  int64_t a, b;
+  seq_range(p.offsets, s, R, &a, &b);
+  double acc = 0.0, n = 0.0;
+  for (int64_t i = tid; i < p.P; i += 256) {
+    const bool c = p.chosen[i] == s, j = p.rejected[i] == s;
+    if (c == j) continue;              // in neither place, or in both
+    double l, g;
+    pair_loss(p, seq, i, &l, &g);
+    const double w = pair_weight(p, i);
+    if (w != 0.0) acc += c ? w * g : -w * g;
+  }
+  acc = block_sum(acc, tmp);
+  if (p.mean) {
+    for (int64_t r = a + tid; r < b; r += 256) n += p.targets[r] >= 0 ? 1.0 : 0.0;
+    n = block_sum(n, tmp);
+    if (n > 0.0) acc /= n;
+  }
+  for (int64_t r = a + tid; r < b; r += 256) coef[r] = p.targets[r] >= 0 ? (float)acc : 0.0f;
+}
+
+// A part of a row's gradient; 0 for rows outside every sequence.
+template <typename T>
+__global__ __launch_bounds__(256) void pref_grad_kernel(
+    const T* __restrict__ z, int64_t R, int C, int64_t ld, float scale, Parts parts, PrefArgs p,
+    const float4* __restrict__ soft, const float* __restrict__ coef, T* __restrict__ grad,
+    int64_t gld) {
+  const PartAt at = part_at(parts.cols, parts.n, C);
+  if (at.r >= R) return;
+  const int64_t r = at.r;
+  const int tid = threadIdx.x;
+  T* g = grad + r * gld + at.lo;
+  const bool in = p.S > 0 && row_counts(r, p.targets, nullptr, p.offsets, p.S);
+  const float k = in ? coef[r] * scale : 0.0f;
+  if (k == 0.0f) {
+    fill_row<T, 256>(g, at.cols, tid, 0.0f);
+    return;
+  }
+  const T* row = z + r * ld + at.lo;
+  HeldRow<T, 256, kPartPieces> h;
+  h.load(row, at.cols, tid);
+  const float4 f = soft[r];
+  const RowSoft s{f.x, f.y, f.z, f.w};
+  const float kz = -k / s.Z;
+  h.store_grad(g, s, kz);
+  const int c = p.targets[r] - at.lo;
+  if (c >= 0 && c < at.cols && h.holds(c)) g[c] = (T)fmaf(kz, row_exp(s, (float)row[c]), k);
 }
 
 template <typename T>
-__global__ __launch_bounds__(kNT) void pref_grad_kernel(
-    const T* __restrict__ z, int64_t R, int64_t C, int64_t ld, float scale,
-    const int32_t* __restrict__ targets, const float4* __restrict__ soft,
-    const float* __restrict__ coef, T* __restrict__ grad, int64_t gld) {
-  for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
-    const float k = coef[r] * scale;
-    T* g = grad + r * gld;
-    if (k == 0.0f) {
-      for (int64_t c = threadIdx.x; c < C; c += kNT) g[c] = (T)0.0f;
-      continue;
-    }
-    const T* row = z + r * ld;
-    const int64_t t = targets[r];
-    const float4 f = soft[r];
-    const RowSoft s{f.x, f.y, f.z, f.w};
-    const float kz = -k / s.Z;
-    for (int64_t c = threadIdx.x; c < C; c += kNT) {
-      const float e = row_exp(s, (float)row[c]);
-      g[c] = (T)(c == t ? fmaf(kz, e, k) : kz * e);
-    }
-  }
+hipError_t parts_t(const Rows& a, const Parts& p, const int32_t* targets, const float* weight,
+                   const int32_t* offsets, int64_t S, float2* out, hipStream_t s) {
+  hipLaunchKernelGGL(parts_kernel<T>, linear_grid(a.R * p.n), dim3(256), 0, s, (const T*)a.z, a.R,
+                     (int)a.C, a.ld, a.scale, p, targets, weight, offsets, S, out);
+  return hipGetLastError();
 }
 
 template <typename T>
 hipError_t preference_t(const Rows& a, const PrefArgs& p, char* ws, hipStream_t s) {
-  const PrefLayout w = pref_layout(a.R, p.S);
+  const RowsLayout w = pref_layout(a.R, a.C, p.S, a.dtype);
+  const Parts parts = plan_parts(a.R, a.C, sizeof(T));
+  float2* mz = (float2*)(ws + w.parts);
   float4* soft = (float4*)(ws + w.soft);
-  double* logp = (double*)(ws + w.logp);
   float* coef = (float*)(ws + w.coef);
   double* seq = (double*)(ws + w.seq);
   hipError_t e;
-  if (a.R > 0) {
-    hipLaunchKernelGGL(pref_rows_kernel<T>, dim3(grid_of(a.R)), dim3(kNT), 0, s, (const T*)a.z,
-                       a.R, a.C, a.ld, a.scale, p.targets, p.offsets, p.S, soft, logp, coef);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
   if (p.S > 0) {
-    hipLaunchKernelGGL(pref_seq_kernel, dim3(grid_of(p.S)), dim3(64), 0, s, p, a.R, logp, seq);
+    e = parts_t<T>(a, parts, p.targets, nullptr, p.offsets, p.S, mz, s);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(pref_seq_kernel<T>, linear_grid(p.S), dim3(64), 0, s, p, (const T*)a.z, a.R,
+                       (int)a.C, a.ld, a.scale, mz, parts.n, soft, seq);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(pref_pairs_kernel, dim3(grid_of(p.S + 1)), dim3(256), 0, s, p, a.R, seq,
-                     coef);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (a.grad && a.R > 0) {
-    hipLaunchKernelGGL(pref_grad_kernel<T>, dim3(grid_of(a.R)), dim3(kNT), 0, s, (const T*)a.z,
-                       a.R, a.C, a.ld, a.scale, p.targets, soft, coef, (T*)a.grad, a.grad_ld);
-    e = hipGetLastError();
-  }
-  return e;
+  hipLaunchKernelGGL(pref_pairs_kernel, linear_grid(p.S + 1), dim3(256), 0, s, p, a.R, seq, coef);
+  if ((e = hipGetLastError()) != hipSuccess || !a.grad) return e;
+  hipLaunchKernelGGL(pref_grad_kernel<T>, linear_grid(a.R * parts.n), dim3(256), 0, s,
+                     (const T*)a.z, a.R, (int)a.C, a.ld, a.scale, parts, p, soft, coef,
+                     (T*)a.grad, a.grad_ld);
+  return hipGetLastError();
 }
 
 template <typename T>
-hipError_t logprob_fwd_t(const Rows& a, const int32_t* targets, float* logp, float* lse,
+hipError_t logprob_fwd_t(const Rows& a, const int32_t* targets, float* logp, float* lse, char* ws,
                          hipStream_t s) {
-  hipLaunchKernelGGL(logprob_fwd_kernel<T>, dim3(grid_of(a.R)), dim3(kNT), 0, s, (const T*)a.z,
-                     a.R, a.C, a.ld, a.scale, targets, logp, lse);
+  const Parts parts = plan_parts(a.R, a.C, sizeof(T));
+  float2* mz = (float2*)ws;
+  hipError_t e = parts_t<T>(a, parts, targets, nullptr, nullptr, 0, mz, s);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(logprob_finish_kernel<T>, group_grid<64>(a.R), dim3(256), 0, s,
+                     (const T*)a.z, a.R, (int)a.C, a.ld, a.scale, targets, mz, parts.n, logp, lse);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t logprob_bwd_t(const Rows& a, const int32_t* targets, const float* lse,
                          const float* dlogp, hipStream_t s) {
-  hipLaunchKernelGGL(logprob_bwd_kernel<T>, dim3(grid_of(a.R)), dim3(kNT), 0, s, (const T*)a.z,
-                     a.R, a.C, a.ld, a.scale, targets, lse, dlogp, (T*)a.grad, a.grad_ld);
+  const Parts parts = plan_parts(a.R, a.C, sizeof(T));
+  hipLaunchKernelGGL(logprob_bwd_kernel<T>, linear_grid(a.R * parts.n), dim3(256), 0, s,
+                     (const T*)a.z, a.R, (int)a.C, a.ld, a.scale, parts, targets, lse, dlogp,
+                     (T*)a.grad, a.grad_ld);
   return hipGetLastError();
 }
 
 }  // namespace
 
+hipError_t run_parts(const Rows& a, const Parts& p, const int32_t* targets, const float* weight,
+                     const int32_t* offsets, int64_t S, float2* out, hipStream_t s) {
+  if (a.dtype == LIK_F16) return parts_t<_Float16>(a, p, targets, weight, offsets, S, out, s);
+  if (a.dtype == LIK_BF16) return parts_t<__bf16>(a, p, targets, weight, offsets, S, out, s);
+  return parts_t<float>(a, p, targets, weight, offsets, S, out, s);
+}
+
 hipError_t run_logprob_fwd(const Rows& a, const int32_t* targets, float* logp, float* lse,
-                           hipStream_t s) {
-  if (a.dtype == LIK_F16) return logprob_fwd_t<_Float16>(a, targets, logp, lse, s);
-  if (a.dtype == LIK_BF16) return logprob_fwd_t<__bf16>(a, targets, logp, lse, s);
-  return logprob_fwd_t<float>(a, targets, logp, lse, s);
+                           char* ws, hipStream_t s) {
+  if (a.dtype == LIK_F16) return logprob_fwd_t<_Float16>(a, targets, logp, lse, ws, s);
+  if (a.dtype == LIK_BF16) return logprob_fwd_t<__bf16>(a, targets, logp, lse, ws, s);
+  return logprob_fwd_t<float>(a, targets, logp, lse, ws, s);
 }
 
 hipError_t run_logprob_bwd(const Rows& a, const int32_t* targets, const float* lse,

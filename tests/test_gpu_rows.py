@@ -71,6 +71,8 @@ def draw(R, C, seed, spread=3.0):
 # sizes around the widths kernels step in, one column, one row, long rows
 SIZES = [(1, 1), (3, 2), (5, 17), (4, 64), (9, 255), (6, 1000), (3, 4097), (130, 520), (2, 33001),
          (3, 70000), (1, 140001)]
+# rows enough to fill the chip, which are held whole in registers where they fit
+MANY = [(256, 9001), (259, 33001), (256, 70001)]
 TYPES = [F16, BF16, F32]
 
 
@@ -182,7 +184,7 @@ def distill_case(R, C, K, rest, dtype, scale, seed, weight=None, idx=None, val=N
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("R,C", SIZES)
+@pytest.mark.parametrize("R,C", SIZES + MANY)
 @pytest.mark.parametrize("rest", [False, True])
 def test_distill(R, C, dtype, rest):
     K = [1, 5, 32, 100][(R + C) % 4]
@@ -280,7 +282,7 @@ def policy_case(z, t, dtype, scale, seed, weight=None, kl=0.1, low=0.2, high=0.3
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("R,C", SIZES)
+@pytest.mark.parametrize("R,C", SIZES + MANY)
 def test_policy(R, C, dtype):
     say(f"[rows] policy {R} x {C} {dtype}")
     rng, z, t = draw(R, C, 3 * R + C)
