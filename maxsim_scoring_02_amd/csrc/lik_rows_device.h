@@ -292,87 +292,120 @@ __device__ __forceinline__ float piece_sum(piece p, const RowSoft& s, uint32_t o
   return a + b;
 }
 
-// k * e for every element
-template <typename T>
-__device__ __forceinline__ piece piece_grad(piece p, const RowSoft& s, float k) {
-  float f[PieceOf<T>::N];
-  unpack<T>(p, f);
-#pragma unroll
-  for (int i = 0; i < PieceOf<T>::N; ++i) f[i] = k * row_exp(s, f[i]);
-  return pack<T>(f);
-}
-
 // Waits for this wave's loads (and stores): vmcnt(0) alone.
 __device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }
 
-// `C` columns from `row` as 16-byte pieces, dealt to GT threads in turn, the
-// first NV of every thread held in registers; the columns behind the last
-// whole piece, one to a thread, in `last`.  No column is touched twice.
+// Elements before the first 16-byte boundary at or behind p, at most C.
+template <typename T>
+__device__ __forceinline__ int head_of(const T* p, int C) {
+  const int h = (int)((16 - ((uintptr_t)p & 15)) & 15) / (int)sizeof(T);
+  return h < C ? h : C;
+}
+
+// How GT threads share `C` columns: a head up to a 16-byte boundary of what
+// `at` points to and a tail behind the last whole piece, one column to a
+// thread, and between them 16-byte pieces, dealt to the threads in turn.
+template <typename T, int GT>
+struct Deal {
+  static constexpr int N = PieceOf<T>::N;
+  int tid, head, pieces, edges;        // edges: columns of the head and the tail
+
+  __device__ __forceinline__ Deal() {}
+  __device__ __forceinline__ Deal(const T* at, int C, int t) {
+    tid = t;
+    head = head_of(at, C);
+    pieces = (C - head) / N;
+    edges = C - pieces * N;
+  }
+  __device__ __forceinline__ bool has(int i) const { return i * GT + tid < pieces; }
+  __device__ __forceinline__ int column(int i) const { return head + (i * GT + tid) * N; }
+  __device__ __forceinline__ bool has_edge() const { return tid < edges; }
+  __device__ __forceinline__ int edge() const { return tid < head ? tid : tid + pieces * N; }
+  // whether column c is this thread's
+  __device__ __forceinline__ bool holds(int c) const {
+    const int p = c - head;
+    if (p >= 0 && p < pieces * N) return p / N % GT == tid;
+    return tid == (p < 0 ? c : c - pieces * N);
+  }
+};
+
+// The columns of a Deal in registers: NV pieces a thread at most and an edge.
+// The pieces are aligned to the gradient's row where one is written (an
+// unaligned store costs more than an unaligned load: 4096 x 131071 bf16 policy
+// loss 508 us without it), else to the logits'.
 template <typename T, int GT, int NV, bool Once = true>
 struct HeldRow {
   static constexpr int N = PieceOf<T>::N;
   static constexpr int64_t kColumns = (int64_t)GT * NV * N;
+  Deal<T, GT> deal;
   piece d[NV];
-  float last;
-  int tid, pieces, tail;
+  float edge;
 
-  __device__ __forceinline__ void load(const T* __restrict__ row, int C, int t) {
-    tid = t;
-    pieces = C / N;
-    tail = C - pieces * N;
+  __device__ __forceinline__ void load(const T* __restrict__ row, int C, int tid, const T* grad) {
+    deal = Deal<T, GT>(grad ? grad : row, C, tid);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       d[i] = no_logits<T>();
-      if (i * GT < pieces && i * GT + tid < pieces) d[i] = load_piece<Once>(row + (i * GT + tid) * N);
+      if (i * GT < deal.pieces && deal.has(i)) d[i] = load_piece<Once>(row + deal.column(i));
     }
-    last = -kInf;
-    if (tid < tail) last = (float)row[pieces * N + tid];
+    edge = -kInf;
+    if (deal.has_edge()) edge = (float)row[deal.edge()];
   }
   __device__ __forceinline__ float max() const {
-    float m = last;
+    float m = edge;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (i * GT < pieces) m = piece_max<T>(d[i], m);
+      if (i * GT < deal.pieces) m = piece_max<T>(d[i], m);
     return m;
   }
-  // `listed`: a bit per column that is left out of the sum, or null
+  // `listed`: a bit per column that is left out of the sum (and a word behind
+  // the last), or null
   __device__ __forceinline__ float sum(const RowSoft& s, const uint32_t* listed) const {
-    float z = row_exp(s, last);
-    if (listed && tid < tail) {
-      const int c = pieces * N + tid;
+    float z = row_exp(s, edge);
+    if (listed && deal.has_edge()) {
+      const int c = deal.edge();
       if (listed[c >> 5] >> (c & 31) & 1) z = 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (i * GT < pieces) {
+      if (i * GT < deal.pieces) {
         uint32_t out = 0;
-        if (listed && i * GT + tid < pieces) {
-          const int c = (i * GT + tid) * N;
-          out = listed[c >> 5] >> (c & 31) & ((1u << N) - 1);
+        if (listed && deal.has(i)) {
+          const int c = deal.column(i);
+          const uint64_t w = (uint64_t)listed[(c >> 5) + 1] << 32 | listed[c >> 5];
+          out = (uint32_t)(w >> (c & 31)) & ((1u << N) - 1);
         }
         z += piece_sum<T>(d[i], s, out);
       }
     }
     return z;
   }
-  // g = k e.  The pieces are all here by now; said once, before the stores, it
-  // keeps the compiler from waiting for every store before the next piece.
-  __device__ __forceinline__ void store_grad(T* __restrict__ g, const RowSoft& s, float k) const {
+  // g = f(logit).  The pieces are all here by now; said once, before the
+  // stores, it keeps the compiler from waiting for every store before the next
+  // piece.
+  template <typename F>
+  __device__ __forceinline__ void store(T* __restrict__ g, F f) const {
     wait_loads();
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (i * GT < pieces && i * GT + tid < pieces)
-        store_piece(g + (i * GT + tid) * N, piece_grad<T>(d[i], s, k));
-    if (tid < tail) g[pieces * N + tid] = (T)(k * row_exp(s, last));
+    for (int i = 0; i < NV; ++i) {
+      if (i * GT < deal.pieces && deal.has(i)) {
+        float x[N];
+        unpack<T>(d[i], x);
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] = f(x[j]);
+        store_piece(g + deal.column(i), pack<T>(x));
+      }
+    }
+    if (deal.has_edge()) g[deal.edge()] = (T)f(edge);
   }
-  // whether this thread holds column c
-  __device__ __forceinline__ bool holds(int c) const {
-    const int p = c / N;
-    return p < pieces ? p % GT == tid : c - pieces * N == tid;
+  // g = k e
+  __device__ __forceinline__ void store_grad(T* __restrict__ g, const RowSoft& s, float k) const {
+    store(g, [&](float x) { return k * row_exp(s, x); });
   }
+  __device__ __forceinline__ bool holds(int c) const { return deal.holds(c); }
 };
 
-// Zeros, NaN or any constant over a row.
+// A constant over a row.
 template <typename T, int GT>
 __device__ __forceinline__ void fill_row(T* __restrict__ g, int C, int tid, float v) {
   constexpr int N = PieceOf<T>::N;
@@ -380,9 +413,9 @@ __device__ __forceinline__ void fill_row(T* __restrict__ g, int C, int tid, floa
 #pragma unroll
   for (int i = 0; i < N; ++i) f[i] = v;
   const piece p = pack<T>(f);
-  const int pieces = C / N;
-  for (int i = tid; i < pieces; i += GT) store_piece(g + (int64_t)i * N, p);
-  if (tid < C - pieces * N) g[(int64_t)pieces * N + tid] = (T)v;
+  const Deal<T, GT> deal(g, C, tid);
+  for (int i = 0; deal.has(i); ++i) store_piece(g + deal.column(i), p);
+  if (deal.has_edge()) g[deal.edge()] = (T)v;
 }
 
 // The softmax of a group's columns: each wave's (m, Z), merged in LDS.  `tmp`

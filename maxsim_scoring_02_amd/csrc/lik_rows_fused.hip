@@ -15,23 +15,30 @@ namespace lik {
 
 namespace {
 
-// loss = sum_r w_r l_r, rows of weight 0 left out
-__global__ __launch_bounds__(256) void weighted_sum_kernel(const float* __restrict__ l,
-                                                           const float* __restrict__ w, int64_t R,
-                                                           float* __restrict__ loss) {
-  __shared__ double tmp[4];
+// loss = sum_r w_r l_r, rows of weight 0 left out.  One workgroup, so that the
+// order is fixed; eight rows a thread are in flight at once.
+__global__ __launch_bounds__(1024) void weighted_sum_kernel(const float* __restrict__ l,
+                                                            const float* __restrict__ w, int64_t R,
+                                                            float* __restrict__ loss) {
+  __shared__ double tmp[16];
   double acc = 0.0;
-  for (int64_t r = threadIdx.x; r < R; r += 256) {
-    const float k = w ? w[r] : 1.0f;
-    if (k != 0.0f) acc += (double)k * (double)l[r];
+  for (int64_t r0 = threadIdx.x; r0 < R; r0 += 8 * 1024) {
+    float x[8], k[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t r = r0 + i * 1024;
+      x[i] = r < R ? l[r] : 0.0f;
+      k[i] = r < R ? (w ? w[r] : 1.0f) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (k[i] != 0.0f) acc += (double)k[i] * (double)x[i];
   }
   acc = wave_sum(acc);
   if ((threadIdx.x & 63) == 0) tmp[wave_id()] = acc;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    acc = (tmp[0] + tmp[1]) + (tmp[2] + tmp[3]);
-    *loss = (float)(w ? acc : acc / (double)R);
-  }
+  acc = wave_sum((threadIdx.x & 63) < 16 ? tmp[threadIdx.x & 63] : 0.0);
+  if (threadIdx.x == 0) *loss = (float)(w ? acc : acc / (double)R);
 }
 
 template <typename T>
@@ -90,7 +97,7 @@ void policy_held_kernel(const PolicyArgs<T> a) {
     return;
   }
   HeldRow<T, GT, NV> h;
-  h.load(a.z + r * a.ld, a.C, tid);
+  h.load(a.z + r * a.ld, a.C, tid, g);
   const PolicyRow x = policy_row(a, r, t, w);
   const RowSoft s = held_softmax<GT>(h, a.scale, nullptr, tmp);
   const float k = policy_finish(a, r, x, s, tid == 0);
@@ -120,7 +127,7 @@ __global__ __launch_bounds__(256) void policy_parts_kernel(const PolicyArgs<T> a
     return;
   }
   HeldRow<T, 256, kPartPieces> h;
-  if (g) h.load(a.z + r * a.ld + at.lo, at.cols, tid);
+  if (g) h.load(a.z + r * a.ld + at.lo, at.cols, tid, g);
   const PolicyRow x = policy_row(a, r, t, w);
   const RowSoft s = merge_parts(mz + r * parts.n, parts.n, a.scale);
   const float k = policy_finish(a, r, x, s, at.p == 0 && tid == 0);
@@ -159,7 +166,7 @@ constexpr int32_t kAgain = 1 << 24;
 static_assert(kDistillMaxC < kAgain, "a column and its mark share a word");
 
 __host__ __device__ inline size_t teacher_bytes(int C, int K) {
-  return ((size_t)K * 12 + 4 + ((size_t)C + 31) / 32 * 4 + 15) / 16 * 16;
+  return ((size_t)K * 12 + 4 + ((size_t)C + 31) / 32 * 4 + 4 + 15) / 16 * 16;
 }
 __device__ __forceinline__ TeacherList teacher_at(char* p, int K) {
   TeacherList L;
@@ -219,7 +226,7 @@ template <typename T, int GT>
 __device__ __forceinline__ void teacher_fill(const DistillArgs<T>& a, const TeacherList& L,
                                              int64_t r, const T* row, int tid, int32_t j0,
                                              float t0) {
-  const int words = (a.C + 31) / 32;
+  const int words = (a.C + 31) / 32 + 1;
   for (int i = tid; i < words; i += GT) L.listed[i] = 0;
   if (tid == 0) *L.flags = 0;
   group_sync<GT>();
@@ -343,7 +350,7 @@ void distill_held_kernel(const DistillArgs<T> a) {
   float t0;
   teacher_ahead(a, r, tid, &j0, &t0);
   HeldRow<T, GT, NV> h;
-  h.load(row, a.C, tid);
+  h.load(row, a.C, tid, g);
   teacher_fill<T, GT>(a, L, r, row, tid, j0, t0);
   const int flags = *L.flags;
   const bool with_rest = a.t_lse != nullptr;
@@ -372,17 +379,17 @@ template <typename T>
 __global__ __launch_bounds__(256) void distill_stats_kernel(const DistillArgs<T> a, Parts parts,
                                                             float2* __restrict__ mz) {
   __shared__ float tmp[8];
-  __shared__ uint32_t listed[256 * kPartPieces * PieceOf<T>::N / 32];
+  __shared__ uint32_t listed[256 * kPartPieces * PieceOf<T>::N / 32 + 1];
   const PartAt at = part_at(parts.cols, parts.n, a.C);
   if (at.r >= a.R) return;
   const int64_t r = at.r;
   const int tid = threadIdx.x;
   if (a.weight && a.weight[r] == 0.0f) return;
   HeldRow<T, 256, kPartPieces, false> h;
-  h.load(a.z + r * a.ld + at.lo, at.cols, tid);
+  h.load(a.z + r * a.ld + at.lo, at.cols, tid, nullptr);
   const bool with_rest = a.t_lse != nullptr;
   if (with_rest) {
-    for (int i = tid; i < (at.cols + 31) / 32; i += 256) listed[i] = 0;
+    for (int i = tid; i < (at.cols + 31) / 32 + 1; i += 256) listed[i] = 0;
     __syncthreads();
     for (int k = tid; k < a.K; k += 256) {
       const int64_t c = (int64_t)a.idx[r * a.K + k] - at.lo;
@@ -418,7 +425,7 @@ __global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T>
   float t0;
   teacher_ahead(a, r, tid, &j0, &t0);
   HeldRow<T, 256, kPartPieces> h;
-  if (g) h.load(row + at.lo, at.cols, tid);
+  if (g) h.load(row + at.lo, at.cols, tid, g + at.lo);
   teacher_fill<T, 256>(a, L, r, row, tid, j0, t0);
   const int flags = *L.flags;
   const bool with_rest = a.t_lse != nullptr;
@@ -501,7 +508,7 @@ hipError_t distill_t(const Rows& a, const int32_t* idx, const float* val, int64_
 }
 
 hipError_t weighted_sum(const float* l, const float* w, int64_t R, float* loss, hipStream_t s) {
-  hipLaunchKernelGGL(weighted_sum_kernel, dim3(1), dim3(256), 0, s, l, w, R, loss);
+  hipLaunchKernelGGL(weighted_sum_kernel, dim3(1), dim3(1024), 0, s, l, w, R, loss);
   return hipGetLastError();
 }
 

@@ -17,7 +17,8 @@ __device__ __forceinline__ bool row_counts(int64_t r, const int32_t* targets, co
   return !offsets || (r >= offsets[0] && r < offsets[S]);
 }
 
-template <typename T>
+// Once: nothing looks at the rows again.
+template <typename T, bool Once>
 __global__ __launch_bounds__(256) void parts_kernel(const T* __restrict__ z, int64_t R, int C,
                                                     int64_t ld, float scale, Parts parts,
                                                     const int32_t* __restrict__ targets,
@@ -27,8 +28,8 @@ __global__ __launch_bounds__(256) void parts_kernel(const T* __restrict__ z, int
   __shared__ float tmp[8];
   const PartAt at = part_at(parts.cols, parts.n, C);
   if (at.r >= R || !row_counts(at.r, targets, weight, offsets, S)) return;
-  HeldRow<T, 256, kPartPieces, false> h;
-  h.load(z + at.r * ld + at.lo, at.cols, threadIdx.x);
+  HeldRow<T, 256, kPartPieces, Once> h;
+  h.load(z + at.r * ld + at.lo, at.cols, threadIdx.x, nullptr);
   const RowSoft s = held_softmax<256, true>(h, scale, nullptr, tmp);
   if (threadIdx.x == 0) out[at.r * parts.n + at.p] = make_float2(s.m, s.Z);
 }
@@ -62,7 +63,6 @@ __global__ __launch_bounds__(256) void logprob_bwd_kernel(
     const T* __restrict__ z, int64_t R, int C, int64_t ld, float scale, Parts parts,
     const int32_t* __restrict__ targets, const float* __restrict__ lse,
     const float* __restrict__ dlogp, T* __restrict__ grad, int64_t gld) {
-  constexpr int N = PieceOf<T>::N;
   const PartAt at = part_at(parts.cols, parts.n, C);
   if (at.r >= R) return;
   const int64_t r = at.r;
@@ -77,21 +77,10 @@ __global__ __launch_bounds__(256) void logprob_bwd_kernel(
   const float k = t < C ? d * scale : __builtin_nanf("");
   const float l = lse[r];
   HeldRow<T, 256, kPartPieces> h;
-  h.load(row, at.cols, tid);
-  wait_loads();
+  h.load(row, at.cols, tid, g);
   // y - lse is rounded once, relative to itself, before it is scaled
   auto prob = [&](float x) { return exp2_fast(fmaf(x, scale, -l) * kLog2e); };
-#pragma unroll
-  for (int i = 0; i < kPartPieces; ++i) {
-    if (i * 256 < h.pieces && i * 256 + tid < h.pieces) {
-      float f[N];
-      unpack<T>(h.d[i], f);
-#pragma unroll
-      for (int j = 0; j < N; ++j) f[j] = -k * prob(f[j]);
-      store_piece(g + (i * 256 + tid) * N, pack<T>(f));
-    }
-  }
-  if (tid < h.tail) g[h.pieces * N + tid] = (T)(-k * prob(h.last));
+  h.store(g, [&](float x) { return -k * prob(x); });
   const int c = t - at.lo;
   if (c >= 0 && c < at.cols && h.holds(c)) g[c] = (T)fmaf(-k, prob((float)row[c]), k);
 }
@@ -228,7 +217,8 @@ __global__ __launch_bounds__(256) void pref_pairs_kernel(PrefArgs p, int64_t R,
   for (int64_t r = a + tid; r < b; r += 256) coef[r] = p.targets[r] >= 0 ? (float)acc : 0.0f;
 }
 
-// A part of a row's gradient; 0 for rows outside every sequence.
+// A part of a row's gradient; 0 for rows outside every sequence.  The rows run
+// backwards: those that the first look read last are still in the caches.
 template <typename T>
 __global__ __launch_bounds__(256) void pref_grad_kernel(
     const T* __restrict__ z, int64_t R, int C, int64_t ld, float scale, Parts parts, PrefArgs p,
@@ -236,7 +226,7 @@ __global__ __launch_bounds__(256) void pref_grad_kernel(
     int64_t gld) {
   const PartAt at = part_at(parts.cols, parts.n, C);
   if (at.r >= R) return;
-  const int64_t r = at.r;
+  const int64_t r = R - 1 - at.r;
   const int tid = threadIdx.x;
   T* g = grad + r * gld + at.lo;
   const bool in = p.S > 0 && row_counts(r, p.targets, nullptr, p.offsets, p.S);
@@ -247,7 +237,7 @@ __global__ __launch_bounds__(256) void pref_grad_kernel(
   }
   const T* row = z + r * ld + at.lo;
   HeldRow<T, 256, kPartPieces> h;
-  h.load(row, at.cols, tid);
+  h.load(row, at.cols, tid, g);
   const float4 f = soft[r];
   const RowSoft s{f.x, f.y, f.z, f.w};
   const float kz = -k / s.Z;
@@ -256,10 +246,10 @@ __global__ __launch_bounds__(256) void pref_grad_kernel(
   if (c >= 0 && c < at.cols && h.holds(c)) g[c] = (T)fmaf(kz, row_exp(s, (float)row[c]), k);
 }
 
-template <typename T>
+template <typename T, bool Once>
 hipError_t parts_t(const Rows& a, const Parts& p, const int32_t* targets, const float* weight,
                    const int32_t* offsets, int64_t S, float2* out, hipStream_t s) {
-  hipLaunchKernelGGL(parts_kernel<T>, linear_grid(a.R * p.n), dim3(256), 0, s, (const T*)a.z, a.R,
+  hipLaunchKernelGGL((parts_kernel<T, Once>), linear_grid(a.R * p.n), dim3(256), 0, s, (const T*)a.z, a.R,
                      (int)a.C, a.ld, a.scale, p, targets, weight, offsets, S, out);
   return hipGetLastError();
 }
@@ -274,7 +264,7 @@ hipError_t preference_t(const Rows& a, const PrefArgs& p, char* ws, hipStream_t 
   double* seq = (double*)(ws + w.seq);
   hipError_t e;
   if (p.S > 0) {
-    e = parts_t<T>(a, parts, p.targets, nullptr, p.offsets, p.S, mz, s);
+    e = parts_t<T, false>(a, parts, p.targets, nullptr, p.offsets, p.S, mz, s);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(pref_seq_kernel<T>, linear_grid(p.S), dim3(64), 0, s, p, (const T*)a.z, a.R,
                        (int)a.C, a.ld, a.scale, mz, parts.n, soft, seq);
@@ -293,7 +283,7 @@ hipError_t logprob_fwd_t(const Rows& a, const int32_t* targets, float* logp, flo
                          hipStream_t s) {
   const Parts parts = plan_parts(a.R, a.C, sizeof(T));
   float2* mz = (float2*)ws;
-  hipError_t e = parts_t<T>(a, parts, targets, nullptr, nullptr, 0, mz, s);
+  hipError_t e = parts_t<T, true>(a, parts, targets, nullptr, nullptr, 0, mz, s);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(logprob_finish_kernel<T>, group_grid<64>(a.R), dim3(256), 0, s,
                      (const T*)a.z, a.R, (int)a.C, a.ld, a.scale, targets, mz, parts.n, logp, lse);
@@ -314,9 +304,9 @@ hipError_t logprob_bwd_t(const Rows& a, const int32_t* targets, const float* lse
 
 hipError_t run_parts(const Rows& a, const Parts& p, const int32_t* targets, const float* weight,
                      const int32_t* offsets, int64_t S, float2* out, hipStream_t s) {
-  if (a.dtype == LIK_F16) return parts_t<_Float16>(a, p, targets, weight, offsets, S, out, s);
-  if (a.dtype == LIK_BF16) return parts_t<__bf16>(a, p, targets, weight, offsets, S, out, s);
-  return parts_t<float>(a, p, targets, weight, offsets, S, out, s);
+  if (a.dtype == LIK_F16) return parts_t<_Float16, false>(a, p, targets, weight, offsets, S, out, s);
+  if (a.dtype == LIK_BF16) return parts_t<__bf16, false>(a, p, targets, weight, offsets, S, out, s);
+  return parts_t<float, false>(a, p, targets, weight, offsets, S, out, s);
 }
 
 hipError_t run_logprob_fwd(const Rows& a, const int32_t* targets, float* logp, float* lse,
