@@ -10,7 +10,9 @@ exception is raised.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 import re
 from typing import Optional, Tuple
@@ -417,9 +419,30 @@ def _row_outs(R: int, device, *shapes) -> list:
     return [make(s, dtype=torch.float32, device=device) for s in shapes]
 
 
+@functools.lru_cache(maxsize=1024)
+def _rows_workspace_bytes(op: int, R: int, C: int, S: int, dt: int) -> int:
+    return lib().lik_rows_workspace_bytes(op, R, C, S, dt)
+
+
 def _rows_workspace(op: int, R: int, C: int, S: int, dt: int, device) -> Tuple:
-    n = lib().lik_rows_workspace_bytes(op, R, C, S, dt)
+    n = _rows_workspace_bytes(op, R, C, S, dt)
     return _workspace(n, device), n
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+_NOTHING = contextlib.nullcontext()
+
+
+def _current(device):
+    """Makes the tensors' device the current one for the call."""
+    return _NOTHING if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _stream_of(device):
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def lik_logprob_rows_fwd(logits, targets, scale=1.0) -> Tuple:
@@ -429,11 +452,11 @@ def lik_logprob_rows_fwd(logits, targets, scale=1.0) -> Tuple:
     dt, R, C, ld = _rows(logits)
     dev = logits.device
     t = _row_arg(targets, (R,), "targets", dev, torch.int32)
-    with torch.cuda.device(dev):
+    with _current(dev):
         logp, lse = _row_outs(R, dev, (R,), (R,))
         ws, wsb = _rows_workspace(LIK_ROWS_LOGPROB_FWD, R, C, 0, dt, dev)
-        _check(lib().lik_logprob_rows_fwd(_ptr(logits), dt, R, C, ld, _ptr(t), float(scale),
-                                          _ptr(logp), _ptr(lse), _ptr(ws), wsb, _stream()))
+        _check(lib().lik_logprob_rows_fwd(_addr(logits), dt, R, C, ld, _addr(t), float(scale),
+                                          _addr(logp), _addr(lse), _addr(ws), wsb, _stream_of(dev)))
     return logp, lse
 
 
@@ -446,9 +469,9 @@ def lik_logprob_rows_bwd(logits, targets, lse, grad_logp, scale=1.0, grad_out=No
     lse = _row_arg(lse, (R,), "lse", dev)
     g = _row_arg(grad_logp, (R,), "grad_logp", dev)
     grad, gld = _row_grad(logits, True, grad_out)
-    with torch.cuda.device(dev):
-        _check(lib().lik_logprob_rows_bwd(_ptr(logits), dt, R, C, ld, _ptr(t), float(scale),
-                                          _ptr(lse), _ptr(g), _ptr(grad), gld, _stream()))
+    with _current(dev):
+        _check(lib().lik_logprob_rows_bwd(_addr(logits), dt, R, C, ld, _addr(t), float(scale),
+                                          _addr(lse), _addr(g), _addr(grad), gld, _stream_of(dev)))
     return grad
 
 
@@ -470,12 +493,12 @@ def lik_distill_rows(logits, teacher_idx, teacher_logits, teacher_lse=None, scal
     tl = _row_arg(teacher_lse, (R,), "teacher_lse", dev)
     w = _row_arg(row_weight, (R,), "row_weight", dev)
     grad, gld = _row_grad(logits, want_grad, grad_out)
-    with torch.cuda.device(dev):
+    with _current(dev):
         row_loss, loss = _row_outs(R, dev, (R,), (1,))
         ws, wsb = _rows_workspace(LIK_ROWS_DISTILL, R, C, 0, dt, dev)
-        _check(lib().lik_distill_rows(_ptr(logits), dt, R, C, ld, _ptr(idx), _ptr(val), K,
-                                      _ptr(tl), float(scale), _ptr(w), _ptr(row_loss),
-                                      _ptr(loss), _ptr(grad), gld, _ptr(ws), wsb, _stream()))
+        _check(lib().lik_distill_rows(_addr(logits), dt, R, C, ld, _addr(idx), _addr(val), K,
+                                      _addr(tl), float(scale), _addr(w), _addr(row_loss),
+                                      _addr(loss), _addr(grad), gld, _addr(ws), wsb, _stream_of(dev)))
     return loss, row_loss, grad
 
 
@@ -493,13 +516,13 @@ def lik_policy_rows(logits, targets, old_logp, advantage, ref_logp=None, scale=1
     ref = _row_arg(ref_logp, (R,), "ref_logp", dev)
     w = _row_arg(row_weight, (R,), "row_weight", dev)
     grad, gld = _row_grad(logits, want_grad, grad_out)
-    with torch.cuda.device(dev):
+    with _current(dev):
         row_loss, logp, loss = _row_outs(R, dev, (R,), (R,), (1,))
         ws, wsb = _rows_workspace(LIK_ROWS_POLICY, R, C, 0, dt, dev)
-        _check(lib().lik_policy_rows(_ptr(logits), dt, R, C, ld, _ptr(t), _ptr(old), _ptr(adv),
-                                     _ptr(ref), float(scale), float(clip_low), float(clip_high),
-                                     float(kl_coef), _ptr(w), _ptr(row_loss), _ptr(logp),
-                                     _ptr(loss), _ptr(grad), gld, _ptr(ws), wsb, _stream()))
+        _check(lib().lik_policy_rows(_addr(logits), dt, R, C, ld, _addr(t), _addr(old), _addr(adv),
+                                     _addr(ref), float(scale), float(clip_low), float(clip_high),
+                                     float(kl_coef), _addr(w), _addr(row_loss), _addr(logp),
+                                     _addr(loss), _addr(grad), gld, _addr(ws), wsb, _stream_of(dev)))
     return loss, row_loss, logp, grad
 
 
@@ -524,14 +547,14 @@ def lik_preference_rows(logits, targets, seq_offsets, chosen, rejected, ref_logp
     ref = _row_arg(ref_logp, (S,), "ref_logp", dev)
     w = _row_arg(pair_weight, (P,), "pair_weight", dev)
     grad, gld = _row_grad(logits, want_grad, grad_out)
-    with torch.cuda.device(dev):
+    with _current(dev):
         pair_loss, seq, loss = _row_outs(R, dev, (P,), (S,), (1,))
         ws, wsb = _rows_workspace(LIK_ROWS_PREFERENCE, R, C, S, dt, dev)
         _check(lib().lik_preference_rows(
-            _ptr(logits), dt, R, C, ld, _ptr(t), _ptr(off), S, _ptr(c), _ptr(r), P, _ptr(ref),
+            _addr(logits), dt, R, C, ld, _addr(t), _addr(off), S, _addr(c), _addr(r), P, _addr(ref),
             int(kind), float(beta), float(margin), float(smoothing), int(bool(mean_logp)),
-            float(scale), _ptr(w), _ptr(pair_loss), _ptr(seq), _ptr(loss), _ptr(grad), gld,
-            _ptr(ws), wsb, _stream()))
+            float(scale), _addr(w), _addr(pair_loss), _addr(seq), _addr(loss), _addr(grad), gld,
+            _addr(ws), wsb, _stream_of(dev)))
     return loss, pair_loss, seq, grad
 
 

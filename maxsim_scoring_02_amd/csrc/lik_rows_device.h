@@ -19,6 +19,10 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
+#include "lik_rows_kernels.h"
+
 namespace lik {
 
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -257,9 +261,12 @@ __device__ __forceinline__ piece load_piece(const T* p) {
   if constexpr (Once) return __builtin_nontemporal_load(q);
   return *q;
 }
-template <typename T>
+// Far: past the caches.
+template <bool Far, typename T>
 __device__ __forceinline__ void store_piece(T* p, piece v) {
-  *reinterpret_cast<piece_u2*>(p) = v;
+  piece_u2* q = reinterpret_cast<piece_u2*>(p);
+  if constexpr (Far) __builtin_nontemporal_store(v, q);
+  else *q = v;
 }
 
 template <typename T>
@@ -383,9 +390,8 @@ struct HeldRow {
   // g = f(logit).  The pieces are all here by now; said once, before the
   // stores, it keeps the compiler from waiting for every store before the next
   // piece.
-  template <typename F>
-  __device__ __forceinline__ void store(T* __restrict__ g, F f) const {
-    wait_loads();
+  template <bool Far, typename F>
+  __device__ __forceinline__ void store_as(T* __restrict__ g, F f) const {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (i * GT < deal.pieces && deal.has(i)) {
@@ -393,14 +399,21 @@ struct HeldRow {
         unpack<T>(d[i], x);
 #pragma unroll
         for (int j = 0; j < N; ++j) x[j] = f(x[j]);
-        store_piece(g + deal.column(i), pack<T>(x));
+        store_piece<Far>(g + deal.column(i), pack<T>(x));
       }
     }
+  }
+  template <typename F>
+  __device__ __forceinline__ void store(T* __restrict__ g, bool far, F f) const {
+    wait_loads();
+    if (far) store_as<true>(g, f);
+    else store_as<false>(g, f);
     if (deal.has_edge()) g[deal.edge()] = (T)f(edge);
   }
   // g = k e
-  __device__ __forceinline__ void store_grad(T* __restrict__ g, const RowSoft& s, float k) const {
-    store(g, [&](float x) { return k * row_exp(s, x); });
+  __device__ __forceinline__ void store_grad(T* __restrict__ g, bool far, const RowSoft& s,
+                                             float k) const {
+    store(g, far, [&](float x) { return k * row_exp(s, x); });
   }
   __device__ __forceinline__ bool holds(int c) const { return deal.holds(c); }
 };
@@ -414,7 +427,7 @@ __device__ __forceinline__ void fill_row(T* __restrict__ g, int C, int tid, floa
   for (int i = 0; i < N; ++i) f[i] = v;
   const piece p = pack<T>(f);
   const Deal<T, GT> deal(g, C, tid);
-  for (int i = 0; deal.has(i); ++i) store_piece(g + deal.column(i), p);
+  for (int i = 0; deal.has(i); ++i) store_piece<false>(g + deal.column(i), p);
   if (deal.has_edge()) g[deal.edge()] = (T)v;
 }
 
@@ -471,19 +484,33 @@ __device__ __forceinline__ int64_t group_row() {
 template <int GT>
 __device__ __forceinline__ int group_tid() { return GT == 64 ? threadIdx.x & 63 : threadIdx.x; }
 
-// The part of a row that a workgroup of 256 threads takes in a grid of R * n.
+// The part of a row that a group of GT threads takes in a grid of R * n groups.
 struct PartAt {
   int64_t r;
   int p, lo, cols;
 };
-__device__ __forceinline__ PartAt part_at(int cols, int n, int C) {
+template <int GT>
+__device__ __forceinline__ PartAt part_at(const Parts& parts, int C) {
   PartAt x;
-  const int64_t b = linear_block();
-  x.r = b / n;
-  x.p = (int)(b - x.r * n);
-  x.lo = x.p * cols;
-  x.cols = C - x.lo < cols ? C - x.lo : cols;
+  const int64_t b = group_row<GT>();
+  if constexpr (GT == 64) {              // whole rows
+    x.r = b;
+    x.p = x.lo = 0;
+    x.cols = C;
+    return x;
+  }
+  x.r = b / parts.n;
+  x.p = (int)(b - x.r * parts.n);
+  x.lo = x.p * parts.cols;
+  x.cols = C - x.lo < parts.cols ? C - x.lo : parts.cols;
   return x;
+}
+
+// Calls f with the parts' group size as a constant.
+template <typename F>
+inline hipError_t parts_dispatch(const Parts& parts, F f) {
+  if (parts.gt == 64) return f(std::integral_constant<int, 64>());
+  return f(std::integral_constant<int, 256>());
 }
 
 // Policy loss of one row and its slope dl/dlogp.  x = logp - old, away =

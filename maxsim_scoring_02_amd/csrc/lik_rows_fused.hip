@@ -6,8 +6,6 @@
 // read once and the gradient written once, which is all the traffic there is.
 #include <hip/hip_runtime.h>
 
-#include <type_traits>
-
 #include "lik_rows_device.h"
 #include "lik_rows_kernels.h"
 
@@ -54,6 +52,7 @@ struct PolicyArgs {
   float *row_loss, *logp;
   T* grad;
   int64_t gld;
+  bool far;
 };
 
 // What a row's loss needs beside its softmax, loaded ahead of it.
@@ -103,7 +102,7 @@ void policy_held_kernel(const PolicyArgs<T> a) {
   const float k = policy_finish(a, r, x, s, tid == 0);
   if (g) {
     const float kz = -k / s.Z;
-    h.store_grad(g, s, kz);
+    h.store_grad(g, a.far, s, kz);
     // the same thread stored the column just before
     if (t < a.C && h.holds(t)) g[t] = (T)fmaf(kz, row_exp(s, x.zt), k);
   }
@@ -112,8 +111,8 @@ void policy_held_kernel(const PolicyArgs<T> a) {
 // Rows in parts, the second look: loss (part 0) and gradient.
 template <typename T>
 __global__ __launch_bounds__(256) void policy_parts_kernel(const PolicyArgs<T> a, Parts parts,
-                                                           const float2* __restrict__ mz) {
-  const PartAt at = part_at(parts.cols, parts.n, a.C);
+                                                           const float2* __restrict__ mz, int n) {
+  const PartAt at = part_at<256>(parts, a.C);
   if (at.r >= a.R) return;
   const int64_t r = at.r;
   const int tid = threadIdx.x;
@@ -126,14 +125,14 @@ __global__ __launch_bounds__(256) void policy_parts_kernel(const PolicyArgs<T> a
     if (g) fill_row<T, 256>(g, at.cols, tid, 0.0f);
     return;
   }
-  HeldRow<T, 256, kPartPieces> h;
+  HeldRow<T, 256, kGradPieces> h;
   if (g) h.load(a.z + r * a.ld + at.lo, at.cols, tid, g);
   const PolicyRow x = policy_row(a, r, t, w);
-  const RowSoft s = merge_parts(mz + r * parts.n, parts.n, a.scale);
+  const RowSoft s = merge_parts(mz + r * n, n, a.scale);
   const float k = policy_finish(a, r, x, s, at.p == 0 && tid == 0);
   if (g) {
     const float kz = -k / s.Z;
-    h.store_grad(g, s, kz);
+    h.store_grad(g, a.far, s, kz);
     const int c = t - at.lo;
     if (c >= 0 && c < at.cols && h.holds(c)) g[c] = (T)fmaf(kz, row_exp(s, x.zt), k);
   }
@@ -152,6 +151,7 @@ struct DistillArgs {
   float* row_loss;
   T* grad;
   int64_t gld;
+  bool far;
 };
 
 // The teacher's list of one row in LDS, and a bitmap of its columns.
@@ -367,7 +367,7 @@ void distill_held_kernel(const DistillArgs<T> a) {
   const DistillRow d = distill_row(x, lt, with_rest, a.C, k, &s);
   if (tid == 0) a.row_loss[r] = flags & 1 ? __builtin_nanf("") : d.loss;
   if (g) {
-    h.store_grad(g, s, d.off);
+    h.store_grad(g, a.far, s, d.off);
     group_sync<GT>();
     teacher_grad<T, GT>(L, a.K, a.scale, lt, s, d.on, k, flags, g, 0, a.C, tid);
   }
@@ -379,13 +379,13 @@ template <typename T>
 __global__ __launch_bounds__(256) void distill_stats_kernel(const DistillArgs<T> a, Parts parts,
                                                             float2* __restrict__ mz) {
   __shared__ float tmp[8];
-  __shared__ uint32_t listed[256 * kPartPieces * PieceOf<T>::N / 32 + 1];
-  const PartAt at = part_at(parts.cols, parts.n, a.C);
+  __shared__ uint32_t listed[256 * kLookPieces * PieceOf<T>::N / 32 + 1];
+  const PartAt at = part_at<256>(parts, a.C);
   if (at.r >= a.R) return;
   const int64_t r = at.r;
   const int tid = threadIdx.x;
   if (a.weight && a.weight[r] == 0.0f) return;
-  HeldRow<T, 256, kPartPieces, false> h;
+  HeldRow<T, 256, kLookPieces, false> h;
   h.load(a.z + r * a.ld + at.lo, at.cols, tid, nullptr);
   const bool with_rest = a.t_lse != nullptr;
   if (with_rest) {
@@ -404,9 +404,9 @@ __global__ __launch_bounds__(256) void distill_stats_kernel(const DistillArgs<T>
 // The second look: loss (part 0) and gradient.
 template <typename T>
 __global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T> a, Parts parts,
-                                                            const float2* __restrict__ mz) {
+                                                            const float2* __restrict__ mz, int n) {
   extern __shared__ char lists[];
-  const PartAt at = part_at(parts.cols, parts.n, a.C);
+  const PartAt at = part_at<256>(parts, a.C);
   if (at.r >= a.R) return;
   const int64_t r = at.r;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -424,7 +424,7 @@ __global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T>
   int32_t j0;
   float t0;
   teacher_ahead(a, r, tid, &j0, &t0);
-  HeldRow<T, 256, kPartPieces> h;
+  HeldRow<T, 256, kGradPieces> h;
   if (g) h.load(row + at.lo, at.cols, tid, g + at.lo);
   teacher_fill<T, 256>(a, L, r, row, tid, j0, t0);
   const int flags = *L.flags;
@@ -434,14 +434,14 @@ __global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T>
     if (g) fill_row<T, 256>(g + at.lo, at.cols, tid, 0.0f);
     return;
   }
-  RowSoft s = merge_parts(mz + r * parts.n, parts.n, a.scale);
+  RowSoft s = merge_parts(mz + r * n, n, a.scale);
   const double lt = with_rest ? (double)a.t_lse[r] : teacher_ln(L, a.K, a.scale, lane);
   const TeacherSums x = teacher_sums(L, a.K, a.scale, lt, s, lane);
   const float k = w * a.scale + (flags & 1 ? __builtin_nanf("") : 0.0f);
   const DistillRow d = distill_row(x, lt, with_rest, a.C, k, &s);
   if (first) a.row_loss[r] = flags & 1 ? __builtin_nanf("") : d.loss;
   if (g) {
-    h.store_grad(g + at.lo, s, d.off);
+    h.store_grad(g + at.lo, a.far, s, d.off);
     __syncthreads();
     teacher_grad<T, 256>(L, a.K, a.scale, lt, s, d.on, k, flags, g, at.lo, at.lo + at.cols, tid);
   }
@@ -466,7 +466,7 @@ hipError_t policy_t(const Rows& a, const int32_t* targets, const float* old_logp
                     const float* ref, float low, float high, float kl, const float* weight,
                     float* row_loss, float* logp, char* ws, hipStream_t s) {
   const PolicyArgs<T> p{(const T*)a.z, a.R, a.ld, (int)a.C, a.scale, targets, old_logp, adv, ref,
-                        low, high, kl, weight, row_loss, logp, (T*)a.grad, a.grad_ld};
+                        low, high, kl, weight, row_loss, logp, (T*)a.grad, a.grad_ld, a.far()};
   if (rows_held(a.R, a.C, a.dtype))
     return held_dispatch<T>(a.C, [&](auto gt, auto nv) {
       constexpr int GT = decltype(gt)::value, NV = decltype(nv)::value;
@@ -474,12 +474,12 @@ hipError_t policy_t(const Rows& a, const int32_t* targets, const float* old_logp
                          dim3(group_threads<GT>()), 0, s, p);
       return hipGetLastError();
     });
-  Parts parts = plan_parts(a.R, a.C, sizeof(T));
+  const Parts look = look_parts(a.R, a.C, a.dtype), parts = grad_parts(a.R, a.C, a.dtype);
   float2* mz = (float2*)ws;
-  hipError_t e = run_parts(a, parts, targets, weight, nullptr, 0, mz, s);
+  hipError_t e = run_parts(a, look, targets, weight, nullptr, 0, mz, s);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(policy_parts_kernel<T>, linear_grid(a.R * parts.n), dim3(256), 0, s, p, parts,
-                     mz);
+                     mz, look.n);
   return hipGetLastError();
 }
 
@@ -488,7 +488,7 @@ hipError_t distill_t(const Rows& a, const int32_t* idx, const float* val, int64_
                      const float* t_lse, const float* weight, float* row_loss, char* ws,
                      hipStream_t s) {
   const DistillArgs<T> p{(const T*)a.z, a.R, a.ld, (int)a.C, (int)K, a.scale, idx, val, t_lse,
-                         weight, row_loss, (T*)a.grad, a.grad_ld};
+                         weight, row_loss, (T*)a.grad, a.grad_ld, a.far()};
   const size_t lds = teacher_bytes((int)a.C, (int)K);
   if (rows_held(a.R, a.C, a.dtype))
     return held_dispatch<T>(a.C, [&](auto gt, auto nv) {
@@ -497,13 +497,14 @@ hipError_t distill_t(const Rows& a, const int32_t* idx, const float* val, int64_
                          dim3(group_threads<GT>()), lds * (GT == 64 ? 4 : 1), s, p);
       return hipGetLastError();
     });
-  Parts parts = plan_parts(a.R, a.C, sizeof(T));
+  const Parts look = look_parts(a.R, a.C, a.dtype), parts = grad_parts(a.R, a.C, a.dtype);
   float2* mz = (float2*)ws;
-  const dim3 grid = linear_grid(a.R * parts.n);
-  hipLaunchKernelGGL(distill_stats_kernel<T>, grid, dim3(256), 0, s, p, parts, mz);
+  hipLaunchKernelGGL(distill_stats_kernel<T>, linear_grid(a.R * look.n), dim3(256), 0, s, p, look,
+                     mz);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(distill_parts_kernel<T>, grid, dim3(256), lds, s, p, parts, mz);
+  hipLaunchKernelGGL(distill_parts_kernel<T>, linear_grid(a.R * parts.n), dim3(256), lds, s, p,
+                     parts, mz, look.n);
   return hipGetLastError();
 }
 

@@ -15,29 +15,60 @@ constexpr int64_t kDistillMaxC = int64_t(1) << 20;   // the bitmap of listed col
 inline size_t rows_up(size_t n) { return (n + 255) / 256 * 256; }
 
 // A row cut into parts: part p holds columns [p * cols, (p + 1) * cols), the
-// last what is left.  A part is what 256 threads hold in kPartPieces 16-byte
-// pieces each at most.
-constexpr int kPartPieces = 8;
-constexpr int64_t kPartGroups = 512;     // workgroups that fill the chip
+// last what is left.  A part is taken by a group of gt threads (one wave or 256
+// threads) with at most `pieces` 16-byte pieces each.
 struct Parts {
-  int cols, n;
+  int cols, n, gt;
 };
-// At most kPartPieces pieces a thread; fewer while the rows are too few to
-// fill the chip.
-inline Parts plan_parts(int64_t R, int64_t C, int64_t elem_bytes) {
+constexpr int64_t kPartGroups = 512;     // workgroups that fill the chip
+// Short rows go to one wave whole, four rows a workgroup.  Longer ones are cut
+// into as few parts as hold them, or more while the rows are too few to fill
+// the chip.
+inline Parts plan_parts(int64_t R, int64_t C, int64_t elem_bytes, int pieces) {
+  Parts p;
+  const int64_t wave = 64 * 16 / elem_bytes;
+  if (C <= wave * pieces && C <= 2048) {
+    p.cols = (int)C;
+    p.n = 1;
+    p.gt = 64;
+    return p;
+  }
   const int64_t step = 256 * 16 / elem_bytes;          // one piece a thread
   const int64_t most = (C + step - 1) / step;
-  int64_t n = (C + step * kPartPieces - 1) / (step * kPartPieces);
+  int64_t n = (C + step * pieces - 1) / (step * pieces);
   const int64_t want = (kPartGroups + R - 1) / R;
   if (n < want) n = want < most ? want : most;
-  Parts p;
   p.cols = (int)(((C + n - 1) / n + step - 1) / step * step);
   p.n = (int)((C + p.cols - 1) / p.cols);
+  p.gt = 256;
   return p;
 }
 
+// Pieces a thread holds at the first look (4096 x 100003 bf16
+// log-probabilities: 2, 4, 8, 16 pieces 164, 130, 124, 133 us) and at most at
+// the second (gradients).
+constexpr int kLookPieces = 8;
+constexpr int kGradPieces = 4;
+
+// Gradients too large for the 256 MB cache behind the L2s are stored past the
+// caches, smaller ones stay there for what reads them next (gradient of
+// 2048 x 50001 f16 log-probabilities, 205 MB: 63 us against 70 past the caches;
+// of 4096 x 100003 bf16, 819 MB: 298 against 284).
+constexpr int64_t kFarBytes = int64_t(256) << 20;
+
 inline int64_t elem_bytes_of(lik_dtype t) {
   return t == LIK_F32 ? 4 : (t == LIK_F16 || t == LIK_BF16 ? 2 : 0);
+}
+
+inline Parts look_parts(int64_t R, int64_t C, lik_dtype dtype) {
+  return plan_parts(R, C, elem_bytes_of(dtype), kLookPieces);
+}
+// Large gradients run best with two pieces a thread (4096 x 100003 bf16 270 us
+// against 284 with four), those that stay in the cache with four (2048 x 50001
+// f16 63 us against 67).
+inline Parts grad_parts(int64_t R, int64_t C, lik_dtype dtype) {
+  const int64_t b = elem_bytes_of(dtype);
+  return plan_parts(R, C, b, R * C * b > kFarBytes ? 2 : kGradPieces);
 }
 
 // Workspace layouts.
@@ -51,7 +82,7 @@ struct RowsLayout {
 };
 inline RowsLayout parts_layout(int64_t R, int64_t C, lik_dtype dtype) {
   RowsLayout w;
-  w.bytes = rows_up((size_t)R * plan_parts(R, C, elem_bytes_of(dtype)).n * 8);
+  w.bytes = rows_up((size_t)R * look_parts(R, C, dtype).n * 8);
   return w;
 }
 inline RowsLayout pref_layout(int64_t R, int64_t C, int64_t S, lik_dtype dtype) {
@@ -76,6 +107,7 @@ struct Rows {
   float scale;
   void* grad;          // or null
   int64_t grad_ld;
+  bool far() const { return R * C * elem_bytes_of(dtype) > kFarBytes; }
 };
 
 hipError_t run_logprob_fwd(const Rows& a, const int32_t* targets, float* logp, float* lse,

@@ -18,20 +18,20 @@ __device__ __forceinline__ bool row_counts(int64_t r, const int32_t* targets, co
 }
 
 // Once: nothing looks at the rows again.
-template <typename T, bool Once>
+template <typename T, int GT, bool Once>
 __global__ __launch_bounds__(256) void parts_kernel(const T* __restrict__ z, int64_t R, int C,
                                                     int64_t ld, float scale, Parts parts,
                                                     const int32_t* __restrict__ targets,
                                                     const float* __restrict__ weight,
                                                     const int32_t* __restrict__ offsets, int64_t S,
                                                     float2* __restrict__ out) {
-  __shared__ float tmp[8];
-  const PartAt at = part_at(parts.cols, parts.n, C);
+  __shared__ float tmp[2 * (GT / 64)];
+  const PartAt at = part_at<GT>(parts, C);
   if (at.r >= R || !row_counts(at.r, targets, weight, offsets, S)) return;
-  HeldRow<T, 256, kPartPieces, Once> h;
-  h.load(z + at.r * ld + at.lo, at.cols, threadIdx.x, nullptr);
-  const RowSoft s = held_softmax<256, true>(h, scale, nullptr, tmp);
-  if (threadIdx.x == 0) out[at.r * parts.n + at.p] = make_float2(s.m, s.Z);
+  HeldRow<T, GT, kLookPieces, Once> h;
+  h.load(z + at.r * ld + at.lo, at.cols, group_tid<GT>(), nullptr);
+  const RowSoft s = held_softmax<GT, true>(h, scale, nullptr, tmp);
+  if (group_tid<GT>() == 0) out[at.r * parts.n + at.p] = make_float2(s.m, s.Z);
 }
 
 // One wave a row: log-probability and log-sum-exp from the row's parts.
@@ -58,29 +58,29 @@ __global__ __launch_bounds__(256) void logprob_finish_kernel(
 }
 
 // A part of a row: k ([c == t] - exp(y - lse)).
-template <typename T>
+template <typename T, int GT>
 __global__ __launch_bounds__(256) void logprob_bwd_kernel(
     const T* __restrict__ z, int64_t R, int C, int64_t ld, float scale, Parts parts,
     const int32_t* __restrict__ targets, const float* __restrict__ lse,
-    const float* __restrict__ dlogp, T* __restrict__ grad, int64_t gld) {
-  const PartAt at = part_at(parts.cols, parts.n, C);
+    const float* __restrict__ dlogp, T* __restrict__ grad, int64_t gld, bool far) {
+  const PartAt at = part_at<GT>(parts, C);
   if (at.r >= R) return;
   const int64_t r = at.r;
-  const int tid = threadIdx.x, t = targets[r];
+  const int tid = group_tid<GT>(), t = targets[r];
   const float d = dlogp[r];
   T* g = grad + r * gld + at.lo;
   if (t < 0 || d == 0.0f) {
-    fill_row<T, 256>(g, at.cols, tid, 0.0f);
+    fill_row<T, GT>(g, at.cols, tid, 0.0f);
     return;
   }
   const T* row = z + r * ld + at.lo;
   const float k = t < C ? d * scale : __builtin_nanf("");
   const float l = lse[r];
-  HeldRow<T, 256, kPartPieces> h;
+  HeldRow<T, GT, kGradPieces> h;
   h.load(row, at.cols, tid, g);
   // y - lse is rounded once, relative to itself, before it is scaled
   auto prob = [&](float x) { return exp2_fast(fmaf(x, scale, -l) * kLog2e); };
-  h.store(g, [&](float x) { return -k * prob(x); });
+  h.store(g, far, [&](float x) { return -k * prob(x); });
   const int c = t - at.lo;
   if (c >= 0 && c < at.cols && h.holds(c)) g[c] = (T)fmaf(-k, prob((float)row[c]), k);
 }
@@ -217,31 +217,30 @@ __global__ __launch_bounds__(256) void pref_pairs_kernel(PrefArgs p, int64_t R,
   for (int64_t r = a + tid; r < b; r += 256) coef[r] = p.targets[r] >= 0 ? (float)acc : 0.0f;
 }
 
-// A part of a row's gradient; 0 for rows outside every sequence.  The rows run
-// backwards: those that the first look read last are still in the caches.
-template <typename T>
+// A part of a row's gradient; 0 for rows outside every sequence.
+template <typename T, int GT>
 __global__ __launch_bounds__(256) void pref_grad_kernel(
     const T* __restrict__ z, int64_t R, int C, int64_t ld, float scale, Parts parts, PrefArgs p,
     const float4* __restrict__ soft, const float* __restrict__ coef, T* __restrict__ grad,
-    int64_t gld) {
-  const PartAt at = part_at(parts.cols, parts.n, C);
+    int64_t gld, bool far) {
+  const PartAt at = part_at<GT>(parts, C);
   if (at.r >= R) return;
-  const int64_t r = R - 1 - at.r;
-  const int tid = threadIdx.x;
+  const int64_t r = at.r;
+  const int tid = group_tid<GT>();
   T* g = grad + r * gld + at.lo;
   const bool in = p.S > 0 && row_counts(r, p.targets, nullptr, p.offsets, p.S);
   const float k = in ? coef[r] * scale : 0.0f;
   if (k == 0.0f) {
-    fill_row<T, 256>(g, at.cols, tid, 0.0f);
+    fill_row<T, GT>(g, at.cols, tid, 0.0f);
     return;
   }
   const T* row = z + r * ld + at.lo;
-  HeldRow<T, 256, kPartPieces> h;
+  HeldRow<T, GT, kGradPieces, false> h;      // what the caches kept of the first look
   h.load(row, at.cols, tid, g);
   const float4 f = soft[r];
   const RowSoft s{f.x, f.y, f.z, f.w};
   const float kz = -k / s.Z;
-  h.store_grad(g, s, kz);
+  h.store_grad(g, far, s, kz);
   const int c = p.targets[r] - at.lo;
   if (c >= 0 && c < at.cols && h.holds(c)) g[c] = (T)fmaf(kz, row_exp(s, (float)row[c]), k);
 }
@@ -249,39 +248,46 @@ __global__ __launch_bounds__(256) void pref_grad_kernel(
 template <typename T, bool Once>
 hipError_t parts_t(const Rows& a, const Parts& p, const int32_t* targets, const float* weight,
                    const int32_t* offsets, int64_t S, float2* out, hipStream_t s) {
-  hipLaunchKernelGGL((parts_kernel<T, Once>), linear_grid(a.R * p.n), dim3(256), 0, s, (const T*)a.z, a.R,
-                     (int)a.C, a.ld, a.scale, p, targets, weight, offsets, S, out);
-  return hipGetLastError();
+  return parts_dispatch(p, [&](auto gt) {
+    constexpr int GT = decltype(gt)::value;
+    hipLaunchKernelGGL((parts_kernel<T, GT, Once>), group_grid<GT>(a.R * p.n), dim3(256), 0, s,
+                       (const T*)a.z, a.R, (int)a.C, a.ld, a.scale, p, targets, weight, offsets, S,
+                       out);
+    return hipGetLastError();
+  });
 }
 
 template <typename T>
 hipError_t preference_t(const Rows& a, const PrefArgs& p, char* ws, hipStream_t s) {
   const RowsLayout w = pref_layout(a.R, a.C, p.S, a.dtype);
-  const Parts parts = plan_parts(a.R, a.C, sizeof(T));
+  const Parts look = look_parts(a.R, a.C, a.dtype), parts = grad_parts(a.R, a.C, a.dtype);
   float2* mz = (float2*)(ws + w.parts);
   float4* soft = (float4*)(ws + w.soft);
   float* coef = (float*)(ws + w.coef);
   double* seq = (double*)(ws + w.seq);
   hipError_t e;
   if (p.S > 0) {
-    e = parts_t<T, false>(a, parts, p.targets, nullptr, p.offsets, p.S, mz, s);
+    e = parts_t<T, false>(a, look, p.targets, nullptr, p.offsets, p.S, mz, s);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(pref_seq_kernel<T>, linear_grid(p.S), dim3(64), 0, s, p, (const T*)a.z, a.R,
-                       (int)a.C, a.ld, a.scale, mz, parts.n, soft, seq);
+                       (int)a.C, a.ld, a.scale, mz, look.n, soft, seq);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   hipLaunchKernelGGL(pref_pairs_kernel, linear_grid(p.S + 1), dim3(256), 0, s, p, a.R, seq, coef);
   if ((e = hipGetLastError()) != hipSuccess || !a.grad) return e;
-  hipLaunchKernelGGL(pref_grad_kernel<T>, linear_grid(a.R * parts.n), dim3(256), 0, s,
-                     (const T*)a.z, a.R, (int)a.C, a.ld, a.scale, parts, p, soft, coef,
-                     (T*)a.grad, a.grad_ld);
-  return hipGetLastError();
+  return parts_dispatch(parts, [&](auto gt) {
+    constexpr int GT = decltype(gt)::value;
+    hipLaunchKernelGGL((pref_grad_kernel<T, GT>), group_grid<GT>(a.R * parts.n), dim3(256), 0, s,
+                       (const T*)a.z, a.R, (int)a.C, a.ld, a.scale, parts, p, soft, coef,
+                       (T*)a.grad, a.grad_ld, a.far());
+    return hipGetLastError();
+  });
 }
 
 template <typename T>
 hipError_t logprob_fwd_t(const Rows& a, const int32_t* targets, float* logp, float* lse, char* ws,
                          hipStream_t s) {
-  const Parts parts = plan_parts(a.R, a.C, sizeof(T));
+  const Parts parts = look_parts(a.R, a.C, a.dtype);
   float2* mz = (float2*)ws;
   hipError_t e = parts_t<T, true>(a, parts, targets, nullptr, nullptr, 0, mz, s);
   if (e != hipSuccess) return e;
@@ -293,11 +299,14 @@ hipError_t logprob_fwd_t(const Rows& a, const int32_t* targets, float* logp, flo
 template <typename T>
 hipError_t logprob_bwd_t(const Rows& a, const int32_t* targets, const float* lse,
                          const float* dlogp, hipStream_t s) {
-  const Parts parts = plan_parts(a.R, a.C, sizeof(T));
-  hipLaunchKernelGGL(logprob_bwd_kernel<T>, linear_grid(a.R * parts.n), dim3(256), 0, s,
-                     (const T*)a.z, a.R, (int)a.C, a.ld, a.scale, parts, targets, lse, dlogp,
-                     (T*)a.grad, a.grad_ld);
-  return hipGetLastError();
+  const Parts parts = grad_parts(a.R, a.C, a.dtype);
+  return parts_dispatch(parts, [&](auto gt) {
+    constexpr int GT = decltype(gt)::value;
+    hipLaunchKernelGGL((logprob_bwd_kernel<T, GT>), group_grid<GT>(a.R * parts.n), dim3(256), 0, s,
+                       (const T*)a.z, a.R, (int)a.C, a.ld, a.scale, parts, targets, lse, dlogp,
+                       (T*)a.grad, a.grad_ld, a.far());
+    return hipGetLastError();
+  });
 }
 
 }  // namespace
