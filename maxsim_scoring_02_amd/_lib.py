@@ -406,17 +406,17 @@ def _row_grad(logits: torch.Tensor, want: bool, out: Optional[torch.Tensor]) -> 
             raise ValueError("grad_out given without want_grad")
         return None, 0
     if out is None:
-        out = torch.empty(tuple(logits.shape), dtype=logits.dtype, device=logits.device)
+        out = torch.empty_like(logits, memory_format=torch.contiguous_format)
     elif (out.shape != logits.shape or out.dtype != logits.dtype or
           out.device != logits.device):
         raise ValueError("grad_out must have the logits' shape, type and device")
     return out, _row_stride(out, "grad_out")
 
 
-def _row_outs(R: int, device, *shapes) -> list:
+def _row_outs(R: int, device, *lengths) -> list:
     """float32 outputs; a call without rows writes none of them, so they are 0 then."""
     make = torch.empty if R else torch.zeros
-    return [make(s, dtype=torch.float32, device=device) for s in shapes]
+    return [make(n, dtype=torch.float32, device=device) for n in lengths]
 
 
 @functools.lru_cache(maxsize=1024)
@@ -441,7 +441,13 @@ def _current(device):
     return _NOTHING if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
+# the current stream's handle without a Stream object around it, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_of(device):
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -453,7 +459,7 @@ def lik_logprob_rows_fwd(logits, targets, scale=1.0) -> Tuple:
     dev = logits.device
     t = _row_arg(targets, (R,), "targets", dev, torch.int32)
     with _current(dev):
-        logp, lse = _row_outs(R, dev, (R,), (R,))
+        logp, lse = _row_outs(R, dev, R, R)
         ws, wsb = _rows_workspace(LIK_ROWS_LOGPROB_FWD, R, C, 0, dt, dev)
         _check(lib().lik_logprob_rows_fwd(_addr(logits), dt, R, C, ld, _addr(t), float(scale),
                                           _addr(logp), _addr(lse), _addr(ws), wsb, _stream_of(dev)))
@@ -494,7 +500,7 @@ def lik_distill_rows(logits, teacher_idx, teacher_logits, teacher_lse=None, scal
     w = _row_arg(row_weight, (R,), "row_weight", dev)
     grad, gld = _row_grad(logits, want_grad, grad_out)
     with _current(dev):
-        row_loss, loss = _row_outs(R, dev, (R,), (1,))
+        row_loss, loss = _row_outs(R, dev, R, 1)
         ws, wsb = _rows_workspace(LIK_ROWS_DISTILL, R, C, 0, dt, dev)
         _check(lib().lik_distill_rows(_addr(logits), dt, R, C, ld, _addr(idx), _addr(val), K,
                                       _addr(tl), float(scale), _addr(w), _addr(row_loss),
@@ -517,7 +523,7 @@ def lik_policy_rows(logits, targets, old_logp, advantage, ref_logp=None, scale=1
     w = _row_arg(row_weight, (R,), "row_weight", dev)
     grad, gld = _row_grad(logits, want_grad, grad_out)
     with _current(dev):
-        row_loss, logp, loss = _row_outs(R, dev, (R,), (R,), (1,))
+        row_loss, logp, loss = _row_outs(R, dev, R, R, 1)
         ws, wsb = _rows_workspace(LIK_ROWS_POLICY, R, C, 0, dt, dev)
         _check(lib().lik_policy_rows(_addr(logits), dt, R, C, ld, _addr(t), _addr(old), _addr(adv),
                                      _addr(ref), float(scale), float(clip_low), float(clip_high),
@@ -548,7 +554,7 @@ def lik_preference_rows(logits, targets, seq_offsets, chosen, rejected, ref_logp
     w = _row_arg(pair_weight, (P,), "pair_weight", dev)
     grad, gld = _row_grad(logits, want_grad, grad_out)
     with _current(dev):
-        pair_loss, seq, loss = _row_outs(R, dev, (P,), (S,), (1,))
+        pair_loss, seq, loss = _row_outs(R, dev, P, S, 1)
         ws, wsb = _rows_workspace(LIK_ROWS_PREFERENCE, R, C, S, dt, dev)
         _check(lib().lik_preference_rows(
             _addr(logits), dt, R, C, ld, _addr(t), _addr(off), S, _addr(c), _addr(r), P, _addr(ref),

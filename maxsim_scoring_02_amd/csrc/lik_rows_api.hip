@@ -108,11 +108,9 @@ size_t lik_rows_workspace_bytes(lik_rows_op op, int64_t R, int64_t C, int64_t n_
     case LIK_ROWS_LOGPROB_BWD:
       return 0;
     case LIK_ROWS_LOGPROB_FWD:
-      return R == 0 || C == 0 ? 0 : lik::parts_layout(R, C, dtype).bytes;
     case LIK_ROWS_DISTILL:
     case LIK_ROWS_POLICY:
-      return R == 0 || C == 0 || lik::rows_held(R, C, dtype) ? 0
-                                                             : lik::parts_layout(R, C, dtype).bytes;
+      return R == 0 || C == 0 ? 0 : lik::parts_layout(R, C, dtype).bytes;
     case LIK_ROWS_PREFERENCE:
       if (n_seqs < 0 || mul_ok({n_seqs, 64}) < 0) return SIZE_MAX;
       return R == 0 || C == 0 ? 0 : lik::pref_layout(R, C, n_seqs, dtype).bytes;

@@ -247,6 +247,13 @@ __device__ __forceinline__ piece pack(const float* f) {
   }
 }
 
+// Element c of a row piece below 4 GB: a 32-bit offset beside a scalar address.
+template <typename T>
+__device__ __forceinline__ T* at_column(T* p, int c) {
+  typedef typename std::conditional<std::is_const<T>::value, const char, char>::type byte;
+  return reinterpret_cast<T*>(reinterpret_cast<byte*>(p) + (uint32_t)c * (uint32_t)sizeof(T));
+}
+
 // -inf in every element
 template <typename T>
 __device__ __forceinline__ piece no_logits() {
@@ -261,11 +268,11 @@ __device__ __forceinline__ piece load_piece(const T* p) {
   if constexpr (Once) return __builtin_nontemporal_load(q);
   return *q;
 }
-// Far: past the caches.
-template <bool Far, typename T>
-__device__ __forceinline__ void store_piece(T* p, piece v) {
+// far: past the caches.
+template <typename T>
+__device__ __forceinline__ void store_piece(T* p, piece v, bool far) {
   piece_u2* q = reinterpret_cast<piece_u2*>(p);
-  if constexpr (Far) __builtin_nontemporal_store(v, q);
+  if (far) __builtin_nontemporal_store(v, q);
   else *q = v;
 }
 
@@ -302,6 +309,17 @@ __device__ __forceinline__ float piece_sum(piece p, const RowSoft& s, uint32_t o
 // Waits for this wave's loads (and stores): vmcnt(0) alone.
 __device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }
 
+// A uniform value that the compiler takes for a new one: comparisons with it are
+// made where they are used and not kept in scalar registers from use to use.
+__device__ __forceinline__ int opaque(int x) {
+  x = __builtin_amdgcn_readfirstlane(x);
+  asm("" : "+s"(x));
+  return x;
+}
+
+// The same for a piece: what was unpacked of it is not kept for later.
+__device__ __forceinline__ void opaque_piece(piece& p) { asm("" : "+v"(p)); }
+
 // Elements before the first 16-byte boundary at or behind p, at most C.
 template <typename T>
 __device__ __forceinline__ int head_of(const T* p, int C) {
@@ -336,84 +354,107 @@ struct Deal {
   }
 };
 
-// The columns of a Deal in registers: NV pieces a thread at most and an edge.
-// The pieces are aligned to the gradient's row where one is written (an
-// unaligned store costs more than an unaligned load: 4096 x 131071 bf16 policy
-// loss 508 us without it), else to the logits'.
-template <typename T, int GT, int NV, bool Once = true>
+// The columns of a Deal on chip: an edge and NV pieces a thread at most in
+// registers, NL more in LDS (at `lds`, NL * GT * 16 bytes, for the rows whose
+// registers alone would leave one workgroup a CU).  The pieces are aligned to
+// the gradient's row where one is written (an unaligned store costs more than
+// an unaligned load: 4096 x 131071 bf16 policy loss 508 us against 437), else to
+// the logits'; with NL to the logits', which go to LDS directly.
+template <typename T, int GT, int NV, bool Once = true, int NL = 0>
 struct HeldRow {
   static constexpr int N = PieceOf<T>::N;
-  static constexpr int64_t kColumns = (int64_t)GT * NV * N;
+  static constexpr int64_t kColumns = (int64_t)GT * (NV + NL) * N;
+  static constexpr int kLdsBytes = NL * GT * 16;
   Deal<T, GT> deal;
   piece d[NV];
   float edge;
+  char* lds;
 
+  // `grad`: where its gradient goes, or null
   __device__ __forceinline__ void load(const T* __restrict__ row, int C, int tid, const T* grad) {
-    deal = Deal<T, GT>(grad ? grad : row, C, tid);
+    deal = Deal<T, GT>(grad && NL == 0 ? grad : row, C, tid);
+    if constexpr (NL > 0) {
+      // lane l's piece lands at the wave's base + 16 l
+#pragma unroll
+      for (int i = 0; i < NL; ++i)
+        if (deal.has(NV + i))
+          __builtin_amdgcn_global_load_lds(
+              (const __attribute__((address_space(1))) void*)at_column(row, deal.column(NV + i)),
+              (__attribute__((address_space(3))) void*)(lds + (i * (GT / 64) + wave_id()) * 1024),
+              16, 0, Once ? 2 : 0);
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       d[i] = no_logits<T>();
-      if (i * GT < deal.pieces && deal.has(i)) d[i] = load_piece<Once>(row + deal.column(i));
+      if (deal.has(i)) d[i] = load_piece<Once>(at_column(row, deal.column(i)));
     }
     edge = -kInf;
     if (deal.has_edge()) edge = (float)row[deal.edge()];
   }
-  __device__ __forceinline__ float max() const {
+  __device__ __forceinline__ piece held(int i) const {
+    if constexpr (NL > 0)
+      if (i >= NV)
+        return deal.has(i) ? *(const piece*)(lds + ((i - NV) * GT + deal.tid) * 16) : no_logits<T>();
+    return d[i];
+  }
+  __device__ __forceinline__ float max() {
     float m = edge;
+    const int pieces = opaque(deal.pieces);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (i * GT < deal.pieces) m = piece_max<T>(d[i], m);
+      if (i * GT < pieces) m = piece_max<T>(d[i], m);
+    if constexpr (NL > 0) {
+      // a wave reads back only what its own lanes loaded into LDS
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+      for (int i = NV; i < NV + NL; ++i)
+        if (i * GT < pieces) m = piece_max<T>(held(i), m);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) opaque_piece(d[i]);
     return m;
   }
   // `listed`: a bit per column that is left out of the sum (and a word behind
   // the last), or null
-  __device__ __forceinline__ float sum(const RowSoft& s, const uint32_t* listed) const {
+  __device__ __forceinline__ float sum(const RowSoft& s, const uint32_t* listed) {
     float z = row_exp(s, edge);
     if (listed && deal.has_edge()) {
       const int c = deal.edge();
       if (listed[c >> 5] >> (c & 31) & 1) z = 0.0f;
     }
+    const int pieces = opaque(deal.pieces);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (i * GT < deal.pieces) {
+    for (int i = 0; i < NV + NL; ++i) {
+      if (i * GT < pieces) {
         uint32_t out = 0;
         if (listed && deal.has(i)) {
           const int c = deal.column(i);
           const uint64_t w = (uint64_t)listed[(c >> 5) + 1] << 32 | listed[c >> 5];
           out = (uint32_t)(w >> (c & 31)) & ((1u << N) - 1);
         }
-        z += piece_sum<T>(d[i], s, out);
+        z += piece_sum<T>(held(i), s, out);
       }
     }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) opaque_piece(d[i]);
     return z;
   }
-  // g = f(logit).  The pieces are all here by now; said once, before the
-  // stores, it keeps the compiler from waiting for every store before the next
-  // piece.
-  template <bool Far, typename F>
-  __device__ __forceinline__ void store_as(T* __restrict__ g, F f) const {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (i * GT < deal.pieces && deal.has(i)) {
-        float x[N];
-        unpack<T>(d[i], x);
-#pragma unroll
-        for (int j = 0; j < N; ++j) x[j] = f(x[j]);
-        store_piece<Far>(g + deal.column(i), pack<T>(x));
-      }
-    }
-  }
+  // g = f(logit).  The pieces are all here by now; said once, before the stores,
+  // it keeps the compiler from waiting for every store before the next piece.
   template <typename F>
   __device__ __forceinline__ void store(T* __restrict__ g, bool far, F f) const {
     wait_loads();
-    if (far) store_as<true>(g, f);
-    else store_as<false>(g, f);
+#pragma unroll
+    for (int i = 0; i < NV + NL; ++i) {
+      if (deal.has(i)) {
+        float x[N];
+        unpack<T>(held(i), x);
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] = f(x[j]);
+        store_piece(at_column(g, deal.column(i)), pack<T>(x), far);
+      }
+    }
     if (deal.has_edge()) g[deal.edge()] = (T)f(edge);
-  }
-  // g = k e
-  __device__ __forceinline__ void store_grad(T* __restrict__ g, bool far, const RowSoft& s,
-                                             float k) const {
-    store(g, far, [&](float x) { return k * row_exp(s, x); });
   }
   __device__ __forceinline__ bool holds(int c) const { return deal.holds(c); }
 };
@@ -427,7 +468,7 @@ __device__ __forceinline__ void fill_row(T* __restrict__ g, int C, int tid, floa
   for (int i = 0; i < N; ++i) f[i] = v;
   const piece p = pack<T>(f);
   const Deal<T, GT> deal(g, C, tid);
-  for (int i = 0; deal.has(i); ++i) store_piece<false>(g + deal.column(i), p);
+  for (int i = 0; deal.has(i); ++i) store_piece(at_column(g, deal.column(i)), p, false);
   if (deal.has_edge()) g[deal.edge()] = (T)v;
 }
 
@@ -435,7 +476,7 @@ __device__ __forceinline__ void fill_row(T* __restrict__ g, int C, int tid, floa
 // holds two floats per wave.  With Part the columns are one part of a row, and
 // one without a finite logit has Z = 0.
 template <int GT, bool Part = false, typename Held>
-__device__ __forceinline__ RowSoft held_softmax(const Held& h, float scale, const uint32_t* listed,
+__device__ __forceinline__ RowSoft held_softmax(Held& h, float scale, const uint32_t* listed,
                                                 float* tmp) {
   const RowSoft w = part_ref(wave_max(h.max()), scale);
   const float Z = wave_sum(h.sum(w, listed));
@@ -472,7 +513,7 @@ __device__ __forceinline__ int64_t linear_block() {
   return (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
 }
 
-// One group of GT threads a row: workgroups of 256 threads at least.
+// Groups of GT threads: workgroups of 256 threads at least.
 template <int GT>
 constexpr int group_threads() { return GT == 64 ? 256 : GT; }
 template <int GT>

@@ -4,6 +4,9 @@
 // Held rows (HeldRow): a group of threads loads its row once into registers,
 // takes the statistics and writes the gradient from there, so the logits are
 // read once and the gradient written once, which is all the traffic there is.
+// One group a row: the rows on a CU are out of step, and one's loads overlap
+// another's exponentials and stores.  (Groups that kept taking rows, with the
+// next row's loads between the stores, were 4 to 25% slower.)
 #include <hip/hip_runtime.h>
 
 #include "lik_rows_device.h"
@@ -80,35 +83,41 @@ __device__ __forceinline__ float policy_finish(const PolicyArgs<T>& a, int64_t r
   return x.w * slope * a.scale;
 }
 
-template <typename T, int GT, int NV>
-__global__ __launch_bounds__(group_threads<GT>()) __attribute__((amdgpu_waves_per_eu(4)))
+// Waves per SIMD that the held kernels' registers allow, with few pieces a
+// thread and with many.
+constexpr int held_waves(int nv, int few) { return nv <= 4 ? few : 4; }
+constexpr int kPolicyWaves = 8, kDistillWaves = 6;
+
+template <typename T, int GT, int NV, int NL>
+__global__ __launch_bounds__(group_threads<GT>()) __attribute__((amdgpu_waves_per_eu(held_waves(NV, kPolicyWaves))))
 void policy_held_kernel(const PolicyArgs<T> a) {
+  extern __shared__ char lds[];
   __shared__ float tmp[2 * (GT / 64)];
   const int64_t r = group_row<GT>();
   if (r >= a.R) return;
   const int tid = group_tid<GT>();
   const int t = a.targets[r];
   const float w = a.weight ? a.weight[r] : 1.0f / (float)a.R;
-  T* g = a.grad ? a.grad + r * a.gld : nullptr;
+  T* g = a.grad + r * a.gld;
   if (t < 0 || w == 0.0f) {
     if (tid == 0) a.row_loss[r] = a.logp[r] = 0.0f;
-    if (g) fill_row<T, GT>(g, a.C, tid, 0.0f);
+    fill_row<T, GT>(g, a.C, tid, 0.0f);
     return;
   }
-  HeldRow<T, GT, NV> h;
+  HeldRow<T, GT, NV, true, NL> h;
+  h.lds = lds;
   h.load(a.z + r * a.ld, a.C, tid, g);
   const PolicyRow x = policy_row(a, r, t, w);
   const RowSoft s = held_softmax<GT>(h, a.scale, nullptr, tmp);
   const float k = policy_finish(a, r, x, s, tid == 0);
-  if (g) {
-    const float kz = -k / s.Z;
-    h.store_grad(g, a.far, s, kz);
-    // the same thread stored the column just before
-    if (t < a.C && h.holds(t)) g[t] = (T)fmaf(kz, row_exp(s, x.zt), k);
-  }
+  const float kz = -k / s.Z;
+  h.store(g, a.far, [&](float z) { return kz * row_exp(s, z); });
+  // the same thread stored the column just before
+  if (t < a.C && h.holds(t)) g[t] = (T)fmaf(kz, row_exp(s, x.zt), k);
 }
 
-// Rows in parts, the second look: loss (part 0) and gradient.
+// Rows in parts, the second look: loss (part 0) and, where one is asked for,
+// gradient.
 template <typename T>
 __global__ __launch_bounds__(256) void policy_parts_kernel(const PolicyArgs<T> a, Parts parts,
                                                            const float2* __restrict__ mz, int n) {
@@ -132,9 +141,10 @@ __global__ __launch_bounds__(256) void policy_parts_kernel(const PolicyArgs<T> a
   const float k = policy_finish(a, r, x, s, at.p == 0 && tid == 0);
   if (g) {
     const float kz = -k / s.Z;
-    h.store_grad(g, a.far, s, kz);
     const int c = t - at.lo;
-    if (c >= 0 && c < at.cols && h.holds(c)) g[c] = (T)fmaf(kz, row_exp(s, x.zt), k);
+    const bool mine = c >= 0 && c < at.cols && h.holds(c);
+    h.store(g, a.far, [&](float z) { return kz * row_exp(s, z); });
+    if (mine) g[c] = (T)fmaf(kz, row_exp(s, x.zt), k);
   }
 }
 
@@ -327,19 +337,18 @@ __device__ __forceinline__ void teacher_grad(const TeacherList& L, int K, float 
 }
 
 template <typename T, int GT, int NV>
-__global__ __launch_bounds__(group_threads<GT>()) __attribute__((amdgpu_waves_per_eu(4)))
+__global__ __launch_bounds__(group_threads<GT>()) __attribute__((amdgpu_waves_per_eu(held_waves(NV, kDistillWaves))))
 void distill_held_kernel(const DistillArgs<T> a) {
   __shared__ float tmp[2 * (GT / 64)];
   extern __shared__ char lists[];
   const int64_t r = group_row<GT>();
   if (r >= a.R) return;
-  const int tid = group_tid<GT>();
-  const int lane = threadIdx.x & 63;
+  const int tid = group_tid<GT>(), lane = threadIdx.x & 63;
   const float w = a.weight ? a.weight[r] : 1.0f / (float)a.R;
-  T* g = a.grad ? a.grad + r * a.gld : nullptr;
+  T* g = a.grad + r * a.gld;
   if (w == 0.0f) {
     if (tid == 0) a.row_loss[r] = 0.0f;
-    if (g) fill_row<T, GT>(g, a.C, tid, 0.0f);
+    fill_row<T, GT>(g, a.C, tid, 0.0f);
     return;
   }
   const T* row = a.z + r * a.ld;
@@ -357,7 +366,7 @@ void distill_held_kernel(const DistillArgs<T> a) {
   if (!with_rest && !(flags & 5)) {
     // no entry with mass
     if (tid == 0) a.row_loss[r] = 0.0f;
-    if (g) fill_row<T, GT>(g, a.C, tid, 0.0f);
+    fill_row<T, GT>(g, a.C, tid, 0.0f);
     return;
   }
   RowSoft s = held_softmax<GT>(h, a.scale, with_rest ? L.listed : nullptr, tmp);
@@ -366,11 +375,9 @@ void distill_held_kernel(const DistillArgs<T> a) {
   const float k = w * a.scale + (flags & 1 ? __builtin_nanf("") : 0.0f);
   const DistillRow d = distill_row(x, lt, with_rest, a.C, k, &s);
   if (tid == 0) a.row_loss[r] = flags & 1 ? __builtin_nanf("") : d.loss;
-  if (g) {
-    h.store_grad(g, a.far, s, d.off);
-    group_sync<GT>();
-    teacher_grad<T, GT>(L, a.K, a.scale, lt, s, d.on, k, flags, g, 0, a.C, tid);
-  }
+  h.store(g, a.far, [&](float z) { return d.off * row_exp(s, z); });
+  group_sync<GT>();
+  teacher_grad<T, GT>(L, a.K, a.scale, lt, s, d.on, k, flags, g, 0, a.C, tid);
 }
 
 // Rows in parts, the first look: each part's (m, Z), listed columns left out of
@@ -441,24 +448,44 @@ __global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T>
   const DistillRow d = distill_row(x, lt, with_rest, a.C, k, &s);
   if (first) a.row_loss[r] = flags & 1 ? __builtin_nanf("") : d.loss;
   if (g) {
-    h.store_grad(g + at.lo, a.far, s, d.off);
+    h.store(g + at.lo, a.far, [&](float z) { return d.off * row_exp(s, z); });
     __syncthreads();
     teacher_grad<T, 256>(L, a.K, a.scale, lt, s, d.on, k, flags, g, at.lo, at.lo + at.cols, tid);
   }
 }
 
-// Calls f with the group size and pieces per thread that hold C columns.
-template <typename T, typename F>
+// Whether rows of at most `most` bytes are held whole, each read once, or taken
+// in parts with a second look for the gradient.
+bool rows_held(int64_t R, int64_t C, lik_dtype dtype, int64_t most) {
+  const int64_t bytes = C * elem_bytes_of(dtype);
+  return bytes <= most && (R >= 256 || bytes <= 16384);
+}
+
+// Calls f with the group size, the pieces per thread in registers and those in
+// LDS that hold C columns.
+template <typename T, bool Lds, typename F>
 hipError_t held_dispatch(int64_t C, F f) {
-#define LIK_HELD(GT, NV) \
-  if (C <= HeldRow<T, GT, NV>::kColumns) return f(std::integral_constant<int, GT>(), std::integral_constant<int, NV>());
-  LIK_HELD(64, 4)
-  LIK_HELD(64, 16)
-  LIK_HELD(256, 16)
-  LIK_HELD(512, 16)
-  LIK_HELD(1024, 16)
+#define LIK_HELD(GT, NV, NL)                                                     \
+  if (C <= HeldRow<T, GT, NV, true, NL>::kColumns)                               \
+    return f(std::integral_constant<int, GT>(), std::integral_constant<int, NV>(), \
+             std::integral_constant<int, NL>());
+  LIK_HELD(64, 4, 0)
+  LIK_HELD(64, 16, 0)
+  LIK_HELD(256, 16, 0)
+  LIK_HELD(512, 16, 0)
+  LIK_HELD(1024, 16, 0)
+  if constexpr (Lds) LIK_HELD(1024, 23, 9)
 #undef LIK_HELD
   return hipErrorInvalidValue;
+}
+
+// More dynamic LDS than a kernel has by default is asked for once a device and
+// kernel; asking again costs little beside the launch of so large a row.
+template <typename K>
+hipError_t allow_lds(K kernel, size_t bytes) {
+  if (bytes <= 65536) return hipSuccess;
+  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
 template <typename T>
@@ -467,14 +494,18 @@ hipError_t policy_t(const Rows& a, const int32_t* targets, const float* old_logp
                     float* row_loss, float* logp, char* ws, hipStream_t s) {
   const PolicyArgs<T> p{(const T*)a.z, a.R, a.ld, (int)a.C, a.scale, targets, old_logp, adv, ref,
                         low, high, kl, weight, row_loss, logp, (T*)a.grad, a.grad_ld, a.far()};
-  if (rows_held(a.R, a.C, a.dtype))
-    return held_dispatch<T>(a.C, [&](auto gt, auto nv) {
-      constexpr int GT = decltype(gt)::value, NV = decltype(nv)::value;
-      hipLaunchKernelGGL((policy_held_kernel<T, GT, NV>), group_grid<GT>(a.R),
-                         dim3(group_threads<GT>()), 0, s, p);
+  if (a.grad && rows_held(a.R, a.C, a.dtype, 32 * 1024 * 16))
+    return held_dispatch<T, true>(a.C, [&](auto gt, auto nv, auto nl) {
+      constexpr int GT = decltype(gt)::value, NV = decltype(nv)::value, NL = decltype(nl)::value;
+      constexpr size_t lds = HeldRow<T, GT, NV, true, NL>::kLdsBytes;
+      const hipError_t e = allow_lds(policy_held_kernel<T, GT, NV, NL>, lds);
+      if (e != hipSuccess) return e;
+      hipLaunchKernelGGL((policy_held_kernel<T, GT, NV, NL>), group_grid<GT>(a.R),
+                         dim3(group_threads<GT>()), lds, s, p);
       return hipGetLastError();
     });
-  const Parts look = look_parts(a.R, a.C, a.dtype), parts = grad_parts(a.R, a.C, a.dtype);
+  const Parts look = look_parts(a.R, a.C, a.dtype);
+  const Parts parts = a.grad ? grad_parts(a.R, a.C, a.dtype) : Parts{(int)a.C, 1, 256};
   float2* mz = (float2*)ws;
   hipError_t e = run_parts(a, look, targets, weight, nullptr, 0, mz, s);
   if (e != hipSuccess) return e;
@@ -490,14 +521,15 @@ hipError_t distill_t(const Rows& a, const int32_t* idx, const float* val, int64_
   const DistillArgs<T> p{(const T*)a.z, a.R, a.ld, (int)a.C, (int)K, a.scale, idx, val, t_lse,
                          weight, row_loss, (T*)a.grad, a.grad_ld, a.far()};
   const size_t lds = teacher_bytes((int)a.C, (int)K);
-  if (rows_held(a.R, a.C, a.dtype))
-    return held_dispatch<T>(a.C, [&](auto gt, auto nv) {
+  if (a.grad && rows_held(a.R, a.C, a.dtype, 16 * 1024 * 16))
+    return held_dispatch<T, false>(a.C, [&](auto gt, auto nv, auto) {
       constexpr int GT = decltype(gt)::value, NV = decltype(nv)::value;
       hipLaunchKernelGGL((distill_held_kernel<T, GT, NV>), group_grid<GT>(a.R),
                          dim3(group_threads<GT>()), lds * (GT == 64 ? 4 : 1), s, p);
       return hipGetLastError();
     });
-  const Parts look = look_parts(a.R, a.C, a.dtype), parts = grad_parts(a.R, a.C, a.dtype);
+  const Parts look = look_parts(a.R, a.C, a.dtype);
+  const Parts parts = a.grad ? grad_parts(a.R, a.C, a.dtype) : Parts{(int)a.C, 1, 256};
   float2* mz = (float2*)ws;
   hipLaunchKernelGGL(distill_stats_kernel<T>, linear_grid(a.R * look.n), dim3(256), 0, s, p, look,
                      mz);
@@ -514,11 +546,6 @@ hipError_t weighted_sum(const float* l, const float* w, int64_t R, float* loss, 
 }
 
 }  // namespace
-
-bool rows_held(int64_t R, int64_t C, lik_dtype dtype) {
-  const int64_t bytes = C * elem_bytes_of(dtype);
-  return bytes <= 16384 * 16 && (R >= 256 || bytes <= 16384);
-}
 
 hipError_t run_policy(const Rows& a, const int32_t* targets, const float* old_logp,
                       const float* adv, const float* ref, float low, float high, float kl,

@@ -95,10 +95,6 @@ inline RowsLayout pref_layout(int64_t R, int64_t C, int64_t S, lik_dtype dtype) 
   return w;
 }
 
-// Whether a fused operator holds whole rows in registers, each read once, or
-// takes them in parts with a second look for the gradient.
-bool rows_held(int64_t R, int64_t C, lik_dtype dtype);
-
 // What every operator takes of its rows.
 struct Rows {
   const void* z;

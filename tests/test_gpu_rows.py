@@ -72,7 +72,7 @@ def draw(R, C, seed, spread=3.0):
 SIZES = [(1, 1), (3, 2), (5, 17), (4, 64), (9, 255), (6, 1000), (3, 4097), (130, 520), (2, 33001),
          (3, 70000), (1, 140001)]
 # rows enough to fill the chip, which are held whole in registers where they fit
-MANY = [(256, 9001), (259, 33001), (256, 70001)]
+MANY = [(256, 9001), (259, 33001), (256, 70001), (256, 131007)]
 TYPES = [F16, BF16, F32]
 
 
@@ -282,7 +282,7 @@ def policy_case(z, t, dtype, scale, seed, weight=None, kl=0.1, low=0.2, high=0.3
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("R,C", SIZES + MANY)
+@pytest.mark.parametrize("R,C", SIZES + MANY + [(256, 150001), (256, 262145)])
 def test_policy(R, C, dtype):
     say(f"[rows] policy {R} x {C} {dtype}")
     rng, z, t = draw(R, C, 3 * R + C)
@@ -492,6 +492,15 @@ def test_preference(R, C, S, P, dtype):
     pad, shift = [(0, 0), (3, 1), (8, 8)][S % 3]
     pref_case(R, C, S, P, dtype, [1.0, 0.5, 2.0][C % 3], R + C, kind, S % 2 == 0, weight=weight,
               pad=pad, shift=shift, use_ref=P != 4)
+
+
+@pytest.mark.parametrize("R,S,P", [(2049, 40, 20), (600, 257, 30), (300, 40, 513), (2048, 256, 512),
+                                   (1, 1, 0)])
+@pytest.mark.parametrize("mean", [False, True])
+def test_preference_many_rows_sequences_pairs(R, S, P, mean):
+    # both sides of where the sequences and pairs share one workgroup
+    say(f"[rows] preference {R} rows {S} sequences {P} pairs mean {mean}")
+    pref_case(R, 24, S, P, F32, 1.0, 79, 0, mean)
 
 
 @pytest.mark.parametrize("kind,margin,smoothing", [(0, 0.5, 0.0), (0, 0.0, 0.2), (0, -0.3, 0.5),
