@@ -72,12 +72,13 @@ typedef enum {
 
 /*
  * Workspace bytes of one call: the same R, C and dtype; n_seqs the number of
- * sequences S (lik_preference_rows; ignored otherwise).  Returns 0 for calls
- * that need none and for zero-sized ones; SIZE_MAX for sizes that overflow or
- * an unknown op or dtype.
+ * sequences S (lik_preference_rows; ignored otherwise); flags bit 0: a
+ * gradient will be asked for (a call that differs may need more and then
+ * returns LIK_ERR_INVALID_ARG).  Returns 0 for calls that need none and for
+ * zero-sized ones; SIZE_MAX for sizes that overflow or an unknown op or dtype.
  */
 size_t lik_rows_workspace_bytes(lik_rows_op op, int64_t R, int64_t C,
-                                int64_t n_seqs, lik_dtype dtype);
+                                int64_t n_seqs, lik_dtype dtype, int flags);
 
 /*
  * logp[r] = y[r, t_r] - lse[r] and lse[r], float32.  Both 0 for rows left out;

@@ -69,7 +69,7 @@ SIGNATURES = {
 # include/lik_rows.h
 _ROWS = [_P, _I, _I64, _I64, _I64]                 # logits, dtype, R, C, ld
 ROWS_SIGNATURES = {
-    "lik_rows_workspace_bytes": ([_I, _I64, _I64, _I64, _I], _SZ),
+    "lik_rows_workspace_bytes": ([_I, _I64, _I64, _I64, _I, _I], _SZ),
     "lik_logprob_rows_fwd": (_ROWS + [_P, _F, _P, _P, _P, _SZ, _P], _I),
     "lik_logprob_rows_bwd": (_ROWS + [_P, _F, _P, _P, _P, _I64, _P], _I),
     "lik_distill_rows": (_ROWS + [_P, _P, _I64, _P, _F, _P, _P, _P, _P, _I64, _P, _SZ, _P], _I),
@@ -388,14 +388,14 @@ def _row_arg(x, shape, name: str, device, dtype=torch.float32):
     arguments may be int32 or int64 (values past int32 count as out of range)."""
     if x is None:
         return None
-    if tuple(x.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(x.shape)}")
+    if x.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(x.shape)}")
     if x.device != device:
         raise ValueError(f"{name} must be on the logits' device")
-    if dtype == torch.int32 and x.dtype == torch.int64:
-        x = x.clamp(-1, 2 ** 31 - 1).to(torch.int32)
     if x.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, not {x.dtype}")
+        if dtype != torch.int32 or x.dtype != torch.int64:
+            raise ValueError(f"{name} must be {dtype}, not {x.dtype}")
+        x = x.clamp(-1, 2 ** 31 - 1).to(torch.int32)
     return x.contiguous()
 
 
@@ -420,12 +420,12 @@ def _row_outs(R: int, device, *lengths) -> list:
 
 
 @functools.lru_cache(maxsize=1024)
-def _rows_workspace_bytes(op: int, R: int, C: int, S: int, dt: int) -> int:
-    return lib().lik_rows_workspace_bytes(op, R, C, S, dt)
+def _rows_workspace_bytes(op: int, R: int, C: int, S: int, dt: int, flags: int) -> int:
+    return lib().lik_rows_workspace_bytes(op, R, C, S, dt, flags)
 
 
-def _rows_workspace(op: int, R: int, C: int, S: int, dt: int, device) -> Tuple:
-    n = _rows_workspace_bytes(op, R, C, S, dt)
+def _rows_workspace(op: int, R: int, C: int, S: int, dt: int, grad, device) -> Tuple:
+    n = _rows_workspace_bytes(op, R, C, S, dt, 0 if grad is None else 1)
     return _workspace(n, device), n
 
 
@@ -460,7 +460,7 @@ def lik_logprob_rows_fwd(logits, targets, scale=1.0) -> Tuple:
     t = _row_arg(targets, (R,), "targets", dev, torch.int32)
     with _current(dev):
         logp, lse = _row_outs(R, dev, R, R)
-        ws, wsb = _rows_workspace(LIK_ROWS_LOGPROB_FWD, R, C, 0, dt, dev)
+        ws, wsb = _rows_workspace(LIK_ROWS_LOGPROB_FWD, R, C, 0, dt, None, dev)
         _check(lib().lik_logprob_rows_fwd(_addr(logits), dt, R, C, ld, _addr(t), float(scale),
                                           _addr(logp), _addr(lse), _addr(ws), wsb, _stream_of(dev)))
     return logp, lse
@@ -501,7 +501,7 @@ def lik_distill_rows(logits, teacher_idx, teacher_logits, teacher_lse=None, scal
     grad, gld = _row_grad(logits, want_grad, grad_out)
     with _current(dev):
         row_loss, loss = _row_outs(R, dev, R, 1)
-        ws, wsb = _rows_workspace(LIK_ROWS_DISTILL, R, C, 0, dt, dev)
+        ws, wsb = _rows_workspace(LIK_ROWS_DISTILL, R, C, 0, dt, grad, dev)
         _check(lib().lik_distill_rows(_addr(logits), dt, R, C, ld, _addr(idx), _addr(val), K,
                                       _addr(tl), float(scale), _addr(w), _addr(row_loss),
                                       _addr(loss), _addr(grad), gld, _addr(ws), wsb, _stream_of(dev)))
@@ -524,7 +524,7 @@ def lik_policy_rows(logits, targets, old_logp, advantage, ref_logp=None, scale=1
     grad, gld = _row_grad(logits, want_grad, grad_out)
     with _current(dev):
         row_loss, logp, loss = _row_outs(R, dev, R, R, 1)
-        ws, wsb = _rows_workspace(LIK_ROWS_POLICY, R, C, 0, dt, dev)
+        ws, wsb = _rows_workspace(LIK_ROWS_POLICY, R, C, 0, dt, grad, dev)
         _check(lib().lik_policy_rows(_addr(logits), dt, R, C, ld, _addr(t), _addr(old), _addr(adv),
                                      _addr(ref), float(scale), float(clip_low), float(clip_high),
                                      float(kl_coef), _addr(w), _addr(row_loss), _addr(logp),
@@ -555,7 +555,7 @@ def lik_preference_rows(logits, targets, seq_offsets, chosen, rejected, ref_logp
     grad, gld = _row_grad(logits, want_grad, grad_out)
     with _current(dev):
         pair_loss, seq, loss = _row_outs(R, dev, P, S, 1)
-        ws, wsb = _rows_workspace(LIK_ROWS_PREFERENCE, R, C, S, dt, dev)
+        ws, wsb = _rows_workspace(LIK_ROWS_PREFERENCE, R, C, S, dt, grad, dev)
         _check(lib().lik_preference_rows(
             _addr(logits), dt, R, C, ld, _addr(t), _addr(off), S, _addr(c), _addr(r), P, _addr(ref),
             int(kind), float(beta), float(margin), float(smoothing), int(bool(mean_logp)),

@@ -72,7 +72,7 @@ lik_status maybe4(const void* p, const char* name) {
 
 lik_status check_workspace(lik_rows_op op, const lik::Rows& a, int64_t S, const void* ws,
                            size_t ws_bytes) {
-  const size_t need = lik_rows_workspace_bytes(op, a.R, a.C, S, a.dtype);
+  const size_t need = lik_rows_workspace_bytes(op, a.R, a.C, S, a.dtype, a.grad ? 1 : 0);
   if (need == SIZE_MAX) return fail(LIK_ERR_INVALID_ARG, "sizes overflow");
   if (need == 0) return LIK_OK;
   if (!ws || ws_bytes < need)
@@ -100,7 +100,7 @@ bool finite(float x) { return x - x == 0.0f; }
 extern "C" {
 
 size_t lik_rows_workspace_bytes(lik_rows_op op, int64_t R, int64_t C, int64_t n_seqs,
-                                lik_dtype dtype) {
+                                lik_dtype dtype, int flags) {
   const int64_t size = lik::elem_bytes_of(dtype);
   if (!size || R < 0 || C < 0 || mul_ok({R, C, size}) < 0 || mul_ok({R, 64}) < 0) return SIZE_MAX;
   if (R > kMaxRows || C > kMaxRows) return SIZE_MAX;
@@ -108,9 +108,16 @@ size_t lik_rows_workspace_bytes(lik_rows_op op, int64_t R, int64_t C, int64_t n_
     case LIK_ROWS_LOGPROB_BWD:
       return 0;
     case LIK_ROWS_LOGPROB_FWD:
+      if (R == 0 || C == 0 || lik::look_parts(R, C, dtype).n == 1) return 0;
+      return lik::parts_layout(R, C, dtype).bytes;
     case LIK_ROWS_DISTILL:
     case LIK_ROWS_POLICY:
-      return R == 0 || C == 0 ? 0 : lik::parts_layout(R, C, dtype).bytes;
+      if (R == 0 || C == 0) return 0;
+      if ((flags & 1) && lik::rows_held(R, C, dtype, op == LIK_ROWS_POLICY
+                                                          ? lik::kPolicyHeldBytes
+                                                          : lik::kDistillHeldBytes))
+        return 0;
+      return lik::parts_layout(R, C, dtype).bytes;
     case LIK_ROWS_PREFERENCE:
       if (n_seqs < 0 || mul_ok({n_seqs, 64}) < 0) return SIZE_MAX;
       return R == 0 || C == 0 ? 0 : lik::pref_layout(R, C, n_seqs, dtype).bytes;

@@ -196,6 +196,37 @@ __device__ __forceinline__ RowSoft merge_parts(const float2* __restrict__ parts,
   return s;
 }
 
+// The parts (m, Z) of a row as one softmax, by one lane.
+__device__ __forceinline__ RowSoft lane_merge(const float2* __restrict__ part, int n, float scale) {
+  constexpr int kAhead = 8;              // loads in flight; most rows have no more parts
+  float2 x[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) x[i] = i < n ? part[i] : make_float2(-kInf, 0.0f);
+  float m = -kInf;
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) m = fmaxf(m, x[i].x);
+#pragma unroll 8
+  for (int i = kAhead; i < n; ++i) m = fmaxf(m, part[i].x);
+  RowSoft s = row_ref(m, scale);
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (i < n) s.Z += x[i].y * part_factor(s, x[i].x, scale);
+#pragma unroll 8
+  for (int i = kAhead; i < n; ++i) s.Z += part[i].y * part_factor(s, part[i].x, scale);
+  if (m == -kInf) s.Z = __builtin_nanf("");
+  return s;
+}
+
+// Sum over 256 threads, in every thread.
+__device__ __forceinline__ double block_sum(double v, double* tmp) {
+  v = wave_sum(v);
+  if ((threadIdx.x & 63) == 0) tmp[wave_id()] = v;
+  __syncthreads();
+  v = (tmp[0] + tmp[1]) + (tmp[2] + tmp[3]);
+  __syncthreads();
+  return v;
+}
+
 // ---------------------------------------------------------------------------
 // 16-byte pieces of a row
 // ---------------------------------------------------------------------------
@@ -525,15 +556,16 @@ __device__ __forceinline__ int64_t group_row() {
 template <int GT>
 __device__ __forceinline__ int group_tid() { return GT == 64 ? threadIdx.x & 63 : threadIdx.x; }
 
-// The part of a row that a group of GT threads takes in a grid of R * n groups.
+// The part of a row that a group of GT threads takes in a grid of `skip` and
+// then R * n groups.
 struct PartAt {
   int64_t r;
   int p, lo, cols;
 };
 template <int GT>
-__device__ __forceinline__ PartAt part_at(const Parts& parts, int C) {
+__device__ __forceinline__ PartAt part_at(const Parts& parts, int C, int skip) {
   PartAt x;
-  const int64_t b = group_row<GT>();
+  const int64_t b = group_row<GT>() - skip;
   if constexpr (GT == 64) {              // whole rows
     x.r = b;
     x.p = x.lo = 0;

@@ -116,36 +116,78 @@ void policy_held_kernel(const PolicyArgs<T> a) {
   if (t < a.C && h.holds(t)) g[t] = (T)fmaf(kz, row_exp(s, x.zt), k);
 }
 
-// Rows in parts, the second look: loss (part 0) and, where one is asked for,
-// gradient.
+// Rows in parts, the second look: the gradient, a workgroup a part.
 template <typename T>
-__global__ __launch_bounds__(256) void policy_parts_kernel(const PolicyArgs<T> a, Parts parts,
-                                                           const float2* __restrict__ mz, int n) {
-  const PartAt at = part_at<256>(parts, a.C);
-  if (at.r >= a.R) return;
+__device__ __forceinline__ void policy_part(const PolicyArgs<T>& a, const PartAt& at,
+                                            const float2* __restrict__ mz, int n) {
   const int64_t r = at.r;
   const int tid = threadIdx.x;
   const int t = a.targets[r];
   const float w = a.weight ? a.weight[r] : 1.0f / (float)a.R;
-  T* g = a.grad ? a.grad + r * a.gld + at.lo : nullptr;
-  if (!g && at.p != 0) return;
+  T* g = a.grad + r * a.gld + at.lo;
   if (t < 0 || w == 0.0f) {
-    if (at.p == 0 && tid == 0) a.row_loss[r] = a.logp[r] = 0.0f;
-    if (g) fill_row<T, 256>(g, at.cols, tid, 0.0f);
+    fill_row<T, 256>(g, at.cols, tid, 0.0f);
     return;
   }
   HeldRow<T, 256, kGradPieces> h;
-  if (g) h.load(a.z + r * a.ld + at.lo, at.cols, tid, g);
+  h.load(a.z + r * a.ld + at.lo, at.cols, tid, g);
   const PolicyRow x = policy_row(a, r, t, w);
   const RowSoft s = merge_parts(mz + r * n, n, a.scale);
-  const float k = policy_finish(a, r, x, s, at.p == 0 && tid == 0);
-  if (g) {
-    const float kz = -k / s.Z;
-    const int c = t - at.lo;
-    const bool mine = c >= 0 && c < at.cols && h.holds(c);
-    h.store(g, a.far, [&](float z) { return kz * row_exp(s, z); });
-    if (mine) g[c] = (T)fmaf(kz, row_exp(s, x.zt), k);
+  const float k = policy_finish(a, r, x, s, false);
+  const float kz = -k / s.Z;
+  h.store(g, a.far, [&](float z) { return kz * row_exp(s, z); });
+  const int c = t - at.lo;
+  if (c >= 0 && c < at.cols && h.holds(c)) g[c] = (T)fmaf(kz, row_exp(s, x.zt), k);
+}
+
+// Losses and log-probabilities of the rows first, first + step, ..., a lane a
+// row, and the thread's share of the weighted sum.
+template <typename T>
+__device__ __forceinline__ double policy_scalars(const PolicyArgs<T>& a, int64_t first, int64_t step,
+                                                 const float2* __restrict__ mz, int n) {
+  double acc = 0.0;
+  for (int64_t r = first; r < a.R; r += step) {
+    const int t = a.targets[r];
+    const float w = a.weight ? a.weight[r] : 1.0f;
+    if (t < 0 || w == 0.0f) {
+      a.row_loss[r] = a.logp[r] = 0.0f;
+      continue;
+    }
+    const PolicyRow x = policy_row(a, r, t, w);
+    policy_finish(a, r, x, lane_merge(mz + r * n, n, a.scale), true);
+    acc += (double)w * (double)a.row_loss[r];
   }
+  return acc;
+}
+
+// Block 0: every row's loss and their sum, beside the others' gradient, so that
+// few rows need no third launch.
+constexpr int64_t kPolicyScalarRows = 1024;
+template <typename T>
+__global__ __launch_bounds__(256) void policy_parts_kernel(const PolicyArgs<T> a, Parts parts,
+                                                           const float2* __restrict__ mz, int n,
+                                                           float* __restrict__ loss) {
+  __shared__ double tmp[4];
+  if (linear_block() == 0) {
+    const double acc = block_sum(policy_scalars(a, threadIdx.x, 256, mz, n), tmp);
+    if (threadIdx.x == 0) *loss = (float)(a.weight ? acc : acc / (double)a.R);
+    return;
+  }
+  const PartAt at = part_at<256>(parts, a.C, 1);
+  if (at.r < a.R) policy_part(a, at, mz, n);
+}
+
+// Many rows: the scalars by a grid of their own.
+template <typename T>
+__global__ __launch_bounds__(256) void policy_scalars_kernel(const PolicyArgs<T> a,
+                                                             const float2* __restrict__ mz, int n) {
+  policy_scalars(a, linear_block() * 256 + threadIdx.x, a.R, mz, n);
+}
+template <typename T>
+__global__ __launch_bounds__(256) void policy_grad_kernel(const PolicyArgs<T> a, Parts parts,
+                                                          const float2* __restrict__ mz, int n) {
+  const PartAt at = part_at<256>(parts, a.C, 0);
+  if (at.r < a.R) policy_part(a, at, mz, n);
 }
 
 template <typename T>
@@ -387,7 +429,7 @@ __global__ __launch_bounds__(256) void distill_stats_kernel(const DistillArgs<T>
                                                             float2* __restrict__ mz) {
   __shared__ float tmp[8];
   __shared__ uint32_t listed[256 * kLookPieces * PieceOf<T>::N / 32 + 1];
-  const PartAt at = part_at<256>(parts, a.C);
+  const PartAt at = part_at<256>(parts, a.C, 0);
   if (at.r >= a.R) return;
   const int64_t r = at.r;
   const int tid = threadIdx.x;
@@ -413,7 +455,7 @@ template <typename T>
 __global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T> a, Parts parts,
                                                             const float2* __restrict__ mz, int n) {
   extern __shared__ char lists[];
-  const PartAt at = part_at<256>(parts, a.C);
+  const PartAt at = part_at<256>(parts, a.C, 0);
   if (at.r >= a.R) return;
   const int64_t r = at.r;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -454,13 +496,6 @@ __global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T>
   }
 }
 
-// Whether rows of at most `most` bytes are held whole, each read once, or taken
-// in parts with a second look for the gradient.
-bool rows_held(int64_t R, int64_t C, lik_dtype dtype, int64_t most) {
-  const int64_t bytes = C * elem_bytes_of(dtype);
-  return bytes <= most && (R >= 256 || bytes <= 16384);
-}
-
 // Calls f with the group size, the pieces per thread in registers and those in
 // LDS that hold C columns.
 template <typename T, bool Lds, typename F>
@@ -488,14 +523,19 @@ hipError_t allow_lds(K kernel, size_t bytes) {
                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
+hipError_t weighted_sum(const float* l, const float* w, int64_t R, float* loss, hipStream_t s) {
+  hipLaunchKernelGGL(weighted_sum_kernel, dim3(1), dim3(1024), 0, s, l, w, R, loss);
+  return hipGetLastError();
+}
+
 template <typename T>
 hipError_t policy_t(const Rows& a, const int32_t* targets, const float* old_logp, const float* adv,
                     const float* ref, float low, float high, float kl, const float* weight,
-                    float* row_loss, float* logp, char* ws, hipStream_t s) {
+                    float* row_loss, float* logp, float* loss, char* ws, hipStream_t s) {
   const PolicyArgs<T> p{(const T*)a.z, a.R, a.ld, (int)a.C, a.scale, targets, old_logp, adv, ref,
                         low, high, kl, weight, row_loss, logp, (T*)a.grad, a.grad_ld, a.far()};
-  if (a.grad && rows_held(a.R, a.C, a.dtype, 32 * 1024 * 16))
-    return held_dispatch<T, true>(a.C, [&](auto gt, auto nv, auto nl) {
+  if (a.grad && rows_held(a.R, a.C, a.dtype, kPolicyHeldBytes)) {
+    const hipError_t e = held_dispatch<T, true>(a.C, [&](auto gt, auto nv, auto nl) {
       constexpr int GT = decltype(gt)::value, NV = decltype(nv)::value, NL = decltype(nl)::value;
       constexpr size_t lds = HeldRow<T, GT, NV, true, NL>::kLdsBytes;
       const hipError_t e = allow_lds(policy_held_kernel<T, GT, NV, NL>, lds);
@@ -504,14 +544,28 @@ hipError_t policy_t(const Rows& a, const int32_t* targets, const float* old_logp
                          dim3(group_threads<GT>()), lds, s, p);
       return hipGetLastError();
     });
+    return e != hipSuccess ? e : weighted_sum(row_loss, weight, a.R, loss, s);
+  }
   const Parts look = look_parts(a.R, a.C, a.dtype);
-  const Parts parts = a.grad ? grad_parts(a.R, a.C, a.dtype) : Parts{(int)a.C, 1, 256};
+  const Parts parts = grad_parts(a.R, a.C, a.dtype);
+  const int64_t n_parts = a.grad ? a.R * parts.n : 0;
   float2* mz = (float2*)ws;
   hipError_t e = run_parts(a, look, targets, weight, nullptr, 0, mz, s);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(policy_parts_kernel<T>, linear_grid(a.R * parts.n), dim3(256), 0, s, p, parts,
+  if (a.R <= kPolicyScalarRows) {
+    hipLaunchKernelGGL(policy_parts_kernel<T>, linear_grid(n_parts + 1), dim3(256), 0, s, p, parts,
+                       mz, look.n, loss);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(policy_scalars_kernel<T>, linear_grid((a.R + 255) / 256), dim3(256), 0, s, p,
                      mz, look.n);
-  return hipGetLastError();
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (n_parts) {
+    hipLaunchKernelGGL(policy_grad_kernel<T>, linear_grid(n_parts), dim3(256), 0, s, p, parts, mz,
+                       look.n);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  return weighted_sum(row_loss, weight, a.R, loss, s);
 }
 
 template <typename T>
@@ -521,7 +575,7 @@ hipError_t distill_t(const Rows& a, const int32_t* idx, const float* val, int64_
   const DistillArgs<T> p{(const T*)a.z, a.R, a.ld, (int)a.C, (int)K, a.scale, idx, val, t_lse,
                          weight, row_loss, (T*)a.grad, a.grad_ld, a.far()};
   const size_t lds = teacher_bytes((int)a.C, (int)K);
-  if (a.grad && rows_held(a.R, a.C, a.dtype, 16 * 1024 * 16))
+  if (a.grad && rows_held(a.R, a.C, a.dtype, kDistillHeldBytes))
     return held_dispatch<T, false>(a.C, [&](auto gt, auto nv, auto) {
       constexpr int GT = decltype(gt)::value, NV = decltype(nv)::value;
       hipLaunchKernelGGL((distill_held_kernel<T, GT, NV>), group_grid<GT>(a.R),
@@ -540,37 +594,25 @@ hipError_t distill_t(const Rows& a, const int32_t* idx, const float* val, int64_
   return hipGetLastError();
 }
 
-hipError_t weighted_sum(const float* l, const float* w, int64_t R, float* loss, hipStream_t s) {
-  hipLaunchKernelGGL(weighted_sum_kernel, dim3(1), dim3(1024), 0, s, l, w, R, loss);
-  return hipGetLastError();
-}
-
 }  // namespace
 
 hipError_t run_policy(const Rows& a, const int32_t* targets, const float* old_logp,
                       const float* adv, const float* ref, float low, float high, float kl,
-                      const float* weight, float* row_loss, float* logp, float* loss,
-                      char* ws, hipStream_t s) {
-  hipError_t e;
-  if (a.dtype == LIK_F16)
-    e = policy_t<_Float16>(a, targets, old_logp, adv, ref, low, high, kl, weight, row_loss, logp, ws, s);
-  else if (a.dtype == LIK_BF16)
-    e = policy_t<__bf16>(a, targets, old_logp, adv, ref, low, high, kl, weight, row_loss, logp, ws, s);
-  else
-    e = policy_t<float>(a, targets, old_logp, adv, ref, low, high, kl, weight, row_loss, logp, ws, s);
-  return e != hipSuccess ? e : weighted_sum(row_loss, weight, a.R, loss, s);
+                      const float* weight, float* row_loss, float* logp, float* loss, char* ws,
+                      hipStream_t s) {
+  const auto run = a.dtype == LIK_F16    ? policy_t<_Float16>
+                   : a.dtype == LIK_BF16 ? policy_t<__bf16>
+                                         : policy_t<float>;
+  return run(a, targets, old_logp, adv, ref, low, high, kl, weight, row_loss, logp, loss, ws, s);
 }
 
 hipError_t run_distill(const Rows& a, const int32_t* idx, const float* val, int64_t K,
                        const float* t_lse, const float* weight, float* row_loss, float* loss,
                        char* ws, hipStream_t s) {
-  hipError_t e;
-  if (a.dtype == LIK_F16)
-    e = distill_t<_Float16>(a, idx, val, K, t_lse, weight, row_loss, ws, s);
-  else if (a.dtype == LIK_BF16)
-    e = distill_t<__bf16>(a, idx, val, K, t_lse, weight, row_loss, ws, s);
-  else
-    e = distill_t<float>(a, idx, val, K, t_lse, weight, row_loss, ws, s);
+  const auto run = a.dtype == LIK_F16    ? distill_t<_Float16>
+                   : a.dtype == LIK_BF16 ? distill_t<__bf16>
+                                         : distill_t<float>;
+  const hipError_t e = run(a, idx, val, K, t_lse, weight, row_loss, ws, s);
   return e != hipSuccess ? e : weighted_sum(row_loss, weight, a.R, loss, s);
 }
 

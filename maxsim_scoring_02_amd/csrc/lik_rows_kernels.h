@@ -50,12 +50,21 @@ inline Parts plan_parts(int64_t R, int64_t C, int64_t elem_bytes, int pieces) {
 constexpr int kLookPieces = 8;
 constexpr int kGradPieces = 4;
 
-// Gradients too large for the 256 MB cache behind the L2s are stored past the
-// caches, smaller ones stay there for what reads them next (gradient of
-// 2048 x 50001 f16 log-probabilities, 205 MB: 63 us against 70 past the caches;
-// of 4096 x 100003 bf16, 819 MB: 298 against 284).
-constexpr int64_t kFarBytes = int64_t(256) << 20;
+// Logits that with their gradient exceed the 256 MB cache behind the L2s are
+// read and written past the caches; less stays there for what comes next.  With
+// other tensors in between, as in training: gradient of 2048 x 50001 f16
+// log-probabilities (205 MB) 68 us past the caches, 72 through them; of
+// 4096 x 100003 bf16 (819 MB) 284 against 298; preference of 2000 x 32768 f16
+// (131 MB) no difference.
+constexpr int64_t kFarBytes = int64_t(128) << 20;
 
+// Whether rows of at most `most` bytes are held on chip, each read once, or
+// taken in parts with a second look for the gradient: too few rows leave most
+// of the chip idle unless they are short.  Rows of up to 256 KB fit 1024
+// threads' registers, up to 512 KB registers and LDS, which distillation needs
+// for its lists.
+constexpr int64_t kDistillHeldBytes = 16 * 1024 * 16;
+constexpr int64_t kPolicyHeldBytes = 32 * 1024 * 16;
 inline int64_t elem_bytes_of(lik_dtype t) {
   return t == LIK_F32 ? 4 : (t == LIK_F16 || t == LIK_BF16 ? 2 : 0);
 }
@@ -69,6 +78,11 @@ inline Parts look_parts(int64_t R, int64_t C, lik_dtype dtype) {
 inline Parts grad_parts(int64_t R, int64_t C, lik_dtype dtype) {
   const int64_t b = elem_bytes_of(dtype);
   return plan_parts(R, C, b, R * C * b > kFarBytes ? 2 : kGradPieces);
+}
+
+inline bool rows_held(int64_t R, int64_t C, lik_dtype dtype, int64_t most) {
+  const int64_t bytes = C * elem_bytes_of(dtype);
+  return bytes <= most && (R >= 256 || bytes <= 16384);
 }
 
 // Workspace layouts.

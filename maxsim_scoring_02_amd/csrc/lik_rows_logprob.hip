@@ -26,12 +26,41 @@ __global__ __launch_bounds__(256) void parts_kernel(const T* __restrict__ z, int
                                                     const int32_t* __restrict__ offsets, int64_t S,
                                                     float2* __restrict__ out) {
   __shared__ float tmp[2 * (GT / 64)];
-  const PartAt at = part_at<GT>(parts, C);
+  const PartAt at = part_at<GT>(parts, C, 0);
   if (at.r >= R || !row_counts(at.r, targets, weight, offsets, S)) return;
   HeldRow<T, GT, kLookPieces, Once> h;
   h.load(z + at.r * ld + at.lo, at.cols, group_tid<GT>(), nullptr);
   const RowSoft s = held_softmax<GT, true>(h, scale, nullptr, tmp);
   if (group_tid<GT>() == 0) out[at.r * parts.n + at.p] = make_float2(s.m, s.Z);
+}
+
+// A row's two outputs.
+__device__ __forceinline__ void logprob_write(const RowSoft& s, float zt, float scale, int64_t r,
+                                              float* logp, float* lse) {
+  const double ln_sum = row_ln_sum(s);
+  logp[r] = (float)row_logp(s, zt, scale, ln_sum);
+  lse[r] = (float)((double)scale * (double)s.m + ln_sum);
+}
+
+// Rows of one part: look and finish in one.
+template <typename T, int GT>
+__global__ __launch_bounds__(256) void logprob_rows_kernel(
+    const T* __restrict__ z, int64_t R, int C, int64_t ld, float scale,
+    const int32_t* __restrict__ targets, float* __restrict__ logp, float* __restrict__ lse) {
+  __shared__ float tmp[2 * (GT / 64)];
+  const int64_t r = group_row<GT>();
+  if (r >= R) return;
+  const int tid = group_tid<GT>(), t = targets[r];
+  if (t < 0) {
+    if (tid == 0) logp[r] = lse[r] = 0.0f;
+    return;
+  }
+  const T* row = z + r * ld;
+  HeldRow<T, GT, kLookPieces> h;
+  h.load(row, C, tid, nullptr);
+  const float zt = t < C ? (float)row[t] : __builtin_nanf("");
+  const RowSoft s = held_softmax<GT>(h, scale, nullptr, tmp);
+  if (tid == 0) logprob_write(s, zt, scale, r, logp, lse);
 }
 
 // One wave a row: log-probability and log-sum-exp from the row's parts.
@@ -43,18 +72,14 @@ __global__ __launch_bounds__(256) void logprob_finish_kernel(
   const int64_t r = group_row<64>();
   if (r >= R) return;
   const int t = targets[r];
-  float lp = 0.0f, l = 0.0f;
-  if (t >= 0) {
-    const float zt = t < C ? (float)z[r * ld + t] : __builtin_nanf("");
-    const RowSoft s = merge_parts(mz + r * n, n, scale);
-    const double ln_sum = row_ln_sum(s);
-    lp = (float)row_logp(s, zt, scale, ln_sum);
-    l = (float)((double)scale * (double)s.m + ln_sum);
+  const bool write = (threadIdx.x & 63) == 0;
+  if (t < 0) {
+    if (write) logp[r] = lse[r] = 0.0f;
+    return;
   }
-  if ((threadIdx.x & 63) == 0) {
-    logp[r] = lp;
-    lse[r] = l;
-  }
+  const float zt = t < C ? (float)z[r * ld + t] : __builtin_nanf("");
+  const RowSoft s = merge_parts(mz + r * n, n, scale);
+  if (write) logprob_write(s, zt, scale, r, logp, lse);
 }
 
 // A part of a row: k ([c == t] - exp(y - lse)).
@@ -63,7 +88,7 @@ __global__ __launch_bounds__(256) void logprob_bwd_kernel(
     const T* __restrict__ z, int64_t R, int C, int64_t ld, float scale, Parts parts,
     const int32_t* __restrict__ targets, const float* __restrict__ lse,
     const float* __restrict__ dlogp, T* __restrict__ grad, int64_t gld, bool far) {
-  const PartAt at = part_at<GT>(parts, C);
+  const PartAt at = part_at<GT>(parts, C, 0);
   if (at.r >= R) return;
   const int64_t r = at.r;
   const int tid = group_tid<GT>(), t = targets[r];
@@ -94,27 +119,6 @@ __device__ __forceinline__ void seq_range(const int32_t* offsets, int64_t s, int
   *b = y > R ? R : y;
 }
 
-// The parts (m, Z) of a row as one softmax, by one lane.
-__device__ __forceinline__ RowSoft lane_merge(const float2* __restrict__ part, int n, float scale) {
-  constexpr int kAhead = 8;              // loads in flight; most rows have no more parts
-  float2 x[kAhead];
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) x[i] = i < n ? part[i] : make_float2(-kInf, 0.0f);
-  float m = -kInf;
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) m = fmaxf(m, x[i].x);
-#pragma unroll 8
-  for (int i = kAhead; i < n; ++i) m = fmaxf(m, part[i].x);
-  RowSoft s = row_ref(m, scale);
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i)
-    if (i < n) s.Z += x[i].y * part_factor(s, x[i].x, scale);
-#pragma unroll 8
-  for (int i = kAhead; i < n; ++i) s.Z += part[i].y * part_factor(s, part[i].x, scale);
-  if (m == -kInf) s.Z = __builtin_nanf("");
-  return s;
-}
-
 // What the preference kernels share.
 template <typename T>
 struct PrefRows {
@@ -135,16 +139,6 @@ __device__ __forceinline__ double pref_row(const PrefRows<T>& a, int64_t r, int 
   const RowSoft f = lane_merge(a.mz + r * a.n, a.n, a.scale);
   a.soft[r] = make_float4(f.m, f.c, f.A, f.Z);
   return row_logp(f, zt, a.scale, row_ln_sum(f));
-}
-
-// Sum over 256 threads, in every thread.
-__device__ __forceinline__ double block_sum(double v, double* tmp) {
-  v = wave_sum(v);
-  if ((threadIdx.x & 63) == 0) tmp[wave_id()] = v;
-  __syncthreads();
-  v = (tmp[0] + tmp[1]) + (tmp[2] + tmp[3]);
-  __syncthreads();
-  return v;
 }
 
 // One workgroup per sequence, a lane per row: L_s.
@@ -315,7 +309,7 @@ __global__ __launch_bounds__(256) void pref_grad_kernel(
     const T* __restrict__ z, int64_t R, int C, int64_t ld, float scale, Parts parts, PrefArgs p,
     const float4* __restrict__ soft, const float* __restrict__ coef, T* __restrict__ grad,
     int64_t gld, bool far) {
-  const PartAt at = part_at<GT>(parts, C);
+  const PartAt at = part_at<GT>(parts, C, 0);
   if (at.r >= R) return;
   const int64_t r = at.r;
   const int tid = group_tid<GT>();
@@ -389,6 +383,13 @@ template <typename T>
 hipError_t logprob_fwd_t(const Rows& a, const int32_t* targets, float* logp, float* lse, char* ws,
                          hipStream_t s) {
   const Parts parts = look_parts(a.R, a.C, a.dtype);
+  if (parts.n == 1)
+    return parts_dispatch(parts, [&](auto gt) {
+      constexpr int GT = decltype(gt)::value;
+      hipLaunchKernelGGL((logprob_rows_kernel<T, GT>), group_grid<GT>(a.R), dim3(256), 0, s,
+                         (const T*)a.z, a.R, (int)a.C, a.ld, a.scale, targets, logp, lse);
+      return hipGetLastError();
+    });
   float2* mz = (float2*)ws;
   hipError_t e = parts_t<T>(a, parts, true, targets, nullptr, nullptr, 0, mz, s);
   if (e != hipSuccess) return e;

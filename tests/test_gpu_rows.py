@@ -294,6 +294,33 @@ def test_policy(R, C, dtype):
                 shift=shift, use_ref=R % 2 == 1)
 
 
+def test_policy_in_parts_beyond_one_workgroup_of_scalars():
+    # more rows than one workgroup's share, too long to be held (rows that need
+    # no oracle to be told apart: each is a shift of the same row)
+    say("[rows] policy many long rows")
+    R, C = 1100, 262200
+    g = torch.Generator(device="cuda").manual_seed(3)
+    row = torch.randn(C + R, generator=g, device="cuda").to(BF16)
+    z = torch.stack([row[r:r + C] for r in range(R)])
+    t = torch.arange(R, device="cuda", dtype=torch.int32)
+    t[5] = -1
+    adv = torch.randn(R, generator=g, device="cuda")
+    old = torch.full((R,), -12.0, device="cuda")
+    loss, rows, lp, grad = _lib.lik_policy_rows(z, t, old, adv, clip_high=30.0)
+    loss2, rows2, lp2, _ = _lib.lik_policy_rows(z, t, old, adv, clip_high=30.0, want_grad=False)
+    assert torch.equal(lp, lp2) and torch.equal(rows, rows2) and torch.equal(loss, loss2)
+    for r in (0, 5, 700, 1099):
+        part = _lib.lik_policy_rows(z[r:r + 1], t[r:r + 1], old[r:r + 1], adv[r:r + 1],
+                                    clip_high=30.0, row_weight=f32([1.0 / R]))
+        within(host(lp[r:r + 1]), host(part[2]), 2e-6 * 12 + 1e-30, "logp")
+        assert torch.allclose(grad[r].float(), part[3][0].float(), rtol=2 ** -7, atol=1e-20)
+        if r != 5:
+            ref = torch.log_softmax(z[r].double(), 0)[t[r].long()]
+            assert abs(float(lp[r]) - float(ref)) < (C / 64 + 64) * U
+    assert lp[5] == 0 and torch.all(grad[5] == 0)
+    assert abs(float(loss) - float(rows.double().mean())) <= 4 * U * float(rows.abs().mean())
+
+
 def test_policy_clips_and_borders():
     say("[rows] policy borders")
     rng, z, t = draw(40, 50, 17)

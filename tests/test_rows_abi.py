@@ -132,7 +132,7 @@ def test_refusals_of_each_operator(L, name, kw, status, msg):
 
 
 def test_workspace_is_checked(L):
-    need = L.lik_rows_workspace_bytes(_lib.LIK_ROWS_PREFERENCE, 4, 8, 2, LIK_F32)
+    need = L.lik_rows_workspace_bytes(_lib.LIK_ROWS_PREFERENCE, 4, 8, 2, LIK_F32, 1)
     assert 0 < need < 1 << 30
     for kw in (dict(wsb=need - 1), dict(ws=None)):
         assert call(L, "lik_preference_rows", **kw) == LIK_ERR_INVALID_ARG
@@ -140,12 +140,17 @@ def test_workspace_is_checked(L):
     assert call(L, "lik_preference_rows", ws=P(B.value + 4)) == LIK_ERR_INVALID_ARG
     big = ctypes.c_size_t(-1).value
     w = L.lik_rows_workspace_bytes
-    assert w(_lib.LIK_ROWS_PREFERENCE, -1, 8, 2, LIK_F32) == big
-    assert w(_lib.LIK_ROWS_PREFERENCE, 4, 8, -2, LIK_F32) == big
-    assert w(_lib.LIK_ROWS_POLICY, 4, 8, 0, 9) == big and w(9, 4, 8, 0, LIK_F32) == big
-    assert w(_lib.LIK_ROWS_POLICY, 1 << 40, 1 << 40, 0, LIK_F32) == big
+    assert w(_lib.LIK_ROWS_PREFERENCE, -1, 8, 2, LIK_F32, 1) == big
+    assert w(_lib.LIK_ROWS_PREFERENCE, 4, 8, -2, LIK_F32, 1) == big
+    assert w(_lib.LIK_ROWS_POLICY, 4, 8, 0, 9, 1) == big and w(9, 4, 8, 0, LIK_F32, 1) == big
+    assert w(_lib.LIK_ROWS_POLICY, 1 << 40, 1 << 40, 0, LIK_F32, 1) == big
     for op in range(5):
-        assert w(op, 0, 8, 0, LIK_BF16) == 0
+        assert w(op, 0, 8, 0, LIK_BF16, 0) == 0
+    # held rows need none; a call for the losses alone takes the same rows in parts
+    for op in (_lib.LIK_ROWS_DISTILL, _lib.LIK_ROWS_POLICY):
+        assert w(op, 512, 1000, 0, LIK_BF16, 1) == 0 and w(op, 512, 1000, 0, LIK_BF16, 0) > 0
+    st = call(L, "lik_policy_rows", grad=None, wsb=0)
+    assert st == LIK_ERR_INVALID_ARG and "workspace too small" in L.lik_last_error().decode()
 
 
 @pytest.mark.parametrize("name", sorted(ARGS))
