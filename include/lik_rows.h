@@ -139,7 +139,7 @@ lik_status lik_distill_rows(const void* logits, lik_dtype dtype, int64_t R,
  * Clipped policy loss.  With rho = exp(logp - old_logp) and A = advantage,
  *   l_r = -min(rho A, clamp(rho, 1 - clip_low, 1 + clip_high) A)
  *         + kl_coef (exp(ref_logp - logp) - (ref_logp - logp) - 1),
- * the second term only with ref_logp (NULL: none).  old_logp, advantage and
+ * the second term only with ref_logp (NULL: none) and a kl_coef other than 0.  old_logp, advantage and
  * ref_logp are float32 [R], constants of the gradient; a row at the border of
  * its clip still has the gradient of rho A.  0 <= clip_low <= 1,
  * clip_high >= 0 (infinity: no clip on that side), kl_coef finite.
@@ -172,7 +172,9 @@ lik_status lik_policy_rows(const void* logits, lik_dtype dtype, int64_t R,
  * weight 0 is left out (its pair_loss is written all the same).  A sequence
  * number outside [0, S) makes the pair's loss NaN and takes the pair out of
  * the gradient.  Rows outside every sequence are not read; their gradient is
- * 0.  Rows of a sequence in no pair have gradient 0 too.
+ * 0.  Rows of a sequence in no pair have gradient 0 too.  A NaN in a sequence
+ * (a target >= C, a NaN logit) makes it, its pairs' losses and the gradient of
+ * every sequence in those pairs NaN.
  * pair_loss [P], seq_logp [S], loss [1]: float32.
  */
 lik_status lik_preference_rows(const void* logits, lik_dtype dtype, int64_t R,

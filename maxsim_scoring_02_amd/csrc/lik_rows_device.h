@@ -505,16 +505,21 @@ __device__ __forceinline__ void fill_row(T* __restrict__ g, int C, int tid, floa
 
 // The softmax of a group's columns: each wave's (m, Z), merged in LDS.  `tmp`
 // holds two floats per wave.  With Part the columns are one part of a row, and
-// one without a finite logit has Z = 0.
-template <int GT, bool Part = false, typename Held>
+// one without a finite logit has Z = 0.  `meet` is done before the group meets.
+struct Nothing {
+  __device__ void operator()() const {}
+};
+template <int GT, bool Part = false, typename Held, typename F = Nothing>
 __device__ __forceinline__ RowSoft held_softmax(Held& h, float scale, const uint32_t* listed,
-                                                float* tmp) {
+                                                float* tmp, F meet = F()) {
   const RowSoft w = part_ref(wave_max(h.max()), scale);
   const float Z = wave_sum(h.sum(w, listed));
   RowSoft s;
+  meet();
   if constexpr (GT == 64) {
     s = row_ref(w.m, scale);
     s.Z = Z;
+    group_sync<GT>();
   } else {
     constexpr int W = GT / 64;
     const int lane = threadIdx.x & 63;

@@ -74,7 +74,7 @@ __device__ __forceinline__ float policy_finish(const PolicyArgs<T>& a, int64_t r
                                                const PolicyRow& x, const RowSoft& s, bool write) {
   const double lp = row_logp(s, x.zt, a.scale, row_ln_sum(s));
   float l, slope;
-  policy_loss((float)(lp - (double)x.old), x.adv, a.low, a.high, a.ref != nullptr,
+  policy_loss((float)(lp - (double)x.old), x.adv, a.low, a.high, a.ref != nullptr && a.kl != 0.0f,
               (float)((double)x.ref - lp), a.kl, &l, &slope);
   if (write) {
     a.row_loss[r] = l;
@@ -209,7 +209,7 @@ struct DistillArgs {
 // The teacher's list of one row in LDS, and a bitmap of its columns.
 struct TeacherList {
   int32_t* col;        // column, -1 absent, | kAgain behind the column's first entry
-  float* t;            // teacher logit
+  float* p;            // teacher logit, then its probability
   float* zs;           // the student's logit there
   int* flags;          // 1: a column >= C, 2: a column twice, 4: an entry with mass
   uint32_t* listed;
@@ -217,13 +217,14 @@ struct TeacherList {
 constexpr int32_t kAgain = 1 << 24;
 static_assert(kDistillMaxC < kAgain, "a column and its mark share a word");
 
+// a word behind the bitmap's last, which HeldRow::sum may read
 __host__ __device__ inline size_t teacher_bytes(int C, int K) {
   return ((size_t)K * 12 + 4 + ((size_t)C + 31) / 32 * 4 + 4 + 15) / 16 * 16;
 }
 __device__ __forceinline__ TeacherList teacher_at(char* p, int K) {
   TeacherList L;
   L.col = (int32_t*)p;
-  L.t = (float*)p + K;
+  L.p = (float*)p + K;
   L.zs = (float*)p + 2 * K;
   L.flags = (int*)p + 3 * K;
   L.listed = (uint32_t*)p + 3 * K + 1;
@@ -231,10 +232,10 @@ __device__ __forceinline__ TeacherList teacher_at(char* p, int K) {
 }
 __device__ __forceinline__ int entry_col(int32_t c) { return c < 0 ? -1 : c & (kAgain - 1); }
 
-// One entry of the list into LDS.
+// One entry of the list into LDS, without the student's logit.
 template <typename T>
-__device__ __forceinline__ void teacher_entry(const DistillArgs<T>& a, const TeacherList& L,
-                                              const T* row, int k, int32_t j, float t) {
+__device__ __forceinline__ void teacher_entry(const DistillArgs<T>& a, const TeacherList& L, int k,
+                                              int32_t j, float t) {
   const bool in = j >= 0 && j < a.C;
   int flags = j >= a.C ? 1 : 0;
   if (in) {
@@ -243,8 +244,7 @@ __device__ __forceinline__ void teacher_entry(const DistillArgs<T>& a, const Tea
     if (t != -kInf) flags |= 4;
   }
   L.col[k] = in ? j : -1;
-  L.t[k] = t;
-  L.zs[k] = in ? (float)row[j] : 0.0f;
+  L.p[k] = t;
   if (flags) atomicOr(L.flags, flags);
 }
 
@@ -261,78 +261,108 @@ __device__ __forceinline__ void teacher_first(const TeacherList& L, int K, int t
   group_sync<GT>();
 }
 
-// A thread's first entry, loaded ahead of the row.
+// A thread's first entry, loaded ahead of the row, and the student's logit there,
+// loaded behind it: loads come back in order, so what needs the entry does not
+// wait for the row, and the logit is not asked for before the row is there.
 template <typename T>
-__device__ __forceinline__ void teacher_ahead(const DistillArgs<T>& a, int64_t r, int tid,
-                                              int32_t* j, float* t) {
-  *j = -1;
-  *t = 0.0f;
-  if (tid < a.K) {
-    *j = a.idx[r * a.K + tid];
-    *t = a.val[r * a.K + tid];
+struct TeacherAhead {
+  int32_t j = -1;
+  float t = 0.0f, z = 0.0f;
+  __device__ __forceinline__ void entry(const DistillArgs<T>& a, int64_t r, int tid) {
+    if (tid < a.K) {
+      j = a.idx[r * a.K + tid];
+      t = a.val[r * a.K + tid];
+    }
   }
-}
+  __device__ __forceinline__ void logit(const DistillArgs<T>& a, const T* row) {
+    if (j >= 0 && j < a.C) z = (float)row[j];
+  }
+};
 
-// The whole list and the bitmap into LDS.
+// The list and the bitmap into LDS; returns the flags.
 template <typename T, int GT>
-__device__ __forceinline__ void teacher_fill(const DistillArgs<T>& a, const TeacherList& L,
-                                             int64_t r, const T* row, int tid, int32_t j0,
-                                             float t0) {
+__device__ __forceinline__ int teacher_fill(const DistillArgs<T>& a, const TeacherList& L,
+                                            int64_t r, int tid, const TeacherAhead<T>& x) {
   const int words = (a.C + 31) / 32 + 1;
   for (int i = tid; i < words; i += GT) L.listed[i] = 0;
   if (tid == 0) *L.flags = 0;
   group_sync<GT>();
-  if (tid < a.K) teacher_entry(a, L, row, tid, j0, t0);
+  if (tid < a.K) teacher_entry(a, L, tid, x.j, x.t);
   for (int k = tid + GT; k < a.K; k += GT)
-    teacher_entry(a, L, row, k, a.idx[r * a.K + k], a.val[r * a.K + k]);
+    teacher_entry(a, L, k, a.idx[r * a.K + k], a.val[r * a.K + k]);
   group_sync<GT>();
-  if (*L.flags & 2) teacher_first<GT>(L, a.K, tid);
+  const int flags = *L.flags;
+  if (flags & 2) teacher_first<GT>(L, a.K, tid);
+  return flags;
 }
 
-// log of the teacher's normaliser, from the list where none was given.  Every
-// wave goes over the whole list, so that no further meeting is needed.
-__device__ __forceinline__ double teacher_ln(const TeacherList& L, int K, float scale, int lane) {
-  float m = -kInf;
-  for (int k = lane; k < K; k += 64)
-    if (L.col[k] >= 0) m = fmaxf(m, L.t[k]);
-  m = wave_max(m);
-  float sum = 0.0f;
-  for (int k = lane; k < K; k += 64)
-    if (L.col[k] >= 0) sum += expf(scale * (L.t[k] - m));
-  return (double)scale * (double)m + (double)logf(wave_sum(sum));
-}
-
-// What the list adds up to against the student's softmax.
+// What the list adds up to.  One wave goes over it (every wave doing so for
+// itself, without LDS between them: 4096 x 65536 bf16 with 64 entries a row
+// 231 us against 226, 4096 x 131072 508 against 500): first, while the row is
+// on its way, the teacher's side ...
 struct TeacherSums {
-  double mass = 0.0;       // teacher probability of the list
-  double terms = 0.0;      // sum p (log p - scale (z - m))
-  double top = 0.0;        // student exponentials of the listed columns
-  double columns = 0.0;    // how many those are
+  double mass;        // teacher probability of the list
+  double terms;       // sum p (log p - scale (z - base))
+  float base;         // m, or 0 where that is infinite
+  float m, Z;         // the listed columns as a part of the student's row
+  int columns;        // how many those are
 };
-__device__ __forceinline__ float teacher_p(float t, float scale, double lt) {
-  return t == -kInf ? 0.0f : expf((float)((double)scale * (double)t - lt));
-}
-__device__ __forceinline__ TeacherSums teacher_sums(const TeacherList& L, int K, float scale,
-                                                    double lt, const RowSoft& s, int lane) {
-  TeacherSums x;
+__device__ __forceinline__ void teacher_probs(const TeacherList& L, int K, float scale,
+                                                const float* t_lse, TeacherSums* x, int lane) {
+  double lt;
+  if (t_lse) {
+    lt = (double)*t_lse;
+  } else {
+    float m = -kInf, sum = 0.0f;
+    for (int k = lane; k < K; k += 64)
+      if (L.col[k] >= 0) m = fmaxf(m, L.p[k]);
+    m = wave_max(m);
+    for (int k = lane; k < K; k += 64)
+      if (L.col[k] >= 0) sum += expf(scale * (L.p[k] - m));
+    lt = (double)scale * (double)m + (double)logf(wave_sum(sum));
+  }
+  x->mass = x->terms = 0.0;
   for (int k = lane; k < K; k += 64) {
+    const float t = L.p[k];
+    const double lp = (double)scale * (double)t - lt;
+    const float p = L.col[k] < 0 || t == -kInf ? 0.0f : expf((float)lp);
+    L.p[k] = p;
+    x->mass += (double)p;
+    if (p != 0.0f) x->terms += (double)p * lp;
+  }
+}
+// ... then the student's.  The same wave; sums in its lane 0.
+template <typename T>
+__device__ __forceinline__ void teacher_sums(const DistillArgs<T>& a, const TeacherList& L,
+                                             const T* row, float z0, TeacherSums* x, int lane) {
+  float m = -kInf;
+#pragma unroll 4
+  for (int k = lane; k < a.K; k += 64) {
     const int32_t c = L.col[k];
-    if (c < 0) continue;
-    const float z = L.zs[k], t = L.t[k];
-    const float p = teacher_p(t, scale, lt);
-    x.mass += (double)p;
-    if (p != 0.0f)
-      x.terms += (double)p * ((double)scale * ((double)t - (double)z + (double)s.m) - lt);
-    if (!(c & kAgain)) {
-      x.top += (double)row_exp(s, z);
-      x.columns += 1.0;
+    float z = z0;
+    if (k >= 64) z = c >= 0 ? (float)row[entry_col(c)] : 0.0f;
+    L.zs[k] = z;
+    if (c >= 0) m = fmaxf(m, z);
+  }
+  const RowSoft s = part_ref(wave_max(m), a.scale);
+  // logits next to float32's ends are told apart only relative to each other
+  x->base = fabsf(s.m) < kInf ? s.m : 0.0f;
+  float Z = 0.0f;
+  int columns = 0;
+  for (int k = lane; k < a.K; k += 64) {
+    const int32_t c = L.col[k];
+    const float z = L.zs[k], p = L.p[k];
+    if (p != 0.0f) x->terms -= (double)p * ((double)a.scale * ((double)z - (double)x->base));
+    if (c >= 0 && !(c & kAgain)) {
+      Z += row_exp(s, z);
+      ++columns;
     }
   }
-  x.mass = wave_sum(x.mass);
-  x.terms = wave_sum(x.terms);
-  x.top = wave_sum(x.top);
-  x.columns = wave_sum(x.columns);
-  return x;
+  x->mass = wave_sum(x->mass);
+  x->terms = wave_sum(x->terms);
+  x->m = s.m;
+  x->Z = wave_sum(Z);
+  x->columns = (int)wave_sum((float)columns);      // at most 1024: exact
 }
 
 // Loss of a row and the factors of its gradient:
@@ -342,15 +372,18 @@ struct DistillRow {
 };
 // s.Z: all columns without the rest's term, else the columns not listed (and
 // the whole sum on return).
-__device__ __forceinline__ DistillRow distill_row(const TeacherSums& x, double lt, bool with_rest,
-                                                  int C, float k, RowSoft* s) {
+__device__ __forceinline__ DistillRow distill_row(const TeacherSums& x, bool with_rest, int C,
+                                                  float scale, float k, RowSoft* s) {
   const float rest = s->Z;
-  if (with_rest) s->Z = (float)((double)rest + x.top);
+  if (with_rest) s->Z = rest + (x.columns ? x.Z * part_factor(*s, x.m, scale) : 0.0f);
   const double ln_sum = row_ln_sum(*s);
-  double l = x.terms + x.mass * ln_sum;
+  // log q = scale (z - m) - ln_sum, so sum p (log p - log q) is
+  double l = x.terms;
+  if (x.mass != 0.0)
+    l += x.mass * ((double)scale * ((double)s->m - (double)x.base) + ln_sum);
   DistillRow d;
   float M = (float)x.mass, cut = 0.0f;
-  if (with_rest && x.columns < (double)C) {
+  if (with_rest && x.columns < C) {
     const float p = x.mass != x.mass ? __builtin_nanf("") : (float)fmax(0.0, 1.0 - x.mass);
     if (p != 0.0f) l += (double)p * ((double)logf(p) - (double)logf(rest / s->Z));
     M = (float)(x.mass + (double)p);
@@ -364,16 +397,16 @@ __device__ __forceinline__ DistillRow distill_row(const TeacherSums& x, double l
 
 // The gradient on the listed columns, over what the row's pass wrote there.
 template <typename T, int GT>
-__device__ __forceinline__ void teacher_grad(const TeacherList& L, int K, float scale, double lt,
-                                             const RowSoft& s, float on, float k, int flags,
-                                             T* __restrict__ g, int lo, int hi, int tid) {
+__device__ __forceinline__ void teacher_grad(const TeacherList& L, int K, const RowSoft& s,
+                                             float on, float k, int flags, T* __restrict__ g,
+                                             int lo, int hi, int tid) {
   for (int i = tid; i < K; i += GT) {
     const int32_t c = L.col[i];
     if (c < lo || c >= hi) continue;             // absent, not the first, or elsewhere
-    double p = (double)teacher_p(L.t[i], scale, lt);
+    double p = (double)L.p[i];
     if (flags & 2)
       for (int j = i + 1; j < K; ++j)
-        if (entry_col(L.col[j]) == c) p += (double)teacher_p(L.t[j], scale, lt);
+        if (entry_col(L.col[j]) == c) p += (double)L.p[j];
     g[c] = (T)(on * row_exp(s, L.zs[i]) - k * (float)p);
   }
 }
@@ -382,10 +415,13 @@ template <typename T, int GT, int NV>
 __global__ __launch_bounds__(group_threads<GT>()) __attribute__((amdgpu_waves_per_eu(held_waves(NV, kDistillWaves))))
 void distill_held_kernel(const DistillArgs<T> a) {
   __shared__ float tmp[2 * (GT / 64)];
+  __shared__ TeacherSums sums[GT == 64 ? 4 : 1];
   extern __shared__ char lists[];
   const int64_t r = group_row<GT>();
   if (r >= a.R) return;
   const int tid = group_tid<GT>(), lane = threadIdx.x & 63;
+  const int group = GT == 64 ? wave_id() : 0;
+  const bool counts = GT == 64 || wave_id() == 0;          // the wave that goes over the list
   const float w = a.weight ? a.weight[r] : 1.0f / (float)a.R;
   T* g = a.grad + r * a.gld;
   if (w == 0.0f) {
@@ -394,16 +430,13 @@ void distill_held_kernel(const DistillArgs<T> a) {
     return;
   }
   const T* row = a.z + r * a.ld;
-  const TeacherList L =
-      teacher_at(lists + (GT == 64 ? wave_id() * teacher_bytes(a.C, a.K) : 0), a.K);
-  // the list's loads go first: what waits for them does not wait for the row
-  int32_t j0;
-  float t0;
-  teacher_ahead(a, r, tid, &j0, &t0);
+  const TeacherList L = teacher_at(lists + group * teacher_bytes(a.C, a.K), a.K);
+  TeacherAhead<T> ahead;
+  ahead.entry(a, r, tid);
   HeldRow<T, GT, NV> h;
   h.load(row, a.C, tid, g);
-  teacher_fill<T, GT>(a, L, r, row, tid, j0, t0);
-  const int flags = *L.flags;
+  if (counts) ahead.logit(a, row);
+  const int flags = teacher_fill<T, GT>(a, L, r, tid, ahead);
   const bool with_rest = a.t_lse != nullptr;
   if (!with_rest && !(flags & 5)) {
     // no entry with mass
@@ -411,15 +444,19 @@ void distill_held_kernel(const DistillArgs<T> a) {
     fill_row<T, GT>(g, a.C, tid, 0.0f);
     return;
   }
-  RowSoft s = held_softmax<GT>(h, a.scale, with_rest ? L.listed : nullptr, tmp);
-  const double lt = with_rest ? (double)a.t_lse[r] : teacher_ln(L, a.K, a.scale, lane);
-  const TeacherSums x = teacher_sums(L, a.K, a.scale, lt, s, lane);
+  TeacherSums x;
+  if (counts) teacher_probs(L, a.K, a.scale, with_rest ? a.t_lse + r : nullptr, &x, lane);
+  RowSoft s = held_softmax<GT>(h, a.scale, with_rest ? L.listed : nullptr, tmp, [&] {
+    if (!counts) return;
+    teacher_sums(a, L, row, ahead.z, &x, lane);
+    if (lane == 0) sums[group] = x;
+  });
   const float k = w * a.scale + (flags & 1 ? __builtin_nanf("") : 0.0f);
-  const DistillRow d = distill_row(x, lt, with_rest, a.C, k, &s);
+  const DistillRow d = distill_row(sums[group], with_rest, a.C, a.scale, k, &s);
   if (tid == 0) a.row_loss[r] = flags & 1 ? __builtin_nanf("") : d.loss;
   h.store(g, a.far, [&](float z) { return d.off * row_exp(s, z); });
   group_sync<GT>();
-  teacher_grad<T, GT>(L, a.K, a.scale, lt, s, d.on, k, flags, g, 0, a.C, tid);
+  teacher_grad<T, GT>(L, a.K, s, d.on, k, flags, g, 0, a.C, tid);
 }
 
 // Rows in parts, the first look: each part's (m, Z), listed columns left out of
@@ -454,11 +491,12 @@ __global__ __launch_bounds__(256) void distill_stats_kernel(const DistillArgs<T>
 template <typename T>
 __global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T> a, Parts parts,
                                                             const float2* __restrict__ mz, int n) {
+  __shared__ TeacherSums sums;
   extern __shared__ char lists[];
   const PartAt at = part_at<256>(parts, a.C, 0);
   if (at.r >= a.R) return;
   const int64_t r = at.r;
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x;
   const float w = a.weight ? a.weight[r] : 1.0f / (float)a.R;
   const bool first = at.p == 0 && tid == 0;
   T* g = a.grad ? a.grad + r * a.gld : nullptr;
@@ -470,29 +508,33 @@ __global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T>
   }
   const T* row = a.z + r * a.ld;
   const TeacherList L = teacher_at(lists, a.K);
-  int32_t j0;
-  float t0;
-  teacher_ahead(a, r, tid, &j0, &t0);
+  TeacherAhead<T> ahead;
+  ahead.entry(a, r, tid);
+  if (wave_id() == 0) ahead.logit(a, row);
   HeldRow<T, 256, kGradPieces> h;
   if (g) h.load(row + at.lo, at.cols, tid, g + at.lo);
-  teacher_fill<T, 256>(a, L, r, row, tid, j0, t0);
-  const int flags = *L.flags;
+  const int flags = teacher_fill<T, 256>(a, L, r, tid, ahead);
   const bool with_rest = a.t_lse != nullptr;
   if (!with_rest && !(flags & 5)) {
     if (first) a.row_loss[r] = 0.0f;
     if (g) fill_row<T, 256>(g + at.lo, at.cols, tid, 0.0f);
     return;
   }
+  if (wave_id() == 0) {
+    TeacherSums x;
+    teacher_probs(L, a.K, a.scale, with_rest ? a.t_lse + r : nullptr, &x, tid);
+    teacher_sums(a, L, row, ahead.z, &x, tid);
+    if (tid == 0) sums = x;
+  }
   RowSoft s = merge_parts(mz + r * n, n, a.scale);
-  const double lt = with_rest ? (double)a.t_lse[r] : teacher_ln(L, a.K, a.scale, lane);
-  const TeacherSums x = teacher_sums(L, a.K, a.scale, lt, s, lane);
+  __syncthreads();
   const float k = w * a.scale + (flags & 1 ? __builtin_nanf("") : 0.0f);
-  const DistillRow d = distill_row(x, lt, with_rest, a.C, k, &s);
+  const DistillRow d = distill_row(sums, with_rest, a.C, a.scale, k, &s);
   if (first) a.row_loss[r] = flags & 1 ? __builtin_nanf("") : d.loss;
   if (g) {
     h.store(g + at.lo, a.far, [&](float z) { return d.off * row_exp(s, z); });
     __syncthreads();
-    teacher_grad<T, 256>(L, a.K, a.scale, lt, s, d.on, k, flags, g, at.lo, at.lo + at.cols, tid);
+    teacher_grad<T, 256>(L, a.K, s, d.on, k, flags, g, at.lo, at.lo + at.cols, tid);
   }
 }
 
@@ -514,8 +556,8 @@ hipError_t held_dispatch(int64_t C, F f) {
   return hipErrorInvalidValue;
 }
 
-// More dynamic LDS than a kernel has by default is asked for once a device and
-// kernel; asking again costs little beside the launch of so large a row.
+// More LDS than a kernel has by default has to be asked for; asking again costs
+// little beside so large a row.
 template <typename K>
 hipError_t allow_lds(K kernel, size_t bytes) {
   if (bytes <= 65536) return hipSuccess;
@@ -589,6 +631,7 @@ hipError_t distill_t(const Rows& a, const int32_t* idx, const float* val, int64_
                      mz);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  if ((e = allow_lds(distill_parts_kernel<T>, lds)) != hipSuccess) return e;
   hipLaunchKernelGGL(distill_parts_kernel<T>, linear_grid(a.R * parts.n), dim3(256), lds, s, p,
                      parts, mz, look.n);
   return hipGetLastError();

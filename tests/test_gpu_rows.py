@@ -207,6 +207,30 @@ def test_distill_list_lengths(R, C, K, rest):
     distill_case(R, C, K, rest, F32, 1.0, 31)
 
 
+@pytest.mark.parametrize("R", [2, 256])
+def test_distill_widest_rows(R):
+    # 2^20 columns: the bitmap of listed columns takes most of LDS
+    say(f"[rows] distill widest {R}")
+    C, K = 1 << 20, 1000
+    g = torch.Generator(device="cuda").manual_seed(4)
+    z = torch.empty((R, C), device="cuda", dtype=BF16).normal_(0, 2, generator=g)
+    idx = torch.randint(0, C, (R, K), generator=g, device="cuda", dtype=torch.int32)
+    idx[:, 7] = idx[:, 3]
+    idx[:, 8] = C - 1
+    val = torch.randn((R, K), generator=g, device="cuda")
+    lse = torch.full((R,), 7.5, device="cuda")
+    for rest in (None, lse):
+        loss, rows, grad = _lib.lik_distill_rows(z, idx, val, rest)
+        for r in (0, R - 1):
+            zr = z[r:r + 1].double().cpu().numpy()
+            rl, rr, rg = oracle.distill_rows(zr, idx[r:r + 1].cpu(), val[r:r + 1].cpu(),
+                                             None if rest is None else [7.5], weight=[1.0 / R])
+            # float32 sums of 2^20 terms in pieces of 2^6 and trees: below 2^-16 relative
+            assert abs(float(rows[r]) - rr[0]) < 2e-5 * max(1.0, abs(rr[0]))
+            off = np.abs(host(grad[r]) - rg[0])
+            assert np.all(off <= 2.0 ** -8 * np.abs(rg[0]) + 4e-5 * np.abs(rg[0]) + 1e-12)
+
+
 def test_distill_odd_lists():
     say("[rows] distill odd lists")
     C = 12
@@ -422,6 +446,10 @@ def test_masked_columns(C, dtype):
     loss, rows, grad = _lib.lik_distill_rows(dev, i32(idx), f32(np.zeros((6, 2))))
     assert np.array_equal(np.isnan(host(rows)), np.arange(6) == 3)
     assert np.isinf(host(rows)[5]) and np.isfinite(host(grad)[keep]).all()
+    with np.errstate(all="ignore"):
+        want = oracle.distill_rows(held, idx, np.zeros((6, 2)))[1]
+    for r in (0, 1, 2, 4):
+        assert host(rows)[r] == want[r] or abs(host(rows)[r] / want[r] - 1) < 1e-5
 
 
 def test_infinite_and_nan_logits_stay_in_their_row():
@@ -521,7 +549,8 @@ def test_preference(R, C, S, P, dtype):
               pad=pad, shift=shift, use_ref=P != 4)
 
 
-@pytest.mark.parametrize("R,S,P", [(2049, 40, 20), (600, 257, 30), (300, 40, 513), (2048, 256, 512),
+@pytest.mark.parametrize("R,S,P", [(513, 40, 20), (300, 257, 30), (300, 40, 513), (512, 256, 512),
+                                   (3000, 300, 700),
                                    (1, 1, 0)])
 @pytest.mark.parametrize("mean", [False, True])
 def test_preference_many_rows_sequences_pairs(R, S, P, mean):
@@ -684,6 +713,101 @@ def test_captured_and_replayed():
         outs = everything()
     for k in (0, 1, 0, 1):
         z_in.copy_(zs[k])
+        want = [x.clone() for x in everything()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(outs, want))
+
+
+def test_offsets_beyond_32_bits():
+    """Rows behind the 2^31st element are the rows they would be in a tensor of
+    their own, and a padded stride reaches as far."""
+    say("[rows] offsets beyond 32 bits")
+    R, C = 16500, 131072
+    g = torch.Generator(device="cuda").manual_seed(5)
+    z = torch.empty((R, C), device="cuda", dtype=BF16).normal_(0, 2, generator=g)
+    assert z.numel() > 2 ** 31
+    t = torch.randint(0, C, (R,), generator=g, device="cuda", dtype=torch.int32)
+    one = torch.ones(R, device="cuda")
+    last = slice(R - 70, R)
+    n = 70.0 / R
+    lp, lse = _lib.lik_logprob_rows_fwd(z, t)
+    lp2, lse2 = _lib.lik_logprob_rows_fwd(z[last].clone(), t[last])
+    within(host(lp[last]), host(lp2), 5e-6, "logp")           # other parts, other sums
+    grad = _lib.lik_logprob_rows_bwd(z, t, lse, one)
+    assert torch.equal(grad[last], _lib.lik_logprob_rows_bwd(z[last].clone(), t[last], lse[last],
+                                                             one[last]))
+    del grad
+    _, rows, _, grad = _lib.lik_policy_rows(z, t, lp, one, row_weight=one)
+    part = _lib.lik_policy_rows(z[last].clone(), t[last], lp[last], one[last],
+                                row_weight=one[last])
+    within(host(rows[last]), host(part[1]), 2e-5, "row_loss")
+    assert torch.allclose(grad[last].float(), part[3].float(), rtol=2 ** -7, atol=1e-12)
+    del grad, part
+    idx = torch.randint(0, C, (R, 8), generator=g, device="cuda", dtype=torch.int32)
+    val = torch.randn((R, 8), generator=g, device="cuda")
+    _, rows, grad = _lib.lik_distill_rows(z, idx, val, row_weight=one)
+    part = _lib.lik_distill_rows(z[last].clone(), idx[last], val[last], row_weight=one[last])
+    within(host(rows[last]), host(part[1]), 2e-5, "row_loss")
+    assert torch.allclose(grad[last].float(), part[2].float(), rtol=2 ** -7, atol=1e-12)
+    del grad, part
+    off = i32([0, R - 70, R - 40, R])
+    _, pairs, seq, grad = _lib.lik_preference_rows(z, t, off, i32([1]), i32([2]))
+    part = _lib.lik_preference_rows(z[last].clone(), t[last], i32([0, 30, 70]), i32([0]), i32([1]))
+    within(host(seq[1:]), host(part[2]), 70 * 5e-6, "seq_logp")
+    assert torch.all(grad[0] == 0)
+    assert torch.allclose(grad[last].float(), part[3].float(), rtol=2 ** -7, atol=1e-12)
+
+
+def test_millions_of_short_rows():
+    # more groups than one dimension of a grid holds
+    say("[rows] millions of rows")
+    R, C = (1 << 22) + 5, 3
+    g = torch.Generator(device="cuda").manual_seed(6)
+    z = torch.randn((R, C), generator=g, device="cuda")
+    t = torch.randint(-1, C, (R,), generator=g, device="cuda", dtype=torch.int32)
+    ls = torch.log_softmax(z.double(), 1)
+    on = t >= 0
+    ref = torch.where(on, ls.gather(1, t.long().clamp(min=0)[:, None])[:, 0], 0.0)
+    lp, lse = _lib.lik_logprob_rows_fwd(z, t)
+    assert float((lp - ref).abs().max()) < 2e-6               # |logp| < 16
+    want = -ls.exp()
+    want[torch.arange(R, device="cuda")[on], t[on].long()] += 1
+    want = torch.where(on[:, None], want, 0.0)
+    one = torch.ones(R, device="cuda")
+    assert float((_lib.lik_logprob_rows_bwd(z, t, lse, one) - want).abs().max()) < 2e-6
+    loss, rows, _, grad = _lib.lik_policy_rows(z, t, lp, one, row_weight=one)
+    assert float((grad + want).abs().max()) < 4e-6
+    assert abs(float(loss) + int(on.sum())) < 1e-5 * R
+    idx, val = t[:, None].contiguous(), torch.zeros((R, 1), device="cuda")
+    loss, rows, grad = _lib.lik_distill_rows(z, idx, val, row_weight=one)
+    assert float((rows + ref).abs().max()) < 4e-6 and float((grad + want).abs().max()) < 4e-6
+
+
+def test_captured_long_rows():
+    # held in registers and LDS, and in parts, on replays of one graph
+    say("[rows] graph of long rows")
+    g = torch.Generator(device="cuda").manual_seed(7)
+    R, C = 256, 70001
+    zs = [torch.empty((R, C), device="cuda").normal_(0, 2, generator=g) for _ in range(2)]
+    z = zs[0].clone()
+    t = torch.randint(0, C, (R,), generator=g, device="cuda", dtype=torch.int32)
+    one, old = torch.ones(R, device="cuda"), torch.full((R,), -12.0, device="cuda")
+
+    def everything():
+        few = slice(0, 9)
+        return [*_lib.lik_policy_rows(z, t, old, one),
+                *_lib.lik_policy_rows(z[few], t[few], old[few], one[few]),
+                *_lib.lik_distill_rows(z, t[:, None], one[:, None], one)]
+
+    everything()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = everything()
+    for k in (1, 0, 1):
+        z.copy_(zs[k])
         want = [x.clone() for x in everything()]
         torch.cuda.synchronize()
         graph.replay()
