@@ -316,21 +316,12 @@ __device__ __forceinline__ float piece_max(piece p, float m) {
   return m;
 }
 
-// Sum of the piece's exponentials; bit i of `out` leaves element i out.
-template <typename T>
-__device__ __forceinline__ float piece_sum(piece p, const RowSoft& s, uint32_t out) {
-  float f[PieceOf<T>::N];
-  unpack<T>(p, f);
-#pragma unroll
-  for (int i = 0; i < PieceOf<T>::N; ++i) f[i] = row_exp(s, f[i]);
-  if (out) {
-#pragma unroll
-    for (int i = 0; i < PieceOf<T>::N; ++i)
-      if (out >> i & 1) f[i] = 0.0f;
-  }
+// Sum of N values in one fixed tree.
+template <int N>
+__device__ __forceinline__ float piece_total(const float* f) {
   float a = f[0], b = f[1];
 #pragma unroll
-  for (int i = 2; i < PieceOf<T>::N; i += 2) {
+  for (int i = 2; i < N; i += 2) {
     a += f[i];
     b += f[i + 1];
   }
@@ -377,11 +368,17 @@ struct Deal {
   __device__ __forceinline__ int column(int i) const { return head + (i * GT + tid) * N; }
   __device__ __forceinline__ bool has_edge() const { return tid < edges; }
   __device__ __forceinline__ int edge() const { return tid < head ? tid : tid + pieces * N; }
-  // whether column c is this thread's
-  __device__ __forceinline__ bool holds(int c) const {
+  // the thread that has column c, and as a bit the number of its piece that c is
+  // in (no bit for an edge)
+  __device__ __forceinline__ int owner(int c, uint32_t* piece_bit) const {
     const int p = c - head;
-    if (p >= 0 && p < pieces * N) return p / N % GT == tid;
-    return tid == (p < 0 ? c : c - pieces * N);
+    const bool in = p >= 0 && p < pieces * N;
+    *piece_bit = in ? 1u << (p / N / GT & 31) : 0u;
+    return in ? p / N % GT : (p < 0 ? c : c - pieces * N);
+  }
+  __device__ __forceinline__ bool holds(int c) const {
+    uint32_t bit;
+    return owner(c, &bit) == tid;
   }
 };
 
@@ -445,25 +442,32 @@ struct HeldRow {
     for (int i = 0; i < NV; ++i) opaque_piece(d[i]);
     return m;
   }
-  // `listed`: a bit per column that is left out of the sum (and a word behind
-  // the last), or null
-  __device__ __forceinline__ float sum(const RowSoft& s, const uint32_t* listed) {
+  // Columns left out of the sum: `out` points to a bit per column (and a word
+  // behind the last) or is null, bit i of `hit` says whether this thread's piece
+  // i has one, which few do.
+  __device__ __forceinline__ float sum(const RowSoft& s, const uint32_t* out, uint32_t hit) {
     float z = row_exp(s, edge);
-    if (listed && deal.has_edge()) {
+    if (out && deal.has_edge()) {
       const int c = deal.edge();
-      if (listed[c >> 5] >> (c & 31) & 1) z = 0.0f;
+      if (out[c >> 5] >> (c & 31) & 1) z = 0.0f;
     }
     const int pieces = opaque(deal.pieces);
 #pragma unroll
     for (int i = 0; i < NV + NL; ++i) {
       if (i * GT < pieces) {
-        uint32_t out = 0;
-        if (listed && deal.has(i)) {
+        float f[N];
+        unpack<T>(held(i), f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) f[j] = row_exp(s, f[j]);
+        if (out && hit >> i & 1) {
           const int c = deal.column(i);
-          const uint64_t w = (uint64_t)listed[(c >> 5) + 1] << 32 | listed[c >> 5];
-          out = (uint32_t)(w >> (c & 31)) & ((1u << N) - 1);
+          const uint64_t w = (uint64_t)out[(c >> 5) + 1] << 32 | out[c >> 5];
+          const uint32_t bits = (uint32_t)(w >> (c & 31));
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if (bits >> j & 1) f[j] = 0.0f;
         }
-        z += piece_sum<T>(held(i), s, out);
+        z += piece_total<N>(f);
       }
     }
 #pragma unroll
@@ -505,15 +509,17 @@ __device__ __forceinline__ void fill_row(T* __restrict__ g, int C, int tid, floa
 
 // The softmax of a group's columns: each wave's (m, Z), merged in LDS.  `tmp`
 // holds two floats per wave.  With Part the columns are one part of a row, and
-// one without a finite logit has Z = 0.  `meet` is done before the group meets.
+// one without a finite logit has Z = 0.  `out` and `hit` as for HeldRow::sum;
+// `meet` is done before the group meets.
 struct Nothing {
   __device__ void operator()() const {}
 };
 template <int GT, bool Part = false, typename Held, typename F = Nothing>
-__device__ __forceinline__ RowSoft held_softmax(Held& h, float scale, const uint32_t* listed,
-                                                float* tmp, F meet = F()) {
+__device__ __forceinline__ RowSoft held_softmax(Held& h, float scale, float* tmp,
+                                                const uint32_t* out = nullptr, uint32_t hit = 0,
+                                                F meet = F()) {
   const RowSoft w = part_ref(wave_max(h.max()), scale);
-  const float Z = wave_sum(h.sum(w, listed));
+  const float Z = wave_sum(h.sum(w, out, hit));
   RowSoft s;
   meet();
   if constexpr (GT == 64) {

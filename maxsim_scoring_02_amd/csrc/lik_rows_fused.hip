@@ -108,7 +108,7 @@ void policy_held_kernel(const PolicyArgs<T> a) {
   h.lds = lds;
   h.load(a.z + r * a.ld, a.C, tid, g);
   const PolicyRow x = policy_row(a, r, t, w);
-  const RowSoft s = held_softmax<GT>(h, a.scale, nullptr, tmp);
+  const RowSoft s = held_softmax<GT>(h, a.scale, tmp);
   const float k = policy_finish(a, r, x, s, tid == 0);
   const float kz = -k / s.Z;
   h.store(g, a.far, [&](float z) { return kz * row_exp(s, z); });
@@ -213,28 +213,34 @@ struct TeacherList {
   float* zs;           // the student's logit there
   int* flags;          // 1: a column >= C, 2: a column twice, 4: an entry with mass
   uint32_t* listed;
-};
+  int32_t* next;       // the entries of a thread's own columns as a list, -1 at
+  int32_t* head;       // its end, so that the thread that wrote a column's
+};                     // gradient can write it again without a meeting
 constexpr int32_t kAgain = 1 << 24;
 static_assert(kDistillMaxC < kAgain, "a column and its mark share a word");
 
 // a word behind the bitmap's last, which HeldRow::sum may read
-__host__ __device__ inline size_t teacher_bytes(int C, int K) {
-  return ((size_t)K * 12 + 4 + ((size_t)C + 31) / 32 * 4 + 4 + 15) / 16 * 16;
+__host__ __device__ inline size_t teacher_bytes(int C, int K, int threads) {
+  return ((size_t)K * 16 + 4 + ((size_t)C + 31) / 32 * 4 + 4 + threads * 4 + 15) / 16 * 16;
 }
-__device__ __forceinline__ TeacherList teacher_at(char* p, int K) {
+__device__ __forceinline__ TeacherList teacher_at(char* p, int C, int K) {
   TeacherList L;
   L.col = (int32_t*)p;
   L.p = (float*)p + K;
   L.zs = (float*)p + 2 * K;
-  L.flags = (int*)p + 3 * K;
-  L.listed = (uint32_t*)p + 3 * K + 1;
+  L.next = (int32_t*)p + 3 * K;
+  L.flags = (int*)p + 4 * K;
+  L.listed = (uint32_t*)p + 4 * K + 1;
+  L.head = (int32_t*)L.listed + (C + 31) / 32 + 1;
   return L;
 }
 __device__ __forceinline__ int entry_col(int32_t c) { return c < 0 ? -1 : c & (kAgain - 1); }
 
-// One entry of the list into LDS, without the student's logit.
-template <typename T>
-__device__ __forceinline__ void teacher_entry(const DistillArgs<T>& a, const TeacherList& L, int k,
+// One entry of the list into LDS, without the student's logit.  `deal` shares
+// the columns from lo on, of which there are `cols`.
+template <typename T, int GT>
+__device__ __forceinline__ void teacher_entry(const DistillArgs<T>& a, const TeacherList& L,
+                                              const Deal<T, GT> deal, int lo, int cols, int k,
                                               int32_t j, float t) {
   const bool in = j >= 0 && j < a.C;
   int flags = j >= a.C ? 1 : 0;
@@ -242,6 +248,10 @@ __device__ __forceinline__ void teacher_entry(const DistillArgs<T>& a, const Tea
     const uint32_t bit = 1u << (j & 31);
     if (atomicOr(&L.listed[j >> 5], bit) & bit) flags |= 2;
     if (t != -kInf) flags |= 4;
+    if (j >= lo && j - lo < cols) {
+      uint32_t piece_bit;
+      L.next[k] = atomicExch(&L.head[deal.owner(j - lo, &piece_bit)], k);
+    }
   }
   L.col[k] = in ? j : -1;
   L.p[k] = t;
@@ -282,14 +292,16 @@ struct TeacherAhead {
 // The list and the bitmap into LDS; returns the flags.
 template <typename T, int GT>
 __device__ __forceinline__ int teacher_fill(const DistillArgs<T>& a, const TeacherList& L,
-                                            int64_t r, int tid, const TeacherAhead<T>& x) {
+                                            int64_t r, int tid, const TeacherAhead<T>& x,
+                                            const Deal<T, GT> deal, int lo, int cols) {
   const int words = (a.C + 31) / 32 + 1;
   for (int i = tid; i < words; i += GT) L.listed[i] = 0;
+  L.head[tid] = -1;
   if (tid == 0) *L.flags = 0;
   group_sync<GT>();
-  if (tid < a.K) teacher_entry(a, L, tid, x.j, x.t);
+  if (tid < a.K) teacher_entry<T, GT>(a, L, deal, lo, cols, tid, x.j, x.t);
   for (int k = tid + GT; k < a.K; k += GT)
-    teacher_entry(a, L, k, a.idx[r * a.K + k], a.val[r * a.K + k]);
+    teacher_entry<T, GT>(a, L, deal, lo, cols, k, a.idx[r * a.K + k], a.val[r * a.K + k]);
   group_sync<GT>();
   const int flags = *L.flags;
   if (flags & 2) teacher_first<GT>(L, a.K, tid);
@@ -395,20 +407,33 @@ __device__ __forceinline__ DistillRow distill_row(const TeacherSums& x, bool wit
   return d;
 }
 
-// The gradient on the listed columns, over what the row's pass wrote there.
+// The pieces of this thread that have a listed column, a bit each.
 template <typename T, int GT>
-__device__ __forceinline__ void teacher_grad(const TeacherList& L, int K, const RowSoft& s,
-                                             float on, float k, int flags, T* __restrict__ g,
-                                             int lo, int hi, int tid) {
-  for (int i = tid; i < K; i += GT) {
-    const int32_t c = L.col[i];
-    if (c < lo || c >= hi) continue;             // absent, not the first, or elsewhere
-    double p = (double)L.p[i];
-    if (flags & 2)
-      for (int j = i + 1; j < K; ++j)
-        if (entry_col(L.col[j]) == c) p += (double)L.p[j];
-    g[c] = (T)(on * row_exp(s, L.zs[i]) - k * (float)p);
+__device__ __forceinline__ uint32_t teacher_hit(const TeacherList& L, const Deal<T, GT> deal) {
+  uint32_t hit = 0, bit;
+  for (int k = L.head[deal.tid]; k >= 0; k = L.next[k]) {
+    deal.owner(entry_col(L.col[k]), &bit);
+    hit |= bit;
   }
+  return hit;
+}
+
+// The gradient on the listed columns, over what the same thread wrote there with
+// the row.
+__device__ __forceinline__ float teacher_grad(const TeacherList& L, int K, int k, const RowSoft& s,
+                                              float on, float weight, int flags) {
+  double p = (double)L.p[k];
+  if (flags & 2)
+    for (int j = k + 1; j < K; ++j)
+      if (entry_col(L.col[j]) == L.col[k]) p += (double)L.p[j];
+  return on * row_exp(s, L.zs[k]) - weight * (float)p;
+}
+template <typename T>
+__device__ __forceinline__ void teacher_grads(const TeacherList& L, int K, const RowSoft& s,
+                                              float on, float weight, int flags,
+                                              T* __restrict__ g, int tid) {
+  for (int k = L.head[tid]; k >= 0; k = L.next[k])
+    if (!(L.col[k] & kAgain)) g[L.col[k]] = (T)teacher_grad(L, K, k, s, on, weight, flags);
 }
 
 template <typename T, int GT, int NV>
@@ -430,13 +455,13 @@ void distill_held_kernel(const DistillArgs<T> a) {
     return;
   }
   const T* row = a.z + r * a.ld;
-  const TeacherList L = teacher_at(lists + group * teacher_bytes(a.C, a.K), a.K);
+  const TeacherList L = teacher_at(lists + group * teacher_bytes(a.C, a.K, GT), a.C, a.K);
   TeacherAhead<T> ahead;
   ahead.entry(a, r, tid);
   HeldRow<T, GT, NV> h;
   h.load(row, a.C, tid, g);
   if (counts) ahead.logit(a, row);
-  const int flags = teacher_fill<T, GT>(a, L, r, tid, ahead);
+  const int flags = teacher_fill<T, GT>(a, L, r, tid, ahead, h.deal, 0, a.C);
   const bool with_rest = a.t_lse != nullptr;
   if (!with_rest && !(flags & 5)) {
     // no entry with mass
@@ -446,7 +471,8 @@ void distill_held_kernel(const DistillArgs<T> a) {
   }
   TeacherSums x;
   if (counts) teacher_probs(L, a.K, a.scale, with_rest ? a.t_lse + r : nullptr, &x, lane);
-  RowSoft s = held_softmax<GT>(h, a.scale, with_rest ? L.listed : nullptr, tmp, [&] {
+  const uint32_t hit = with_rest ? teacher_hit(L, h.deal) : 0;
+  RowSoft s = held_softmax<GT>(h, a.scale, tmp, with_rest ? L.listed : nullptr, hit, [&] {
     if (!counts) return;
     teacher_sums(a, L, row, ahead.z, &x, lane);
     if (lane == 0) sums[group] = x;
@@ -455,8 +481,7 @@ void distill_held_kernel(const DistillArgs<T> a) {
   const DistillRow d = distill_row(sums[group], with_rest, a.C, a.scale, k, &s);
   if (tid == 0) a.row_loss[r] = flags & 1 ? __builtin_nanf("") : d.loss;
   h.store(g, a.far, [&](float z) { return d.off * row_exp(s, z); });
-  group_sync<GT>();
-  teacher_grad<T, GT>(L, a.K, s, d.on, k, flags, g, 0, a.C, tid);
+  teacher_grads(L, a.K, s, d.on, k, flags, g, tid);
 }
 
 // Rows in parts, the first look: each part's (m, Z), listed columns left out of
@@ -465,7 +490,7 @@ template <typename T>
 __global__ __launch_bounds__(256) void distill_stats_kernel(const DistillArgs<T> a, Parts parts,
                                                             float2* __restrict__ mz) {
   __shared__ float tmp[8];
-  __shared__ uint32_t listed[256 * kLookPieces * PieceOf<T>::N / 32 + 1];
+  __shared__ uint32_t listed[256 * kLookPieces * PieceOf<T>::N / 32 + 1], hits[256];
   const PartAt at = part_at<256>(parts, a.C, 0);
   if (at.r >= a.R) return;
   const int64_t r = at.r;
@@ -476,14 +501,21 @@ __global__ __launch_bounds__(256) void distill_stats_kernel(const DistillArgs<T>
   const bool with_rest = a.t_lse != nullptr;
   if (with_rest) {
     for (int i = tid; i < (at.cols + 31) / 32 + 1; i += 256) listed[i] = 0;
+    hits[tid] = 0;
     __syncthreads();
     for (int k = tid; k < a.K; k += 256) {
-      const int64_t c = (int64_t)a.idx[r * a.K + k] - at.lo;
-      if (c >= 0 && c < at.cols) atomicOr(&listed[c >> 5], 1u << (c & 31));
+      const int64_t j = (int64_t)a.idx[r * a.K + k] - at.lo;
+      if (j < 0 || j >= at.cols) continue;
+      const int c = (int)j;
+      uint32_t bit;
+      const int owner = h.deal.owner(c, &bit);
+      atomicOr(&listed[c >> 5], 1u << (c & 31));
+      if (bit) atomicOr(&hits[owner], bit);
     }
     __syncthreads();
   }
-  const RowSoft s = held_softmax<256, true>(h, a.scale, with_rest ? listed : nullptr, tmp);
+  const uint32_t hit = with_rest ? hits[tid] : 0;
+  const RowSoft s = held_softmax<256, true>(h, a.scale, tmp, with_rest ? listed : nullptr, hit);
   if (tid == 0) mz[r * parts.n + at.p] = make_float2(s.m, s.Z);
 }
 
@@ -507,13 +539,14 @@ __global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T>
     return;
   }
   const T* row = a.z + r * a.ld;
-  const TeacherList L = teacher_at(lists, a.K);
+  const TeacherList L = teacher_at(lists, a.C, a.K);
   TeacherAhead<T> ahead;
   ahead.entry(a, r, tid);
   if (wave_id() == 0) ahead.logit(a, row);
   HeldRow<T, 256, kGradPieces> h;
   if (g) h.load(row + at.lo, at.cols, tid, g + at.lo);
-  const int flags = teacher_fill<T, 256>(a, L, r, tid, ahead);
+  else h.deal = Deal<T, 256>(row + at.lo, at.cols, tid);
+  const int flags = teacher_fill<T, 256>(a, L, r, tid, ahead, h.deal, at.lo, at.cols);
   const bool with_rest = a.t_lse != nullptr;
   if (!with_rest && !(flags & 5)) {
     if (first) a.row_loss[r] = 0.0f;
@@ -533,8 +566,7 @@ __global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T>
   if (first) a.row_loss[r] = flags & 1 ? __builtin_nanf("") : d.loss;
   if (g) {
     h.store(g + at.lo, a.far, [&](float z) { return d.off * row_exp(s, z); });
-    __syncthreads();
-    teacher_grad<T, 256>(L, a.K, s, d.on, k, flags, g, at.lo, at.lo + at.cols, tid);
+    teacher_grads(L, a.K, s, d.on, k, flags, g, tid);
   }
 }
 
@@ -616,12 +648,14 @@ hipError_t distill_t(const Rows& a, const int32_t* idx, const float* val, int64_
                      hipStream_t s) {
   const DistillArgs<T> p{(const T*)a.z, a.R, a.ld, (int)a.C, (int)K, a.scale, idx, val, t_lse,
                          weight, row_loss, (T*)a.grad, a.grad_ld, a.far()};
-  const size_t lds = teacher_bytes((int)a.C, (int)K);
   if (a.grad && rows_held(a.R, a.C, a.dtype, kDistillHeldBytes))
     return held_dispatch<T, false>(a.C, [&](auto gt, auto nv, auto) {
       constexpr int GT = decltype(gt)::value, NV = decltype(nv)::value;
+      const size_t lds = teacher_bytes((int)a.C, (int)K, GT) * (GT == 64 ? 4 : 1);
+      const hipError_t e = allow_lds(distill_held_kernel<T, GT, NV>, lds);
+      if (e != hipSuccess) return e;
       hipLaunchKernelGGL((distill_held_kernel<T, GT, NV>), group_grid<GT>(a.R),
-                         dim3(group_threads<GT>()), lds * (GT == 64 ? 4 : 1), s, p);
+                         dim3(group_threads<GT>()), lds, s, p);
       return hipGetLastError();
     });
   const Parts look = look_parts(a.R, a.C, a.dtype);
@@ -631,6 +665,7 @@ hipError_t distill_t(const Rows& a, const int32_t* idx, const float* val, int64_
                      mz);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  const size_t lds = teacher_bytes((int)a.C, (int)K, 256);
   if ((e = allow_lds(distill_parts_kernel<T>, lds)) != hipSuccess) return e;
   hipLaunchKernelGGL(distill_parts_kernel<T>, linear_grid(a.R * parts.n), dim3(256), lds, s, p,
                      parts, mz, look.n);

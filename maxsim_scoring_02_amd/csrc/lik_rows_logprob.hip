@@ -30,7 +30,7 @@ __global__ __launch_bounds__(256) void parts_kernel(const T* __restrict__ z, int
   if (at.r >= R || !row_counts(at.r, targets, weight, offsets, S)) return;
   HeldRow<T, GT, kLookPieces, Once> h;
   h.load(z + at.r * ld + at.lo, at.cols, group_tid<GT>(), nullptr);
-  const RowSoft s = held_softmax<GT, true>(h, scale, nullptr, tmp);
+  const RowSoft s = held_softmax<GT, true>(h, scale, tmp);
   if (group_tid<GT>() == 0) out[at.r * parts.n + at.p] = make_float2(s.m, s.Z);
 }
 
@@ -59,7 +59,7 @@ __global__ __launch_bounds__(256) void logprob_rows_kernel(
   HeldRow<T, GT, kLookPieces> h;
   h.load(row, C, tid, nullptr);
   const float zt = t < C ? (float)row[t] : __builtin_nanf("");
-  const RowSoft s = held_softmax<GT>(h, scale, nullptr, tmp);
+  const RowSoft s = held_softmax<GT>(h, scale, tmp);
   if (tid == 0) logprob_write(s, zt, scale, r, logp, lse);
 }
 

@@ -200,7 +200,8 @@ def test_distill(R, C, dtype, rest):
 
 
 @pytest.mark.parametrize("rest", [False, True])
-@pytest.mark.parametrize("R,C,K", [(3, 40, 1024), (2, 5000, 1024), (3, 9, 0), (200, 30, 30)])
+@pytest.mark.parametrize("R,C,K", [(3, 40, 1024), (2, 5000, 1024), (2, 3900, 1023), (3, 9, 0),
+                                   (200, 30, 30), (256, 9000, 700)])
 def test_distill_list_lengths(R, C, K, rest):
     # 1024 entries over 40 columns: every column many times; none; all columns
     say(f"[rows] distill lists {R} x {C} K {K} rest {rest}")
