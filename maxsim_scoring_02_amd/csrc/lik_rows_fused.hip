@@ -571,7 +571,12 @@ __global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T>
 }
 
 // Calls f with the group size, the pieces per thread in registers and those in
-// LDS that hold C columns.
+// LDS that hold C columns.  The policy loss hardly tells group sizes apart;
+// distillation, with more to do for a row, has its 8 KB rows done by one wave
+// each in 77 us where 256 threads take 96 (16384 x 4096 bf16), 16 KB rows by 256
+// in 67 where one wave takes 75 (8192 x 8192), 64 KB rows by 512 in 107 where 256
+// take 111 (4096 x 32768), and 128 KB rows by 512 in 228 where 1024 take 295
+// (4096 x 65536).
 template <typename T, bool Lds, typename F>
 hipError_t held_dispatch(int64_t C, F f) {
 #define LIK_HELD(GT, NV, NL)                                                     \
@@ -579,8 +584,10 @@ hipError_t held_dispatch(int64_t C, F f) {
     return f(std::integral_constant<int, GT>(), std::integral_constant<int, NV>(), \
              std::integral_constant<int, NL>());
   LIK_HELD(64, 4, 0)
-  LIK_HELD(64, 16, 0)
-  LIK_HELD(256, 16, 0)
+  LIK_HELD(64, 8, 0)
+  LIK_HELD(256, 4, 0)
+  LIK_HELD(256, 8, 0)
+  LIK_HELD(512, 8, 0)
   LIK_HELD(512, 16, 0)
   LIK_HELD(1024, 16, 0)
   if constexpr (Lds) LIK_HELD(1024, 23, 9)
