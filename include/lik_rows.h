@@ -82,7 +82,8 @@ size_t lik_rows_workspace_bytes(lik_rows_op op, int64_t R, int64_t C,
 
 /*
  * logp[r] = y[r, t_r] - lse[r] and lse[r], float32.  Both 0 for rows left out;
- * for a target >= C logp is NaN and lse is the row's.
+ * for a target >= C logp is NaN and lse is the row's.  (lse is a float32: the
+ * backward's probabilities are off by its rounding, 2^-24 |lse| relative.)
  */
 lik_status lik_logprob_rows_fwd(const void* logits, lik_dtype dtype, int64_t R,
                                 int64_t C, int64_t ld, const int32_t* targets,
