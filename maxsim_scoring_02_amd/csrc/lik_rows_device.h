@@ -127,16 +127,18 @@ struct RowSoft {
   float m, c, A, Z;
 };
 
-// c and A from a maximum.  Where m * c overflows float32 (a row of the type's
-// lowest values), logits that differ at all differ by more than any exponent,
-// so the power of two that brings m next to 2^64 serves as c: equal logits
-// still give 1 and smaller ones 0.  An infinite m gives NaN throughout.
+// c and A from a maximum.  Up to |A| = 2^31 the factor 2^(mc - A) of A's rounding
+// is at most 2^64, and sums of it stay in range.  From there on (rows of an empty
+// document's -1e9 at a temperature, of the type's lowest values) logits that
+// differ at all differ by 2^64 and more in their exponentials, so the power of two
+// that brings m next to 2^64 serves as c: equal logits still give 1 and smaller
+// ones 0.  An infinite m gives NaN throughout.
 __device__ __forceinline__ RowSoft row_ref(float m, float scale) {
   RowSoft r;
   r.m = m;
   r.c = scale * kLog2e;
   r.A = m * r.c;
-  if (!(fabsf(r.A) < 1e38f) && fabsf(m) < kInf) {
+  if (!(fabsf(r.A) < 0x1p31f) && fabsf(m) < kInf) {
     r.c = ldexpf(1.0f, 64 - ilogbf(m));
     r.A = m * r.c;
   }

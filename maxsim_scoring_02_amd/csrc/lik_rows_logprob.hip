@@ -110,8 +110,12 @@ __global__ __launch_bounds__(256) void logprob_bwd_kernel(
   const float l = lse[r];
   HeldRow<T, GT, kGradPieces> h;
   h.load(row, at.cols, tid, g);
-  // y - lse is rounded once, relative to itself, before it is scaled
-  auto prob = [&](float x) { return exp2_fast(fmaf(x, scale, -l) * kLog2e); };
+  // y - lse is rounded once, relative to itself, before it is scaled.  Not above
+  // 0, which only the rounding of a very large lse would make it.
+  auto prob = [&](float x) {
+    const float d = fmaf(x, scale, -l);
+    return exp2_fast((d > 0.0f ? 0.0f : d) * kLog2e);
+  };
   const int c = t - at.lo;
   const bool mine = c >= 0 && c < at.cols && h.holds(c);
   h.store(g, far, [&](float x) { return -k * prob(x); });

@@ -453,6 +453,44 @@ def test_masked_columns(C, dtype):
         assert host(rows)[r] == want[r] or abs(host(rows)[r] / want[r] - 1) < 1e-5
 
 
+@pytest.mark.parametrize("scale", [1.0, 1.4, 1.5, 20.0, 1e6])
+@pytest.mark.parametrize("C", [5, 700, 9000])
+def test_rows_of_empty_documents(C, scale):
+    """Scores of empty documents, -1e9: a row of nothing else is uniform, whatever
+    the scale, and beside one real score they have probability 0."""
+    say(f"[rows] empty documents {C} scale {scale}")
+    z = np.full((4, C), -1e9, dtype=np.float32)
+    z[1, 3] = 4.0
+    z[2, 1:3] = [7.0, 7.0]
+    z[3] = 1e9
+    t = np.array([0, 3, 1, 4])
+    dev = f32(z)
+    lp, lse = _lib.lik_logprob_rows_fwd(dev, i32(t), scale)
+    want = oracle.logprob_rows(z, t, float(np.float32(scale)))[0]
+    assert np.allclose(want, [-np.log(C), 0, -np.log(2), -np.log(C)], atol=1e-6)
+    within(host(lp), want, 1e-5, "logp")
+    one = f32(np.ones(4))
+    _, rows, _, grad = _lib.lik_policy_rows(dev, i32(t), lp, one, scale=scale, row_weight=one)
+    ref = oracle.policy_rows(z, t, want, np.ones(4), scale=float(np.float32(scale)),
+                             weight=np.ones(4))
+    within(host(grad), ref[3], 2e-5 * scale, "policy gradient")
+    idx = np.stack([t, (t + 1) % C], 1)
+    val = np.array([[0.0, -1.0 / scale]] * 4, dtype=np.float32)
+    for rest in (None, np.full(4, 1.0, dtype=np.float32)):
+        _, rows, grad = _lib.lik_distill_rows(dev, i32(idx), f32(val), f32(rest), scale)
+        with np.errstate(all="ignore"):
+            rl = oracle.distill_rows(z, idx, val, rest, float(np.float32(scale)))
+        for r in (0, 3):
+            assert abs(host(rows)[r] - rl[1][r]) < 1e-5
+            within(host(grad)[r], rl[2][r], 1e-5 * scale, "distill gradient")
+    seq = _lib.lik_preference_rows(dev, i32(t), i32([0, 1, 2, 3, 4]), i32([0]), i32([1]),
+                                   scale=scale)[2]
+    within(host(seq), want, 1e-5, "sequences")
+    # a float32 lse of -1e9 * scale has lost log C, but no probability leaves [0, 1]
+    g = host(_lib.lik_logprob_rows_bwd(dev, i32(t), lse, one, scale))
+    assert np.all(np.abs(g) <= scale) and np.allclose(g[1], 0, atol=1e-5 * scale)
+
+
 def test_infinite_and_nan_logits_stay_in_their_row():
     say("[rows] nan and inf logits")
     rng, z, t = draw(4, 900, 9)
