@@ -160,11 +160,13 @@ __device__ __forceinline__ RowSoft part_ref(float m, float scale) {
 
 // What a part's sum counts for in a row with the maximum s.m: 1 where the
 // maxima are the same, nothing beside a maximum so large that only equal
-// logits count.
+// logits count.  The part's sum is relative to its A, the rounded product, so
+// the product is rounded here too and never joined with the subtraction.
 __device__ __forceinline__ float part_factor(const RowSoft& s, float m, float scale) {
-  const float c = scale * kLog2e;
+#pragma clang fp contract(off)
+  const float c = scale * kLog2e, A = m * c;
   if (m == s.m) return 1.0f;
-  return s.c == c ? exp2_fast(m * c - s.A) : 0.0f;
+  return s.c == c ? exp2_fast(A - s.A) : 0.0f;
 }
 
 // ln(Z 2^-(mc - A)), the log-sum-exp relative to the maximum.  The logarithm

@@ -491,6 +491,24 @@ def test_rows_of_empty_documents(C, scale):
     assert np.all(np.abs(g) <= scale) and np.allclose(g[1], 0, atol=1e-5 * scale)
 
 
+@pytest.mark.parametrize("offset,spread,dtype", [(2e4, 3.0, F32), (-3e6, 3.0, F32), (1e8, 40.0, F32),
+                                                 (-4e3, 8.0, F16), (3e3, 40.0, BF16)])
+@pytest.mark.parametrize("R,C", [(6, 900), (5, 9001), (256, 9001), (3, 70000)])
+def test_rows_far_from_zero(R, C, offset, spread, dtype):
+    """A common offset of a row's logits changes nothing but the log-sum-exp: the
+    bounds know no offset, whichever waves and parts share the row."""
+    say(f"[rows] {R} x {C} at {offset} {dtype}")
+    rng, z, t = draw(R, C, 50)
+    z = (z * (spread / 3) + offset).astype(np.float32)
+    check_logprob(on_gpu(z, dtype)[0], on_gpu(z, dtype)[1], t, 1.0)
+    policy_case(z, t, dtype, 1.0, 51)
+    dev, held = on_gpu(z, dtype)
+    seq = _lib.lik_preference_rows(dev, i32(t), i32(np.arange(R + 1)), i32([0]), i32([1]))[2]
+    want = oracle.logprob_rows(held, t, 1.0)[0]
+    _, _, _, ln_z = row_bounds(held, 1.0)
+    within(host(seq), want, np.where(t >= 0, logp_bound(want, ln_z, np.abs(want)), 0.0), "seq_logp")
+
+
 def test_infinite_and_nan_logits_stay_in_their_row():
     say("[rows] nan and inf logits")
     rng, z, t = draw(4, 900, 9)
