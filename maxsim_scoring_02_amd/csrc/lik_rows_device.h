@@ -188,7 +188,8 @@ __device__ __forceinline__ double row_logp(const RowSoft& r, float z, float scal
 }
 
 // The parts (m, Z) of a row as one softmax, by one wave.  A row all of -inf has
-// none: NaN.
+// none: NaN.  With Part they are those of some of its columns, which may be.
+template <bool Part = false>
 __device__ __forceinline__ RowSoft merge_parts(const float2* __restrict__ parts, int n, float scale) {
   const int lane = threadIdx.x & 63;
   float m = -kInf;
@@ -196,7 +197,7 @@ __device__ __forceinline__ RowSoft merge_parts(const float2* __restrict__ parts,
   RowSoft s = row_ref(wave_max(m), scale);
   float Z = 0.0f;
   for (int i = lane; i < n; i += 64) Z += parts[i].y * part_factor(s, parts[i].x, scale);
-  s.Z = s.m == -kInf ? __builtin_nanf("") : wave_sum(Z);
+  s.Z = !Part && s.m == -kInf ? __builtin_nanf("") : wave_sum(Z);
   return s;
 }
 
@@ -446,15 +447,33 @@ struct HeldRow {
     for (int i = 0; i < NV; ++i) opaque_piece(d[i]);
     return m;
   }
-  // Columns left out of the sum: `out` points to a bit per column (and a word
-  // behind the last) or is null, bit i of `hit` says whether this thread's piece
-  // i has one, which few do.
-  __device__ __forceinline__ float sum(const RowSoft& s, const uint32_t* out, uint32_t hit) {
-    float z = row_exp(s, edge);
-    if (out && deal.has_edge()) {
+  // Takes columns out of the row, which -inf replaces: `out` points to a bit per
+  // column (and a word behind the last), bit i of `hit` says whether this
+  // thread's piece i has one, which few do.
+  __device__ __forceinline__ void drop(const uint32_t* out, uint32_t hit) {
+    static_assert(NL == 0, "pieces in LDS are not dropped from");
+    if (deal.has_edge()) {
       const int c = deal.edge();
-      if (out[c >> 5] >> (c & 31) & 1) z = 0.0f;
+      if (out[c >> 5] >> (c & 31) & 1) edge = -kInf;
     }
+    const piece none = no_logits<T>();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (hit >> i & 1) {
+        const int c = deal.column(i);
+        const uint64_t w = (uint64_t)out[(c >> 5) + 1] << 32 | out[c >> 5];
+        const uint32_t bits = (uint32_t)(w >> (c & 31));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t b = bits >> (j * N / 4);
+          const uint32_t gone = N == 4 ? 0 - (b & 1) : (b & 1) * 0xffffu | (b >> 1 & 1) * 0xffff0000u;
+          d[i][j] = (d[i][j] & ~gone) | (none[j] & gone);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ float sum(const RowSoft& s) {
+    float z = row_exp(s, edge);
     const int pieces = opaque(deal.pieces);
 #pragma unroll
     for (int i = 0; i < NV + NL; ++i) {
@@ -463,14 +482,6 @@ struct HeldRow {
         unpack<T>(held(i), f);
 #pragma unroll
         for (int j = 0; j < N; ++j) f[j] = row_exp(s, f[j]);
-        if (out && hit >> i & 1) {
-          const int c = deal.column(i);
-          const uint64_t w = (uint64_t)out[(c >> 5) + 1] << 32 | out[c >> 5];
-          const uint32_t bits = (uint32_t)(w >> (c & 31));
-#pragma unroll
-          for (int j = 0; j < N; ++j)
-            if (bits >> j & 1) f[j] = 0.0f;
-        }
         z += piece_total<N>(f);
       }
     }
@@ -513,17 +524,15 @@ __device__ __forceinline__ void fill_row(T* __restrict__ g, int C, int tid, floa
 
 // The softmax of a group's columns: each wave's (m, Z), merged in LDS.  `tmp`
 // holds two floats per wave.  With Part the columns are one part of a row, and
-// one without a finite logit has Z = 0.  `out` and `hit` as for HeldRow::sum;
-// `meet` is done before the group meets.
+// one without a finite logit has Z = 0.  `meet` is done before the group meets.
 struct Nothing {
   __device__ void operator()() const {}
 };
 template <int GT, bool Part = false, typename Held, typename F = Nothing>
 __device__ __forceinline__ RowSoft held_softmax(Held& h, float scale, float* tmp,
-                                                const uint32_t* out = nullptr, uint32_t hit = 0,
                                                 F meet = F()) {
   const RowSoft w = part_ref(wave_max(h.max()), scale);
-  const float Z = wave_sum(h.sum(w, out, hit));
+  const float Z = wave_sum(h.sum(w));
   RowSoft s;
   meet();
   if constexpr (GT == 64) {

@@ -384,33 +384,46 @@ __device__ __forceinline__ void teacher_sums(const DistillArgs<T>& a, const Teac
   x->columns = (int)wave_sum((float)columns);      // at most 1024: exact
 }
 
-// Loss of a row and the factors of its gradient:
-//   listed columns  on * e - k p,   others  off * e   (k = w scale)
+// Loss of a row and its gradient: k = w scale,
+//   on * e - k p    on listed columns, e as in `row`, the softmax of all columns
+//   off * e         on the others, e as in `others`: theirs where the rest has a
+//                   term (so that they are told apart however far below the
+//                   listed ones they lie), else the row's
 struct DistillRow {
   float loss, on, off;
+  RowSoft row, others;
 };
-// s.Z: all columns without the rest's term, else the columns not listed (and
-// the whole sum on return).
+// s: the softmax of all columns, or with_rest of those not listed.
 __device__ __forceinline__ DistillRow distill_row(const TeacherSums& x, bool with_rest, int C,
-                                                  float scale, float k, RowSoft* s) {
-  const float rest = s->Z;
-  if (with_rest) s->Z = rest + (x.columns ? x.Z * part_factor(*s, x.m, scale) : 0.0f);
-  const double ln_sum = row_ln_sum(*s);
+                                                  float scale, float k, const RowSoft& s) {
+  DistillRow d;
+  d.row = d.others = s;
+  if (with_rest) {
+    if (s.m == -kInf) d.others.A = 0.0f;                // every e is 0
+    d.row = row_ref(fmaxf(s.m, x.m), scale);
+    d.row.Z = s.Z * part_factor(d.row, s.m, scale);
+    if (x.columns) d.row.Z += x.Z * part_factor(d.row, x.m, scale);
+  }
+  if (d.row.m == -kInf) d.row.Z = __builtin_nanf("");
+  const double ln_sum = row_ln_sum(d.row);
   // log q = scale (z - m) - ln_sum, so sum p (log p - log q) is
   double l = x.terms;
   if (x.mass != 0.0)
-    l += x.mass * ((double)scale * ((double)s->m - (double)x.base) + ln_sum);
-  DistillRow d;
-  float M = (float)x.mass, cut = 0.0f;
+    l += x.mass * ((double)scale * ((double)d.row.m - (double)x.base) + ln_sum);
+  const float M = (float)x.mass;
+  d.on = d.off = k * (M / d.row.Z);
   if (with_rest && x.columns < C) {
     const float p = x.mass != x.mass ? __builtin_nanf("") : (float)fmax(0.0, 1.0 - x.mass);
-    if (p != 0.0f) l += (double)p * ((double)logf(p) - (double)logf(rest / s->Z));
-    M = (float)(x.mass + (double)p);
-    cut = rest == 0.0f ? M / s->Z : p / rest;    // nothing left to write to: e = 0 there
+    // sum p (log p - log q) over the rest; q is 0 where no column is finite
+    if (p != 0.0f)
+      l += (double)p * ((double)logf(p) - (s.Z == 0.0f ? -(double)kInf
+                                                       : row_logp(d.row, s.m, scale, ln_sum) +
+                                                             row_ln_sum(s)));
+    const float all = (float)(x.mass + (double)p);
+    d.on = k * (all / d.row.Z);
+    d.off = d.on * part_factor(d.row, s.m, scale) - (s.Z == 0.0f ? 0.0f : k * (p / s.Z));
   }
   d.loss = (float)l;
-  d.on = k * (M / s->Z);
-  d.off = k * (M / s->Z - cut);
   return d;
 }
 
@@ -482,21 +495,21 @@ void distill_held_kernel(const DistillArgs<T> a) {
   }
   TeacherSums x;
   if (counts) teacher_probs(L, a.K, a.scale, with_rest ? a.t_lse + r : nullptr, &x, lane);
-  const uint32_t hit = with_rest ? teacher_hit(L, h.deal) : 0;
-  RowSoft s = held_softmax<GT>(h, a.scale, tmp, with_rest ? L.listed : nullptr, hit, [&] {
+  if (with_rest) h.drop(L.listed, teacher_hit(L, h.deal));
+  const RowSoft s = held_softmax<GT, true>(h, a.scale, tmp, [&] {
     if (!counts) return;
     teacher_sums(a, L, row, ahead.z, &x, lane);
     if (lane == 0) sums[group] = x;
   });
   const float k = w * a.scale + (flags & 1 ? __builtin_nanf("") : 0.0f);
-  const DistillRow d = distill_row(sums[group], with_rest, a.C, a.scale, k, &s);
+  const DistillRow d = distill_row(sums[group], with_rest, a.C, a.scale, k, s);
   if (tid == 0) a.row_loss[r] = flags & 1 ? __builtin_nanf("") : d.loss;
-  h.store(g, a.far, [&](float z) { return d.off * row_exp(s, z); });
-  teacher_grads(L, a.K, s, d.on, k, flags, g, tid);
+  h.store(g, a.far, [&](float z) { return d.off * row_exp(d.others, z); });
+  teacher_grads(L, a.K, d.row, d.on, k, flags, g, tid);
 }
 
-// Rows in parts, the first look: each part's (m, Z), listed columns left out of
-// Z where the rest has a term of its own.
+// Rows in parts, the first look: each part's (m, Z), listed columns left out
+// where the rest has a term of its own.
 template <typename T>
 __global__ __launch_bounds__(256) void distill_stats_kernel(const DistillArgs<T> a, Parts parts,
                                                             float2* __restrict__ mz) {
@@ -524,9 +537,9 @@ __global__ __launch_bounds__(256) void distill_stats_kernel(const DistillArgs<T>
       if (bit) atomicOr(&hits[owner], bit);
     }
     __syncthreads();
+    h.drop(listed, hits[tid]);
   }
-  const uint32_t hit = with_rest ? hits[tid] : 0;
-  const RowSoft s = held_softmax<256, true>(h, a.scale, tmp, with_rest ? listed : nullptr, hit);
+  const RowSoft s = held_softmax<256, true>(h, a.scale, tmp);
   if (tid == 0) mz[r * parts.n + at.p] = make_float2(s.m, s.Z);
 }
 
@@ -570,14 +583,14 @@ __global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T>
     teacher_sums(a, L, row, ahead.z, &x, tid);
     if (tid == 0) sums = x;
   }
-  RowSoft s = merge_parts(mz + r * n, n, a.scale);
+  const RowSoft s = merge_parts<true>(mz + r * n, n, a.scale);
   __syncthreads();
   const float k = w * a.scale + (flags & 1 ? __builtin_nanf("") : 0.0f);
-  const DistillRow d = distill_row(sums, with_rest, a.C, a.scale, k, &s);
+  const DistillRow d = distill_row(sums, with_rest, a.C, a.scale, k, s);
   if (first) a.row_loss[r] = flags & 1 ? __builtin_nanf("") : d.loss;
   if (g) {
-    h.store(g + at.lo, a.far, [&](float z) { return d.off * row_exp(s, z); });
-    teacher_grads(L, a.K, s, d.on, k, flags, g, tid);
+    h.store(g + at.lo, a.far, [&](float z) { return d.off * row_exp(d.others, z); });
+    teacher_grads(L, a.K, d.row, d.on, k, flags, g, tid);
   }
 }
 

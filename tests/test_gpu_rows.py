@@ -502,11 +502,36 @@ def test_rows_far_from_zero(R, C, offset, spread, dtype):
     z = (z * (spread / 3) + offset).astype(np.float32)
     check_logprob(on_gpu(z, dtype)[0], on_gpu(z, dtype)[1], t, 1.0)
     policy_case(z, t, dtype, 1.0, 51)
+    idx = np.stack([rng.permutation(C)[:20] for _ in range(R)])
+    val = rng.standard_normal((R, 20)).astype(np.float32)
+    for lse in (None, np.full(R, 4.0, dtype=np.float32)):
+        distill_case(R, C, 20, lse is not None, dtype, 1.0, 52, idx=idx, val=val, lse=lse, z=z)
     dev, held = on_gpu(z, dtype)
     seq = _lib.lik_preference_rows(dev, i32(t), i32(np.arange(R + 1)), i32([0]), i32([1]))[2]
     want = oracle.logprob_rows(held, t, 1.0)[0]
     _, _, _, ln_z = row_bounds(held, 1.0)
     within(host(seq), want, np.where(t >= 0, logp_bound(want, ln_z, np.abs(want)), 0.0), "seq_logp")
+
+
+@pytest.mark.parametrize("gap", [60.0, 120.0, 300.0, -120.0])
+@pytest.mark.parametrize("R,C,dtype", [(6, 900, F32), (5, 9001, F16), (256, 9001, BF16), (3, 70000, F32)])
+def test_distill_rest_far_from_the_list(R, C, dtype, gap):
+    """The columns not listed `gap` below the listed ones, further than float32's
+    exponentials of one maximum reach: their term and its gradient are finite."""
+    say(f"[rows] distill {R} x {C} rest {gap} below {dtype}")
+    rng, z, _ = draw(R, C, 60, 2.0)
+    idx = np.stack([rng.permutation(C)[:9] for _ in range(R)])
+    at = np.take_along_axis(z, idx, 1)
+    np.put_along_axis(z, idx, at + gap, 1)
+    val = rng.standard_normal((R, 9)).astype(np.float32)
+    loss, rows, grad = distill_case(R, C, 9, True, dtype, 1.0, 61, idx=idx, val=val,
+                                    lse=np.full(R, 4.0, dtype=np.float32), z=z)
+    assert torch.isfinite(loss).all() and torch.isfinite(grad).all()
+    if gap > 0:                  # no mass of the student's on the rest: p_rest in all
+        rest = grad.double().clone()
+        rest.scatter_(1, torch.from_numpy(idx).cuda(), 0)
+        p = 1 - np.exp(val.astype(np.float64) - 4).sum(1)
+        assert np.allclose(rest.sum(1).cpu().numpy(), -p / R, rtol=2e-2, atol=0)
 
 
 def test_infinite_and_nan_logits_stay_in_their_row():
