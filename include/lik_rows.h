@@ -22,6 +22,8 @@
  * The conventions of lik.h hold (memory, stream, workspace, errors,
  * determinism, reentrancy), and for every operator here:
  *
+ * Rows.  A call without rows (R == 0) is a successful no-op that writes no
+ *   output, a preference loss over empty sequences among them.
  * Logits.  float16, bfloat16 or float32 (LIK_F16, LIK_BF16, LIK_F32), row r
  *   at logits + r * ld elements (ld >= C), columns dense, aligned to the
  *   element.  Every exponential, sum and statistic is float32 or wider.
@@ -125,6 +127,9 @@ lik_status lik_logprob_rows_bwd(const void* logits, lik_dtype dtype, int64_t R,
  * term (with it).  An entry with column >= C makes the row's loss and gradient
  * NaN.  K <= 1024 and C <= 2^20 (LIK_ERR_UNSUPPORTED beyond).  The usual
  * factor of the squared temperature is the caller's, in row_weight.
+ * teacher_lse is a float32, so p_rest is off by up to 2^-22 (1 + |teacher_lse|):
+ * where the student leaves no finite column outside the list, pass NULL, for
+ * what rounding leaves of p_rest is set against a q_rest of 0 (infinite loss).
  * row_loss [R] float32, loss [1] float32.
  */
 lik_status lik_distill_rows(const void* logits, lik_dtype dtype, int64_t R,
@@ -140,9 +145,9 @@ lik_status lik_distill_rows(const void* logits, lik_dtype dtype, int64_t R,
  * Clipped policy loss.  With rho = exp(logp - old_logp) and A = advantage,
  *   l_r = -min(rho A, clamp(rho, 1 - clip_low, 1 + clip_high) A)
  *         + kl_coef (exp(ref_logp - logp) - (ref_logp - logp) - 1),
- * the second term only with ref_logp (NULL: none) and a kl_coef other than 0.  old_logp, advantage and
- * ref_logp are float32 [R], constants of the gradient; a row at the border of
- * its clip still has the gradient of rho A.  0 <= clip_low <= 1,
+ * the second term only with ref_logp (NULL: none) and a kl_coef other than 0.
+ * old_logp, advantage and ref_logp are float32 [R], constants of the gradient;
+ * a row at the border of its clip still has the gradient of rho A.  0 <= clip_low <= 1,
  * clip_high >= 0 (infinity: no clip on that side), kl_coef finite.
  * row_loss, logp [R] float32, loss [1] float32.
  */
@@ -176,7 +181,8 @@ lik_status lik_policy_rows(const void* logits, lik_dtype dtype, int64_t R,
  * 0.  Rows of a sequence in no pair have gradient 0 too.  A NaN in a sequence
  * (a target >= C, a NaN logit) makes it, its pairs' losses and the gradient of
  * every sequence in those pairs NaN.
- * pair_loss [P], seq_logp [S], loss [1]: float32.
+ * pair_loss [P], seq_logp [S], loss [1]: float32.  S x P <= 2^40
+ * (LIK_ERR_UNSUPPORTED beyond).
  */
 lik_status lik_preference_rows(const void* logits, lik_dtype dtype, int64_t R,
                                int64_t C, int64_t ld, const int32_t* targets,

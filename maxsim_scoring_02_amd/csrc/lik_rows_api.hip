@@ -17,7 +17,6 @@ using lik::ok;
 
 constexpr int64_t kMaxRows = INT32_MAX;
 
-
 // What every operator checks: sizes, type, scale, logits and gradient.
 // `done` is set when there is nothing to do.
 lik_status check_rows(const lik::Rows& a, bool need_grad, bool* done) {
@@ -247,6 +246,9 @@ lik_status lik_preference_rows(const void* logits, lik_dtype dtype, int64_t R, i
   if (done) return ok();
   if (S > kMaxRows || P > kMaxRows)
     return fail(LIK_ERR_UNSUPPORTED, "S and P must be below 2^31");
+  if (S > 0 && P > lik::kPrefMaxProduct / S)
+    return fail(LIK_ERR_UNSUPPORTED, "S x P must be at most 2^40 (got %lld x %lld)", (long long)S,
+                (long long)P);
   LIK_TRY(need4(targets, "targets"));
   LIK_TRY(need4(seq_offsets, "seq_offsets"));
   if (P > 0) {

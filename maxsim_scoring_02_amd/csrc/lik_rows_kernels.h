@@ -11,6 +11,10 @@ namespace lik {
 
 constexpr int64_t kDistillMaxK = 1024;
 constexpr int64_t kDistillMaxC = int64_t(1) << 20;   // the bitmap of listed columns fits LDS
+// Sequences times pairs of a preference loss: every sequence looks through the
+// pairs for its own, 8.4 ms at 2^34, which atomics would save, and the order of
+// the sums with them.
+constexpr int64_t kPrefMaxProduct = int64_t(1) << 40;
 
 inline size_t rows_up(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -89,7 +93,6 @@ inline bool rows_held(int64_t R, int64_t C, lik_dtype dtype, int64_t most) {
 struct RowsLayout {
   size_t parts = 0;    // [R][n] float2 (m, Z)
   size_t soft = 0;     // preference: [R] float4 (m, c, A, Z) of each row
-  size_t logp = 0;     // preference: [R] double
   size_t coef = 0;     // preference: [R] float, dl/dlogp of each row
   size_t seq = 0;      // preference: [S] double, sequence log-probabilities
   size_t bytes = 0;
@@ -102,8 +105,7 @@ inline RowsLayout parts_layout(int64_t R, int64_t C, lik_dtype dtype) {
 inline RowsLayout pref_layout(int64_t R, int64_t C, int64_t S, lik_dtype dtype) {
   RowsLayout w = parts_layout(R, C, dtype);
   w.soft = w.bytes;
-  w.logp = rows_up(w.soft + (size_t)R * 16);
-  w.coef = rows_up(w.logp + (size_t)R * 8);
+  w.coef = rows_up(w.soft + (size_t)R * 16);
   w.seq = rows_up(w.coef + (size_t)R * 4);
   w.bytes = rows_up(w.seq + (size_t)S * 8);
   return w;

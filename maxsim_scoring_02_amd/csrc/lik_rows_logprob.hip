@@ -214,8 +214,9 @@ __device__ __forceinline__ double pair_weight(const PrefArgs& p, int64_t i) {
   return p.weight ? (double)p.weight[i] : 1.0 / (double)p.P;
 }
 
-// Block 0: the pairs' losses and their sum.  Block 1 + s, one sequence: dl/dL_s
-// from every pair it is in, in the pairs' order by lane, onto its rows.
+// Block 0: the pairs' losses and their sum.  Block 1 + s, one sequence (for the
+// gradient): dl/dL_s from every pair it is in, in the pairs' order by lane, onto
+// its rows.
 __global__ __launch_bounds__(256) void pref_pairs_kernel(PrefArgs p, int64_t R,
                                                          const double* __restrict__ seq,
                                                          float* __restrict__ coef) {
@@ -379,8 +380,8 @@ hipError_t preference_t(const Rows& a, const PrefArgs& p, char* ws, hipStream_t 
       hipLaunchKernelGGL(pref_seq_kernel<T>, linear_grid(p.S), dim3(256), 0, s, p, rows);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(pref_pairs_kernel, linear_grid(p.S + 1), dim3(256), 0, s, p, a.R, seq,
-                       coef);
+    hipLaunchKernelGGL(pref_pairs_kernel, linear_grid(a.grad ? p.S + 1 : 1), dim3(256), 0, s, p,
+                       a.R, seq, coef);
   }
   if ((e = hipGetLastError()) != hipSuccess || !a.grad) return e;
   return parts_dispatch(parts, [&](auto gt) {

@@ -769,6 +769,37 @@ def test_bitwise_reproducible_and_on_another_stream():
     assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+def test_two_streams_at_once():
+    """Calls in flight on two streams at the same time, each with workspaces of
+    its own, and their results those of the calls one by one."""
+    say("[rows] two streams")
+    data = []
+    for seed in (70, 71):
+        rng, z, t = draw(200, 70000, seed)
+        data.append((on_gpu(z, BF16)[0], i32(np.maximum(t, 0)), i32(rng.integers(0, 70000, (200, 30))),
+                     f32(rng.standard_normal((200, 30))), i32(np.arange(0, 201, 10)),
+                     i32(rng.integers(0, 20, 30)), i32(rng.integers(0, 20, 30)),
+                     f32(rng.standard_normal(200))))
+
+    def everything(z, t, idx, val, off, c, r, v):
+        lp, lse = _lib.lik_logprob_rows_fwd(z, t)
+        return [lp, lse, _lib.lik_logprob_rows_bwd(z, t, lse, v), *_lib.lik_distill_rows(z, idx, val, v),
+                *_lib.lik_policy_rows(z, t, lp, v), *_lib.lik_preference_rows(z, t, off, c, r)]
+
+    want = [everything(*d) for d in data]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(everything(*data[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for g in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip(g, want[i]))
+
+
 def test_captured_and_replayed():
     """Every operator in one captured graph, replayed on new inputs with eager
     work of the same calls between the replays."""

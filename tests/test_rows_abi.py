@@ -208,3 +208,14 @@ def test_binding_checks_shapes_strides_and_types():
             _lib._row_grad(z, True, out)
     with pytest.raises(ValueError, match="want_grad"):
         _lib._row_grad(z, False, z)
+
+
+@pytest.mark.parametrize("S,P,fine", [(1 << 20, 1 << 20, True), (1 << 20, (1 << 20) + 1, False),
+                                      (1 << 30, 1 << 30, False), (2 ** 31 - 1, 512, True),
+                                      (0, 2 ** 31 - 1, True)])
+def test_preference_sequences_times_pairs(L, S, P, fine):
+    if fine and torch.cuda.is_available():
+        pytest.skip("a GPU is present; the pointers are not real")
+    st = call(L, "lik_preference_rows", S=S, P=P, wsb=1 << 40)
+    assert st == LIK_ERR_UNSUPPORTED
+    assert ("device" if fine else "S x P") in L.lik_last_error().decode()
