@@ -112,9 +112,9 @@ size_t lik_rows_workspace_bytes(lik_rows_op op, int64_t R, int64_t C, int64_t n_
     case LIK_ROWS_DISTILL:
     case LIK_ROWS_POLICY:
       if (R == 0 || C == 0) return 0;
-      if ((flags & 1) && lik::rows_held(R, C, dtype, op == LIK_ROWS_POLICY
-                                                          ? lik::kPolicyHeldBytes
-                                                          : lik::kDistillHeldBytes))
+      // a long teacher's list takes the longest rows in parts
+      if ((flags & 1) &&
+          lik::rows_held(R, C, dtype, op == LIK_ROWS_POLICY ? lik::kHeldBytes : lik::kRegisterBytes))
         return 0;
       return lik::parts_layout(R, C, dtype).bytes;
     case LIK_ROWS_PREFERENCE:

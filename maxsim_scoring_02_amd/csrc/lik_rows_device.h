@@ -373,18 +373,13 @@ struct Deal {
   __device__ __forceinline__ int column(int i) const { return head + (i * GT + tid) * N; }
   __device__ __forceinline__ bool has_edge() const { return tid < edges; }
   __device__ __forceinline__ int edge() const { return tid < head ? tid : tid + pieces * N; }
-  // the thread that has column c, and as a bit the number of its piece that c is
-  // in (no bit for an edge)
-  __device__ __forceinline__ int owner(int c, uint32_t* piece_bit) const {
+  // the thread that has column c
+  __device__ __forceinline__ int owner(int c) const {
     const int p = c - head;
     const bool in = p >= 0 && p < pieces * N;
-    *piece_bit = in ? 1u << (p / N / GT & 31) : 0u;
     return in ? p / N % GT : (p < 0 ? c : c - pieces * N);
   }
-  __device__ __forceinline__ bool holds(int c) const {
-    uint32_t bit;
-    return owner(c, &bit) == tid;
-  }
+  __device__ __forceinline__ bool holds(int c) const { return owner(c) == tid; }
 };
 
 // The columns of a Deal on chip: an edge and NV pieces a thread at most in
@@ -437,8 +432,7 @@ struct HeldRow {
     for (int i = 0; i < NV; ++i)
       if (i * GT < pieces) m = piece_max<T>(d[i], m);
     if constexpr (NL > 0) {
-      // a wave reads back only what its own lanes loaded into LDS
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      landed();
 #pragma unroll
       for (int i = NV; i < NV + NL; ++i)
         if (i * GT < pieces) m = piece_max<T>(held(i), m);
@@ -447,30 +441,31 @@ struct HeldRow {
     for (int i = 0; i < NV; ++i) opaque_piece(d[i]);
     return m;
   }
-  // Takes columns out of the row, which -inf replaces: `out` points to a bit per
-  // column (and a word behind the last), bit i of `hit` says whether this
-  // thread's piece i has one, which few do.
-  __device__ __forceinline__ void drop(const uint32_t* out, uint32_t hit) {
-    static_assert(NL == 0, "pieces in LDS are not dropped from");
-    if (deal.has_edge()) {
-      const int c = deal.edge();
-      if (out[c >> 5] >> (c & 31) & 1) edge = -kInf;
+  // LDS pieces are here (a wave reads back only what its own lanes loaded).
+  __device__ __forceinline__ void landed() const {
+    if constexpr (NL > 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+  // Takes a column of this thread out of the row: -inf in its place.  After
+  // landed().
+  __device__ __forceinline__ void drop(int c) {
+    const int p = c - deal.head, i = p / N / GT, j = p % N;
+    if (p < 0 || p >= deal.pieces * N) {
+      edge = -kInf;
+      return;
     }
     const piece none = no_logits<T>();
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (hit >> i & 1) {
-        const int c = deal.column(i);
-        const uint64_t w = (uint64_t)out[(c >> 5) + 1] << 32 | out[c >> 5];
-        const uint32_t bits = (uint32_t)(w >> (c & 31));
+    for (int k = 0; k < NV; ++k) {
+      if (i == k) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t b = bits >> (j * N / 4);
-          const uint32_t gone = N == 4 ? 0 - (b & 1) : (b & 1) * 0xffffu | (b >> 1 & 1) * 0xffff0000u;
-          d[i][j] = (d[i][j] & ~gone) | (none[j] & gone);
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t gone = w != j / (N / 4) ? 0u : N == 4 ? ~0u : 0xffffu << (j % 2 * 16);
+          d[k][w] = (d[k][w] & ~gone) | (none[w] & gone);
         }
       }
     }
+    if constexpr (NL > 0)
+      if (i >= NV) reinterpret_cast<T*>(lds + ((i - NV) * GT + deal.tid) * 16)[j] = (T)-kInf;
   }
   __device__ __forceinline__ float sum(const RowSoft& s) {
     float z = row_exp(s, edge);

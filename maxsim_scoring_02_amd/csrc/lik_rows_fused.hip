@@ -96,7 +96,7 @@ constexpr int kPolicyWaves = 8, kDistillWaves = 6;
 template <typename T, int GT, int NV, int NL>
 __global__ __launch_bounds__(group_threads<GT>()) __attribute__((amdgpu_waves_per_eu(held_waves(NV, kPolicyWaves))))
 void policy_held_kernel(const PolicyArgs<T> a) {
-  extern __shared__ char lds[];
+  extern __shared__ __attribute__((aligned(16))) char lds[];
   __shared__ float tmp[2 * (GT / 64)];
   const int64_t r = group_row<GT>();
   if (r >= a.R) return;
@@ -213,69 +213,79 @@ struct DistillArgs {
   bool far;
 };
 
-// The teacher's list of one row in LDS, and a bitmap of its columns.
+// The teacher's list of one row in LDS.  Each thread has a chain of entries: those
+// of the columns that a Deal gives to it, and in a kernel that has a part of the
+// row others besides.  So a column's entries are all in one chain, and the thread
+// that wrote a column's gradient can write it again without a meeting.
 struct TeacherList {
   int32_t* col;        // column, -1 absent, | kAgain behind the column's first entry
   float* p;            // teacher logit, then its probability
   float* zs;           // the student's logit there
-  int* flags;          // 1: a column >= C, 2: a column twice, 4: an entry with mass
-  uint32_t* listed;
-  int32_t* next;       // the entries of a thread's own columns as a list, -1 at
-  int32_t* head;       // its end, so that the thread that wrote a column's
-};                     // gradient can write it again without a meeting
+  int32_t* next;       // next entry of the chain, -1 at its end
+  int* flags;          // 1: a column >= C, 4: an entry with mass
+  int32_t* head;       // first entry of each thread's chain
+};
 constexpr int32_t kAgain = 1 << 24;
 static_assert(kDistillMaxC < kAgain, "a column and its mark share a word");
 
-// a word behind the bitmap's last, which HeldRow::sum may read
-__host__ __device__ inline size_t teacher_bytes(int C, int K, int threads) {
-  return ((size_t)K * 16 + 4 + ((size_t)C + 31) / 32 * 4 + 4 + threads * 4 + 15) / 16 * 16;
+__host__ __device__ inline size_t teacher_bytes(int K, int threads) {
+  return ((size_t)K * 16 + 4 + threads * 4 + 15) / 16 * 16;
 }
-__device__ __forceinline__ TeacherList teacher_at(char* p, int C, int K) {
+__device__ __forceinline__ TeacherList teacher_at(char* p, int K) {
   TeacherList L;
   L.col = (int32_t*)p;
   L.p = (float*)p + K;
   L.zs = (float*)p + 2 * K;
   L.next = (int32_t*)p + 3 * K;
   L.flags = (int*)p + 4 * K;
-  L.listed = (uint32_t*)p + 4 * K + 1;
-  L.head = (int32_t*)L.listed + (C + 31) / 32 + 1;
+  L.head = (int32_t*)p + 4 * K + 1;
   return L;
 }
-__device__ __forceinline__ int entry_col(int32_t c) { return c < 0 ? -1 : c & (kAgain - 1); }
+__device__ __forceinline__ int entry_col(int32_t c) { return c & (kAgain - 1); }
 
-// One entry of the list into LDS, without the student's logit.  `deal` shares
-// the columns from lo on, of which there are `cols`.
+// The columns that a kernel's group has, from lo on, shared by `deal`, and the
+// chain of any column.
+template <typename T, int GT>
+struct TeacherAt {
+  Deal<T, GT> deal;
+  int lo, cols;
+  __device__ __forceinline__ bool has(int j) const { return j >= lo && j - lo < cols; }
+  __device__ __forceinline__ int chain(int j) const {
+    return has(j) ? deal.owner(j - lo) : j & (GT - 1);
+  }
+};
+
+// One entry of the list into LDS, without the student's logit.
 template <typename T, int GT>
 __device__ __forceinline__ void teacher_entry(const DistillArgs<T>& a, const TeacherList& L,
-                                              const Deal<T, GT> deal, int lo, int cols, int k,
-                                              int32_t j, float t) {
+                                              const TeacherAt<T, GT>& at, int k, int32_t j, float t) {
   const bool in = j >= 0 && j < a.C;
   int flags = j >= a.C ? 1 : 0;
   if (in) {
-    const uint32_t bit = 1u << (j & 31);
-    if (atomicOr(&L.listed[j >> 5], bit) & bit) flags |= 2;
     if (t != -kInf) flags |= 4;
-    if (j >= lo && j - lo < cols) {
-      uint32_t piece_bit;
-      L.next[k] = atomicExch(&L.head[deal.owner(j - lo, &piece_bit)], k);
-    }
+    L.next[k] = atomicExch(&L.head[at.chain(j)], k);
   }
   L.col[k] = in ? j : -1;
   L.p[k] = t;
   if (flags) atomicOr(L.flags, flags);
 }
 
-// The list's second look, where a column is listed twice: its first entry
-// stands for it.  Which thread marked the bitmap first does not matter.
-template <int GT>
-__device__ __forceinline__ void teacher_first(const TeacherList& L, int K, int tid) {
-  for (int k = tid; k < K; k += GT) {
+// Marks what is listed a second time, by one wave: a column's first entry stands
+// for it.  The order within the chains does not matter.
+template <typename T, int GT>
+__device__ __forceinline__ bool teacher_again(const TeacherList& L, const TeacherAt<T, GT>& at,
+                                              int K, int lane) {
+  bool any = false;
+  for (int k = lane; k < K; k += 64) {
     const int32_t c = L.col[k];
-    bool first = true;
-    for (int i = 0; i < k; ++i) first &= entry_col(L.col[i]) != c;
-    if (!first && c >= 0) L.col[k] = c | kAgain;
+    if (c < 0) continue;
+    bool again = false;
+    for (int i = L.head[at.chain(c)]; i >= 0; i = L.next[i])
+      if (i < k) again |= entry_col(L.col[i]) == c;
+    if (again) L.col[k] = c | kAgain;
+    any |= again;
   }
-  group_sync<GT>();
+  return __any(any);
 }
 
 // A thread's first entry, loaded ahead of the row, and the student's logit there,
@@ -296,23 +306,19 @@ struct TeacherAhead {
   }
 };
 
-// The list and the bitmap into LDS; returns the flags.
+// The list into LDS; returns the flags.
 template <typename T, int GT>
 __device__ __forceinline__ int teacher_fill(const DistillArgs<T>& a, const TeacherList& L,
                                             int64_t r, int tid, const TeacherAhead<T>& x,
-                                            const Deal<T, GT> deal, int lo, int cols) {
-  const int words = (a.C + 31) / 32 + 1;
-  for (int i = tid; i < words; i += GT) L.listed[i] = 0;
+                                            const TeacherAt<T, GT>& at) {
   L.head[tid] = -1;
   if (tid == 0) *L.flags = 0;
   group_sync<GT>();
-  if (tid < a.K) teacher_entry<T, GT>(a, L, deal, lo, cols, tid, x.j, x.t);
+  if (tid < a.K) teacher_entry(a, L, at, tid, x.j, x.t);
   for (int k = tid + GT; k < a.K; k += GT)
-    teacher_entry<T, GT>(a, L, deal, lo, cols, k, a.idx[r * a.K + k], a.val[r * a.K + k]);
+    teacher_entry(a, L, at, k, a.idx[r * a.K + k], a.val[r * a.K + k]);
   group_sync<GT>();
-  const int flags = *L.flags;
-  if (flags & 2) teacher_first<GT>(L, a.K, tid);
-  return flags;
+  return *L.flags;
 }
 
 // What the list adds up to.  One wave goes over it (every wave doing so for
@@ -325,6 +331,7 @@ struct TeacherSums {
   float base;         // m, or 0 where that is infinite
   float m, Z;         // the listed columns as a part of the student's row
   int columns;        // how many those are
+  bool again;         // a column is listed twice
 };
 __device__ __forceinline__ void teacher_probs(const TeacherList& L, int K, float scale,
                                                 const float* t_lse, TeacherSums* x, int lane) {
@@ -427,45 +434,36 @@ __device__ __forceinline__ DistillRow distill_row(const TeacherSums& x, bool wit
   return d;
 }
 
-// The pieces of this thread that have a listed column, a bit each.
-template <typename T, int GT>
-__device__ __forceinline__ uint32_t teacher_hit(const TeacherList& L, const Deal<T, GT> deal) {
-  uint32_t hit = 0, bit;
-  for (int k = L.head[deal.tid]; k >= 0; k = L.next[k]) {
-    deal.owner(entry_col(L.col[k]), &bit);
-    hit |= bit;
-  }
-  return hit;
-}
-
 // The gradient on the listed columns, over what the same thread wrote there with
 // the row.
 __device__ __forceinline__ float teacher_grad(const TeacherList& L, int K, int k, const RowSoft& s,
-                                              float on, float weight, int flags) {
+                                              float on, float weight, bool again) {
   double p = (double)L.p[k];
-  if (flags & 2)
+  if (again)
     for (int j = k + 1; j < K; ++j)
-      if (entry_col(L.col[j]) == L.col[k]) p += (double)L.p[j];
+      if (L.col[j] == (L.col[k] | kAgain)) p += (double)L.p[j];
   return on * row_exp(s, L.zs[k]) - weight * (float)p;
 }
-template <typename T>
-__device__ __forceinline__ void teacher_grads(const TeacherList& L, int K, const RowSoft& s,
-                                              float on, float weight, int flags,
-                                              T* __restrict__ g, int tid) {
-  for (int k = L.head[tid]; k >= 0; k = L.next[k])
-    if (!(L.col[k] & kAgain)) g[L.col[k]] = (T)teacher_grad(L, K, k, s, on, weight, flags);
+template <typename T, int GT>
+__device__ __forceinline__ void teacher_grads(const TeacherList& L, const TeacherAt<T, GT>& at,
+                                              int K, const RowSoft& s, float on, float weight,
+                                              bool again, T* __restrict__ g) {
+  for (int k = L.head[at.deal.tid]; k >= 0; k = L.next[k]) {
+    const int32_t c = L.col[k];
+    if (!(c & kAgain) && at.has(c)) g[c] = (T)teacher_grad(L, K, k, s, on, weight, again);
+  }
 }
 
 // Rows held on chip.  4096 x 65536 bf16 with 64 entries a row and the rest's
 // term: 200 to 215 us from card to card, 5.0 to 5.4 TB/s, 5 to 10% behind the policy
 // loss on the same rows: the list costs meetings and LDS passes in a row's life,
 // and the listed columns' second stores 2%.
-template <typename T, int GT, int NV>
+template <typename T, int GT, int NV, int NL>
 __global__ __launch_bounds__(group_threads<GT>()) __attribute__((amdgpu_waves_per_eu(held_waves(NV, kDistillWaves))))
 void distill_held_kernel(const DistillArgs<T> a) {
   __shared__ float tmp[2 * (GT / 64)];
   __shared__ TeacherSums sums[GT == 64 ? 4 : 1];
-  extern __shared__ char lists[];
+  extern __shared__ __attribute__((aligned(16))) char lists[];
   const int64_t r = group_row<GT>();
   if (r >= a.R) return;
   const int tid = group_tid<GT>(), lane = threadIdx.x & 63;
@@ -479,23 +477,32 @@ void distill_held_kernel(const DistillArgs<T> a) {
     return;
   }
   const T* row = a.z + r * a.ld;
-  const TeacherList L = teacher_at(lists + group * teacher_bytes(a.C, a.K, GT), a.C, a.K);
   TeacherAhead<T> ahead;
   ahead.entry(a, r, tid);
-  HeldRow<T, GT, NV> h;
+  HeldRow<T, GT, NV, true, NL> h;
+  h.lds = lists;
+  const TeacherList L = teacher_at(lists + h.kLdsBytes + group * teacher_bytes(a.K, GT), a.K);
   h.load(row, a.C, tid, g);
   if (counts) ahead.logit(a, row);
-  const int flags = teacher_fill<T, GT>(a, L, r, tid, ahead, h.deal, 0, a.C);
+  const TeacherAt<T, GT> at{h.deal, 0, a.C};
+  const int flags = teacher_fill(a, L, r, tid, ahead, at);
   const bool with_rest = a.t_lse != nullptr;
   if (!with_rest && !(flags & 5)) {
     // no entry with mass
+    h.landed();                         // before the LDS goes to another group
     if (tid == 0) a.row_loss[r] = 0.0f;
     fill_row<T, GT>(g, a.C, tid, 0.0f);
     return;
   }
   TeacherSums x;
-  if (counts) teacher_probs(L, a.K, a.scale, with_rest ? a.t_lse + r : nullptr, &x, lane);
-  if (with_rest) h.drop(L.listed, teacher_hit(L, h.deal));
+  if (counts) {
+    x.again = teacher_again(L, at, a.K, lane);
+    teacher_probs(L, a.K, a.scale, with_rest ? a.t_lse + r : nullptr, &x, lane);
+  }
+  if (with_rest) {
+    h.landed();
+    for (int k = L.head[tid]; k >= 0; k = L.next[k]) h.drop(entry_col(L.col[k]));
+  }
   const RowSoft s = held_softmax<GT, true>(h, a.scale, tmp, [&] {
     if (!counts) return;
     teacher_sums(a, L, row, ahead.z, &x, lane);
@@ -505,7 +512,7 @@ void distill_held_kernel(const DistillArgs<T> a) {
   const DistillRow d = distill_row(sums[group], with_rest, a.C, a.scale, k, s);
   if (tid == 0) a.row_loss[r] = flags & 1 ? __builtin_nanf("") : d.loss;
   h.store(g, a.far, [&](float z) { return d.off * row_exp(d.others, z); });
-  teacher_grads(L, a.K, d.row, d.on, k, flags, g, tid);
+  teacher_grads(L, at, a.K, d.row, d.on, k, sums[group].again, g);
 }
 
 // Rows in parts, the first look: each part's (m, Z), listed columns left out
@@ -514,7 +521,7 @@ template <typename T>
 __global__ __launch_bounds__(256) void distill_stats_kernel(const DistillArgs<T> a, Parts parts,
                                                             float2* __restrict__ mz) {
   __shared__ float tmp[8];
-  __shared__ uint32_t listed[256 * kLookPieces * PieceOf<T>::N / 32 + 1], hits[256];
+  __shared__ int32_t head[256], next[kDistillMaxK], col[kDistillMaxK];
   const PartAt at = part_at<256>(parts, a.C, 0);
   if (at.r >= a.R) return;
   const int64_t r = at.r;
@@ -524,20 +531,16 @@ __global__ __launch_bounds__(256) void distill_stats_kernel(const DistillArgs<T>
   h.load(a.z + r * a.ld + at.lo, at.cols, tid, nullptr);
   const bool with_rest = a.t_lse != nullptr;
   if (with_rest) {
-    for (int i = tid; i < (at.cols + 31) / 32 + 1; i += 256) listed[i] = 0;
-    hits[tid] = 0;
+    head[tid] = -1;
     __syncthreads();
     for (int k = tid; k < a.K; k += 256) {
-      const int64_t j = (int64_t)a.idx[r * a.K + k] - at.lo;
-      if (j < 0 || j >= at.cols) continue;
-      const int c = (int)j;
-      uint32_t bit;
-      const int owner = h.deal.owner(c, &bit);
-      atomicOr(&listed[c >> 5], 1u << (c & 31));
-      if (bit) atomicOr(&hits[owner], bit);
+      const int64_t c = (int64_t)a.idx[r * a.K + k] - at.lo;
+      if (c < 0 || c >= at.cols) continue;
+      col[k] = (int)c;
+      next[k] = atomicExch(&head[h.deal.owner((int)c)], k);
     }
     __syncthreads();
-    h.drop(listed, hits[tid]);
+    for (int k = head[tid]; k >= 0; k = next[k]) h.drop(col[k]);
   }
   const RowSoft s = held_softmax<256, true>(h, a.scale, tmp);
   if (tid == 0) mz[r * parts.n + at.p] = make_float2(s.m, s.Z);
@@ -548,37 +551,39 @@ template <typename T>
 __global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T> a, Parts parts,
                                                             const float2* __restrict__ mz, int n) {
   __shared__ TeacherSums sums;
-  extern __shared__ char lists[];
-  const PartAt at = part_at<256>(parts, a.C, 0);
-  if (at.r >= a.R) return;
-  const int64_t r = at.r;
+  extern __shared__ __attribute__((aligned(16))) char lists[];
+  const PartAt part = part_at<256>(parts, a.C, 0);
+  if (part.r >= a.R) return;
+  const int64_t r = part.r;
   const int tid = threadIdx.x;
   const float w = a.weight ? a.weight[r] : 1.0f / (float)a.R;
-  const bool first = at.p == 0 && tid == 0;
+  const bool first = part.p == 0 && tid == 0;
   T* g = a.grad ? a.grad + r * a.gld : nullptr;
-  if (!g && at.p != 0) return;
+  if (!g && part.p != 0) return;
   if (w == 0.0f) {
     if (first) a.row_loss[r] = 0.0f;
-    if (g) fill_row<T, 256>(g + at.lo, at.cols, tid, 0.0f);
+    if (g) fill_row<T, 256>(g + part.lo, part.cols, tid, 0.0f);
     return;
   }
   const T* row = a.z + r * a.ld;
-  const TeacherList L = teacher_at(lists, a.C, a.K);
+  const TeacherList L = teacher_at(lists, a.K);
   TeacherAhead<T> ahead;
   ahead.entry(a, r, tid);
   if (wave_id() == 0) ahead.logit(a, row);
   HeldRow<T, 256, kGradPieces> h;
-  if (g) h.load(row + at.lo, at.cols, tid, g + at.lo);
-  else h.deal = Deal<T, 256>(row + at.lo, at.cols, tid);
-  const int flags = teacher_fill<T, 256>(a, L, r, tid, ahead, h.deal, at.lo, at.cols);
+  if (g) h.load(row + part.lo, part.cols, tid, g + part.lo);
+  else h.deal = Deal<T, 256>(row + part.lo, part.cols, tid);
+  const TeacherAt<T, 256> at{h.deal, part.lo, part.cols};
+  const int flags = teacher_fill(a, L, r, tid, ahead, at);
   const bool with_rest = a.t_lse != nullptr;
   if (!with_rest && !(flags & 5)) {
     if (first) a.row_loss[r] = 0.0f;
-    if (g) fill_row<T, 256>(g + at.lo, at.cols, tid, 0.0f);
+    if (g) fill_row<T, 256>(g + part.lo, part.cols, tid, 0.0f);
     return;
   }
   if (wave_id() == 0) {
     TeacherSums x;
+    x.again = teacher_again(L, at, a.K, tid);
     teacher_probs(L, a.K, a.scale, with_rest ? a.t_lse + r : nullptr, &x, tid);
     teacher_sums(a, L, row, ahead.z, &x, tid);
     if (tid == 0) sums = x;
@@ -589,8 +594,8 @@ __global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T>
   const DistillRow d = distill_row(sums, with_rest, a.C, a.scale, k, s);
   if (first) a.row_loss[r] = flags & 1 ? __builtin_nanf("") : d.loss;
   if (g) {
-    h.store(g + at.lo, a.far, [&](float z) { return d.off * row_exp(d.others, z); });
-    teacher_grads(L, a.K, d.row, d.on, k, flags, g, tid);
+    h.store(g + part.lo, a.far, [&](float z) { return d.off * row_exp(d.others, z); });
+    teacher_grads(L, at, a.K, d.row, d.on, k, sums.again, g);
   }
 }
 
@@ -601,7 +606,7 @@ __global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T>
 // in 67 where one wave takes 75 (8192 x 8192), 64 KB rows by 512 in 107 where 256
 // take 111 (4096 x 32768), and 128 KB rows by 512 in 228 where 1024 take 295
 // (4096 x 65536).
-template <typename T, bool Lds, typename F>
+template <typename T, typename F>
 hipError_t held_dispatch(int64_t C, F f) {
 #define LIK_HELD(GT, NV, NL)                                                     \
   if (C <= HeldRow<T, GT, NV, true, NL>::kColumns)                               \
@@ -614,7 +619,7 @@ hipError_t held_dispatch(int64_t C, F f) {
   LIK_HELD(512, 8, 0)
   LIK_HELD(512, 16, 0)
   LIK_HELD(1024, 16, 0)
-  if constexpr (Lds) LIK_HELD(1024, 23, 9)
+  LIK_HELD(1024, 23, 9)
 #undef LIK_HELD
   return hipErrorInvalidValue;
 }
@@ -639,8 +644,8 @@ hipError_t policy_t(const Rows& a, const int32_t* targets, const float* old_logp
                     float* row_loss, float* logp, float* loss, char* ws, hipStream_t s) {
   const PolicyArgs<T> p{(const T*)a.z, a.R, a.ld, (int)a.C, a.scale, targets, old_logp, adv, ref,
                         low, high, kl, weight, row_loss, logp, (T*)a.grad, a.grad_ld, a.far()};
-  if (a.grad && rows_held(a.R, a.C, a.dtype, kPolicyHeldBytes)) {
-    const hipError_t e = held_dispatch<T, true>(a.C, [&](auto gt, auto nv, auto nl) {
+  if (a.grad && rows_held(a.R, a.C, a.dtype, kHeldBytes)) {
+    const hipError_t e = held_dispatch<T>(a.C, [&](auto gt, auto nv, auto nl) {
       constexpr int GT = decltype(gt)::value, NV = decltype(nv)::value, NL = decltype(nl)::value;
       constexpr size_t lds = HeldRow<T, GT, NV, true, NL>::kLdsBytes;
       const hipError_t e = allow_lds(policy_held_kernel<T, GT, NV, NL>, lds);
@@ -679,13 +684,14 @@ hipError_t distill_t(const Rows& a, const int32_t* idx, const float* val, int64_
                      hipStream_t s) {
   const DistillArgs<T> p{(const T*)a.z, a.R, a.ld, (int)a.C, (int)K, a.scale, idx, val, t_lse,
                          weight, row_loss, (T*)a.grad, a.grad_ld, a.far()};
-  if (a.grad && rows_held(a.R, a.C, a.dtype, kDistillHeldBytes))
-    return held_dispatch<T, false>(a.C, [&](auto gt, auto nv, auto) {
-      constexpr int GT = decltype(gt)::value, NV = decltype(nv)::value;
-      const size_t lds = teacher_bytes((int)a.C, (int)K, GT) * (GT == 64 ? 4 : 1);
-      const hipError_t e = allow_lds(distill_held_kernel<T, GT, NV>, lds);
+  if (a.grad && rows_held(a.R, a.C, a.dtype, K > kDistillLdsK ? kRegisterBytes : kHeldBytes))
+    return held_dispatch<T>(a.C, [&](auto gt, auto nv, auto nl) {
+      constexpr int GT = decltype(gt)::value, NV = decltype(nv)::value, NL = decltype(nl)::value;
+      const size_t lds = HeldRow<T, GT, NV, true, NL>::kLdsBytes +
+                         teacher_bytes((int)K, GT) * (GT == 64 ? 4 : 1);
+      const hipError_t e = allow_lds(distill_held_kernel<T, GT, NV, NL>, lds);
       if (e != hipSuccess) return e;
-      hipLaunchKernelGGL((distill_held_kernel<T, GT, NV>), group_grid<GT>(a.R),
+      hipLaunchKernelGGL((distill_held_kernel<T, GT, NV, NL>), group_grid<GT>(a.R),
                          dim3(group_threads<GT>()), lds, s, p);
       return hipGetLastError();
     });
@@ -696,7 +702,7 @@ hipError_t distill_t(const Rows& a, const int32_t* idx, const float* val, int64_
                      mz);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const size_t lds = teacher_bytes((int)a.C, (int)K, 256);
+  const size_t lds = teacher_bytes((int)K, 256);
   if ((e = allow_lds(distill_parts_kernel<T>, lds)) != hipSuccess) return e;
   hipLaunchKernelGGL(distill_parts_kernel<T>, linear_grid(a.R * parts.n), dim3(256), lds, s, p,
                      parts, mz, look.n);

@@ -10,7 +10,7 @@
 namespace lik {
 
 constexpr int64_t kDistillMaxK = 1024;
-constexpr int64_t kDistillMaxC = int64_t(1) << 20;   // the bitmap of listed columns fits LDS
+constexpr int64_t kDistillMaxC = int64_t(1) << 20;   // a listed column has 24 bits
 // Sequences times pairs of a preference loss: every sequence looks through the
 // pairs for its own, 8.4 ms at 2^34, which atomics would save, and the order of
 // the sums with them.
@@ -65,10 +65,11 @@ constexpr int64_t kFarBytes = int64_t(128) << 20;
 // Whether rows of at most `most` bytes are held on chip, each read once, or
 // taken in parts with a second look for the gradient: too few rows leave most
 // of the chip idle unless they are short.  Rows of up to 256 KB fit 1024
-// threads' registers, up to 512 KB registers and LDS, which distillation needs
-// for its lists.
-constexpr int64_t kDistillHeldBytes = 16 * 1024 * 16;
-constexpr int64_t kPolicyHeldBytes = 32 * 1024 * 16;
+// threads' registers, up to 512 KB registers and LDS, next to a teacher's list of
+// at most kDistillLdsK entries.
+constexpr int64_t kRegisterBytes = 16 * 1024 * 16;
+constexpr int64_t kHeldBytes = 32 * 1024 * 16;
+constexpr int64_t kDistillLdsK = 700;
 inline int64_t elem_bytes_of(lik_dtype t) {
   return t == LIK_F32 ? 4 : (t == LIK_F16 || t == LIK_BF16 ? 2 : 0);
 }

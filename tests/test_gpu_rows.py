@@ -232,6 +232,39 @@ def test_distill_widest_rows(R):
             assert np.all(off <= 2.0 ** -8 * np.abs(rg[0]) + 4e-5 * np.abs(rg[0]) + 1e-12)
 
 
+@pytest.mark.parametrize("dtype,C,K", [(F32, 65537, 20), (F32, 131072, 700), (F32, 100003, 701),
+                                       (BF16, 131075, 64), (F16, 200001, 33), (BF16, 262144, 5)])
+@pytest.mark.parametrize("rest", [False, True])
+def test_distill_rows_partly_in_lds(dtype, C, K, rest):
+    """Rows of 256 to 512 KB, with lists on both sides of what fits beside them;
+    columns listed twice, in the row's first and last, and rows without a list."""
+    say(f"[rows] distill 256 x {C} K {K} rest {rest} {dtype}")
+    R = 256
+    g = torch.Generator(device="cuda").manual_seed(C)
+    z = torch.empty((R, C), device="cuda", dtype=dtype).normal_(0, 2, generator=g)
+    idx = torch.randint(0, C, (R, K), generator=g, device="cuda", dtype=torch.int32)
+    idx[:, 1], idx[:, 2], idx[:, 3], idx[:, 4] = 0, C - 1, 0, -1
+    idx[1] = -1
+    val = torch.randn((R, K), generator=g, device="cuda")
+    lse = torch.full((R,), 7.5, device="cuda") if rest else None
+    w = torch.full((R,), 0.5, device="cuda")
+    w[3] = 0
+    loss, rows, grad = _lib.lik_distill_rows(z, idx, val, lse, row_weight=w)
+    none = _lib.lik_distill_rows(z, idx, val, lse, row_weight=w, want_grad=False)
+    for r in (0, 1, 3, 100, R - 1):
+        rl, rr, rg = oracle.distill_rows(host(z[r:r + 1]), idx[r:r + 1].cpu(), val[r:r + 1].cpu(),
+                                         [7.5] if rest else None, weight=host(w[r:r + 1]))
+        # float32 sums of up to 2^18 terms, 2^8 a thread and trees: below 2^-16
+        assert abs(float(rows[r]) - rr[0]) < 2e-5 * max(1.0, abs(rr[0]))
+        assert abs(float(none[1][r]) - rr[0]) < 2e-5 * max(1.0, abs(rr[0]))
+        # w scale (M q - p_rest q / q_rest - p): what is subtracted is at most 2 w q
+        q = np.exp(host(z[r]) - oracle.logprob_rows(host(z[r:r + 1]), [0])[1])
+        half, tiny = torch.finfo(dtype).eps / 2, 2.0 ** -25 if dtype == F16 else 1e-12
+        assert np.all(np.abs(host(grad[r]) - rg[0]) <= half * np.abs(rg[0]) +
+                      4e-5 * (np.abs(rg[0]) + 2 * 0.5 * q) + tiny)
+    assert torch.equal(_lib.lik_distill_rows(z, idx, val, lse, row_weight=w)[2], grad)
+
+
 def test_distill_odd_lists():
     say("[rows] distill odd lists")
     C = 12
