@@ -107,7 +107,7 @@ size_t lik_rows_workspace_bytes(lik_rows_op op, int64_t R, int64_t C, int64_t n_
     case LIK_ROWS_LOGPROB_BWD:
       return 0;
     case LIK_ROWS_LOGPROB_FWD:
-      if (R == 0 || C == 0 || lik::look_parts(R, C, dtype).n == 1) return 0;
+      if (R == 0 || C == 0 || lik::logprob_held(R, C, dtype)) return 0;
       return lik::parts_layout(R, C, dtype).bytes;
     case LIK_ROWS_DISTILL:
     case LIK_ROWS_POLICY:

@@ -65,9 +65,11 @@ constexpr int64_t kFarBytes = int64_t(128) << 20;
 
 // Whether rows of at most `most` bytes are held on chip, each read once, or
 // taken in parts with a second look for the gradient: too few rows leave most
-// of the chip idle unless they are short.  Rows of up to 256 KB fit 1024
-// threads' registers, up to 512 KB registers and LDS, next to a teacher's list of
-// at most kDistillLdsK entries.
+// of the chip idle unless they are short (distillation with the rest's term, in
+// parts in brackets: 8 x 32000 bf16 13.5 us (16), 8 x 131072 bf16 21 (16), 64 x
+// 100003 bf16 21 (21), 192 x 131072 f32 44 (62); policy 128 x 131072 f32 34 (37)).
+// Rows of up to 256 KB fit 1024 threads' registers, up to 512 KB registers and
+// LDS, next to a teacher's list of at most kDistillLdsK entries.
 constexpr int64_t kRegisterBytes = 16 * 1024 * 16;
 constexpr int64_t kHeldBytes = 32 * 1024 * 16;
 constexpr int64_t kDistillLdsK = 700;
@@ -88,7 +90,16 @@ inline Parts grad_parts(int64_t R, int64_t C, lik_dtype dtype) {
 
 inline bool rows_held(int64_t R, int64_t C, lik_dtype dtype, int64_t most) {
   const int64_t bytes = C * elem_bytes_of(dtype);
-  return bytes <= most && (R >= 256 || bytes <= 16384);
+  return bytes <= most && (R >= 128 || bytes <= 65536);
+}
+
+// Log-probabilities in one launch: rows of one part, and rows of up to 256 KB by
+// 1024 threads while every row has a CU of its own.  bf16, in two launches in
+// brackets: 1 x 32000 9.1 us (12.3), 8 x 131072 9.2 (12.1), 256 x 65536 9.2 (13),
+// 256 x 131072 14.6 (14.5); 1024 x 131072 52 (44), 4096 x 32000 47 (43).
+inline bool logprob_held(int64_t R, int64_t C, lik_dtype dtype) {
+  return look_parts(R, C, dtype).n == 1 ||
+         (R <= 256 && C * elem_bytes_of(dtype) <= kRegisterBytes);
 }
 
 // Workspace layouts.

@@ -47,9 +47,9 @@ __device__ __forceinline__ void logprob_write(const RowSoft& s, float zt, float 
   lse[r] = (float)((double)scale * (double)s.m + ln_sum);
 }
 
-// Rows of one part: look and finish in one.
-template <typename T, int GT>
-__global__ __launch_bounds__(256) void logprob_rows_kernel(
+// Rows held whole: look and finish in one.
+template <typename T, int GT, int NV>
+__global__ __launch_bounds__(group_threads<GT>()) void logprob_rows_kernel(
     const T* __restrict__ z, int64_t R, int C, int64_t ld, float scale,
     const int32_t* __restrict__ targets, float* __restrict__ logp, float* __restrict__ lse) {
   __shared__ float tmp[2 * (GT / 64)];
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(256) void logprob_rows_kernel(
     return;
   }
   const T* row = z + r * ld;
-  HeldRow<T, GT, kLookPieces> h;
+  HeldRow<T, GT, NV> h;
   h.load(row, C, tid, nullptr);
   const float zt = t < C ? (float)row[t] : __builtin_nanf("");
   const RowSoft s = held_softmax<GT>(h, scale, tmp);
@@ -398,13 +398,23 @@ template <typename T>
 hipError_t logprob_fwd_t(const Rows& a, const int32_t* targets, float* logp, float* lse, char* ws,
                          hipStream_t s) {
   const Parts parts = look_parts(a.R, a.C, a.dtype);
+  const auto whole = [&](auto gt, auto nv) {
+    constexpr int GT = decltype(gt)::value, NV = decltype(nv)::value;
+    hipLaunchKernelGGL((logprob_rows_kernel<T, GT, NV>), group_grid<GT>(a.R),
+                       dim3(group_threads<GT>()), 0, s, (const T*)a.z, a.R, (int)a.C, a.ld, a.scale,
+                       targets, logp, lse);
+    return hipGetLastError();
+  };
   if (parts.n == 1)
     return parts_dispatch(parts, [&](auto gt) {
-      constexpr int GT = decltype(gt)::value;
-      hipLaunchKernelGGL((logprob_rows_kernel<T, GT>), group_grid<GT>(a.R), dim3(256), 0, s,
-                         (const T*)a.z, a.R, (int)a.C, a.ld, a.scale, targets, logp, lse);
-      return hipGetLastError();
+      return whole(gt, std::integral_constant<int, kLookPieces>());
     });
+  if (logprob_held(a.R, a.C, a.dtype)) {
+    const std::integral_constant<int, 1024> gt;
+    if (a.C <= HeldRow<T, 1024, 4>::kColumns) return whole(gt, std::integral_constant<int, 4>());
+    if (a.C <= HeldRow<T, 1024, 8>::kColumns) return whole(gt, std::integral_constant<int, 8>());
+    return whole(gt, std::integral_constant<int, 16>());
+  }
   float2* mz = (float2*)ws;
   hipError_t e = parts_t<T>(a, parts, true, targets, nullptr, nullptr, 0, mz, s);
   if (e != hipSuccess) return e;

@@ -116,6 +116,18 @@ def test_logprob(R, C, dtype):
     assert torch.all(buf[~written] == 7)
 
 
+@pytest.mark.parametrize("R,C,dtype", [(256, 20001, F32), (257, 20001, F32), (300, 33000, BF16),
+                                       (2, 65536, F32), (2, 65537, F32), (127, 40000, F16),
+                                       (128, 40000, F16)])
+def test_rows_held_and_in_parts(R, C, dtype):
+    # both sides of where rows are held whole
+    say(f"[rows] held or parts {R} x {C} {dtype}")
+    rng, z, t = draw(R, C, 80)
+    check_logprob(*on_gpu(z, dtype, 3, 1), t, 1.0)
+    policy_case(z, t, dtype, 0.5, 81, pad=3, shift=1)
+    distill_case(R, C, 12, True, dtype, 2.0, 82, pad=3, shift=1)
+
+
 def distill_case(R, C, K, rest, dtype, scale, seed, weight=None, idx=None, val=None, lse=None,
                  z=None, pad=0, shift=0):
     rng, zz, _ = draw(R, C, seed)
