@@ -610,8 +610,10 @@ inline hipError_t parts_dispatch(const Parts& parts, F f) {
 __device__ __forceinline__ void policy_loss(float x, float adv, float low, float high, bool with_kl,
                                             float away, float kl, float* loss, float* slope) {
   const float rho = expf(x);
-  const float u = adv == 0.0f ? 0.0f : rho * adv;
-  const float v = adv == 0.0f ? 0.0f : fminf(fmaxf(rho, 1.0f - low), 1.0f + high) * adv;
+  // without an advantage 0, also where rho overflows; a NaN stays one
+  const bool none = adv == 0.0f && rho == rho;
+  const float u = none ? 0.0f : rho * adv;
+  const float v = none ? 0.0f : fminf(fmaxf(rho, 1.0f - low), 1.0f + high) * adv;
   const bool flows = adv >= 0.0f ? rho <= 1.0f + high : rho >= 1.0f - low;
   float l = u != u ? u : -fminf(u, v);
   float g = flows || u != u ? -u : 0.0f;

@@ -1,0 +1,60 @@
+"""GPU checks of the row losses at their edges.  Helpers as in test_gpu_rows.py."""
+
+import numpy as np
+import pytest
+import torch
+
+from maxsim_scoring_02_amd import _lib
+from parity import say
+from test_gpu_rows import BF16, F16, F32, host
+
+pytestmark = pytest.mark.gpu
+
+INF, NAN = float("inf"), float("nan")
+
+
+def normal(R, C, dtype, seed):
+    """Logits [R, C] and targets [R] made on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    z = torch.empty((R, C), device="cuda", dtype=dtype).normal_(0, 2, generator=g)
+    return z, torch.randint(0, C, (R,), generator=g, device="cuda", dtype=torch.int32)
+
+
+def same(x, where):
+    return np.array_equal(host(x), where)
+
+
+# one wave, 256 threads, 1024 threads, partly in LDS, in parts, many rows in parts
+FORMS = [(9, 33, F32), (9, 9001, F16), (128, 70001, BF16), (130, 140001, BF16), (9, 70001, F32),
+         (1030, 262200, BF16)]
+
+
+@pytest.mark.parametrize("R,C,dtype", FORMS)
+@pytest.mark.parametrize("kl", [0.0, 0.1])
+def test_policy_without_advantage_keeps_nan(R, C, dtype, kl):
+    """An advantage of 0 (a group of rollouts with equal rewards) has loss 0 and no
+    gradient, but a row without a log-probability stays NaN."""
+    say(f"[rows] policy advantage 0 {R} x {C} {dtype} kl {kl}")
+    z, t = normal(R, C, dtype, 90)
+    t[1], t[5], t[6] = C, 2 ** 31 - 1, -1       # two out of range, one left out
+    z[2, C - 1] = NAN
+    z[3] = -INF
+    z[4, C // 2] = INF
+    t[7], z[7] = 2, -INF                        # left out by its weight
+    bad = np.zeros(R, dtype=bool)
+    bad[1:6] = True
+    w = torch.ones(R, device="cuda")
+    w[7] = 0.0
+    old, ref = torch.full((R,), -5.0, device="cuda"), torch.full((R,), -6.0, device="cuda")
+    old[8] = -500.0                             # a ratio that overflows: inf * 0
+    args = (z, t, old, torch.zeros(R, device="cuda"), ref)
+    loss, rows, lp, grad = _lib.lik_policy_rows(*args, kl_coef=kl, row_weight=w)
+    none = _lib.lik_policy_rows(*args, kl_coef=kl, row_weight=w, want_grad=False)
+    for l, r, p in ((loss, rows, lp), none[:3]):
+        assert torch.isnan(l).all()
+        assert same(torch.isnan(r), bad) and same(torch.isnan(p), bad)
+    assert same(torch.isnan(grad).all(1), bad) and same(torch.isnan(grad).any(1), bad)
+    if kl == 0:
+        good = torch.from_numpy(~bad).cuda()
+        assert torch.all(rows[good] == 0) and torch.all(none[1][good] == 0)
+        assert torch.all(grad[good] == 0)
