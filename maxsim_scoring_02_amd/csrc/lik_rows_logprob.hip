@@ -210,6 +210,12 @@ __device__ __forceinline__ void pair_loss(const PrefArgs& p, const double* seq, 
   }
 }
 
+// What a pair of this slope adds to a sequence that it sets first (c), second (j)
+// or against itself: then 0, or NaN where the slope is.
+__device__ __forceinline__ double pair_part(double slope, bool c, bool j) {
+  return (c ? slope : 0.0) - (j ? slope : 0.0);
+}
+
 __device__ __forceinline__ double pair_weight(const PrefArgs& p, int64_t i) {
   return p.weight ? (double)p.weight[i] : 1.0 / (double)p.P;
 }
@@ -242,11 +248,11 @@ __global__ __launch_bounds__(256) void pref_pairs_kernel(PrefArgs p, int64_t R,
   double acc = 0.0, n = 0.0;
   for (int64_t i = tid; i < p.P; i += 256) {
     const bool c = p.chosen[i] == s, j = p.rejected[i] == s;
-    if (c == j) continue;              // in neither place, or in both
+    if (!c && !j) continue;
     double l, g;
     pair_loss(p, seq, i, &l, &g);
     const double w = pair_weight(p, i);
-    if (w != 0.0) acc += c ? w * g : -w * g;
+    if (w != 0.0) acc += pair_part(w * g, c, j);
   }
   acc = block_sum(acc, tmp);
   if (p.mean) {
@@ -309,7 +315,7 @@ __global__ __launch_bounds__(1024) void pref_small_kernel(PrefArgs p, PrefRows<T
     double d = 0.0;
     for (int i = lane; i < p.P; i += 64) {
       const bool c = p.chosen[i] == s, j = p.rejected[i] == s;
-      if (c != j) d += c ? slope[i] : -slope[i];
+      if (c || j) d += pair_part(slope[i], c, j);
     }
     d = wave_sum(d) / count[s];
     for (int64_t r = lo + lane; r < hi; r += 64) a.coef[r] = p.targets[r] >= 0 ? (float)d : 0.0f;

@@ -159,12 +159,12 @@ def preference_rows(z, targets, offsets, chosen, rejected, ref=None, kind=SIGMOI
             up = np.exp(-np.logaddexp(0, h))           # sigmoid(-h)
             slope = beta * (smoothing * (1 - up) - (1 - smoothing) * up)
         elif kind == HINGE:
-            losses[i] = max(0.0, 1 - h)
-            slope = -beta if h < 1 else 0.0
+            losses[i] = 0.0 if h >= 1 else 1 - h
+            slope = -beta if h < 1 else (h if np.isnan(h) else 0.0)
         else:
             losses[i] = (d - 0.5 / beta) ** 2
             slope = 2 * (d - 0.5 / beta)
-        if w[i] != 0 and c != r:
+        if w[i] != 0 and (c != r or np.isnan(slope)):
             d_seq[c] += w[i] * slope
             d_seq[r] -= w[i] * slope
     d_row = np.zeros(R)

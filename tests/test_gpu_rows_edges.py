@@ -6,7 +6,7 @@ import torch
 
 from maxsim_scoring_02_amd import _lib
 from parity import say
-from test_gpu_rows import BF16, F16, F32, host
+from test_gpu_rows import BF16, F16, F32, f32, host, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +58,32 @@ def test_policy_without_advantage_keeps_nan(R, C, dtype, kl):
         good = torch.from_numpy(~bad).cuda()
         assert torch.all(rows[good] == 0) and torch.all(none[1][good] == 0)
         assert torch.all(grad[good] == 0)
+
+
+@pytest.mark.parametrize("kind", [_lib.LIK_PREF_SIGMOID, _lib.LIK_PREF_HINGE, _lib.LIK_PREF_SQUARE])
+@pytest.mark.parametrize("R,S", [(30, 6), (900, 300)])
+@pytest.mark.parametrize("mean", [False, True])
+def test_pair_of_a_sequence_with_itself(R, S, kind, mean):
+    """Its difference is 0, and so is its part of the gradient; with a NaN in the
+    sequence the pair's loss and the sequence's gradient are NaN."""
+    say(f"[rows] preference with itself {R} rows kind {kind} mean {mean}")
+    n = R // S
+    z, t = normal(R, 50, F32, 92)
+    off = i32(np.arange(0, R + 1, n))
+    args = dict(kind=kind, beta=0.5, mean_logp=mean)
+    one = _lib.lik_preference_rows(z, t, off, i32([1, 3]), i32([2, 3]), pair_weight=f32([1, 4]), **args)
+    ref = _lib.lik_preference_rows(z, t, off, i32([1]), i32([2]), pair_weight=f32([1]), **args)
+    assert torch.equal(one[3], ref[3]) and torch.all(one[3][3 * n:4 * n] == 0)
+    z[3 * n + 1, 7] = NAN
+    t[3 * n + 2] = -1
+    loss, pairs, seq, grad = _lib.lik_preference_rows(z, t, off, i32([1, 3]), i32([2, 3]),
+                                                      pair_weight=f32([1, 4]), **args)
+    assert torch.isnan(loss).all() and same(torch.isnan(pairs), [False, True])
+    rows = np.zeros(R, dtype=bool)
+    rows[3 * n:4 * n] = True
+    rows[3 * n + 2] = False                     # left out
+    assert same(torch.isnan(grad).all(1), rows) and same(torch.isnan(grad).any(1), rows)
+    assert torch.equal(grad[n:3 * n], ref[3][n:3 * n])
+    # without weight the pair is left out of the sum and the gradient
+    out = _lib.lik_preference_rows(z, t, off, i32([1, 3]), i32([2, 3]), pair_weight=f32([1, 0]), **args)
+    assert torch.isfinite(out[0]).all() and torch.isfinite(out[3]).all()

@@ -115,3 +115,15 @@ def test_preference_by_hand():
     assert out[0] == pytest.approx(math.log1p(math.exp(-2 * d)))
     assert oracle.preference_rows(z, [1, 0], [0, 1, 2], [0], [1], kind=oracle.rows.SQUARE,
                                   beta=2.0)[0] == pytest.approx((d - 0.25) ** 2)
+
+
+@pytest.mark.parametrize("kind", [oracle.rows.SIGMOID, oracle.rows.HINGE, oracle.rows.SQUARE])
+def test_preference_nan_reaches_its_pairs(kind):
+    # sequence 1 holds a NaN: its pairs, one of them with itself, and their sequences
+    z = _z(6, 4, 5)
+    z[1, 3] = np.nan
+    _, pairs, seq, grad, _ = oracle.preference_rows(z, [1, 2, 0, 4], [0, 1, 2, 3, 4], [1, 0, 2],
+                                                    [1, 2, 3], kind=kind)
+    assert np.array_equal(np.isnan(pairs), [True, False, False]) and np.isnan(seq[1])
+    assert np.array_equal(np.isnan(grad).all(1), [False, True, False, False])
+    assert np.isfinite(grad[[0, 2, 3]]).all()
