@@ -421,9 +421,10 @@ __device__ __forceinline__ DistillRow distill_row(const TeacherSums& x, bool wit
   d.on = d.off = k * (M / d.row.Z);
   if (with_rest && x.columns < C) {
     const float p = x.mass != x.mass ? __builtin_nanf("") : (float)fmax(0.0, 1.0 - x.mass);
-    // sum p (log p - log q) over the rest; q is 0 where no column is finite
+    // sum p (log p - log q) over the rest; q is 0 where no column is finite, and
+    // ln_sum NaN where none of the whole row is
     if (p != 0.0f)
-      l += (double)p * ((double)logf(p) - (s.Z == 0.0f ? -(double)kInf
+      l += (double)p * ((double)logf(p) - (s.Z == 0.0f ? -(double)kInf - ln_sum
                                                        : row_logp(d.row, s.m, scale, ln_sum) +
                                                              row_ln_sum(s)));
     const float all = (float)(x.mass + (double)p);

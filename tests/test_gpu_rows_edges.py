@@ -87,3 +87,33 @@ def test_pair_of_a_sequence_with_itself(R, S, kind, mean):
     # without weight the pair is left out of the sum and the gradient
     out = _lib.lik_preference_rows(z, t, off, i32([1, 3]), i32([2, 3]), pair_weight=f32([1, 0]), **args)
     assert torch.isfinite(out[0]).all() and torch.isfinite(out[3]).all()
+
+
+@pytest.mark.parametrize("R,C,dtype", FORMS[:5])
+def test_distill_rows_all_masked_without_listed_mass(R, C, dtype):
+    """A row all of -inf has no softmax: NaN, with only the rest's term to it too
+    (no entry listed, or entries without mass)."""
+    say(f"[rows] distill all masked {R} x {C} {dtype}")
+    z, t = normal(R, C, dtype, 94)
+    z[1:4] = -INF
+    idx = torch.stack([t, (t + 1) % C], 1).int()
+    val = torch.zeros((R, 2), device="cuda")
+    idx[1] = -1
+    val[2] = -INF
+    idx[4] = -1
+    val[5] = -INF
+    lse = torch.full((R,), 3.0, device="cuda")
+    loss, rows, grad = _lib.lik_distill_rows(z, idx, val, lse)
+    none = _lib.lik_distill_rows(z, idx, val, lse, want_grad=False)
+    bad = np.isin(np.arange(R), [1, 2, 3])
+    for l, r in ((loss, rows), none[:2]):
+        assert torch.isnan(l).all() and same(torch.isnan(r), bad)
+        assert torch.isfinite(r[torch.from_numpy(~bad).cuda()]).all()
+    assert same(torch.isnan(grad).all(1), bad) and same(torch.isnan(grad).any(1), bad)
+    # a student that rules out all that is not listed still has an infinite loss
+    z, t = normal(R, C, dtype, 95)
+    z[0] = -INF
+    z[0, :2] = 1.0
+    idx = i32(np.tile([0, 1], (R, 1)))
+    rows = _lib.lik_distill_rows(z, idx, val.zero_(), lse)[1]
+    assert rows[0] == INF and torch.isfinite(rows[1:]).all()
