@@ -145,7 +145,8 @@ lik_status lik_distill_rows(const void* logits, lik_dtype dtype, int64_t R,
  * Clipped policy loss.  With rho = exp(logp - old_logp) and A = advantage,
  *   l_r = -min(rho A, clamp(rho, 1 - clip_low, 1 + clip_high) A)
  *         + kl_coef (exp(ref_logp - logp) - (ref_logp - logp) - 1),
- * the second term only with ref_logp (NULL: none) and a kl_coef other than 0.
+ * the second term only with ref_logp (NULL: none) and a kl_coef other than 0;
+ * it is infinite where either of the two rules the target out.
  * old_logp, advantage and ref_logp are float32 [R], constants of the gradient;
  * a row at the border of its clip still has the gradient of rho A.  0 <= clip_low <= 1,
  * clip_high >= 0 (infinity: no clip on that side), kl_coef finite.

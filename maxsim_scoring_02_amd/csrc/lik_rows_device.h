@@ -619,11 +619,11 @@ __device__ __forceinline__ void policy_loss(float x, float adv, float low, float
   float g = flows || u != u ? -u : 0.0f;
   if (with_kl) {
     const float em1 = expm1f(away);
-    // exp(d) - d - 1 cancels near 0: its series there
+    // exp(d) - d - 1 cancels near 0: its series there.  Infinite at both ends (not inf - inf).
     const float d = away;
     const float series = d * d * (0.5f + d * (1.0f / 6 + d * (1.0f / 24 + d * (1.0f / 120 +
                          d * (1.0f / 720 + d * (1.0f / 5040 + d * (1.0f / 40320)))))));
-    l += kl * (fabsf(d) < 0.5f ? series : em1 - d);
+    l += kl * (fabsf(d) < 0.5f ? series : em1 < kInf ? em1 - d : em1);
     g -= kl * em1;
   }
   *loss = l;

@@ -117,3 +117,25 @@ def test_distill_rows_all_masked_without_listed_mass(R, C, dtype):
     idx = i32(np.tile([0, 1], (R, 1)))
     rows = _lib.lik_distill_rows(z, idx, val.zero_(), lse)[1]
     assert rows[0] == INF and torch.isfinite(rows[1:]).all()
+
+
+@pytest.mark.parametrize("R,C,dtype", FORMS[:5])
+def test_policy_kl_of_an_impossible_token(R, C, dtype):
+    """exp(d) - d - 1 for a target that the student (d = inf) or the reference
+    (d = -inf) rules out is infinite, not undefined."""
+    say(f"[rows] policy KL of impossible tokens {R} x {C} {dtype}")
+    z, t = normal(R, C, dtype, 93)
+    z[2, int(t[2])] = -INF
+    ref = torch.full((R,), -6.0, device="cuda")
+    ref[3] = -INF
+    old, adv = torch.full((R,), -5.0, device="cuda"), torch.ones(R, device="cuda")
+    for kl in (0.1, -0.1):
+        loss, rows, lp, grad = _lib.lik_policy_rows(z, t, old, adv, ref, kl_coef=kl)
+        none = _lib.lik_policy_rows(z, t, old, adv, ref, kl_coef=kl, want_grad=False)
+        assert lp[2] == -INF
+        for l, r in ((loss, rows), none[:2]):
+            assert l[0] == INF * kl
+            assert same(torch.isinf(r), np.isin(np.arange(R), [2, 3]))
+            assert r[2] == INF * kl and r[3] == INF * kl
+        keep = [r for r in range(R) if r != 2]
+        assert torch.isfinite(grad[keep]).all() and not torch.isfinite(grad[2, int(t[2])])
