@@ -228,9 +228,6 @@ struct TeacherList {
 constexpr int32_t kAgain = 1 << 24;
 static_assert(kDistillMaxC < kAgain, "a column and its mark share a word");
 
-__host__ __device__ inline size_t teacher_bytes(int K, int threads) {
-  return ((size_t)K * 16 + 4 + threads * 4 + 15) / 16 * 16;
-}
 __device__ __forceinline__ TeacherList teacher_at(char* p, int K) {
   TeacherList L;
   L.col = (int32_t*)p;
@@ -626,13 +623,13 @@ hipError_t held_dispatch(int64_t C, F f) {
   return hipErrorInvalidValue;
 }
 
-// More LDS than a kernel has by default has to be asked for; asking again costs
-// little beside so large a row.
+// Allows a kernel `most` bytes of LDS where this call's are more than it has by
+// default; asking again costs little beside so large a row.
 template <typename K>
-hipError_t allow_lds(K kernel, size_t bytes) {
-  if (bytes <= 65536) return hipSuccess;
+hipError_t allow_lds(K kernel, size_t bytes, size_t most) {
+  if (bytes <= kDefaultLds) return hipSuccess;
   return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)most);
 }
 
 hipError_t weighted_sum(const float* l, const float* w, int64_t R, float* loss, hipStream_t s) {
@@ -650,7 +647,7 @@ hipError_t policy_t(const Rows& a, const int32_t* targets, const float* old_logp
     const hipError_t e = held_dispatch<T>(a.C, [&](auto gt, auto nv, auto nl) {
       constexpr int GT = decltype(gt)::value, NV = decltype(nv)::value, NL = decltype(nl)::value;
       constexpr size_t lds = HeldRow<T, GT, NV, true, NL>::kLdsBytes;
-      const hipError_t e = allow_lds(policy_held_kernel<T, GT, NV, NL>, lds);
+      const hipError_t e = allow_lds(policy_held_kernel<T, GT, NV, NL>, lds, lds);
       if (e != hipSuccess) return e;
       hipLaunchKernelGGL((policy_held_kernel<T, GT, NV, NL>), group_grid<GT>(a.R),
                          dim3(group_threads<GT>()), lds, s, p);
@@ -689,9 +686,10 @@ hipError_t distill_t(const Rows& a, const int32_t* idx, const float* val, int64_
   if (a.grad && rows_held(a.R, a.C, a.dtype, K > kDistillLdsK ? kRegisterBytes : kHeldBytes))
     return held_dispatch<T>(a.C, [&](auto gt, auto nv, auto nl) {
       constexpr int GT = decltype(gt)::value, NV = decltype(nv)::value, NL = decltype(nl)::value;
-      const size_t lds = HeldRow<T, GT, NV, true, NL>::kLdsBytes +
-                         teacher_bytes((int)K, GT) * (GT == 64 ? 4 : 1);
-      const hipError_t e = allow_lds(distill_held_kernel<T, GT, NV, NL>, lds);
+      static_assert(HeldRow<T, GT, NV, true, NL>::kLdsBytes == NL * GT * 16, "distill_lds");
+      const size_t lds = distill_lds(K, GT, NL);
+      const hipError_t e =
+          allow_lds(distill_held_kernel<T, GT, NV, NL>, lds, distill_lds_most(GT, NL));
       if (e != hipSuccess) return e;
       hipLaunchKernelGGL((distill_held_kernel<T, GT, NV, NL>), group_grid<GT>(a.R),
                          dim3(group_threads<GT>()), lds, s, p);
@@ -702,12 +700,11 @@ hipError_t distill_t(const Rows& a, const int32_t* idx, const float* val, int64_
   float2* mz = (float2*)ws;
   hipLaunchKernelGGL(distill_stats_kernel<T>, linear_grid(a.R * look.n), dim3(256), 0, s, p, look,
                      mz);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const size_t lds = teacher_bytes((int)K, 256);
-  if ((e = allow_lds(distill_parts_kernel<T>, lds)) != hipSuccess) return e;
-  hipLaunchKernelGGL(distill_parts_kernel<T>, linear_grid(a.R * parts.n), dim3(256), lds, s, p,
-                     parts, mz, look.n);
+  static_assert(teacher_bytes(kDistillMaxK, 256) <= kDefaultLds, "never has to be allowed");
+  hipLaunchKernelGGL(distill_parts_kernel<T>, linear_grid(a.R * parts.n), dim3(256),
+                     teacher_bytes(K, 256), s, p, parts, mz, look.n);
   return hipGetLastError();
 }
 

@@ -73,6 +73,25 @@ constexpr int64_t kFarBytes = int64_t(128) << 20;
 constexpr int64_t kRegisterBytes = 16 * 1024 * 16;
 constexpr int64_t kHeldBytes = 32 * 1024 * 16;
 constexpr int64_t kDistillLdsK = 700;
+
+// LDS of a teacher's list of K entries for a group of `threads` (TeacherList), and
+// of a held distillation kernel: `held` 16-byte pieces a thread and the lists of a
+// workgroup's groups (four of one wave).
+constexpr size_t teacher_bytes(int64_t K, int threads) {
+  return ((size_t)K * 16 + 4 + (size_t)threads * 4 + 15) / 16 * 16;
+}
+constexpr size_t distill_lds(int64_t K, int threads, int held) {
+  return (size_t)held * threads * 16 + teacher_bytes(K, threads) * (threads == 64 ? 4 : 1);
+}
+// Beyond kDefaultLds a kernel has to be allowed its LDS, an attribute that it has
+// once for all host threads.  So each call sets the most that any call of that
+// kernel takes: less would bind another thread's call between its setting and its
+// launch.
+constexpr size_t kDefaultLds = 65536;
+constexpr size_t distill_lds_most(int threads, int held) {
+  return distill_lds(held ? kDistillLdsK : kDistillMaxK, threads, held);
+}
+
 inline int64_t elem_bytes_of(lik_dtype t) {
   return t == LIK_F32 ? 4 : (t == LIK_F16 || t == LIK_BF16 ? 2 : 0);
 }

@@ -1,5 +1,7 @@
 """GPU checks of the row losses at their edges.  Helpers as in test_gpu_rows.py."""
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -139,3 +141,39 @@ def test_policy_kl_of_an_impossible_token(R, C, dtype):
             assert r[2] == INF * kl and r[3] == INF * kl
         keep = [r for r in range(R) if r != 2]
         assert torch.isfinite(grad[keep]).all() and not torch.isfinite(grad[2, int(t[2])])
+
+
+def test_host_threads_with_lists_of_several_lengths():
+    """Calls from several host threads at once, each on a stream of its own, whose
+    kernels are the same and whose lists need different amounts of LDS beyond the
+    default: every call succeeds, with the results of the calls one by one."""
+    say("[rows] host threads")
+    made = []
+    for R, C, dtype, K in ((256, 900, F32, 1024), (256, 900, F32, 1000), (256, 900, F32, 5),
+                           (256, 70001, F32, 700), (256, 70001, F32, 650), (256, 70001, F32, 3)):
+        z, t = normal(R, C, dtype, 91 + K)
+        idx = torch.randint(0, C, (R, K), device="cuda", dtype=torch.int32)
+        made.append((z, idx, torch.randn((R, K), device="cuda"),
+                     torch.full((R,), 9.0, device="cuda")))
+    want = [_lib.lik_distill_rows(*m) for m in made]
+    torch.cuda.synchronize()
+    got, errors = [[] for _ in made], []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(40):
+                    got[i] = _lib.lik_distill_rows(*made[i])
+            s.synchronize()
+        except Exception as e:                # reported below, by the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(made))]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert not errors, errors
+    for g, w in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(g, w))
