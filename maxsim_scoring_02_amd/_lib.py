@@ -424,8 +424,13 @@ def _rows_workspace_bytes(op: int, R: int, C: int, S: int, dt: int, flags: int) 
     return lib().lik_rows_workspace_bytes(op, R, C, S, dt, flags)
 
 
+_NO_SIZE = ctypes.c_size_t(-1).value
+
+
 def _rows_workspace(op: int, R: int, C: int, S: int, dt: int, grad, device) -> Tuple:
     n = _rows_workspace_bytes(op, R, C, S, dt, 0 if grad is None else 1)
+    if n == _NO_SIZE:                    # sizes that the call itself refuses
+        n = 0
     return _workspace(n, device), n
 
 

@@ -177,3 +177,24 @@ def test_host_threads_with_lists_of_several_lengths():
     assert not errors, errors
     for g, w in zip(got, want):
         assert all(torch.equal(x, y) for x, y in zip(g, w))
+
+
+def test_sizes_beyond_the_library_are_refused_by_it():
+    """2^31 columns or rows: the library's status and message, not an allocation
+    of a workspace that has no size."""
+    say("[rows] sizes beyond the library")
+    for shape in ((1, 2 ** 31), (2 ** 31, 1)):
+        z = torch.empty(shape, dtype=F16, device="cuda")
+        R = shape[0]
+        t = torch.empty(1, dtype=torch.int32, device="cuda").expand(R) if R == 1 else \
+            torch.empty(R, dtype=torch.int32, device="cuda")
+        f = torch.empty(R, dtype=F32, device="cuda")
+        off, one = i32([0, 1]), i32([0])
+        for call in (lambda: _lib.lik_logprob_rows_fwd(z, t),
+                     lambda: _lib.lik_policy_rows(z, t, f, f, want_grad=False),
+                     lambda: _lib.lik_distill_rows(z, t[:, None], f[:, None], want_grad=False),
+                     lambda: _lib.lik_preference_rows(z, t, off, one, one, want_grad=False)):
+            with pytest.raises(_lib.LikError, match="below 2\\^31") as e:
+                call()
+            assert e.value.status == _lib.LIK_ERR_UNSUPPORTED
+        del z, t, f

@@ -219,3 +219,16 @@ def test_preference_sequences_times_pairs(L, S, P, fine):
     st = call(L, "lik_preference_rows", S=S, P=P, wsb=1 << 40)
     assert st == LIK_ERR_UNSUPPORTED
     assert ("device" if fine else "S x P") in L.lik_last_error().decode()
+
+
+@pytest.mark.parametrize("name,op,kw", [
+    ("lik_logprob_rows_fwd", _lib.LIK_ROWS_LOGPROB_FWD, {}),
+    ("lik_distill_rows", _lib.LIK_ROWS_DISTILL, dict(grad=None)),
+    ("lik_policy_rows", _lib.LIK_ROWS_POLICY, dict(grad=None)),
+    ("lik_preference_rows", _lib.LIK_ROWS_PREFERENCE, dict(grad=None))])
+@pytest.mark.parametrize("R,C", [(1, 1 << 31), (1 << 31, 1)])
+def test_sizes_without_a_workspace_are_left_to_the_library(L, name, op, kw, R, C):
+    # the binding makes none and the library says what it does not support
+    assert _lib._rows_workspace(op, R, C, 2, LIK_F16, None, torch.device("cpu")) == (None, 0)
+    assert call(L, name, R=R, C=C, ld=C, dtype=LIK_F16, ws=None, wsb=0, **kw) == LIK_ERR_UNSUPPORTED
+    assert "below 2^31" in L.lik_last_error().decode()
