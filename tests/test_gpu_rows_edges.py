@@ -1,4 +1,8 @@
-"""GPU checks of the row losses at their edges.  Helpers as in test_gpu_rows.py."""
+"""GPU checks of the row losses at their edges: rows without a log-probability,
+pairs of a sequence with itself, calls from several host threads, sizes beyond
+the library's, sums within the terms of a thread, and gradients of 16-bit logits
+against differences.  Helpers and bounds as in test_gpu_rows.py and
+rows_bounds.py."""
 
 import threading
 
@@ -6,9 +10,11 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 from maxsim_scoring_02_amd import _lib
 from parity import say
-from test_gpu_rows import BF16, F16, F32, f32, host, i32
+from rows_bounds import U, logp_bound, rounded, row_bounds
+from test_gpu_rows import BF16, F16, F32, distill_case, f32, host, i32, on_gpu, policy_case, within
 
 pytestmark = pytest.mark.gpu
 
@@ -198,3 +204,113 @@ def test_sizes_beyond_the_library_are_refused_by_it():
                 call()
             assert e.value.status == _lib.LIK_ERR_UNSUPPORTED
         del z, t, f
+
+
+def sum_bound(held, scale):
+    """Error of ln Z as in rows_bounds, with what a kernel's thread sums at most:
+    32 pieces of 8 columns, then trees over lanes, waves and parts whose factors
+    are good to 4 U each, three of them."""
+    q, _, _, _ = row_bounds(held, scale)
+    y = np.asarray(held, dtype=np.float64) * scale
+    x = np.minimum(y.max(1, keepdims=True) - y, 200.0)
+    return U * (2 * (q * x).sum(1) + 4 + min(held.shape[1] / 64, 256) + 18 + 12)
+
+
+# rows of an odd stride, so that they start at every alignment
+LONG = [(130, 520, F32), (6, 9001, BF16), (128, 33001, F16), (128, 131007, BF16), (3, 140001, F16),
+        (128, 100003, F32), (128, 200003, BF16), (2, 300007, F32)]
+
+
+@pytest.mark.parametrize("R,C,dtype", LONG)
+def test_row_sums_within_the_terms_of_a_thread(R, C, dtype):
+    say(f"[rows] sums {R} x {C} {dtype}")
+    rng = np.random.default_rng(R + C)
+    dev, held = on_gpu((rng.standard_normal((R, C)) * 2).astype(np.float32), dtype, 3 + C % 2, 1)
+    t = rng.integers(0, C, R)
+    rl, rs = oracle.logprob_rows(held, t)
+    tol = sum_bound(held, 1.0)
+    logp, lse = _lib.lik_logprob_rows_fwd(dev, i32(t))
+    within(host(logp), rl, logp_bound(rl, tol, np.abs(rl)), "logp")
+    within(host(lse), rs, tol + 2 * U * np.abs(rs), "lse")
+    zero = f32(np.zeros(R))
+    for want in (True, False):
+        lp = _lib.lik_policy_rows(dev, i32(t), zero, zero, want_grad=want)[2]
+        within(host(lp), rl, logp_bound(rl, tol, np.abs(rl)), "policy logp")
+    seq = _lib.lik_preference_rows(dev, i32(t), i32(np.arange(R + 1)), i32([0]), i32([1]))[2]
+    within(host(seq), rl, logp_bound(rl, tol, np.abs(rl)), "preference logp")
+
+
+@pytest.mark.parametrize("R,C,dtype", LONG)
+def test_mass_in_the_first_and_last_columns(R, C, dtype):
+    """Nearly all of a row's probability in the few columns before its first and
+    behind its last aligned piece: one of them left out would change every sum."""
+    say(f"[rows] edges {R} x {C} {dtype}")
+    rng = np.random.default_rng(C)
+    at = dict(pad=3 + C % 2, shift=1)
+    z = np.full((R, C), -25.0, dtype=np.float32)
+    edge = np.r_[0:8, C - 8:C]
+    z[:, edge] = rng.uniform(-0.5, 0.5, (R, 16))
+    t = edge[np.arange(R) % 16]
+    t[R // 2] = C // 2
+    dev, held = on_gpu(z, dtype, **at)
+    rl, rs = oracle.logprob_rows(held, t)
+    tol = sum_bound(held, 1.0)
+    logp, lse = _lib.lik_logprob_rows_fwd(dev, i32(t))
+    within(host(logp), rl, logp_bound(rl, tol, np.abs(rl)), "logp")
+    within(host(lse), rs, tol + 2 * U * np.abs(rs), "lse")
+    policy_case(z, t, dtype, 1.0, 96, **at)
+    idx = np.stack([np.r_[edge[rng.permutation(16)[:5]], C // 3] for _ in range(R)])
+    val = rng.standard_normal((R, 6)).astype(np.float32)
+    for lse in (None, np.full(R, 4.0, dtype=np.float32)):
+        distill_case(R, C, 6, lse is not None, dtype, 1.0, 97, idx=idx, val=val, lse=lse, z=z,
+                     **at)
+
+
+@pytest.mark.parametrize("op", ["logprob", "distill", "policy", "preference"])
+@pytest.mark.parametrize("R,C,dtype", [(7, 100, F16), (7, 100, BF16), (40, 9001, BF16), (12, 20001, F16),
+                                       (3, 131072, BF16), (130, 33001, F16)])
+def test_gradient_of_16_bit_logits_against_differences(op, R, C, dtype):
+    """The gradient of 16-bit logits along a direction against central differences
+    of the loss of the same kernel.  Logits of at most 8 on a grid of 2 h, so that
+    they and both steps are held exactly (h = 2^-4 takes 8 bits, 2^-6 takes 10).
+    Off by the two losses' rounding over the step, by h^2 / 6 of a third derivative
+    (along +-1 at most 2 of a log-softmax, 16 of a ratio, 17 of a pair of four rows:
+    below 32 a row), and by half a step of every gradient entry."""
+    say(f"[rows] differences {op} {R} x {C} {dtype}")
+    h = 2.0 ** -4 if dtype == BF16 else 2.0 ** -6
+    rng = np.random.default_rng(98)
+    z = rng.standard_normal((R, C)).astype(np.float32) * 2
+    t = rng.integers(0, C, R)
+    z[np.arange(R), t] += 2
+    z = np.clip(np.round(z / (2 * h)) * 2 * h, -8 + 2 * h, 8 - 2 * h)
+    v = rng.choice([-1.0, 1.0], size=(R, C))
+    old = oracle.logprob_rows(z, t)[0] - 0.1
+    idx = rng.integers(0, C, size=(R, 4))
+    val = rng.standard_normal((R, 4))
+    one = f32(np.ones(R))
+
+    def run(x, grad):
+        dev, held = on_gpu(x.astype(np.float32), dtype)
+        assert np.array_equal(held, x)
+        if op == "logprob":
+            lp, lse = _lib.lik_logprob_rows_fwd(dev, i32(t))
+            return host(lp).sum(), _lib.lik_logprob_rows_bwd(dev, i32(t), lse, one) if grad else None
+        if op == "distill":
+            _, rows, g = _lib.lik_distill_rows(dev, i32(idx), f32(val), f32(np.full(R, 3.0)),
+                                               row_weight=one, want_grad=grad)
+            return host(rows).sum(), g
+        if op == "policy":
+            _, rows, _, g = _lib.lik_policy_rows(dev, i32(t), f32(old), one, clip_high=9.0, clip_low=1.0,
+                                                 row_weight=one, want_grad=grad)
+            return host(rows).sum(), g
+        _, pairs, _, g = _lib.lik_preference_rows(dev, i32(t), i32([0, 1, min(R, 4)]), i32([0]),
+                                                  i32([1]), beta=0.5, want_grad=grad)
+        return host(pairs).sum(), g
+
+    g = host(run(z, True)[1])
+    up, down = run(z + h * v, False)[0], run(z - h * v, False)[0]
+    size = R * (8 + np.log(C) + 1)
+    tol = 2 * (20 + C / 64) * U * size / (2 * h) + h * h / 6 * R * 32
+    tol += 1.02 * rounded(g, 0.0, dtype).sum()
+    along = float(np.sum(g * v))
+    assert abs((up - down) / (2 * h) - along) <= tol, (along, (up - down) / (2 * h), tol)
