@@ -31,8 +31,9 @@
  *   (grad_ld >= C), each entry rounded once from float32; the logits' own
  *   type because it is what the backward of whatever made the logits takes,
  *   and half the traffic for 16-bit logits.  Columns from C to the stride are
- *   left as they were.  It must not overlap the logits.  NULL skips it (the
- *   losses alone then read the logits once).
+ *   left as they were.  From its first to its last element it must lie outside
+ *   the memory from the logits' first to their last (other columns of one matrix
+ *   are refused too).  NULL skips it (the losses alone then read the logits once).
  * scale.  The logit multiplier (1 / temperature), within [2^-64, 2^64].
  * Targets.  int32 columns.  A negative target leaves the row out: its logits
  *   are not read, its outputs and its gradient row are 0.  A target >= C makes
@@ -85,7 +86,8 @@ size_t lik_rows_workspace_bytes(lik_rows_op op, int64_t R, int64_t C,
 /*
  * logp[r] = y[r, t_r] - lse[r] and lse[r], float32.  Both 0 for rows left out;
  * for a target >= C logp is NaN and lse is the row's.  (lse is a float32: the
- * backward's probabilities are off by its rounding, 2^-24 |lse| relative.)
+ * backward's probabilities are off by its rounding, 2^-24 |lse| relative, and
+ * undefined where it overflows.)
  */
 lik_status lik_logprob_rows_fwd(const void* logits, lik_dtype dtype, int64_t R,
                                 int64_t C, int64_t ld, const int32_t* targets,

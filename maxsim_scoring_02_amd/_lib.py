@@ -545,7 +545,8 @@ def lik_preference_rows(logits, targets, seq_offsets, chosen, rejected, ref_logp
     seq_offsets[s] .. seq_offsets[s + 1] - 1, pair p sets sequence chosen[p]
     against rejected[p]; ref_logp [S] or None.  pair_weight [P], None = 1 / P.
     Returns (loss [1], pair_loss [P], seq_logp [S], grad [R, C] in the logits'
-    type or None)."""
+    type or None).  Without any row (R == 0) nothing is computed: every output is
+    0, the losses of pairs of empty sequences too."""
     dt, R, C, ld = _rows(logits)
     dev = logits.device
     if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 1 or chosen.dim() != 1:

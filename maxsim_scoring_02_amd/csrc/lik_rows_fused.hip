@@ -319,9 +319,8 @@ __device__ __forceinline__ int teacher_fill(const DistillArgs<T>& a, const Teach
 }
 
 // What the list adds up to.  One wave goes over it (every wave doing so for
-// itself, without LDS between them: 4096 x 65536 bf16 with 64 entries a row
-// 231 us against 226, 4096 x 131072 508 against 500): first, while the row is
-// on its way, the teacher's side ...
+// itself, without LDS between them, cost 2% of 4096 rows of 65536 and 131072 bf16
+// with 64 entries): first, while the row is on its way, the teacher's side ...
 struct TeacherSums {
   double mass;        // teacher probability of the list
   double terms;       // sum p (log p - scale (z - base))
@@ -452,11 +451,11 @@ __device__ __forceinline__ void teacher_grads(const TeacherList& L, const Teache
   }
 }
 
-// Rows held on chip.  4096 x 65536 bf16 with 64 entries a row and the rest's
-// term: 205 to 218 us, 4.9 to 5.2 TB/s, 10% behind the policy loss on the same
-// rows: the list costs meetings and LDS passes in a row's life, and the listed
-// columns' second stores 2%.  4096 x 131072 f32, partly in LDS, 925 us, 4.6 TB/s
-// (in parts 1675).
+// Rows held on chip.  4096 x 65536 bf16 with 64 entries a row and the rest's term:
+// 208 to 220 us, 4.9 to 5.2 TB/s, a call 221 us (without the rest 219), 11% behind
+// the policy loss on the same rows (198): the list costs meetings and LDS passes in
+// a row's life, and the listed columns' second stores 2%.  4096 x 131072 f32, partly
+// in LDS, 930 us a call, 4.6 TB/s (in parts 1675).
 template <typename T, int GT, int NV, int NL>
 __global__ __launch_bounds__(group_threads<GT>()) __attribute__((amdgpu_waves_per_eu(held_waves(NV, kDistillWaves))))
 void distill_held_kernel(const DistillArgs<T> a) {
@@ -515,7 +514,10 @@ void distill_held_kernel(const DistillArgs<T> a) {
 }
 
 // Rows in parts, the first look: each part's (m, Z), listed columns left out
-// where the rest has a term of its own.
+// where the rest has a term of its own.  256 threads a part however short the row
+// and loads through the caches, also where no gradient follows: without one
+// 65536 x 300 f32 (16 entries) takes 244 us, with it, held, 90; 4096 x 100003 bf16
+// 157 us, the same rows' log-probabilities 111.
 template <typename T>
 __global__ __launch_bounds__(256) void distill_stats_kernel(const DistillArgs<T> a, Parts parts,
                                                             float2* __restrict__ mz) {
@@ -599,12 +601,13 @@ __global__ __launch_bounds__(256) void distill_parts_kernel(const DistillArgs<T>
 }
 
 // Calls f with the group size, the pieces per thread in registers and those in
-// LDS that hold C columns.  The policy loss hardly tells group sizes apart;
-// distillation, with more to do for a row, has its 8 KB rows done by one wave
-// each in 77 us where 256 threads take 96 (16384 x 4096 bf16), 16 KB rows by 256
-// in 67 where one wave takes 75 (8192 x 8192), 64 KB rows by 512 in 103 where 256
-// take 107 (4096 x 32768), and 128 KB rows by 512 in 235 where 256 take 241 and
-// 1024 some 300 (4096 x 65536).
+// LDS that hold C columns.  bf16, us a call of the policy loss / of distillation with
+// 64 entries a row / and with the rest's term:
+//   16384 x 4096    one wave 56 / 77 / 78, 256 threads 56 / 93 / 103
+//   8192 x 8192     one wave 53 / 69 / 73, 256 threads 51 / 64 / 70
+//   4096 x 32768    256 threads 93 / 102 / 106, 512 threads 90 / 100 / 102
+//   4096 x 65536    256 threads 253 / 338 / 346, 512 threads 198 / 219 / 221,
+//                   1024 threads 200 / 269 / 288
 template <typename T, typename F>
 hipError_t held_dispatch(int64_t C, F f) {
 #define LIK_HELD(GT, NV, NL)                                                     \

@@ -10,7 +10,8 @@
 namespace lik {
 
 constexpr int64_t kDistillMaxK = 1024;
-constexpr int64_t kDistillMaxC = int64_t(1) << 20;   // a listed column has 24 bits
+// The widest rows that are tested; a listed column's word would hold 2^24 of them.
+constexpr int64_t kDistillMaxC = int64_t(1) << 20;
 // Sequences times pairs of a preference loss: every sequence looks through the
 // pairs for its own, 8.4 ms at 2^34, which atomics would save, and the order of
 // the sums with them.

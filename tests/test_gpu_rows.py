@@ -222,7 +222,7 @@ def test_distill_list_lengths(R, C, K, rest):
 
 @pytest.mark.parametrize("R", [2, 256])
 def test_distill_widest_rows(R):
-    # 2^20 columns: the bitmap of listed columns takes most of LDS
+    # 2^20 columns, the most that are taken
     say(f"[rows] distill widest {R}")
     C, K = 1 << 20, 1000
     g = torch.Generator(device="cuda").manual_seed(4)
