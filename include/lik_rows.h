@@ -1,6 +1,7 @@
 /*
  * lik_rows.h -- C ABI of the losses over rows of logits (gfx950), beside the
- * row cross-entropy of lik.h (lik_ce_rows).
+ * row cross-entropy of lik.h (lik_ce_rows), and of the verification of drafted
+ * tokens, which makes the tokens and log-probabilities that they train on.
  *
  * A row is R x C logits z: the scores of one query against C documents (a
  * MaxSim forward's [Nq, Nd] or [B, N] output), or a language model's logits
@@ -18,6 +19,8 @@
  *                              gradient
  *   lik_preference_rows        loss on paired log ratios of whole sequences
  *                              of rows, with its gradient
+ *   lik_verify_rows            drafted tokens accepted or turned down, and a
+ *                              token drawn behind the last accepted one
  *
  * The conventions of lik.h hold (memory, stream, workspace, errors,
  * determinism, reentrancy), and for every operator here:
@@ -63,7 +66,8 @@ typedef enum {
   LIK_ROWS_LOGPROB_BWD = 1,
   LIK_ROWS_DISTILL = 2,
   LIK_ROWS_POLICY = 3,
-  LIK_ROWS_PREFERENCE = 4
+  LIK_ROWS_PREFERENCE = 4,
+  LIK_ROWS_VERIFY = 5
 } lik_rows_op;
 
 /* The loss on a pair's log ratio (lik_preference_rows). */
@@ -75,9 +79,10 @@ typedef enum {
 
 /*
  * Workspace bytes of one call: the same R, C and dtype; n_seqs the number of
- * sequences S (lik_preference_rows; ignored otherwise); flags bit 0: a
- * gradient will be asked for (a call that differs may need more and then
- * returns LIK_ERR_INVALID_ARG).  Returns 0 for calls that need none and for
+ * sequences S (lik_preference_rows and lik_verify_rows; ignored otherwise);
+ * flags bit 0: a gradient will be asked for (lik_verify_rows: draft logits will
+ * be given); a call that differs may need more and then returns
+ * LIK_ERR_INVALID_ARG.  Returns 0 for calls that need none and for
  * zero-sized ones; SIZE_MAX for sizes that overflow or an unknown op or dtype.
  */
 size_t lik_rows_workspace_bytes(lik_rows_op op, int64_t R, int64_t C,
@@ -198,6 +203,50 @@ lik_status lik_preference_rows(const void* logits, lik_dtype dtype, int64_t R,
                                float* seq_logp, float* loss, void* grad,
                                int64_t grad_ld, void* workspace,
                                size_t workspace_bytes, void* stream);
+
+/*
+ * Verification of drafted tokens against the probabilities of a target model,
+ * from given random numbers, so that what is emitted is distributed as the
+ * target's own samples.  The rows are the steps of S sequences: sequence s is
+ * rows seq_offsets[s] .. seq_offsets[s+1] - 1 (int32 [S + 1], on the device, not
+ * decreasing, within [0, R]), row r holds the target's logits for the token that
+ * draft_tokens[r] proposes, and the row behind the last draft those for one
+ * token more.  With p = softmax(scale * logits) and q = softmax(draft_scale *
+ * draft_logits) of a row, its draft x is accepted where
+ *   accept_u[r] * q_x < p_x,
+ * and at the first row of a sequence that does not accept (the last one never
+ * does: its draft is not looked at, nor one that is negative, where drafts end
+ * early) a token is drawn by sample_u[s]: the lowest column c with
+ *   sum_{j <= c} w_j > sample_u[s] * sum_j w_j,
+ *   w = max(0, p - q)   where a draft was turned down,
+ *   w = p               behind the last draft, and where rounding leaves no
+ *                       p - q above 0.
+ * draft_logits [R, C] in the logits' type, with a row stride of its own
+ * (draft_ld >= C); the rows of a sequence's last steps and of negative drafts are
+ * not read.  NULL: the drafts were not drawn (copied from the prompt), q_x = 1
+ * and q = 0 elsewhere.  draft_scale within [2^-64, 2^64] (1 with NULL).
+ * accept_u [R] and sample_u [S]: float32 within [0, 1).  A NaN in accept_u does
+ * not accept; a NaN in sample_u draws the token -1; a sample_u of 1 or more draws the
+ * last column with w > 0, one below 0 the first.  A draft >= C has p_x = 0 (and q = 0
+ * with NULL draft_logits).
+ *   tokens [R] int32: the accepted drafts, then the drawn token; -1 in the rows
+ *     behind it and outside the sequences.  They are targets for the
+ *     operators above.
+ *   accepted [S] int32: how many drafts of the sequence were accepted; 0 for
+ *     a sequence without rows.
+ *   logp [R] float32: log p of the emitted token, 0 where tokens has none.
+ * A row whose logits, or whose draft's, have no softmax (all -inf, a NaN, +inf)
+ * ends its sequence with the token -1 and logp NaN.  Probabilities are float32,
+ * sums of them and comparisons float64; the outputs must not overlap the inputs.
+ */
+lik_status lik_verify_rows(const void* logits, lik_dtype dtype, int64_t R,
+                           int64_t C, int64_t ld, const void* draft_logits,
+                           int64_t draft_ld, const int32_t* draft_tokens,
+                           const int32_t* seq_offsets, int64_t S, float scale,
+                           float draft_scale, const float* accept_u,
+                           const float* sample_u, int32_t* tokens,
+                           int32_t* accepted, float* logp, void* workspace,
+                           size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

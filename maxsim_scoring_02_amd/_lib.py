@@ -23,6 +23,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "liblik.so")
 HEADER_PATH = os.path.join(os.path.dirname(PKG), "include", "lik.h")
 ROWS_HEADER_PATH = os.path.join(os.path.dirname(PKG), "include", "lik_rows.h")
+CACHE_HEADER_PATH = os.path.join(os.path.dirname(PKG), "include", "lik_cache.h")
 
 LIK_OK, LIK_ERR_INVALID_ARG, LIK_ERR_UNSUPPORTED, LIK_ERR_HIP = 0, 1, 2, 3
 LIK_F16, LIK_BF16, LIK_F32, LIK_F32_BF16X3 = 0, 1, 2, 3
@@ -30,7 +31,7 @@ LIK_F16, LIK_BF16, LIK_F32, LIK_F32_BF16X3 = 0, 1, 2, 3
  LIK_OP_KD_FWD, LIK_OP_KD_BWD) = range(6)
 
 (LIK_ROWS_LOGPROB_FWD, LIK_ROWS_LOGPROB_BWD, LIK_ROWS_DISTILL, LIK_ROWS_POLICY,
- LIK_ROWS_PREFERENCE) = range(5)
+ LIK_ROWS_PREFERENCE, LIK_ROWS_VERIFY) = range(6)
 LIK_PREF_SIGMOID, LIK_PREF_HINGE, LIK_PREF_SQUARE = range(3)
 
 DTYPE_CODE = {torch.float16: LIK_F16, torch.bfloat16: LIK_BF16, torch.float32: LIK_F32}
@@ -77,6 +78,19 @@ ROWS_SIGNATURES = {
                                  _SZ, _P], _I),
     "lik_preference_rows": (_ROWS + [_P, _P, _I64, _P, _P, _I64, _P, _I, _F, _F, _F, _I, _F, _P,
                                      _P, _P, _P, _P, _I64, _P, _SZ, _P], _I),
+    "lik_verify_rows": (_ROWS + [_P, _I64, _P, _P, _I64, _F, _F, _P, _P, _P, _P, _P, _P, _SZ, _P],
+                        _I),
+}
+
+# include/lik_cache.h
+_CACHE = [_P] * 4 + [_I64] * 6           # codes, scales; blocks, heads, block size, dim, strides
+CACHE_SIGNATURES = {
+    "lik_cache_tables": ([_P, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P],
+                         _I),
+    "lik_cache_append": ([_P, _P, _I, _I64, _I64, _I64, _P] + _CACHE + [_P], _I),
+    "lik_cache_workspace_bytes": ([_I64] * 5 + [_I], _SZ),
+    "lik_cache_attention": ([_P, _I, _I64, _I64, _I64, _P, _P, _I64, _P, _I64, _I64] + _CACHE +
+                            [_F, _P, _I64, _P, _P, _SZ, _P], _I),
 }
 
 
@@ -101,7 +115,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(
                 f"{LIB_PATH} is not built; run `python -m maxsim_scoring_02_amd.build`")
         l = ctypes.CDLL(LIB_PATH)
-        for name, (args, res) in {**SIGNATURES, **ROWS_SIGNATURES}.items():
+        for name, (args, res) in {**SIGNATURES, **ROWS_SIGNATURES, **CACHE_SIGNATURES}.items():
             fn = getattr(l, name)
             fn.argtypes = args
             fn.restype = res
@@ -568,6 +582,213 @@ def lik_preference_rows(logits, targets, seq_offsets, chosen, rejected, ref_logp
             float(scale), _addr(w), _addr(pair_loss), _addr(seq), _addr(loss), _addr(grad), gld,
             _addr(ws), wsb, _stream_of(dev)))
     return loss, pair_loss, seq, grad
+
+
+def lik_verify_rows(logits, draft_tokens, seq_offsets, accept_u, sample_u, draft_logits=None,
+                    scale=1.0, draft_scale=1.0) -> Tuple:
+    """Drafted tokens verified against softmax(scale * logits [R, C]): sequence s
+    is the rows seq_offsets[s] .. seq_offsets[s + 1] - 1, row r has the draft
+    draft_tokens[r] (negative: no draft from here on), the last row none.  Drafts
+    were drawn from softmax(draft_scale * draft_logits [R, C]), or copied (None).
+    accept_u [R] and sample_u [S] are uniform numbers within [0, 1).  Returns
+    (tokens [R] int32: accepted drafts and then the drawn token, -1 elsewhere;
+    accepted [S] int32; logp [R] float32 of the tokens, 0 elsewhere)."""
+    dt, R, C, ld = _rows(logits)
+    dev = logits.device
+    if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 1:
+        raise ValueError("seq_offsets must be [S + 1]")
+    S = seq_offsets.shape[0] - 1
+    x = _row_arg(draft_tokens, (R,), "draft_tokens", dev, torch.int32)
+    off = _row_arg(seq_offsets, (S + 1,), "seq_offsets", dev, torch.int32)
+    u = _row_arg(accept_u, (R,), "accept_u", dev)
+    su = _row_arg(sample_u, (S,), "sample_u", dev)
+    dld = 0
+    if draft_logits is not None:
+        if (draft_logits.shape != logits.shape or draft_logits.dtype != logits.dtype or
+                draft_logits.device != dev):
+            raise ValueError("draft_logits must have the logits' shape, type and device")
+        dld = _row_stride(draft_logits, "draft_logits")
+    with _current(dev):
+        tokens = torch.empty(R, dtype=torch.int32, device=dev)
+        accepted = (torch.empty if R else torch.zeros)(S, dtype=torch.int32, device=dev)
+        logp = torch.empty(R, dtype=torch.float32, device=dev)
+        ws, wsb = _rows_workspace(LIK_ROWS_VERIFY, R, C, S, dt, draft_logits, dev)
+        _check(lib().lik_verify_rows(
+            logits.data_ptr(), dt, R, C, ld, _addr(draft_logits), dld, x.data_ptr(), off.data_ptr(),
+            S, scale, draft_scale, u.data_ptr(), su.data_ptr(), tokens.data_ptr(),
+            accepted.data_ptr(), logp.data_ptr(), _addr(ws), wsb, _stream_of(dev)))
+    return tokens, accepted, logp
+
+
+# ---------------------------------------------------------------------------
+# a paged cache in 8 bits (include/lik_cache.h)
+# ---------------------------------------------------------------------------
+
+_F8 = torch.float8_e4m3fn
+
+
+def _ints(x, shape, name: str, device):
+    """A dense int32 argument of this shape on the device of the others."""
+    if x.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(x.shape)}")
+    if x.dtype != torch.int32:
+        raise ValueError(f"{name} must be torch.int32, not {x.dtype}")
+    if x.device != device:
+        raise ValueError(f"{name} must be on {device}, not {x.device}")
+    return x.contiguous()
+
+
+def _in_place(x, shape, name: str, device):
+    """One that the call changes: as it is."""
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return _ints(x, shape, name, device)
+
+
+def _table(block_table, S: int, device) -> Tuple:
+    """(entries a row, row stride) of a block table."""
+    if block_table.dim() != 2 or block_table.shape[0] != S:
+        raise ValueError(f"block_table must be [{S}, max_blocks], not {tuple(block_table.shape)}")
+    if block_table.dtype != torch.int32 or block_table.device != device:
+        raise ValueError(f"block_table must be torch.int32 on {device}")
+    return block_table.shape[1], _row_stride(block_table, "block_table")
+
+
+def lik_cache_tables(old_len, new_len, block_table, ring, ring_state, block_size, tokens) -> Tuple:
+    """Block tables of requests that go from old_len [S] to new_len [S] tokens:
+    blocks of block_size tokens are taken from the pool of free ones (ring [N]
+    with ring_state [4] = head, count, 0, 0) or given back to it, and
+    block_table [S, max_blocks] is changed to match, all in place, all int32.
+    Returns (granted [S]: the new length, or the old one where the pool or the
+    table is too short; token_offsets [S + 1] of the new tokens; slots [tokens]
+    of the new tokens, -1 where there is none)."""
+    if not old_len.is_cuda:
+        raise ValueError("old_len must be a GPU tensor")
+    if old_len.dim() != 1 or ring.dim() != 1:
+        raise ValueError("old_len must be [S] and ring [N]")
+    dev, S, N = old_len.device, old_len.shape[0], ring.shape[0]
+    old = _ints(old_len, (S,), "old_len", dev)
+    new = _ints(new_len, (S,), "new_len", dev)
+    width, ld = _table(block_table, S, dev)
+    _in_place(ring, (N,), "ring", dev)
+    _in_place(ring_state, (4,), "ring_state", dev)
+    if tokens < 0:
+        raise ValueError("tokens must not be negative")
+    with _current(dev):
+        granted = torch.empty(S, dtype=torch.int32, device=dev)
+        offsets = torch.empty(S + 1, dtype=torch.int32, device=dev)
+        slots = torch.empty(tokens, dtype=torch.int32, device=dev)
+        _check(lib().lik_cache_tables(
+            old.data_ptr(), new.data_ptr(), S, block_size, block_table.data_ptr(), width, ld,
+            ring.data_ptr(), N, ring_state.data_ptr(), granted.data_ptr(), offsets.data_ptr(),
+            slots.data_ptr(), tokens, _stream_of(dev)))
+    return granted, offsets, slots
+
+
+def _blocks(k_cache, v_cache, k_scale, v_scale, device) -> Tuple:
+    """What the C ABI takes of a cache: addresses, sizes and block strides."""
+    if k_cache.dim() != 4 or k_cache.dtype != _F8 or v_cache.dtype != _F8:
+        raise ValueError("k_cache must be [N, heads, block_size, dim] and v_cache "
+                         "[N, heads, dim, block_size], float8_e4m3fn")
+    N, heads, bs, dim = k_cache.shape
+    if v_cache.shape != (N, heads, dim, bs):
+        raise ValueError(f"v_cache must have shape {(N, heads, dim, bs)}, not {tuple(v_cache.shape)}")
+    size = heads * bs * dim
+    strides = []
+    for x, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        a, b, c, d = x.stride()
+        inner, last = x.shape[2:]
+        if d != 1 or c != last or (heads > 1 and b != inner * last) or (N > 1 and a < size):
+            raise ValueError(f"{name} must be dense within a block")
+        strides.append(a if N > 1 else size)
+    for x, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if x.shape != (N, heads) or x.dtype != torch.float32 or not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous float32 of shape {(N, heads)}")
+    if not (device == k_cache.device == v_cache.device == k_scale.device == v_scale.device):
+        raise ValueError(f"the cache must be on {device}")
+    return (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), N,
+            heads, bs, dim, *strides)
+
+
+def _token_stride(x, heads: int, dim: int, name: str) -> int:
+    """Token stride of [T, heads, dim] with dense heads."""
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim:
+        raise ValueError(f"{name} must have shape [T, {heads}, {dim}], not {tuple(x.shape)}")
+    a, b, c = x.stride()
+    if c != 1 or (heads > 1 and b != dim) or (x.shape[0] > 1 and a < heads * dim):
+        raise ValueError(f"{name} must have dense heads and tokens that do not overlap")
+    return a if x.shape[0] > 1 else heads * dim
+
+
+def _tokens(x, name: str) -> int:
+    """dtype code of a tensor of tokens."""
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if x.dtype not in DTYPE_CODE:
+        raise ValueError(f"{name} must be float16, bfloat16 or float32")
+    return DTYPE_CODE[x.dtype]
+
+
+def lik_cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale) -> None:
+    """Writes the keys and values of T tokens, k and v [T, heads, dim], to their
+    slots [T] (int32, negative: none) of the cache in place: k_cache
+    [N, heads, block_size, dim] and v_cache [N, heads, dim, block_size] in
+    float8_e4m3fn, with scales [N, heads] in float32.  The tokens of a block
+    follow each other; a call with a block's first slot starts the block anew."""
+    dt = _tokens(k, "k")
+    dev = k.device
+    if v.shape != k.shape or v.dtype != k.dtype or v.device != dev:
+        raise ValueError("v must have k's shape, type and device")
+    cache = _blocks(k_cache, v_cache, k_scale, v_scale, dev)
+    heads, dim = cache[5], cache[7]
+    kld, vld = _token_stride(k, heads, dim, "k"), _token_stride(v, heads, dim, "v")
+    T = k.shape[0]
+    at = _ints(slots, (T,), "slots", dev)
+    with _current(dev):
+        _check(lib().lik_cache_append(k.data_ptr(), v.data_ptr(), dt, T, kld, vld, at.data_ptr(),
+                                      *cache, _stream_of(dev)))
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_workspace_bytes(T: int, S: int, hq: int, hkv: int, dim: int, dt: int) -> int:
+    n = lib().lik_cache_workspace_bytes(T, S, hq, hkv, dim, dt)
+    return 0 if n == _NO_SIZE else n     # sizes that the call itself refuses
+
+
+def lik_cache_attention(q, q_offsets, kv_len, block_table, k_cache, v_cache, k_scale, v_scale,
+                        scale=None, out=None, want_lse=False) -> Tuple:
+    """Causal attention of q [T, q_heads, dim] over a cache in 8 bits: the rows
+    q_offsets[s] .. q_offsets[s + 1] - 1 are the last tokens of request s, which has
+    kv_len[s] tokens in the blocks of row s of block_table [S, max_blocks] (all
+    int32).  scale None = dim ** -0.5.  Returns (out [T, q_heads, dim] in q's
+    type, lse [T, q_heads] float32 or None); rows that attend to nothing or
+    belong to no request are 0, with lse -inf."""
+    dt = _tokens(q, "q")
+    dev = q.device
+    cache = _blocks(k_cache, v_cache, k_scale, v_scale, dev)
+    hkv, dim = cache[5], cache[7]
+    T, hq = q.shape[0], q.shape[1] if q.dim() > 1 else 0
+    qld = _token_stride(q, hq, dim, "q")
+    if kv_len.dim() != 1:
+        raise ValueError("kv_len must be [S]")
+    S = kv_len.shape[0]
+    off = _ints(q_offsets, (S + 1,), "q_offsets", dev)
+    lens = _ints(kv_len, (S,), "kv_len", dev)
+    width, ld = _table(block_table, S, dev)
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or out.device != dev):
+        raise ValueError("out must have q's shape, type and device")
+    with _current(dev):
+        if out is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        lse = torch.empty((T, hq), dtype=torch.float32, device=dev) if want_lse else None
+        wsb = _attention_workspace_bytes(T, S, hq, hkv, dim, dt)
+        ws = _workspace(wsb, dev)
+        _check(lib().lik_cache_attention(
+            q.data_ptr(), dt, T, hq, qld, off.data_ptr(), lens.data_ptr(), S,
+            block_table.data_ptr(), width, ld, *cache, dim ** -0.5 if scale is None else scale,
+            out.data_ptr(), _token_stride(out, hq, dim, "out"), _addr(lse), _addr(ws), wsb,
+            _stream_of(dev)))
+    return out, lse
 
 
 FORWARD = {"allpairs": lik_maxsim_fwd, "pairwise": lik_maxsim_pairwise_fwd,

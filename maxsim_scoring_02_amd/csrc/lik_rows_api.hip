@@ -69,9 +69,7 @@ lik_status maybe4(const void* p, const char* name) {
   return LIK_OK;
 }
 
-lik_status check_workspace(lik_rows_op op, const lik::Rows& a, int64_t S, const void* ws,
-                           size_t ws_bytes) {
-  const size_t need = lik_rows_workspace_bytes(op, a.R, a.C, S, a.dtype, a.grad ? 1 : 0);
+lik_status check_workspace(size_t need, const void* ws, size_t ws_bytes) {
   if (need == SIZE_MAX) return fail(LIK_ERR_INVALID_ARG, "sizes overflow");
   if (need == 0) return LIK_OK;
   if (!ws || ws_bytes < need)
@@ -79,6 +77,11 @@ lik_status check_workspace(lik_rows_op op, const lik::Rows& a, int64_t S, const 
                 ws ? ws_bytes : (size_t)0);
   if (!aligned16(ws)) return fail(LIK_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   return LIK_OK;
+}
+lik_status check_workspace(lik_rows_op op, const lik::Rows& a, int64_t S, const void* ws,
+                           size_t ws_bytes) {
+  return check_workspace(lik_rows_workspace_bytes(op, a.R, a.C, S, a.dtype, a.grad ? 1 : 0), ws,
+                         ws_bytes);
 }
 
 lik_status launched(hipError_t e) {
@@ -120,6 +123,9 @@ size_t lik_rows_workspace_bytes(lik_rows_op op, int64_t R, int64_t C, int64_t n_
     case LIK_ROWS_PREFERENCE:
       if (n_seqs < 0 || mul_ok({n_seqs, 64}) < 0) return SIZE_MAX;
       return R == 0 || C == 0 ? 0 : lik::pref_layout(R, C, n_seqs, dtype).bytes;
+    case LIK_ROWS_VERIFY:
+      if (n_seqs < 0 || mul_ok({n_seqs, 64}) < 0) return SIZE_MAX;
+      return 0;
   }
   return SIZE_MAX;
 }
@@ -266,6 +272,57 @@ lik_status lik_preference_rows(const void* logits, lik_dtype dtype, int64_t R, i
                         margin, smoothing, mean_logp != 0, pair_weight, pair_loss, seq_logp, loss};
   return launched(lik::run_preference(a, p, static_cast<char*>(workspace),
                                       static_cast<hipStream_t>(stream)));
+}
+
+lik_status lik_verify_rows(const void* logits, lik_dtype dtype, int64_t R, int64_t C, int64_t ld,
+                           const void* draft_logits, int64_t draft_ld,
+                           const int32_t* draft_tokens, const int32_t* seq_offsets, int64_t S,
+                           float scale, float draft_scale, const float* accept_u,
+                           const float* sample_u, int32_t* tokens, int32_t* accepted, float* logp,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  const lik::Rows a{logits, dtype, R, C, ld, scale, nullptr, 0};
+  bool done;
+  LIK_TRY(check_rows(a, false, &done));
+  if (S < 0) return fail(LIK_ERR_INVALID_ARG, "negative size (S %lld)", (long long)S);
+  if (!(draft_scale >= 0x1p-64f && draft_scale <= 0x1p64f))
+    return fail(LIK_ERR_INVALID_ARG, "draft_scale must be within [2^-64, 2^64]");
+  if (done) return ok();
+  if (S > kMaxRows) return fail(LIK_ERR_UNSUPPORTED, "S must be below 2^31");
+  const int64_t size = lik::elem_bytes_of(dtype);
+  if (draft_logits) {
+    if (draft_ld < C)
+      return fail(LIK_ERR_INVALID_ARG, "row stride draft_ld %lld is less than C %lld",
+                  (long long)draft_ld, (long long)C);
+    if (mul_ok({R, draft_ld, size}) < 0)
+      return fail(LIK_ERR_INVALID_ARG, "R x row stride overflows");
+    if (reinterpret_cast<uintptr_t>(draft_logits) % size)
+      return fail(LIK_ERR_INVALID_ARG, "draft_logits must be aligned to their elements");
+  }
+  LIK_TRY(need4(draft_tokens, "draft_tokens"));
+  LIK_TRY(need4(seq_offsets, "seq_offsets"));
+  LIK_TRY(need4(accept_u, "accept_u"));
+  LIK_TRY(need4(tokens, "tokens"));
+  LIK_TRY(need4(logp, "logp"));
+  if (S > 0) {
+    LIK_TRY(need4(sample_u, "sample_u"));
+    LIK_TRY(need4(accepted, "accepted"));
+  }
+  const lik::Span in[] = {{draft_tokens, R * 4}, {accept_u, R * 4}, {seq_offsets, (S + 1) * 4},
+                          {sample_u, S * 4},
+                          {logits, ((R - 1) * ld + C) * size},
+                          {draft_logits, draft_logits ? ((R - 1) * draft_ld + C) * size : 0}};
+  const lik::Span out[] = {{tokens, R * 4}, {logp, R * 4}, {accepted, S * 4}};
+  if (lik::any_overlap(in, out))
+    return fail(LIK_ERR_INVALID_ARG, "an output overlaps an input or another output");
+  const size_t need =
+      lik_rows_workspace_bytes(LIK_ROWS_VERIFY, R, C, S, dtype, draft_logits ? 1 : 0);
+  LIK_TRY(check_workspace(need, workspace, workspace_bytes));
+  LIK_TRY(check_device());
+  const lik::VerifyArgs v{logits, draft_logits, dtype, R, (int)C, ld, draft_ld, draft_tokens,
+                          seq_offsets, S, scale, draft_scale, accept_u, sample_u, tokens,
+                          accepted, logp};
+  return launched(
+      lik::run_verify(v, static_cast<char*>(workspace), static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

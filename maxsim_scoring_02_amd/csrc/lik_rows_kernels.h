@@ -190,4 +190,23 @@ hipError_t run_parts(const Rows& a, const Parts& p, const int32_t* targets, cons
 
 hipError_t run_preference(const Rows& a, const PrefArgs& p, char* ws, hipStream_t s);
 
+struct VerifyArgs {
+  const void* z;
+  const void* d;         // draft logits, or null
+  lik_dtype dtype;
+  int64_t R;
+  int C;
+  int64_t ld, draft_ld;
+  const int32_t* drafts;
+  const int32_t* offsets;
+  int64_t S;
+  float scale, draft_scale;
+  const float* accept_u;
+  const float* sample_u;
+  int32_t* tokens;
+  int32_t* accepted;
+  float* logp;
+};
+hipError_t run_verify(const VerifyArgs& a, char* ws, hipStream_t s);
+
 }  // namespace lik

@@ -25,7 +25,8 @@ Modules:
   the colpali pull request puts on the scores), with its gradient.
 * ``rows``    float64 losses over rows of logits (log-probabilities,
   distillation from top logits, clipped policy loss, preference loss), with
-  their gradients.
+  their gradients, and the verification of drafted tokens.
+* ``cache``   the paged cache in 8 bits: block tables, writes, attention.
 
 Every function here is pinned by the ``-m "not gpu"`` tests (brute force,
 closed forms, finite differences, invariants, integer-exact inputs); none is
@@ -54,5 +55,7 @@ from .rows import (  # noqa: F401
     distill_rows,
     policy_rows,
     preference_rows,
+    verify_rows,
 )
 from . import brute  # noqa: F401
+from . import cache  # noqa: F401

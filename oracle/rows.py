@@ -174,3 +174,41 @@ def preference_rows(z, targets, offsets, chosen, rejected, ref=None, kind=SIGMOI
     on = w != 0
     return (float(np.sum(w[on] * losses[on])), losses, seq,
             logprob_rows_bwd(z, t, d_row, scale), d_row)
+
+
+def verify_rows(z, drafts, offsets, accept_u, sample_u, draft_z=None, scale=1.0, draft_scale=1.0):
+    """(tokens [R], accepted [S], logp [R]) of drafted tokens, by the definition."""
+    z = np.asarray(z, dtype=np.float64)
+    R, C = z.shape
+    S = len(offsets) - 1
+    tokens, accepted, logp = np.full(R, -1), np.zeros(S, dtype=int), np.zeros(R)
+    for s in range(S):
+        lo, hi = max(int(offsets[s]), 0), min(int(offsets[s + 1]), R)
+        for r in range(lo, hi):
+            x = int(drafts[r])
+            more = r + 1 < hi and x >= 0
+            with np.errstate(invalid="ignore"):
+                p, logq, _ = _softmax(scale * z[r])
+                q = np.zeros(C)
+                if more and draft_z is not None:
+                    q = _softmax(draft_scale * np.asarray(draft_z[r], dtype=np.float64))[0]
+                elif more and x < C:
+                    q[x] = 1.0
+            if not (np.isfinite(p).all() and np.isfinite(q).all()):
+                logp[r], accepted[s] = np.nan, r - lo
+                break
+            px, qx = (p[x], q[x]) if more and x < C else (0.0, 1.0 if draft_z is None else 0.0)
+            if more and accept_u[r] * qx < px:
+                tokens[r], logp[r] = x, logq[x]
+                continue
+            w = np.maximum(p - q, 0.0) if more else p
+            if not w.sum() > 0:
+                w = p
+            accepted[s] = r - lo
+            if sample_u[s] == sample_u[s]:
+                c = np.cumsum(w)
+                over = np.nonzero(c > sample_u[s] * c[-1])[0]
+                tokens[r] = over[0] if len(over) else np.nonzero(w > 0)[0][-1]
+                logp[r] = logq[tokens[r]]
+            break
+    return tokens, accepted, logp

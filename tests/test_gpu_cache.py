@@ -1,0 +1,531 @@
+"""GPU parity of the 8-bit cache (block tables, appends, attention) against the
+float64 oracle, through the binding.
+
+Integers and scales have to be equal, codes too (the same numbers rounded to the
+same grid).  Attention, with u = 2^-24 and per row the largest D = sum_k |scale q_k
+k_k| of the scores:
+
+  scores    a query's numbers are rounded to 22 bits of the row's largest at
+            least (only float32 has more: 2^-22), sums over dim terms in float32:
+            (dim u + 2^-22) D, and roundings of the scaled score, 4 u D
+  weights   their exponent's error e above, the exponential's 2 u and its
+            argument's rounding u |x| (x counted by D too): relative
+            e + 4 u (D + 4); rounded to 2^-11 (float32: 2^-22) before the product
+            with the values, or, where they are small beside the largest, to
+            half the smallest number of 16 bits, 2^-25 (2^-36 for float32's two
+            parts at the least) of a reference that is at most 2^8 below it
+  out       the weights' relative error counts twice (sums above and below), the
+            sums over up to L terms in float32, (L / 16 + 64) u of the size of
+            what is summed; then one rounding to the type
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from maxsim_scoring_02_amd import _lib
+from oracle import cache as oc
+from parity import say
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+U = 2.0 ** -24
+TINY = {F16: 2.0 ** -25, BF16: 2.0 ** -133, F32: 2.0 ** -149}
+
+
+def host(x):
+    return x.double().cpu().numpy()
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32).cuda()
+
+
+# ---------------------------------------------------------------------------
+# block tables
+# ---------------------------------------------------------------------------
+
+class Pool:
+    """A table, ring and state on both sides, compared after every call."""
+
+    def __init__(self, N, S, width, bs, seed, pad=0):
+        rng = np.random.default_rng(seed)
+        self.table, self.ring = np.full((S, width), -1), rng.permutation(N)
+        self.state, self.bs = np.array([0, N, 0, 0]), bs
+        self.gpu = torch.full((S, width + pad), 77, dtype=torch.int32, device="cuda")
+        self.g_table = self.gpu[:, :width]
+        self.g_table.fill_(-1)
+        self.g_ring, self.g_state = i32(self.ring), i32(self.state)
+
+    def step(self, old, new, tokens):
+        want = oc.tables(old, new, self.table, self.ring, self.state, self.bs, tokens)
+        got = _lib.lik_cache_tables(i32(old), i32(new), self.g_table, self.g_ring, self.g_state, self.bs, tokens)
+        for x, y, name in zip(got, want, ("granted", "token_offsets", "slots")):
+            assert np.array_equal(x.cpu().numpy(), y), name
+        assert np.array_equal(self.g_table.cpu().numpy(), self.table)
+        assert np.array_equal(self.g_ring.cpu().numpy(), self.ring)
+        assert self.g_state.tolist() == self.state.tolist()
+        assert (self.gpu[:, self.table.shape[1]:] == 77).all()
+        return want
+
+
+@pytest.mark.parametrize("S,N,width,bs,top", [(1, 9, 4, 16, 64), (3, 5, 4, 16, 90), (64, 300, 9, 32, 260),
+                                              (65, 120, 3, 64, 300), (1000, 3000, 12, 16, 190),
+                                              (1025, 900, 5, 128, 700), (7, 2000, 700, 16, 11000)])
+def test_tables(S, N, width, bs, top):
+    say(f"[cache] tables {S} requests, {N} blocks of {bs}")
+    rng = np.random.default_rng(S)
+    pool = Pool(N, S, width, bs, S, pad=S % 3)
+    lens = np.zeros(S, dtype=int)
+    for step in range(6):
+        kind = rng.integers(0, 4, S)
+        new = np.where(kind == 0, lens + 5, np.where(kind == 1, rng.integers(0, top, S), np.where(kind == 2, 0, lens - 3)))
+        T = int(np.maximum(np.maximum(new, 0) - lens, 0).sum())
+        lens, _, _ = pool.step(lens, new, [T, T + 37, max(0, T - 11)][step % 3])
+
+
+def test_tables_at_the_edges():
+    pool = Pool(6, 4, 3, 16, 1)
+    # longer than the table; exactly it; none; the pool's last blocks
+    lens, _, _ = pool.step([0, 0, 0, 0], [49, 48, 0, 33], 200)
+    assert lens.tolist() == [0, 48, 0, 33]
+    lens, _, _ = pool.step(lens, [1, 48, 0, 34], 20)        # nothing is free; growing within a block
+    assert lens.tolist() == [0, 48, 0, 34]
+    lens, _, _ = pool.step(lens, [-5, 0, 0, -1], 3)          # all given back
+    assert lens.tolist() == [0, 0, 0, 0] and pool.state[1] == 6
+    lens, _, _ = pool.step([-3, 0, 0, 0], [2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 16], 10)
+    assert lens.tolist() == [0, 0, 0, 16]
+    pool.step([10 ** 9, 0, 0, 16], [0, 0, 0, 16], 0)          # an old length beyond the table
+
+
+def test_tables_without_requests_or_blocks():
+    state, e = i32([0, 0, 0, 0]), torch.empty(0, dtype=torch.int32, device="cuda")
+    g, off, slots = _lib.lik_cache_tables(e, e, torch.empty((0, 4), dtype=torch.int32, device="cuda"), e, state, 16, 5)
+    assert g.shape == (0,) and off.tolist() == [0] and slots.tolist() == [-1] * 5
+    g, off, slots = _lib.lik_cache_tables(i32([0, 3]), i32([4, 3]), torch.full((2, 1), -1, dtype=torch.int32, device="cuda"),
+                                          e, state, 16, 5)
+    assert g.tolist() == [0, 3] and off.tolist() == [0, 4, 4] and slots.tolist() == [-1] * 5
+    assert state.tolist() == [0, 0, 0, 0]
+
+
+def test_tables_with_a_broken_pool_stay_inside():
+    """Blocks and states that make no sense: nothing outside is touched, no slot is outside."""
+    N, S, bs = 5, 3, 16
+    guard = torch.full((3, 64), 7, dtype=torch.int32, device="cuda")
+    ring = guard[1, 20:20 + N]
+    for state in ([-9, 3, 0, 0], [2 ** 31 - 1, 2 ** 31 - 1, 0, 0], [3, -4, 0, 0], [4, 5, 0, 0]):
+        ring.copy_(i32([99, -1, 2, 2 ** 31 - 1, 0]))
+        _, _, slots = _lib.lik_cache_tables(i32([0, 40, 0]), i32([40, 0, 70]), torch.full((S, 6), -1, dtype=torch.int32, device="cuda"),
+                                            ring, i32(state), bs, 120)
+        s = slots.cpu().numpy()
+        assert s.min() >= -1 and s.max() < N * bs
+        assert (guard[0] == 7).all() and (guard[2] == 7).all()
+        assert (guard[1, :20] == 7).all() and (guard[1, 20 + N:] == 7).all()
+
+
+# ---------------------------------------------------------------------------
+# appends
+# ---------------------------------------------------------------------------
+
+class Cache:
+    """A cache on both sides; blocks lie apart by `gap` blocks in one array."""
+
+    def __init__(self, N, heads, bs, dim, seed, gap=0, fill=True):
+        rng = np.random.default_rng(seed)
+        self.sizes = N, heads, bs, dim
+        self.k = rng.integers(0, 126, (N, heads, bs, dim)).astype(np.uint8)
+        self.v = rng.integers(0, 126, (N, heads, dim, bs)).astype(np.uint8)
+        self.k |= (rng.integers(0, 2, self.k.shape) << 7).astype(np.uint8)
+        self.v |= (rng.integers(0, 2, self.v.shape) << 7).astype(np.uint8)
+        self.ks = np.exp2(rng.integers(-10, -6, (N, heads)).astype(float))
+        self.vs = np.exp2(rng.integers(-10, -6, (N, heads)).astype(float))
+        self.written = None if fill else set()
+        if not fill:                     # memory that holds anything
+            self.k[:], self.v[:] = 0x7f, 0xff
+            self.ks[:], self.vs[:] = np.nan, np.inf
+        size = heads * bs * dim
+        self.buf = torch.full((2 * N * (1 + gap) * size,), 0x55, dtype=torch.uint8, device="cuda")
+        both = self.buf.view(N, 2 * (1 + gap), size)
+        self.gk = both[:, 0].view(N, heads, bs, dim).view(_lib._F8)
+        self.gv = both[:, 1].view(N, heads, dim, bs).view(_lib._F8)
+        self.gk.view(torch.uint8).copy_(torch.from_numpy(self.k))
+        self.gv.view(torch.uint8).copy_(torch.from_numpy(self.v))
+        self.gks, self.gvs = (torch.tensor(x, dtype=F32).cuda() for x in (self.ks, self.vs))
+
+    @property
+    def parts(self):
+        return self.gk, self.gv, self.gks, self.gvs
+
+    def append(self, k, v, slots):
+        """k and v: GPU tensors"""
+        _lib.lik_cache_append(k, v, i32(slots), *self.parts)
+        if self.written is not None:
+            self.written |= set(slots)
+        oc.append_part(host(k), slots, self.k, self.ks)
+        oc.append_part(host(v), slots, self.v.transpose(0, 1, 3, 2), self.vs)
+        self.check()
+
+    def check(self):
+        if self.written is not None:     # slots that hold anything are no matter
+            behind = np.setdiff1d(np.arange(self.sizes[0] * self.sizes[2]), list(self.written))
+            b, o = behind // self.sizes[2], behind % self.sizes[2]
+            self.k[b, :, o] = self.gk.view(torch.uint8).cpu().numpy()[b, :, o]
+            self.v[b, :, :, o] = self.gv.view(torch.uint8).cpu().numpy()[b, :, :, o]
+        for got, want, name in ((self.gks, self.ks, "k_scale"), (self.gvs, self.vs, "v_scale"),
+                                (self.gk.view(torch.uint8), self.k, "k_cache"), (self.gv.view(torch.uint8), self.v, "v_cache")):
+            got = got.cpu().numpy()
+            bad = ~((got == want) | ((got != got) & (want != want)))
+            assert not bad.any(), f"{name}: {bad.sum()} differ, first at {np.argwhere(bad)[0]}: {got[bad][0]} for {want[bad][0]}"
+        rest = self.buf.view(self.sizes[0], -1, self.sizes[1] * self.sizes[2] * self.sizes[3])[:, 2:]
+        assert (rest == 0x55).all()
+
+
+def tokens(T, heads, dim, dtype, seed, spread=2.0, fused=True):
+    """k and v as parts of one array of queries, keys and values, sizes differing by token."""
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, 3, heads, dim, generator=gen) * torch.exp2(spread * torch.randn(T, 3, heads, 1, generator=gen))
+    x = x.to(dtype).cuda()
+    return (x[:, 1], x[:, 2]) if fused else (x[:, 1].contiguous(), x[:, 2].contiguous())
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("heads,bs,dim", [(1, 16, 64), (2, 16, 128), (3, 32, 64), (1, 64, 256), (5, 128, 128), (2, 256, 64)])
+def test_append(heads, bs, dim, dtype):
+    say(f"[cache] append {heads} heads, blocks of {bs}, dim {dim}, {dtype}")
+    rng = np.random.default_rng(bs + dim)
+    c = Cache(9, heads, bs, dim, bs, gap=heads % 2)
+    order = rng.permutation(9)
+    # requests at any place: one token, a few, blocks and a half, none
+    slots, seed = [], 0
+    for b, (first, n) in zip(order[::2], ((0, bs // 2 + 3), (5, 1), (bs - 2, 2), (0, 1))):
+        slots += [b * bs + first + i for i in range(n)]
+    chain = [order[1] * bs + i for i in range(bs)] + [order[3] * bs + i for i in range(bs // 2)]
+    slots = slots + [-1, -1] + chain + [9 * bs, -7, 2 ** 31 - 1]
+    for step in range(3):                # the first written over twice, as drafts are
+        k, v = tokens(len(slots), heads, dim, dtype, 10 * step + heads, fused=step != 1)
+        c.append(k, v, slots)
+        slots = [s + 1 if s >= 0 and s % bs not in (0, bs - 1) else s for s in slots]
+        keep = [i for i in range(len(slots)) if slots[i] < 0 or slots[i] not in slots[:i]]
+        slots = [slots[i] for i in keep]
+
+
+def test_append_one_token_after_another():
+    """A block filled token by token, every one larger than the last at times."""
+    c = Cache(3, 2, 16, 64, 3)
+    for t in range(40):
+        k, v = tokens(1, 2, 64, BF16, t, spread=3.0)
+        c.append(k, v, [t % 16 + 16 * (t // 16)])
+
+
+def test_append_keeps_what_the_format_holds():
+    """Zeros, the smallest and largest numbers, values on and next to rounding's borders."""
+    c = Cache(2, 1, 16, 64, 5)
+    k = torch.zeros(1, 1, 64)
+    c.append(k.cuda(), k.cuda(), [0])
+    assert c.ks[0, 0] == 2.0 ** -40
+    x = torch.tensor(oc.VALUES[:64], dtype=F32)
+    y = torch.tensor(oc.VALUES[63:127], dtype=F32)
+    mid = (x + torch.tensor(oc.VALUES[1:65], dtype=F32)) / 2
+    up = torch.nextafter(mid, torch.tensor(1e9))
+    for a, b in ((x, y), (mid, -mid), (up, -up), (y * 2.0 ** -50, y * 2.0 ** 60), (x * 2.0 ** -120, y * 2.0 ** 110)):
+        both = torch.stack([a, b]).view(2, 1, 64).cuda()
+        c.append(both, -both, [16, 17])
+
+
+def test_append_what_is_not_finite():
+    c = Cache(3, 2, 16, 64, 7)
+    k, v = tokens(4, 2, 64, F16, 1, fused=False)
+    k[1, 0, 5] = math.inf
+    v[2, 1, 63] = math.nan
+    slots = [0, 1, 2, 3]
+    c.append(k, v, slots)
+    assert np.isnan(c.ks[0]).tolist() == [True, False] and np.isnan(c.vs[0]).tolist() == [False, True]
+    k, v = tokens(1, 2, 64, F16, 2)
+    c.append(k, v, [4])                   # it stays so
+    assert np.isnan(c.ks[0]).tolist() == [True, False]
+    c.append(k, v, [0])                   # until the block starts anew
+    assert np.isfinite(c.ks[0]).all() and np.isfinite(c.vs[0]).all()
+
+
+def test_append_over_anything():
+    """Blocks whose memory and scales hold anything, started anew."""
+    c = Cache(4, 2, 32, 64, 8, fill=False)
+    k, v = tokens(50, 2, 64, BF16, 3)
+    c.append(k, v, [32 + i for i in range(32)] + [96 + i for i in range(18)])
+    k, v = tokens(3, 2, 64, BF16, 4)
+    c.append(k, v, [114, 115, 116])
+
+
+def test_append_the_same_slot_twice():
+    c = Cache(3, 2, 16, 128, 9)
+    k, v = tokens(5, 2, 128, F32, 6)
+    c.append(k, v, [17, 17, 18, 17, 18])
+    k, v = tokens(19, 2, 128, F32, 7)     # more tokens than a block has slots
+    c.append(k, v, [32 + i % 4 for i in range(19)])
+
+
+def test_append_many_tokens():
+    c = Cache(70, 4, 16, 64, 10)
+    rng = np.random.default_rng(4)
+    order = rng.permutation(70)
+    slots = [b * 16 + i for b in order[:60] for i in range(16)]
+    k, v = tokens(len(slots), 4, 64, BF16, 11)
+    c.append(k, v, slots)
+
+
+# ---------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------
+
+def setup(n, lens, hq, hkv, dim, bs, dtype, seed, gap=0, pad=0, lead=0, size=1.5):
+    """Requests of n[i] query rows and lens[i] cached tokens, over a cache whose
+    unused parts hold no numbers, `pad` query rows behind the last and `lead`
+    before the first."""
+    rng = np.random.default_rng(seed)
+    blocks = [-(-x // bs) for x in lens]
+    N, S, width = sum(blocks) + 3, len(n), max(blocks + [1]) + 1
+    c = Cache(N, hkv, bs, dim, seed, gap)
+    ids, table, at = rng.permutation(N), np.full((S, width), -1), 0
+    for s, b in enumerate(blocks):
+        table[s, :b] = ids[at:at + b]
+        at += b
+    for s, b in enumerate(blocks):                      # what lies behind the length: codes that are no numbers
+        if lens[s] % bs:
+            c.k[table[s, b - 1], :, lens[s] % bs:] = 0x7f
+            c.v[table[s, b - 1], :, :, lens[s] % bs:] = 0xff
+    free = ids[at:]
+    c.k[free], c.v[free] = 0x7f, 0x7f
+    c.ks[free], c.vs[free] = np.nan, np.nan
+    for g, x in ((c.gk, c.k), (c.gv, c.v)):
+        g.view(torch.uint8).copy_(torch.from_numpy(x))
+    c.gks.copy_(torch.tensor(c.ks)), c.gvs.copy_(torch.tensor(c.vs))
+    off = lead + np.concatenate([[0], np.cumsum(n)])
+    T = int(off[-1]) + pad
+    gen = torch.Generator().manual_seed(seed)
+    # codes times scales are of the size of 0.1 to 2
+    q = (torch.randn(T, hq, dim, generator=gen) * size).to(dtype).cuda()
+    return c, q, off, np.array(lens), table
+
+
+def check_attention(c, q, off, lens, table, scale=None, dtype=None, out=None, qv=None, pad_ld=0):
+    T, hq, dim = q.shape
+    dtype = q.dtype
+    scale = dim ** -0.5 if scale is None else scale
+    wide = torch.full((table.shape[0], table.shape[1] + pad_ld), 3, dtype=torch.int32, device="cuda")
+    gt = wide[:, :table.shape[1]]
+    gt.copy_(i32(table))
+    got, lse = _lib.lik_cache_attention(q if qv is None else qv, i32(off), i32(lens), gt, *c.parts,
+                                        scale=scale, want_lse=True, out=out)
+    if out is not None:
+        assert got is out
+    want, rl, (size, dots, top, count) = oc.attention(host(q), off, lens, table, c.k, c.v, c.ks, c.vs, scale, bounds=True)
+    e = (dim + 8) * U * dots + 2.0 ** -22 * dots
+    w_rel = e + 4 * U * (dots + 4)
+    part = 2.0 ** -22 if dtype == F32 else 2.0 ** -11
+    least = (2.0 ** -36 if dtype == F32 else 2.0 ** -25) * 2.0 ** 8
+    tol = (size * (2 * w_rel + part + (count / 16 + 64) * U)[..., None] + (count * least * top)[..., None])
+    tol = tol + torch.finfo(dtype).eps / 2 * (np.abs(want) + tol) + TINY[dtype]
+    x = host(got)
+    assert np.array_equal(np.isnan(x), np.isnan(want)), "NaN in other places"
+    fine = ~np.isnan(want)
+    off_by = np.abs(x - want)[fine] - tol[fine]
+    assert not (off_by > 0).any(), f"out: {off_by.max():.3e} beyond its bound at {np.argwhere((np.abs(x - want) > tol) & fine)[0]}"
+    x = host(lse)
+    assert np.array_equal(np.isneginf(x), np.isneginf(rl)) and np.array_equal(np.isnan(x), np.isnan(rl))
+    fine = np.isfinite(rl)
+    tol = w_rel + (count / 16 + 64) * U + 4 * U * (np.abs(rl) + 1)
+    assert not (np.abs(x - rl)[fine] > tol[fine]).any(), "lse"
+    return got
+
+
+HEADS = [(1, 1), (4, 2), (8, 1), (6, 2), (3, 3), (40, 4), (17, 1)]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("hq,hkv", HEADS)
+def test_attention(hq, hkv, dim, dtype):
+    bs = [16, 32, 64, 128][(hq + dim // 64) % 4]
+    say(f"[cache] attention {hq} / {hkv} heads, dim {dim}, blocks of {bs}, {dtype}")
+    n = [1, 1, 2, 1, 5, 1, 0, 3]
+    lens = [1, 70, 2, 0, 300, 64, 33, 129]
+    c, q, off, lens, table = setup(n, lens, hq, hkv, dim, bs, dtype, hq + dim, gap=hq % 2, pad=hq % 3)
+    check_attention(c, q, off, lens, table, pad_ld=hq % 4)
+
+
+@pytest.mark.parametrize("bs", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("length", [15, 16, 17, 63, 64, 65, 255, 256, 257, 1030])
+def test_lengths_around_blocks_and_tiles(length, bs):
+    c, q, off, lens, table = setup([1, 2, length], [length, length + 1, length], 4, 2, 64, bs, BF16, length + bs)
+    check_attention(c, q, off, lens, table)
+
+
+@pytest.mark.parametrize("hq,hkv,n,lens,dtype", [
+    (8, 2, [40, 1, 33, 200], [40, 500, 100, 700], BF16), (4, 4, [130, 0, 7], [130, 20, 900], F16),
+    (5, 1, [64, 65], [64, 65], F32), (32, 8, [17, 128], [400, 128], BF16), (2, 1, [257], [300], F16),
+    (12, 2, [31, 100], [1000, 164], F32)])
+def test_prompts(hq, hkv, n, lens, dtype):
+    say(f"[cache] prompts {n} of {lens}, {hq} / {hkv} heads, {dtype}")
+    c, q, off, lens, table = setup(n, lens, hq, hkv, [64, 128][hq % 8 == 0], 16, dtype, hq + n[0], pad=3, lead=2)
+    check_attention(c, q, off, lens, table)
+
+
+@pytest.mark.parametrize("dtype,lens", [(BF16, [9000]), (F16, [5000, 13, 4097]), (F32, [3001, 6000])])
+def test_long_caches(dtype, lens):
+    c, q, off, lens, table = setup([1] * len(lens), lens, 8, 2, 128, 16, dtype, 77)
+    check_attention(c, q, off, lens, table)
+
+
+def test_many_requests():
+    rng = np.random.default_rng(8)
+    lens = rng.integers(0, 120, 700)
+    c, q, off, lens, table = setup(rng.integers(0, 3, 700), list(lens), 2, 1, 64, 16, BF16, 12)
+    check_attention(c, q, off, lens, table)
+
+
+def test_sharp_rows_and_scales_far_apart():
+    """Scores of hundreds; scales of blocks many powers of two apart; scales out of range."""
+    c, q, off, lens, table = setup([1, 3], [400, 333], 4, 1, 64, 16, F16, 5, size=30.0)
+    check_attention(c, q, off, lens, table, scale=1.0)
+    rng = np.random.default_rng(1)
+    used = np.unique(table[table >= 0])
+    c.ks[used] = np.exp2(rng.integers(-16, -8, (len(used), 1)).astype(float))
+    c.vs[used] = np.exp2(rng.integers(-30, 30, (len(used), 1)).astype(float))
+    c.gks.copy_(torch.tensor(c.ks)), c.gvs.copy_(torch.tensor(c.vs))
+    check_attention(c, q.to(F32), off, lens, table, scale=0.05)
+    c.vs[used[:5]], c.vs[used[5:9]] = 0.0, 1e30
+    c.ks[used[3]] = 0.0
+    c.gks.copy_(torch.tensor(c.ks)), c.gvs.copy_(torch.tensor(c.vs))
+    check_attention(c, q.to(F32), off, lens, table, scale=0.01)
+
+
+def test_queries_of_every_size():
+    """Rows of the smallest and largest numbers of their types."""
+    for dtype, sizes in ((F16, (2.0 ** -24, 6e4)), (BF16, (1e-30, 1e30)), (F32, (1e-38, 1e34))):
+        c, q, off, lens, table = setup([1, 4], [100, 90], 2, 1, 64, 16, F32, 6)
+        q = q.cpu() / q.cpu().abs().amax(-1, keepdim=True)
+        for size in sizes:
+            x = (q * size).to(dtype).cuda()
+            check_attention(c, x, off, lens, table, scale=float(np.clip(1.0 / size, 2.0 ** -64, 2.0 ** 64)))
+
+
+def test_nan_where_it_is_attended_to_only():
+    c, q, off, lens, table = setup([4, 2], [100, 64], 4, 2, 64, 16, BF16, 9)
+    c.ks[table[0, 6], 1] = np.nan          # positions 96 .. 99 of the first request, head 1
+    c.vs[table[0, 6], 0] = np.nan
+    c.gks.copy_(torch.tensor(c.ks)), c.gvs.copy_(torch.tensor(c.vs))
+    got = check_attention(c, q, off, lens, table)
+    assert torch.isnan(got[:4]).all() and not torch.isnan(got[4:]).any()
+    lens = np.array([98, 64])              # rows at 94 .. 97: two of them see none of it
+    got = check_attention(c, q, off, lens, table)
+    assert not torch.isnan(got[:2]).any() and torch.isnan(got[2:4]).all()
+    q2 = q.clone()
+    q2[5, 0, 3], q2[5, 3, 0] = math.inf, math.nan
+    check_q = _lib.lik_cache_attention(q2, i32(off), i32([90, 64]), i32(table), *c.parts)[0]
+    clean = _lib.lik_cache_attention(q, i32(off), i32([90, 64]), i32(table), *c.parts)[0]
+    assert torch.isnan(check_q[5, [0, 3]]).all()
+    keep = torch.ones(6, 4, dtype=torch.bool)
+    keep[5, 0] = keep[5, 3] = False
+    assert torch.equal(check_q[keep.cuda()], clean[keep.cuda()])
+
+
+def test_rows_that_see_nothing():
+    # longer queries than what is cached; tables with holes; lengths beyond the table; negative ones
+    c, q, off, lens, table = setup([5, 2, 3, 1, 2], [3, 40, 64, 10, 30], 4, 2, 64, 16, F16, 3, pad=4, lead=3)
+    table[1, 0], table[1, 2], table[2] = -1, 10 ** 6, -5
+    lens[3], lens[4] = -4, 10 ** 9
+    got = check_attention(c, q, off, lens, table)
+    assert not got[:3].any() and not got[-4:].any()
+    # no request at all, no cache at all
+    e = torch.empty(0, dtype=torch.int32, device="cuda")
+    out, lse = _lib.lik_cache_attention(q, i32([0]), e, e.view(0, 3), *c.parts, want_lse=True)
+    assert not out.any() and torch.isneginf(lse).all()
+    none = [x[:0] for x in c.parts]
+    out, lse = _lib.lik_cache_attention(q, i32(off), i32(lens), i32(table), *none, want_lse=True)
+    assert not out.any() and torch.isneginf(lse).all()
+    out, lse = _lib.lik_cache_attention(q, i32(off), i32(lens), i32(table)[:, :0], *c.parts, want_lse=True)
+    assert not out.any() and torch.isneginf(lse).all()
+    # offsets that make no sense stay inside
+    for bad in ([0, 99, 3, 9, -5, 17], [-3, 2, 2, 2 ** 31 - 1, 0, 5]):
+        out, _ = _lib.lik_cache_attention(q, i32(bad), i32(lens), i32(table), *c.parts)
+        assert out.shape == q.shape
+
+
+def test_strided_queries_and_outputs():
+    c, q, off, lens, table = setup([1, 4], [50, 80], 4, 2, 64, 16, BF16, 4)
+    T = q.shape[0]
+    qkv = torch.full((T, 3, 4, 64), 7.0, dtype=BF16, device="cuda")
+    qkv[:, 0] = q
+    buf = torch.full((T, 2, 4, 64), 5.0, dtype=BF16, device="cuda")
+    check_attention(c, q, off, lens, table, out=buf[:, 1], qv=qkv[:, 0])
+    assert (buf[:, 0] == 5).all() and (qkv[:, 1:] == 7).all()
+
+
+def test_blocks_that_requests_share():
+    """A prompt that two requests have in common, and a block twice in one table."""
+    c, q, off, lens, table = setup([1, 2], [100, 100], 4, 2, 64, 16, F16, 14)
+    table[1, :4] = table[0, :4]
+    table[0, 5] = table[0, 2]
+    check_attention(c, q, off, lens, table)
+
+
+def test_offsets_past_32_bits():
+    """Blocks that lie further than 2^32 bytes into their cache."""
+    bs, dim, heads = 256, 128, 8
+    size = heads * bs * dim
+    N = 2 ** 32 // size + 40
+    big_k = torch.zeros((N, heads, bs, dim), dtype=torch.uint8, device="cuda")
+    big_v = torch.zeros((N, heads, dim, bs), dtype=torch.uint8, device="cuda")
+    c, q, off, lens, table = setup([1, 2], [700, 300], 16, 8, dim, bs, BF16, 15)
+    n = c.sizes[0]
+    far = np.arange(N - n, N)
+    big_k[far], big_v[far] = c.gk.view(torch.uint8), c.gv.view(torch.uint8)
+    ks, vs = torch.ones(2, N, heads, device="cuda")
+    ks[far], vs[far] = c.gks, c.gvs
+    moved = i32(np.where(table >= 0, table + N - n, table))
+    parts = big_k.view(_lib._F8), big_v.view(_lib._F8), ks, vs
+    a, _ = _lib.lik_cache_attention(q, i32(off), i32(lens), moved, *parts)
+    b, _ = _lib.lik_cache_attention(q, i32(off), i32(lens), i32(table), *c.parts)
+    assert torch.equal(a, b)
+    k, v = tokens(5, heads, dim, BF16, 1)
+    slots = [(N - 1) * bs + 100 + i for i in range(5)]
+    _lib.lik_cache_append(k, v, i32(slots), *parts)
+    _lib.lik_cache_append(k, v, i32([(n - 1) * bs + 100 + i for i in range(5)]), *c.parts)
+    assert torch.equal(big_k[N - 1], c.gk.view(torch.uint8)[n - 1]) and torch.equal(big_v[N - 1], c.gv.view(torch.uint8)[n - 1])
+
+
+def test_results_do_not_change():
+    c, q, off, lens, table = setup([1, 3, 1, 90], [2000, 900, 30, 700], 8, 2, 128, 16, BF16, 21)
+    a = _lib.lik_cache_attention(q, i32(off), i32(lens), i32(table), *c.parts, want_lse=True)
+    for _ in range(3):
+        b = _lib.lik_cache_attention(q, i32(off), i32(lens), i32(table), *c.parts, want_lse=True)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_binding_on_the_gpu():
+    c, q, off, lens, table = setup([1, 3], [20, 9], 4, 2, 64, 16, BF16, 22)
+    off, lens, table = i32(off), i32(lens), i32(table)
+    bad = [(dict(q=q.double()), "float16"), (dict(q=q[:, :3]), "dense heads|multiple"), (dict(q_offsets=off[:2]), "shape"),
+           (dict(kv_len=lens.long()), "int32"), (dict(block_table=table[:1]), "block_table"),
+           (dict(out=torch.empty_like(q, dtype=F16)), "out must"), (dict(kv_len=lens.cpu()), "must be on"),
+           (dict(scale=0.0), "scale"), (dict(out=q), "overlaps"), (dict(k_scale=c.gks[:, :1]), "k_scale")]
+    good = dict(q=q, q_offsets=off, kv_len=lens, block_table=table, k_cache=c.gk, v_cache=c.gv, k_scale=c.gks,
+                v_scale=c.gvs)
+    for kw, msg in bad:
+        with pytest.raises((ValueError, _lib.LikError), match=msg):
+            _lib.lik_cache_attention(**{**good, **kw})
+    k, v = tokens(4, 2, 64, BF16, 1)
+    slots = i32([0, 1, 2, 3])
+    for a, msg in (((k, v[:3], slots), "shape"), ((k, v, slots[:2]), "shape"), ((k, v.half(), slots), "type"),
+                   ((k[:, :1], v[:, :1], slots), "shape"), ((k, v, slots.long()), "int32")):
+        with pytest.raises(ValueError, match=msg):
+            _lib.lik_cache_append(*a, *c.parts)
+    with pytest.raises(ValueError, match="contiguous"):
+        _lib.lik_cache_tables(lens, lens, table, i32(range(8))[::2], i32([0, 4, 0, 0]), 16, 4)
+    with pytest.raises(_lib.LikError, match="overlaps"):
+        _lib.lik_cache_tables(lens, lens, table, lens, i32([0, 2, 0, 0]), 16, 4)
+    with pytest.raises(_lib.LikError, match="block_size"):
+        _lib.lik_cache_tables(lens, lens, table, i32(range(8)), i32([0, 4, 0, 0]), 20, 4)
