@@ -90,6 +90,7 @@ __device__ __forceinline__ f32x4 mma(half8 a, half8 b, f32x4 c) {
 struct Split {
   int workers;
   int least;                             // fewest tiles a range
+  int64_t tiles;                         // most row tiles of a head
 };
 
 // One request.
@@ -112,60 +113,130 @@ __device__ __forceinline__ Request request_of(const AttendArgs& a, int s) {
   return r;
 }
 
-// The numbering of a head's work, found by the 256 threads of a workgroup: sums
-// over buckets of requests, and the range of a worker.
+// Where a unit of a head's work lies.
+struct Unit {
+  int s;                                 // request
+  int64_t first;                         // units before the request
+  int tile0;                             // row tiles before the request
+  Request r;
+};
+
+// The numbering of a head's work: sums over the requests by a lane each, or, from
+// 65 requests on, over buckets of them by a thread each.
+template <int M>
 struct Plan {
   int64_t total, chunk;
-  int per;                               // requests a bucket
-  const int64_t* before;                 // [257] units before each bucket, in LDS
-};
-template <int M>
-__device__ __forceinline__ Plan make_plan(const AttendArgs& a, const Split& sp, int64_t* lds) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  Plan p;
-  p.per = (a.S + 255) / 256;
-  int64_t units = 0;
-  const int first = tid * p.per, last = first + p.per < a.S ? first + p.per : a.S;
-  for (int s = first; s < last; ++s) {
-    const Request r = request_of<M>(a, s);
-    units += (int64_t)r.row_tiles * r.kv_tiles;
-  }
-  int64_t x = units;
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) {
-    const int64_t y = __shfl_up(x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 63) lds[257 + wave] = x;
-  __syncthreads();
-  for (int w = 0; w < wave; ++w) x += lds[257 + w];
-  lds[tid + 1] = x;
-  if (tid == 0) lds[0] = 0;
-  __syncthreads();
-  p.before = lds;
-  p.total = lds[256];
-  p.chunk = (p.total + sp.workers - 1) / sp.workers;
-  if (p.chunk < sp.least) p.chunk = sp.least;
-  return p;
-}
+  int tiles, per;                        // row tiles; requests a bucket
+  int64_t upto;                          // up to 64 requests: units up to the lane's
+  int tiles_upto;
+  Request mine;
+  const int64_t* before;                 // [257] units, and row tiles, before each bucket, in LDS
+  const int* tiles_before;
 
-// The request that holds unit u, and the units before it.
-template <int M>
-__device__ __forceinline__ void find_unit(const AttendArgs& a, const Plan& p, int64_t u, int* s,
-                                          int64_t* pos, Request* r) {
-  int b = 0;
+  __device__ __forceinline__ void make(const AttendArgs& a, const Split& sp, int64_t* lds) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const bool few = a.S <= 64;
+    per = few ? 1 : (a.S + 255) / 256;
+    int64_t units = 0;
+    int t = 0;
+    mine = Request{0, 0, 0, 0, 0, 1};
+    if (few) {
+      if (lane < a.S) mine = request_of<M>(a, lane);
+      units = (int64_t)mine.row_tiles * mine.kv_tiles;
+      t = mine.row_tiles;
+    } else {
+      const int lo = tid * per, hi = lo + per < a.S ? lo + per : a.S;
+      for (int s = lo; s < hi; ++s) {
+        const Request r = request_of<M>(a, s);
+        units += (int64_t)r.row_tiles * r.kv_tiles;
+        t += r.row_tiles;
+      }
+    }
 #pragma unroll
-  for (int step = 128; step > 0; step /= 2)
-    if (p.before[b + step] <= u) b += step;
-  *s = b * p.per;
-  *pos = p.before[b];
-  for (;; ++*s) {
-    *r = request_of<M>(a, *s);
-    const int64_t units = (int64_t)r->row_tiles * r->kv_tiles;
-    if (u < *pos + units || *s + 1 >= a.S) return;
-    *pos += units;
+    for (int o = 1; o < 64; o *= 2) {
+      const int64_t y = __shfl_up(units, o);
+      const int z = __shfl_up(t, o);
+      if (lane >= o) {
+        units += y;
+        t += z;
+      }
+    }
+    if (few) {
+      upto = units;
+      tiles_upto = t;
+      total = __shfl(units, 63);
+      tiles = __shfl(t, 63);
+    } else {
+      int* lds_t = (int*)(lds + 261);
+      if (lane == 63) {
+        lds[257 + wave] = units;
+        lds_t[257 + wave] = t;
+      }
+      __syncthreads();
+      for (int w = 0; w < wave; ++w) {
+        units += lds[257 + w];
+        t += lds_t[257 + w];
+      }
+      lds[tid + 1] = units;
+      lds_t[tid + 1] = t;
+      if (tid == 0) {
+        lds[0] = 0;
+        lds_t[0] = 0;
+      }
+      __syncthreads();
+      before = lds;
+      tiles_before = lds_t;
+      total = lds[256];
+      tiles = lds_t[256];
+    }
+    total = uniform(total);
+    tiles = __builtin_amdgcn_readfirstlane(tiles);
+    if (total < (int64_t(1) << 31))
+      chunk = ((uint32_t)total + (uint32_t)sp.workers - 1) / (uint32_t)sp.workers;
+    else chunk = (total + sp.workers - 1) / sp.workers;
+    if (chunk < sp.least) chunk = sp.least;
   }
-}
+
+  static __device__ __forceinline__ int64_t uniform(int64_t x) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)x);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)x >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+  }
+  // The request of this lane's number, for all lanes.
+  __device__ __forceinline__ void get(const AttendArgs& a, int s, Unit* u) const {
+    u->s = s;
+    if (a.S > 64) {
+      u->r = request_of<M>(a, s);
+      return;
+    }
+    const auto at = [&](int x) { return __builtin_amdgcn_readlane(x, s); };
+    u->r = Request{at(mine.q0), at(mine.n), at(mine.len), at(mine.rows), at(mine.row_tiles),
+                   at(mine.kv_tiles)};
+  }
+  // The request that holds unit x < total.
+  __device__ __forceinline__ void find(const AttendArgs& a, int64_t x, Unit* u) const {
+    if (a.S <= 64) {
+      const int s = __builtin_ctzll(__ballot(upto > x));
+      get(a, s, u);
+      u->first = uniform(__shfl(upto, s)) - (int64_t)u->r.row_tiles * u->r.kv_tiles;
+      u->tile0 = __builtin_amdgcn_readlane(tiles_upto, s) - u->r.row_tiles;
+      return;
+    }
+    int b = 0;
+#pragma unroll
+    for (int step = 128; step > 0; step /= 2)
+      if (before[b + step] <= x) b += step;
+    u->first = before[b];
+    u->tile0 = tiles_before[b];
+    for (int s = b * per;; ++s) {
+      get(a, s, u);
+      const int64_t units = (int64_t)u->r.row_tiles * u->r.kv_tiles;
+      if (x < u->first + units || s + 1 >= a.S) return;
+      u->first += units;
+      u->tile0 += u->r.row_tiles;
+    }
+  }
+};
 
 // Positions that a row of a request attends to.
 __device__ __forceinline__ int seen_of(const Request& r, int row, int group) {
@@ -180,18 +251,34 @@ __device__ __forceinline__ int tiles_of(const Request& r, int t, int group) {
   return seen > 0 ? (seen + kTile - 1) / kTile : 1;
 }
 
-// Partial sums in the workspace: [head][worker][2] row tiles of M rows.
+// The workspace: [head][worker][2] row tiles of M rows of sums, a worker's first and
+// a later one that it does not end; for every row tile that lies in several ranges
+// where its parts are, and how many row tiles there are.
+struct Piece {
+  int q0, row0, rows, at, n, pad;        // at: first worker * 2 + slot; the others' are slot 0
+};
 struct Partial {
   float* o;                              // [M][D]
   float2* ml;                            // [M]: m, l
 };
 template <int M, int D>
-__device__ __forceinline__ Partial partial_at(char* ws, const AttendArgs& a, const Split& sp,
-                                              int head, int64_t worker, int slot) {
-  const int64_t n = (int64_t)a.kv_heads * sp.workers * 2;
-  const int64_t i = ((int64_t)head * sp.workers + worker) * 2 + slot;
-  return {(float*)ws + i * M * D, (float2*)((float*)ws + n * M * D) + i * M};
-}
+struct Space {
+  char* ws;
+  int64_t parts, tiles;                  // parts of all heads; most row tiles of a head
+  __device__ __host__ Space(char* w, int64_t kv_heads, const Split& sp)
+      : ws(w), parts(kv_heads * sp.workers * 2), tiles(sp.tiles) {}
+  __device__ Partial part(const Split& sp, int head, int64_t i) const {
+    i += (int64_t)head * sp.workers * 2;
+    return {(float*)ws + i * M * D, (float2*)((float*)ws + parts * M * D) + i * M};
+  }
+  __device__ int* count() const { return (int*)(ws + parts * M * (D + 2) * 4); }
+  __device__ Piece* piece(int head, int64_t tile) const {
+    return (Piece*)(count() + 4) + head * tiles + tile;
+  }
+  int64_t bytes(int64_t kv_heads) const {
+    return parts * M * (D + 2) * 4 + 16 + kv_heads * tiles * (int64_t)sizeof(Piece);
+  }
+};
 
 template <typename T>
 __device__ __forceinline__ void store4(T* p, float a, float b, float c, float d) {
@@ -259,38 +346,67 @@ struct RowTile {
     }
   }
 
-  __device__ __forceinline__ void run(const AttendArgs& a, int s, int len, int head, int kt0,
-                                      int kt1, int open, int lane) {
-    const int c = lane & 15, j = lane >> 4, bs = a.block_size;
-    const int shift = __builtin_ctz(bs);
-    const int32_t* table = a.table + (int64_t)s * a.table_ld;
-    const uint8_t* kb = a.k.codes + (int64_t)head * bs * D + j * 16;
-    const uint8_t* vb = a.v.codes + ((int64_t)head * D + c) * bs;
-    for (int kt = kt0; kt < kt1; ++kt) {
-      const int base = kt * kTile;
-      // the lane's own block (16 j), and that of the key row it loads (4 rows each)
-      const int tj = base + j * 16, tk = base + (c >> 2) * 16;
-      int bj = tj < len ? table[tj >> shift] : -1;
-      int bk = tk < len ? table[tk >> shift] : -1;
-      const bool there = (unsigned)bj < (unsigned)a.num_blocks;
-      if (!there) bj = 0;
-      if ((unsigned)bk >= (unsigned)a.num_blocks) bk = 0;
-      const uint8_t* kp = kb + (int64_t)bk * a.k.stride + ((tk & (bs - 1)) + (c & 3)) * D;
-      const uint8_t* vp = vb + (int64_t)bj * a.v.stride + (tj & (bs - 1));
-      u32x4 kr[4][NI], vr[ND];
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-        for (int i = 0; i < NI; ++i) kr[tt][i] = *(const u32x4*)(kp + tt * 4 * D + i * 64);
-#pragma unroll
-      for (int d = 0; d < ND; ++d) vr[d] = *(const u32x4*)(vp + d * 16 * bs);
-      float ks = clamp_scale(a.k.scale[(int64_t)bj * a.kv_heads + head]);
-      float vs = clamp_scale(a.v.scale[(int64_t)bj * a.kv_heads + head]);
-      const bool no_keys = there && ks != ks, no_values = there && vs != vs;
-      if (ks != ks) ks = 1.0f;
-      if (vs != vs) vs = 1.0f;
-      const float lv = __builtin_amdgcn_logf(vs), iv = __builtin_amdgcn_rcpf(vs);
+  // What a tile of 64 tokens brings: the blocks of the lane's own tokens and of the key
+  // row that it loads, 16-byte pieces of keys and values, the scales.
+  struct Blocks {
+    int own, key;
+  };
+  u32x4 kr[4][NI], vr[ND];
+  float ks, vs;
 
+  struct Cursor {
+    const AttendArgs& a;
+    const int32_t* table;
+    const uint8_t *kb, *vb;
+    int head, len, lane, shift;
+    __device__ __forceinline__ Cursor(const AttendArgs& a_, int s, int len_, int head_, int lane_)
+        : a(a_), table(a_.table + (int64_t)s * a_.table_ld), head(head_), len(len_), lane(lane_),
+          shift(__builtin_ctz(a_.block_size)) {
+      kb = a.k.codes + (int64_t)head * a.block_size * D + (lane >> 4) * 16;
+      vb = a.v.codes + ((int64_t)head * D + (lane & 15)) * a.block_size;
+    }
+    __device__ __forceinline__ int own(int kt) const { return kt * kTile + (lane >> 4) * 16; }
+    __device__ __forceinline__ int key(int kt) const { return kt * kTile + (lane & 15) / 4 * 16; }
+    __device__ __forceinline__ Blocks blocks(int kt) const {
+      Blocks b{-1, -1};
+      if (own(kt) < len) b.own = table[own(kt) >> shift];
+      if (key(kt) < len) b.key = table[key(kt) >> shift];
+      return b;
+    }
+    __device__ __forceinline__ bool there(int block) const {
+      return (unsigned)block < (unsigned)a.num_blocks;
+    }
+  };
+  __device__ __forceinline__ void load_keys(const Cursor& c, const Blocks& b, int kt) {
+    const int key = c.there(b.key) ? b.key : 0, own = c.there(b.own) ? b.own : 0;
+    const int o = (c.key(kt) & (c.a.block_size - 1)) + (c.lane & 3);
+    const uint8_t* p = c.kb + (int64_t)key * c.a.k.stride + o * D;
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) kr[tt][i] = *(const u32x4*)(p + tt * 4 * D + i * 64);
+    ks = c.a.k.scale[(int64_t)own * c.a.kv_heads + c.head];
+    vs = c.a.v.scale[(int64_t)own * c.a.kv_heads + c.head];
+  }
+  __device__ __forceinline__ void load_values(const Cursor& c, const Blocks& b, int kt) {
+    const int own = c.there(b.own) ? b.own : 0;
+    const uint8_t* p =
+        c.vb + (int64_t)own * c.a.v.stride + (c.own(kt) & (c.a.block_size - 1));
+#pragma unroll
+    for (int d = 0; d < ND; ++d) vr[d] = *(const u32x4*)(p + d * 16 * c.a.block_size);
+  }
+
+  // Tiles kt0 .. kt1 - 1.  `now` and `next`: the blocks of kt0, whose keys and values
+  // are on their way, and of kt0 + 1.  The next tile's keys are asked for when this
+  // one's are used up, its values behind this one's, its blocks a tile before.
+  __device__ __forceinline__ void run(const Cursor& cur, Blocks now, Blocks next, int kt0, int kt1,
+                                      int open) {
+    const int j = cur.lane >> 4;
+    for (int kt = kt0; kt < kt1; ++kt) {
+      const int base = kt * kTile, tj = base + j * 16;
+      const bool there = cur.there(now.own);
+      Blocks after{-1, -1};
+      if (kt + 2 < kt1) after = cur.blocks(kt + 2);
       f32x4 sc[MT][4];
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
@@ -305,10 +421,19 @@ struct RowTile {
             for (int mt = 0; mt < MT; ++mt) sc[mt][tt] = mma(k8, q[part][mt][i], sc[mt][tt]);
         }
       }
+      ks = clamp_scale(ks);
+      vs = clamp_scale(vs);
+      const bool no_keys = there && ks != ks, no_values = there && vs != vs;
+      const float kf = ks != ks ? 1.0f : ks;
+      const float vf = vs != vs ? 1.0f : vs;
+      const float lv = __builtin_amdgcn_logf(vf), iv = __builtin_amdgcn_rcpf(vf);
+      __builtin_amdgcn_sched_barrier(0);
+      if (kt + 1 < kt1) load_keys(cur, next, kt + 1);
+      __builtin_amdgcn_sched_barrier(0);
       // tokens behind a row's own, behind the length, or in no block
       const bool all = __all(there) && base + kTile <= open;
       if (!all) {
-        const int valid = there ? len - tj : 0;
+        const int valid = there ? cur.len - tj : 0;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           const int lim = there ? seen[mt] - tj : 0;
@@ -355,7 +480,7 @@ struct RowTile {
         for (int tt = 1; tt < 4; ++tt)
           top = fmaxf(top, fmaxf(fmaxf(sc[mt][tt][0], sc[mt][tt][1]),
                                  fmaxf(sc[mt][tt][2], sc[mt][tt][3])));
-        float cf = factor[mt] * ks;
+        float cf = factor[mt] * kf;
         if (cf < 0x1p-126f) cf = 0x1p-126f;          // -inf * 0 would be NaN
         want[mt] = row_max4(fmaf(top, cf, lv));
         moves |= want[mt] > m[mt] + kSlack;
@@ -375,7 +500,7 @@ struct RowTile {
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        float cf = factor[mt] * ks;
+        float cf = factor[mt] * kf;
         if (cf < 0x1p-126f) cf = 0x1p-126f;
         float shiftv = lv - (m[mt] == kNegInf ? 0.0f : m[mt]);
         // The product below is exact and m is rounded: they are apart by up to 2^-24 |m|.
@@ -415,6 +540,11 @@ struct RowTile {
             for (int mt = 0; mt < MT; ++mt) o[mt][d] = mma(v8, p[part][mt][half], o[mt][d]);
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
+      if (kt + 1 < kt1) load_values(cur, next, kt + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      now = next;
+      next = after;
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) l[mt] = row_sum4(l[mt]);
@@ -474,115 +604,167 @@ __device__ __forceinline__ void clear_outside(const AttendArgs& a, int64_t threa
 }
 
 template <typename T, int D, int MT>
-__global__ __launch_bounds__(256, 2) void attend_kernel(AttendArgs a, Split sp, char* ws) {
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_kernel(AttendArgs a, Split sp, char* ws) {
   constexpr int M = 16 * MT;
-  __shared__ int64_t lds[261];
+  __shared__ int64_t lds[261 + 131];
   const int head = blockIdx.x % a.kv_heads, lane = threadIdx.x & 63;
   clear_outside<T>(a, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
   if (a.S == 0) return;
-  const Plan plan = make_plan<M>(a, sp, lds);
+  Plan<M> plan;
+  plan.make(a, sp, lds);
+  const Space<M, D> space(ws, a.kv_heads, sp);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *space.count() = plan.tiles;
   const int64_t worker = (int64_t)(blockIdx.x / a.kv_heads) * 4 +
                          __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   int64_t u = worker * plan.chunk;
   const int64_t u0 = u, u1 = u + plan.chunk < plan.total ? u + plan.chunk : plan.total;
   if (u >= u1) return;
   const int group = a.q_heads / a.kv_heads;
-  int s;
-  int64_t pos;
-  Request r;
-  find_unit<M>(a, plan, u, &s, &pos, &r);
+  Unit at;
+  plan.find(a, u, &at);
   while (u < u1) {
+    const Request& r = at.r;
     const int64_t units = (int64_t)r.row_tiles * r.kv_tiles;
-    if (u >= pos + units) {
-      pos += units;
-      if (++s >= a.S) return;
-      r = request_of<M>(a, s);
+    if (u >= at.first + units) {
+      at.first += units;
+      at.tile0 += r.row_tiles;
+      if (at.s + 1 >= a.S) return;
+      plan.get(a, at.s + 1, &at);
       continue;
     }
-    const int t = (int)((u - pos) / r.kv_tiles);
-    const int64_t first = pos + (int64_t)t * r.kv_tiles;
+    const int64_t in = u - at.first;
+    const int t = in < (int64_t(1) << 31) ? (int)((uint32_t)in / (uint32_t)r.kv_tiles)
+                                          : (int)(in / r.kv_tiles);
+    const int64_t first = at.first + (int64_t)t * r.kv_tiles;
     const int need = tiles_of<M>(r, t, group);
     const int64_t end = first + r.kv_tiles < u1 ? first + r.kv_tiles : u1;
     const int kt0 = (int)(u - first), kt1 = (int)(end - first < need ? end - first : need);
     if (kt0 < kt1) {
-      RowTile<T, D, MT> tile;
+      typedef RowTile<T, D, MT> Tile;
+      Tile tile;
+      const typename Tile::Cursor cur(a, at.s, r.len, head, lane);
+      typename Tile::Blocks now{-1, -1}, next{-1, -1};
+      if (r.len > 0) {
+        now = cur.blocks(kt0);
+        if (kt0 + 1 < kt1) next = cur.blocks(kt0 + 1);
+        tile.load_keys(cur, now, kt0);
+        tile.load_values(cur, now, kt0);
+      }
       tile.load_queries(a, r, t, head, lane);
-      const int seen0 = seen_of(r, t * M, group);
-      if (r.len > 0) tile.run(a, s, r.len, head, kt0, kt1, seen0, lane);
+      if (r.len > 0) tile.run(cur, now, next, kt0, kt1, seen_of(r, t * M, group));
       if (kt0 == 0 && kt1 == need) tile.finish(a, r, t, head, lane);
-      else tile.save(partial_at<M, D>(ws, a, sp, head, worker, u > u0), r, t, lane);
+      else tile.save(space.part(sp, head, worker * 2 + (u > u0)), r, t, lane);
+      if (kt0 == 0 && lane == 0) {
+        const int64_t last = first + need - 1;
+        const int n = kt1 == need ? 0
+                                  : (int)((last < (int64_t(1) << 31) && plan.chunk < (int64_t(1) << 31)
+                                               ? (uint32_t)last / (uint32_t)plan.chunk
+                                               : last / plan.chunk) -
+                                          worker);
+        const int rows = r.rows - t * M < M ? r.rows - t * M : M;
+        *space.piece(head, at.tile0 + t) =
+            Piece{r.q0, t * M, rows, (int)(worker * 2 + (u > u0)), n, 0};
+      }
     }
     u = end;
   }
 }
 
-// Merges the row tile that begins in a worker's range and ends in a later one's.
-// One workgroup per head and worker; most have none.
-template <typename T, int D, int MT>
-__global__ __launch_bounds__(256) void merge_kernel(AttendArgs a, Split sp, char* ws) {
-  constexpr int M = 16 * MT, L = D / 4;          // L lanes a row
-  __shared__ int64_t lds[261];
-  const int head = blockIdx.x % a.kv_heads;
-  const Plan plan = make_plan<M>(a, sp, lds);
-  const int64_t worker = blockIdx.x / a.kv_heads, u0 = worker * plan.chunk;
-  const int64_t u1 = u0 + plan.chunk;
-  if (u1 >= plan.total) return;
-  const int group = a.q_heads / a.kv_heads;
-  int s;
-  int64_t pos;
-  Request r;
-  find_unit<M>(a, plan, u1 - 1, &s, &pos, &r);
-  const int t = (int)((u1 - 1 - pos) / r.kv_tiles);
-  const int64_t first = pos + (int64_t)t * r.kv_tiles;
-  const int64_t end = first + tiles_of<M>(r, t, group);
-  if (first < u0 || end <= u1) return;
-  const int64_t last = (end - 1) / plan.chunk;
-  const int rows = r.rows - t * M < M ? r.rows - t * M : M;
-  const Partial p0 = partial_at<M, D>(ws, a, sp, head, worker, first > u0);
-  for (int i = threadIdx.x / L; i < rows; i += 256 / L) {
-    const int d = threadIdx.x % L * 4;
-    float m = p0.ml[i].x;
-    for (int64_t w = worker + 1; w <= last; ++w)
-      m = fmaxf(m, partial_at<M, D>(ws, a, sp, head, w, 0).ml[i].x);
-    const float ref = m == kNegInf ? 0.0f : m;
-    float k = exp2_fast(p0.ml[i].x - ref), l = p0.ml[i].y * k;
-    f32x4 o = *(const f32x4*)(p0.o + i * D + d) * k;
-#pragma unroll 4
-    for (int64_t w = worker + 1; w <= last; ++w) {
-      const Partial p = partial_at<M, D>(ws, a, sp, head, w, 0);
-      const float2 ml = p.ml[i];
-      k = exp2_fast(ml.x - ref);
-      l = fmaf(ml.y, k, l);
-      o += *(const f32x4*)(p.o + i * D + d) * k;
-    }
-    const int row = t * M + i, token = row / group, h = head * group + row - token * group;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    store4((T*)a.out + (int64_t)(r.q0 + token) * a.out_ld + (int64_t)h * D + d, o[0] * inv,
-           o[1] * inv, o[2] * inv, o[3] * inv);
-    if (a.lse && d == 0)
-      a.lse[(int64_t)(r.q0 + token) * a.q_heads + h] =
-          l == 0.0f ? kNegInf : (float)(kLn2 * ((double)m + log2((double)l)));
+// Merges the parts of a row tile that lies in several ranges.  Workgroup (t, head, y):
+// rows R y .. of row tile t, R of them a time; what threads are left share the parts.
+constexpr int kMergeRows = 1024;         // floats of a row times rows a workgroup
+template <typename T, int D, int MT, int NT>
+__global__ __launch_bounds__(NT) void merge_kernel(AttendArgs a, Split sp, char* ws) {
+  constexpr int M = 16 * MT, L = D / 4, R = kMergeRows / D, G0 = NT / (R * L);
+  __shared__ f32x4 sums[NT];
+  __shared__ float2 mls[NT / L];
+  const Space<M, D> space(ws, a.kv_heads, sp);
+  const int head = blockIdx.y, tile = blockIdx.x;
+  if (tile >= *space.count()) return;
+  const Piece x = *space.piece(head, tile);
+  const int i0 = blockIdx.z * R;
+  if (x.n == 0 || i0 >= x.rows) return;
+  const int here = x.rows - i0 < R ? x.rows - i0 : R;
+  // fewer rows: more groups, each with every G-th part
+  int G = G0, span = R;
+  while (span / 2 >= here) {
+    span /= 2;
+    G *= 2;
   }
+  const int lanes = threadIdx.x / L, i = i0 + lanes % span, g = lanes / span;
+  const int d = threadIdx.x % L * 4;
+  float m = kNegInf, l = 0.0f;
+  f32x4 o = {0, 0, 0, 0};
+  if (i < x.rows) {
+    const int first = x.at / 2;
+    // a part's place: its worker's slot 0, but for the first
+    const auto part = [&](int k) { return space.part(sp, head, k == 0 ? x.at : (first + k) * 2); };
+#pragma unroll 4
+    for (int k = g; k <= x.n; k += G) m = fmaxf(m, part(k).ml[i].x);
+    const float ref = m == kNegInf ? 0.0f : m;
+#pragma unroll 4
+    for (int k = g; k <= x.n; k += G) {
+      const Partial p = part(k);
+      const float2 ml = p.ml[i];
+      const float f = exp2_fast(ml.x - ref);
+      l = fmaf(ml.y, f, l);
+      o += *(const f32x4*)(p.o + i * D + d) * f;
+    }
+  }
+  if (G > 1) {
+    sums[threadIdx.x] = o;
+    if (d == 0) mls[lanes] = make_float2(m, l);
+    __syncthreads();
+    if (g > 0) return;
+    float top = m;
+    for (int k = 1; k < G; ++k) top = fmaxf(top, mls[lanes + k * span].x);
+    const float ref = top == kNegInf ? 0.0f : top, f0 = exp2_fast(m - ref);
+    o = o * f0;
+    l *= f0;
+    for (int k = 1; k < G; ++k) {
+      const float2 ml = mls[lanes + k * span];
+      const float f = exp2_fast(ml.x - ref);
+      l = fmaf(ml.y, f, l);
+      o += sums[threadIdx.x + k * span * L] * f;
+    }
+    m = top;
+  }
+  if (g > 0 || i >= x.rows) return;
+  const int group = a.q_heads / a.kv_heads, row = x.row0 + i, token = row / group;
+  const int h = head * group + row - token * group;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  store4((T*)a.out + (int64_t)(x.q0 + token) * a.out_ld + (int64_t)h * D + d, o[0] * inv,
+         o[1] * inv, o[2] * inv, o[3] * inv);
+  if (a.lse && d == 0)
+    a.lse[(int64_t)(x.q0 + token) * a.q_heads + h] =
+        l == 0.0f ? kNegInf : (float)(kLn2 * ((double)m + log2((double)l)));
 }
 
 int row_tiles_of(int64_t T, int64_t S, int64_t group) {
   return S > 0 && T * group <= 16 * S ? 1 : 2;
 }
-Split split_of(int64_t kv_heads) {
+Split split_of(int64_t T, int64_t S, int64_t q_heads, int64_t kv_heads) {
   constexpr int kWaves = 2048;           // eight a CU
-  int64_t w = (kWaves / 4 + kv_heads - 1) / kv_heads * 4;
-  return {(int)w, 1};
+  const int64_t group = q_heads / kv_heads, M = 16 * row_tiles_of(T, S, group);
+  const int64_t w = (kWaves / 4 + kv_heads - 1) / kv_heads * 4;
+  // every request has a row tile that is not full at most
+  const int64_t tiles = T * group / M + (S < T ? S : T);
+  return {(int)w, 1, tiles};
 }
 
 template <typename T, int D, int MT>
 hipError_t attend_t(const AttendArgs& a, char* ws, hipStream_t s) {
-  const Split sp = split_of(a.kv_heads);
+  const Split sp = split_of(a.T, a.S, a.q_heads, a.kv_heads);
   hipLaunchKernelGGL((attend_kernel<T, D, MT>), dim3(sp.workers / 4 * a.kv_heads), dim3(256), 0, s,
                      a, sp, ws);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.S == 0) return e;
-  hipLaunchKernelGGL((merge_kernel<T, D, MT>), dim3(sp.workers * a.kv_heads), dim3(256), 0, s, a,
-                     sp, ws);
+  // few row tiles leave room for more threads on each
+  const dim3 grid((unsigned)sp.tiles, a.kv_heads, 16 * MT * D / kMergeRows);
+  if (sp.tiles * a.kv_heads <= 512)
+    hipLaunchKernelGGL((merge_kernel<T, D, MT, 1024>), grid, dim3(1024), 0, s, a, sp, ws);
+  else
+    hipLaunchKernelGGL((merge_kernel<T, D, MT, 256>), grid, dim3(256), 0, s, a, sp, ws);
   return hipGetLastError();
 }
 
@@ -604,8 +786,16 @@ hipError_t attend_type(const AttendArgs& a, char* ws, hipStream_t s) {
 size_t attend_workspace(int64_t T, int64_t S, int64_t q_heads, int64_t kv_heads, int64_t dim,
                         lik_dtype dtype) {
   if (S == 0) return 0;
-  const int64_t M = 16 * row_tiles_of(T, S, q_heads / kv_heads);
-  return (size_t)(kv_heads * split_of(kv_heads).workers * 2 * M * (dim + 2) * 4);
+  const Split sp = split_of(T, S, q_heads, kv_heads);
+  const bool one = row_tiles_of(T, S, q_heads / kv_heads) == 1;
+  const auto bytes = [&](auto d) -> int64_t {
+    constexpr int D = decltype(d)::value;
+    return one ? Space<16, D>(nullptr, kv_heads, sp).bytes(kv_heads)
+               : Space<32, D>(nullptr, kv_heads, sp).bytes(kv_heads);
+  };
+  if (dim == 64) return (size_t)bytes(std::integral_constant<int, 64>());
+  if (dim == 128) return (size_t)bytes(std::integral_constant<int, 128>());
+  return (size_t)bytes(std::integral_constant<int, 256>());
 }
 
 hipError_t run_attend(const AttendArgs& a, char* ws, hipStream_t s) {
