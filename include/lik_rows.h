@@ -227,7 +227,7 @@ lik_status lik_preference_rows(const void* logits, lik_dtype dtype, int64_t R,
  * and q = 0 elsewhere.  draft_scale within [2^-64, 2^64] (1 with NULL).
  * accept_u [R] and sample_u [S]: float32 within [0, 1).  A NaN in accept_u does
  * not accept; a NaN in sample_u draws the token -1; a sample_u of 1 or more draws the
- * last column with w > 0, one below 0 the first.  A draft >= C has p_x = 0 (and q = 0
+ * last column with w > 0, one below 0 column 0.  A draft >= C has p_x = 0 (and q = 0
  * with NULL draft_logits).
  *   tokens [R] int32: the accepted drafts, then the drawn token; -1 in the rows
  *     behind it and outside the sequences.  They are targets for the

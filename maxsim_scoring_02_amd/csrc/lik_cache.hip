@@ -114,7 +114,7 @@ __global__ __launch_bounds__(kTablesThreads) void tables_kernel(TablesArgs a) {
     const int h = a.state[0], f = a.state[1], n = (int)(gridDim.x * gridDim.y);
     s_state[0] = N > 0 && h > 0 ? h % N : 0;
     s_state[1] = f < 0 ? 0 : (f > N ? N : f);
-    __threadfence();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
     is_last = n == 1 || atomicAdd(&a.state[2], 1) == n - 1;
   }
   __syncthreads();

@@ -124,8 +124,8 @@ size_t lik_rows_workspace_bytes(lik_rows_op op, int64_t R, int64_t C, int64_t n_
       if (n_seqs < 0 || mul_ok({n_seqs, 64}) < 0) return SIZE_MAX;
       return R == 0 || C == 0 ? 0 : lik::pref_layout(R, C, n_seqs, dtype).bytes;
     case LIK_ROWS_VERIFY:
-      if (n_seqs < 0 || mul_ok({n_seqs, 64}) < 0) return SIZE_MAX;
-      return 0;
+      if (n_seqs < 0 || n_seqs > kMaxRows) return SIZE_MAX;
+      return R == 0 || C == 0 ? 0 : lik::verify_layout(R, C, n_seqs, dtype, flags & 1).bytes;
   }
   return SIZE_MAX;
 }

@@ -207,6 +207,35 @@ struct VerifyArgs {
   int32_t* accepted;
   float* logp;
 };
+// Parts of the rows that are looked at, and of a row that a token is drawn from
+// (256 threads with at most 4 pieces of target and drafter each).
+inline Parts verify_look(int64_t R, int64_t C, lik_dtype dtype, bool drafter) {
+  return look_parts(drafter ? 2 * R : R, C, dtype);
+}
+inline Parts verify_draw(int64_t S, int64_t C, lik_dtype dtype) {
+  const int64_t step = 256 * 16 / elem_bytes_of(dtype);
+  const int64_t most = (C + step - 1) / step;
+  int64_t n = (C + step * 4 - 1) / (step * 4);
+  const int64_t want = S > 0 ? (kPartGroups + S - 1) / S : 1;
+  if (n < want) n = want < most ? want : most;
+  Parts p;
+  // a row's first and last columns are beside its whole pieces: a piece less a part
+  p.cols = (int)(((C + n - 1) / n + step - 1) / step * step);
+  p.n = (int)((C + p.cols - 1) / p.cols);
+  p.gt = 256;
+  return p;
+}
+struct VerifyLayout {
+  size_t sums, done, bytes;              // behind the parts' [rows][n] float2
+};
+inline VerifyLayout verify_layout(int64_t R, int64_t C, int64_t S, lik_dtype dtype, bool drafter) {
+  const int64_t rows = drafter ? 2 * R : R;
+  VerifyLayout w;
+  w.sums = rows_up((size_t)rows * verify_look(R, C, dtype, drafter).n * 8);
+  w.done = rows_up(w.sums + (size_t)S * verify_draw(S, C, dtype).n * 8);
+  w.bytes = rows_up(w.done + (size_t)S * 4);
+  return w;
+}
 hipError_t run_verify(const VerifyArgs& a, char* ws, hipStream_t s);
 
 }  // namespace lik

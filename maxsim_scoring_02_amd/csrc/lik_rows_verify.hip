@@ -1,4 +1,11 @@
-// Verification of drafted tokens (include/lik_rows.h, lik_verify_rows).
+// Verification of drafted tokens (include/lik_rows.h, lik_verify_rows), in two
+// launches.  The first looks at every row of target and drafter once and leaves the
+// (m, Z) of its parts.  In the second a workgroup has a part of the row that its
+// sequence ends at: it finds that row (every workgroup by itself, from the parts), sums
+// the weights w of its columns, and the last of a sequence's workgroups to be done
+// finds the part, and in it the column, that the random number points at.
+// Weights are float32, sums of them float64: a token of a vocabulary of 10^5
+// has an interval of 10^-5 and less, which float32 sums would blur.
 #include <hip/hip_runtime.h>
 
 #include "lik_rows_device.h"
@@ -8,144 +15,402 @@ namespace lik {
 
 namespace {
 
-// A row's softmax by 256 threads: its maximum, then its sum.
+// Rows of a sequence, inside [0, R).
+__device__ __forceinline__ void rows_of(const VerifyArgs& a, int64_t s, int64_t* lo, int64_t* hi) {
+  const int64_t x = a.offsets[s], y = a.offsets[s + 1];
+  *lo = x < 0 ? 0 : x;
+  *hi = y > a.R ? a.R : y;
+}
+
+// Whether a sequence ends behind row r, or r lies in none: by the threads of a group.
+template <int GT>
+__device__ __forceinline__ bool drafts_end(const VerifyArgs& a, int64_t r) {
+  bool end = false;
+  for (int64_t s = group_tid<GT>(); s <= a.S; s += GT) {
+    const int64_t x = a.offsets[s];
+    end |= x == r + 1 || (s == 0 && r < x) || (s == a.S && r >= x);
+  }
+  if constexpr (GT == 64) return __any(end);
+  return __syncthreads_or(end);
+}
+
+// Group b: a part of row b of the targets, then of the drafters.
+template <typename T, int GT, bool Once>
+__global__ __launch_bounds__(256) void verify_look_kernel(VerifyArgs a, Parts parts,
+                                                          float2* __restrict__ out,
+                                                          int* __restrict__ done) {
+  __shared__ float tmp[2 * (GT / 64)];
+  const int tid = group_tid<GT>();
+  const int64_t threads = (int64_t)gridDim.x * gridDim.y * 256;
+  for (int64_t s = linear_block() * 256 + threadIdx.x; s < a.S; s += threads) done[s] = 0;
+  const PartAt at = part_at<GT>(parts, a.C, 0);
+  const bool drafter = at.r >= a.R;
+  const int64_t r = drafter ? at.r - a.R : at.r;
+  if (r >= a.R || (drafter && !a.d)) return;
+  if (drafter) {
+    if (a.drafts[r] < 0 || drafts_end<GT>(a, r)) return;
+  } else if (at.p == 0 && tid == 0) {
+    a.tokens[r] = -1;
+    a.logp[r] = 0.0f;
+  }
+  HeldRow<T, GT, kLookPieces, Once> h;
+  h.load((drafter ? (const T*)a.d + r * a.draft_ld : (const T*)a.z + r * a.ld) + at.lo, at.cols, tid,
+         nullptr);
+  const RowSoft s = held_softmax<GT, true>(h, drafter ? a.draft_scale : a.scale, tmp);
+  if (tid == 0) out[at.r * parts.n + at.p] = make_float2(s.m, s.Z);
+}
+
+// A row against its draft.
+struct Verdict {
+  RowSoft p, q;
+  double ln_sum;
+  bool more, broken, taken;
+};
 template <typename T>
-__device__ RowSoft block_softmax(const T* row, int C, float scale, double* tmp) {
-  __shared__ float top[4];
-  float m = -kInf;
-  for (int c = threadIdx.x; c < C; c += 256) m = fmaxf(m, (float)row[c]);
-  m = wave_max(m);
-  if ((threadIdx.x & 63) == 0) top[wave_id()] = m;
+__device__ __forceinline__ Verdict judge(const VerifyArgs& a, const float2* mz, int n, int64_t r,
+                                         int64_t hi) {
+  Verdict v;
+  const int x = a.drafts[r];
+  v.more = r + 1 < hi && x >= 0;
+  const bool in = v.more && x < a.C;
+  const float zx = in ? (float)((const T*)a.z)[r * a.ld + x] : 0.0f;
+  const float u = v.more ? a.accept_u[r] : 0.0f;
+  v.p = merge_parts(mz + r * n, n, a.scale);
+  v.q = v.p;
+  double qx = 1.0;
+  if (a.d && v.more) {
+    const float dx = in ? (float)((const T*)a.d)[r * a.draft_ld + x] : 0.0f;
+    v.q = merge_parts(mz + (a.R + r) * n, n, a.draft_scale);
+    qx = in ? (double)row_exp(v.q, dx) / (double)v.q.Z : 0.0;
+  }
+  const double px = in ? (double)row_exp(v.p, zx) / (double)v.p.Z : 0.0;
+  v.broken = v.p.Z != v.p.Z || v.q.Z != v.q.Z;
+  v.taken = v.more && !v.broken && (double)u * qx < px;
+  v.ln_sum = row_ln_sum(v.p);
+  return v;
+}
+
+// The weights of a row's columns.
+template <typename T>
+struct Weights {
+  const T *row, *drow;                   // drow: null without a drafter's row
+  RowSoft p, q;
+  float ip, iq;
+  int x;                                 // a draft without a drafter's row, or -1
+
+  __device__ __forceinline__ float of(float z, float d, int c) const {
+    const float pc = row_exp(p, z) * ip;
+    if (drow) return fmaxf(pc - row_exp(q, d) * iq, 0.0f);
+    return c == x ? fmaxf(pc - 1.0f, 0.0f) : pc;
+  }
+  __device__ __forceinline__ float at(int c) const {
+    return of((float)row[c], drow ? (float)drow[c] : 0.0f, c);
+  }
+};
+
+constexpr int kVerifyPieces = 4;
+
+// A part's weights by 256 threads, as 16-byte pieces of the row: sums a piece, the
+// columns before the first and behind the last whole piece first and last.
+template <typename T>
+struct PartWeights {
+  static constexpr int NV = kVerifyPieces, N = PieceOf<T>::N, kSlots = NV + 2;
+  HeldRow<T, 256, NV, false> z, d;
+
+  __device__ __forceinline__ void load(const Weights<T>& w, int lo, int cols) {
+    z.load(w.row + lo, cols, threadIdx.x, nullptr);
+    if (w.drow) d.load(w.drow + lo, cols, threadIdx.x, w.row + lo);
+  }
+  // Weights of piece i in order.
+  __device__ __forceinline__ void piece_of(const Weights<T>& w, int lo, int i, float* f) const {
+    float g[N] = {};
+    unpack<T>(z.d[i], f);
+    if (w.drow) unpack<T>(d.d[i], g);
+    const int c = lo + z.deal.column(i);
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] = w.of(f[j], g[j], c + j);
+  }
+  __device__ __forceinline__ float edge_of(const Weights<T>& w, int lo) const {
+    return w.of(z.edge, w.drow ? d.edge : 0.0f, lo + z.deal.edge());
+  }
+  // This thread's sum in slot k.
+  __device__ __forceinline__ double slot(const Weights<T>& w, int lo, int k) const {
+    if (k == 0 || k == kSlots - 1) {
+      const bool head = threadIdx.x < (unsigned)z.deal.head;
+      return z.deal.has_edge() && head == (k == 0) ? (double)edge_of(w, lo) : 0.0;
+    }
+    if (!z.deal.has(k - 1)) return 0.0;
+    float f[N];
+    piece_of(w, lo, k - 1, f);
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) sum += (double)f[j];
+    return sum;
+  }
+  __device__ __forceinline__ int column_of(int k) const {
+    return k == 0 || k == kSlots - 1 ? z.deal.edge() : z.deal.column(k - 1);
+  }
+};
+
+// Sum over the lanes up to this one.
+__device__ __forceinline__ double lane_scan(double v) {
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) {
+    const double y = __shfl_up(v, o);
+    if ((threadIdx.x & 63) >= (unsigned)o) v += y;
+  }
+  return v;
+}
+
+// The column of a part at which the running sum passes `goal`; the last with a
+// weight where rounding, or a goal beyond the part, leaves none.
+template <typename T>
+__device__ int pick(const Weights<T>& w, int lo, int cols, double goal, double* tmp, int* found) {
+  typedef PartWeights<T> P;
+  P part;
+  part.load(w, lo, cols);
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  double v[P::kSlots];
+#pragma unroll
+  for (int k = 0; k < P::kSlots; ++k) {
+    v[k] = part.slot(w, lo, k);
+    const double sum = wave_sum(v[k]);
+    if (lane == 0) tmp[k * 4 + wave] = sum;
+  }
+  if (threadIdx.x == 0) *found = -1;
   __syncthreads();
-  m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-  RowSoft s = row_ref(m, scale);
-  double Z = 0.0;
-  for (int c = threadIdx.x; c < C; c += 256) Z += (double)row_exp(s, (float)row[c]);
-  s.Z = (float)block_sum(Z, tmp);
-  if (m == -kInf) s.Z = __builtin_nanf("");
-  return s;
+  double before = 0.0, at_before = 0.0;
+  int at = -1, last = -1;
+  for (int k = 0; k < P::kSlots * 4 && at < 0; ++k) {
+    const double sum = tmp[k];
+    if (sum > 0.0) last = k;
+    if (before + sum > goal) {
+      at = k;
+      at_before = before;
+    }
+    before += sum;
+  }
+  const bool beyond = at < 0;
+  if (beyond) at = last;
+  if (at < 0) return -1;
+  if (wave == at % 4) {
+    const int k = at / 4;
+    double mine = 0.0;
+#pragma unroll
+    for (int i = 0; i < P::kSlots; ++i)
+      if (i == k) mine = v[i];
+    const double upto = at_before + lane_scan(mine);
+    const uint64_t over = beyond ? 0 : __ballot(upto > goal), some = __ballot(mine > 0.0);
+    const int who = over ? __builtin_ctzll(over) : 63 - __builtin_clzll(some | 1);
+    if (lane == who) {
+      int c = lo + part.column_of(k), hit = c;
+      if (k > 0 && k < P::kSlots - 1) {
+        double run = upto - mine;
+        hit = -1;
+        int positive = c;
+        for (int j = 0; j < P::N; ++j) {
+          const float x = w.at(c + j);
+          run += (double)x;
+          if (x > 0.0f) positive = c + j;
+          if (over && hit < 0 && run > goal) hit = c + j;
+        }
+        if (hit < 0) hit = positive;
+      }
+      *found = hit;
+    }
+  }
+  __syncthreads();
+  return *found;
 }
 
-// One workgroup per sequence, row after row.
+struct VerifySpace {
+  float2* mz;                            // [2 R][parts of a row]
+  double* sums;                          // [S][parts of a drawn row]
+  int* done;                             // [S]
+};
+
 template <typename T>
-__global__ __launch_bounds__(256) void verify_kernel(VerifyArgs a, const T* z, const T* d) {
-  __shared__ double tmp[4], wave_tot[4];
-  __shared__ int found;
-  const int64_t s = linear_block();
-  const int tid = threadIdx.x;
+__global__ __launch_bounds__(256) void verify_draw_kernel(VerifyArgs a, int look, Parts parts,
+                                                          VerifySpace ws) {
+  __shared__ double tmp[PartWeights<T>::kSlots * 4];
+  __shared__ RowSoft soft[2][4];
+  __shared__ double ln_sums[4];
+  __shared__ int flags[4], last, found;
+  const int64_t s = linear_block() / parts.n;
   if (s >= a.S) return;
-  int64_t lo = a.offsets[s], hi = a.offsets[s + 1];
-  if (lo < 0) lo = 0;
-  if (hi > a.R) hi = a.R;
+  const int part = (int)(linear_block() - s * parts.n);
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
+  int64_t lo, hi;
+  rows_of(a, s, &lo, &hi);
   if (hi <= lo) {
-    if (tid == 0) a.accepted[s] = 0;
+    if (part == 0 && tid == 0) a.accepted[s] = 0;
     return;
   }
+  // four rows at a time, a wave each, until one does not accept
   int64_t r = lo;
-  for (;; ++r) {
-    const int x = a.drafts[r];
-    const bool more = r + 1 < hi && x >= 0;
-    const T* row = z + r * a.ld;
-    const T* drow = d ? d + r * a.draft_ld : nullptr;
-    const RowSoft p = block_softmax(row, a.C, a.scale, tmp);
-    RowSoft q = p;
-    if (drow && more) q = block_softmax(drow, a.C, a.draft_scale, tmp);
-    const double ln_sum = row_ln_sum(p);
-    const bool broken = p.Z != p.Z || q.Z != q.Z;
-    if (more && !broken) {
-      const bool in = x < a.C;
-      const double px = in ? (double)row_exp(p, (float)row[x]) / (double)p.Z : 0.0;
-      double qx = 1.0;
-      if (drow) qx = in ? (double)row_exp(q, (float)drow[x]) / (double)q.Z : 0.0;
-      if ((double)a.accept_u[r] * qx < px) {
-        if (tid == 0) {
-          a.tokens[r] = x;
-          a.logp[r] = (float)row_logp(p, (float)row[x], a.scale, ln_sum);
-        }
-        continue;
-      }
+  int how = 0;
+  for (int64_t r0 = lo;; r0 += 4) {
+    Verdict v;
+    v.taken = false;
+    const bool there = r0 + wave < hi;
+    if (there) v = judge<T>(a, ws.mz, look, r0 + wave, hi);
+    if (lane == 0) {
+      flags[wave] = there ? (v.taken ? 4 : 0) | (v.more ? 1 : 0) | (v.broken ? 2 : 0) : 0;
+      soft[0][wave] = v.p;
+      soft[1][wave] = v.q;
+      ln_sums[wave] = v.ln_sum;
     }
-    // the row that a token is drawn from
-    const auto weight = [&](int c, int how) {
-      const float pc = row_exp(p, (float)row[c]) / p.Z;
-      if (how == 0) return pc;
-      const float qc = drow ? row_exp(q, (float)drow[c]) / q.Z : (c == x ? 1.0f : 0.0f);
-      return fmaxf(pc - qc, 0.0f);
-    };
-    int token = -1;
-    const double u = a.sample_u[s];
-    if (!broken && u == u) {
-      int how = more;
-      double total = 0.0;
-      for (;; how = 0) {
-        double sum = 0.0;
-        for (int c = tid; c < a.C; c += 256) sum += (double)weight(c, how);
-        total = block_sum(sum, tmp);
-        if (total > 0.0 || !how) break;
-      }
-      const double goal = u * total;
-      double before = 0.0;
-      int last = -1;
-      for (int c0 = 0; c0 < a.C && token < 0; c0 += 256) {
-        const int c = c0 + tid;
-        const float w = c < a.C ? weight(c, how) : 0.0f;
-        double upto = w;
-        for (int o = 1; o < 64; o *= 2) {
-          const double y = __shfl_up(upto, o);
-          if ((tid & 63) >= o) upto += y;
-        }
-        if ((tid & 63) == 63) wave_tot[tid >> 6] = upto;
-        if (tid == 0) found = INT32_MAX;
-        __syncthreads();
-        for (int k = 0; k < (tid >> 6); ++k) upto += wave_tot[k];
-        if (c < a.C && before + upto > goal) atomicMin(&found, c);
-        if (c < a.C && w > 0.0f) last = c;
-        __syncthreads();
-        if (found != INT32_MAX) token = found;
-        before += wave_tot[0] + wave_tot[1] + wave_tot[2] + wave_tot[3];
-        __syncthreads();
-      }
-      if (token < 0) {               // u of 1 and more
-        if (tid == 0) found = -1;
-        __syncthreads();
-        atomicMax(&found, last);
-        __syncthreads();
-        token = found;
-      }
+    __syncthreads();
+    int w = 0;
+    while (w < 4 && (flags[w] & 4)) ++w;
+    if (part == 0 && lane == 0 && wave < w) {
+      const int x = a.drafts[r0 + wave];
+      a.tokens[r0 + wave] = x;
+      a.logp[r0 + wave] = (float)row_logp(v.p, (float)((const T*)a.z)[(r0 + wave) * a.ld + x],
+                                          a.scale, v.ln_sum);
     }
-    if (tid == 0) {
-      a.tokens[r] = token;
-      a.logp[r] = token >= 0 ? (float)row_logp(p, (float)row[token], a.scale, ln_sum)
-                             : (broken ? __builtin_nanf("") : 0.0f);
-      a.accepted[s] = (int)(r - lo);
+    if (w < 4) {
+      r = r0 + w;
+      how = w;
+      break;
     }
-    return;
+    __syncthreads();
   }
-}
-
-__global__ void verify_clear_kernel(VerifyArgs a) {
-  const int64_t r = linear_block() * 256 + threadIdx.x;
-  if (r >= a.R) return;
-  a.tokens[r] = -1;
-  a.logp[r] = 0.0f;
+  const int flag = flags[how];
+  const bool more = flag & 1, broken = flag & 2;
+  const double u = (double)a.sample_u[s];
+  if (part == 0 && tid == 0) {
+    a.accepted[s] = (int)(r - lo);
+    if (broken) a.logp[r] = __builtin_nanf("");
+  }
+  if (broken || u != u) return;
+  Weights<T> w;
+  w.row = (const T*)a.z + r * a.ld;
+  w.drow = a.d && more ? (const T*)a.d + r * a.draft_ld : nullptr;
+  w.p = soft[0][how];
+  w.q = soft[1][how];
+  w.ip = 1.0f / w.p.Z;
+  w.iq = 1.0f / w.q.Z;
+  w.x = !a.d && more ? a.drafts[r] : -1;
+  const double ln_sum = ln_sums[how];
+  const auto columns = [&](int p) {
+    const int left = a.C - p * parts.cols;
+    return left < parts.cols ? left : parts.cols;
+  };
+  double* sums = ws.sums + s * parts.n;
+  if (parts.n > 1) {
+    PartWeights<T> mine;
+    mine.load(w, part * parts.cols, columns(part));
+    double sum = 0.0;
+#pragma unroll
+    for (int k = 0; k < PartWeights<T>::kSlots; ++k) sum += mine.slot(w, part * parts.cols, k);
+    sum = block_sum(sum, tmp);
+    if (tid == 0) {
+      // The sum goes past the caches by itself, and has arrived when the count moves: no
+      // cache is written back or dropped for it (a fence of the whole chip in each
+      // workgroup took 256 x 5 rows of 131072 from 435 us to what the table has).
+      __hip_atomic_store(&sums[part], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+      last = __hip_atomic_fetch_add(&ws.done[s], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+             parts.n - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+  }
+  // the sequence's last workgroup: all of w, or all of p where nothing of it is left
+  int token = -1;
+  for (int pass = 0; token < 0 && pass < 2; ++pass) {
+    double total = 0.0;
+    if (pass == 1) {                     // p as it is
+      w.drow = nullptr;
+      w.x = -1;
+    }
+    if (pass == 1 || parts.n == 1) {
+      // a part after the other, into the parts' places
+      for (int p = 0; p < parts.n; ++p) {
+        PartWeights<T> x;
+        x.load(w, p * parts.cols, columns(p));
+        double sum = 0.0;
+#pragma unroll
+        for (int k = 0; k < PartWeights<T>::kSlots; ++k) sum += x.slot(w, p * parts.cols, k);
+        sum = block_sum(sum, tmp);
+        if (tid == 0) __hip_atomic_store(&sums[p], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+      __syncthreads();
+    }
+    // every wave: a lane a part, 64 at a time
+    const auto sum_at = [&](int p) {
+      return p < parts.n
+                 ? __hip_atomic_load(&sums[p], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                 : 0.0;
+    };
+    for (int p0 = 0; p0 < parts.n; p0 += 64) total += __shfl(lane_scan(sum_at(p0 + lane)), 63);
+    if (!(total > 0.0)) continue;
+    if (u < 0.0) {
+      token = 0;
+      break;
+    }
+    const double goal = u * total;
+    double before = 0.0, at_before = 0.0, last_before = 0.0;
+    int at = -1, some = -1;
+    for (int p0 = 0; p0 < parts.n && at < 0; p0 += 64) {
+      const double mine = sum_at(p0 + lane), upto = before + lane_scan(mine);
+      const double up = __shfl_up(upto, 1), start = lane == 0 ? before : up;
+      const uint64_t over = __ballot(upto > goal && p0 + lane < parts.n);
+      const uint64_t any = __ballot(mine > 0.0);
+      if (any) {
+        const int k = 63 - __builtin_clzll(any);
+        some = p0 + k;
+        last_before = __shfl(start, k);
+      }
+      if (over) {
+        const int k = __builtin_ctzll(over);
+        at = p0 + k;
+        at_before = __shfl(start, k);
+      }
+      before = __shfl(upto, 63);
+    }
+    if (at < 0) {
+      at = some;
+      at_before = last_before;
+    }
+    __syncthreads();
+    if (at < 0) break;
+    token = pick(w, at * parts.cols, columns(at), goal - at_before, tmp, &found);
+  }
+  if (tid == 0 && token >= 0) {
+    a.tokens[r] = token;
+    a.logp[r] = (float)row_logp(w.p, (float)w.row[token], a.scale, ln_sum);
+  }
 }
 
 template <typename T>
-hipError_t verify_t(const VerifyArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(verify_clear_kernel, linear_grid((a.R + 255) / 256), dim3(256), 0, s, a);
-  hipError_t e = hipGetLastError();
+hipError_t verify_t(const VerifyArgs& a, char* ws, hipStream_t s) {
+  const int64_t rows = a.d ? 2 * a.R : a.R;
+  const Parts look = verify_look(a.R, a.C, a.dtype, a.d), draw = verify_draw(a.S, a.C, a.dtype);
+  const VerifyLayout at = verify_layout(a.R, a.C, a.S, a.dtype, a.d);
+  const VerifySpace space{(float2*)ws, (double*)(ws + at.sums), (int*)(ws + at.done)};
+  const bool once = rows * a.C * elem_bytes_of(a.dtype) > kFarBytes;
+  hipError_t e = parts_dispatch(look, [&](auto gt) {
+    constexpr int GT = decltype(gt)::value;
+    const auto kernel = once ? verify_look_kernel<T, GT, true> : verify_look_kernel<T, GT, false>;
+    hipLaunchKernelGGL(kernel, group_grid<GT>(rows * look.n), dim3(256), 0, s, a, look, space.mz,
+                       space.done);
+    return hipGetLastError();
+  });
   if (e != hipSuccess || a.S == 0) return e;
-  hipLaunchKernelGGL(verify_kernel<T>, linear_grid(a.S), dim3(256), 0, s, a, (const T*)a.z,
-                     (const T*)a.d);
+  hipLaunchKernelGGL(verify_draw_kernel<T>, linear_grid(a.S * draw.n), dim3(256), 0, s, a, look.n,
+                     draw, space);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t run_verify(const VerifyArgs& a, char* ws, hipStream_t s) {
-  if (a.dtype == LIK_F16) return verify_t<_Float16>(a, s);
-  if (a.dtype == LIK_BF16) return verify_t<__bf16>(a, s);
-  return verify_t<float>(a, s);
+  if (a.dtype == LIK_F16) return verify_t<_Float16>(a, ws, s);
+  if (a.dtype == LIK_BF16) return verify_t<__bf16>(a, ws, s);
+  return verify_t<float>(a, ws, s);
 }
 
 }  // namespace lik
