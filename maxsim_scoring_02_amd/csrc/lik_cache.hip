@@ -1,6 +1,8 @@
 // Block tables and writes of the 8-bit cache (include/lik_cache.h).
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "lik_cache_device.h"
 #include "lik_cache_kernels.h"
 
@@ -242,53 +244,301 @@ __global__ __launch_bounds__(kTablesThreads) void tables_kernel(TablesArgs a) {
 // appends
 // ---------------------------------------------------------------------------
 
-// One wave per token and head: the first token of a block in the call does the
-// block, first its keys, then its values.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+
+// Four numbers of at most 448 as codes, the first in the lowest byte.
+__device__ __forceinline__ uint32_t to_codes(float a, float b, float c, float d) {
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true);
+}
+__device__ __forceinline__ uint32_t recode(uint32_t x, float k) {
+  return to_codes(__builtin_amdgcn_cvt_f32_fp8((int)x, 0) * k, __builtin_amdgcn_cvt_f32_fp8((int)x, 1) * k,
+                  __builtin_amdgcn_cvt_f32_fp8((int)x, 2) * k, __builtin_amdgcn_cvt_f32_fp8((int)x, 3) * k);
+}
+// An unsigned maximum of float32 magnitudes, or of two 16-bit ones in each word: what is
+// not finite is larger than all that is.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  const uint32_t y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+  return y > v ? y : v;
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = dpp_max<0xB1>(v);                  // quad_perm 1,0,3,2
+  v = dpp_max<0x4E>(v);                  // quad_perm 2,3,0,1
+  v = dpp_max<0x141>(v);                 // row_half_mirror
+  v = dpp_max<0x140>(v);                 // row_mirror
+  auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = r[0] > r[1] ? r[0] : r[1];
+  r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return __builtin_amdgcn_readfirstlane((int)(r[0] > r[1] ? r[0] : r[1]));
+}
+
+// Four tokens of a row piece: 8 numbers of a lane each.
 template <typename T>
-__global__ __launch_bounds__(64) void append_kernel(AppendArgs a) {
-  const int t = blockIdx.x, h = blockIdx.y, part = blockIdx.z, lane = threadIdx.x;
-  const int bs = a.block_size, dim = a.dim;
-  const auto block_of = [&](int i) {
-    const int slot = a.slots[i];
-    return slot < 0 || slot / bs >= a.num_blocks ? -1 : slot / bs;
+struct Quad {
+  static constexpr int W = sizeof(T) / 2;        // 16-byte pieces a token
+  u32x4 raw[4][W];
+  // Two numbers over a power of two, rounded to nearest even, into the lower or upper
+  // half of a word of codes.
+  template <bool Upper>
+  static __device__ __forceinline__ s16x2 codes2(s16x2 old, uint32_t a, uint32_t b, float scale) {
+    if constexpr (W == 2)
+      return __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(old, __uint_as_float(a), __uint_as_float(b),
+                                                      scale, Upper);
+    else if constexpr (__is_same(T, __bf16)) {
+      typedef __bf16 pair __attribute__((ext_vector_type(2)));
+      return __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(old, __builtin_bit_cast(pair, a), scale, Upper);
+    } else {
+      typedef _Float16 pair __attribute__((ext_vector_type(2)));
+      return __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(old, __builtin_bit_cast(pair, a), scale, Upper);
+    }
+  }
+  // Dims 4 i .. 4 i + 3 of token k.
+  __device__ __forceinline__ uint32_t dims4(int k, int i, float scale) const {
+    s16x2 r = {0, 0};
+    if constexpr (W == 2) {
+      r = codes2<false>(r, raw[k][i][0], raw[k][i][1], scale);
+      r = codes2<true>(r, raw[k][i][2], raw[k][i][3], scale);
+    } else {
+      r = codes2<false>(r, raw[k][0][2 * i], 0, scale);
+      r = codes2<true>(r, raw[k][0][2 * i + 1], 0, scale);
+    }
+    return __builtin_bit_cast(uint32_t, r);
+  }
+  // Dim i of the four tokens.
+  __device__ __forceinline__ uint32_t tokens4(int i, float scale) const {
+    s16x2 r = {0, 0};
+    if constexpr (W == 2) {
+      r = codes2<false>(r, raw[0][i / 4][i % 4], raw[1][i / 4][i % 4], scale);
+      r = codes2<true>(r, raw[2][i / 4][i % 4], raw[3][i / 4][i % 4], scale);
+    } else {
+      const uint32_t pick = i % 2 ? 0x07060302u : 0x05040100u;
+      const auto both = [&](int k) {
+        return __builtin_amdgcn_perm(raw[k + 1][0][i / 2], raw[k][0][i / 2], pick);
+      };
+      r = codes2<false>(r, both(0), 0, scale);
+      r = codes2<true>(r, both(2), 0, scale);
+    }
+    return __builtin_bit_cast(uint32_t, r);
+  }
+  // The largest magnitude's bits as float32's.
+  __device__ __forceinline__ uint32_t largest() const {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int j = 0; j < W; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t u = raw[k][j][i];
+          if constexpr (W == 2) {
+            const uint32_t x = u & 0x7fffffffu;
+            m = x > m ? x : m;
+          } else {
+            const u16x2 x = __builtin_bit_cast(u16x2, u & 0x7fff7fffu), y = __builtin_bit_cast(u16x2, m);
+            m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(x, y));
+          }
+        }
+    if constexpr (W == 1) {
+      const uint16_t hi = (uint16_t)(m >> 16), lo = (uint16_t)m, x = hi > lo ? hi : lo;
+      if constexpr (__is_same(T, __bf16)) m = (uint32_t)x << 16;
+      else m = __float_as_uint((float)__builtin_bit_cast(_Float16, x)) & 0x7fffffffu;
+    }
+    return m;
+  }
+};
+
+// The tokens of a call that go to one block, first of them at t: a run.  A group of
+// `waves` waves (1, 2 or 4) does a run for one head and one of keys and values, in
+// tiles aligned to the block: a lane has 8 dims of 4 neighbouring tokens, so that four
+// codes of a dim are one word of the value's block, and 8 of a token two words of the
+// key's.  A tile of keys is as wide as a token, one of values as long as 64 tokens or
+// the block, so that both are stored in whole lines.  The group takes the largest
+// number, then the scale, then the codes; a wave with one tile keeps it in registers
+// meanwhile, one with more reads them again from the cache.  A scale is a power of
+// two, so one instruction scales, rounds and packs two codes.
+// log2 of the lanes side by side in a tile of values: as few as there are dims for, so
+// that a tile is as long as 64 tokens or the block.
+__device__ __forceinline__ int append_side(int dim, int shift) {
+  const int most = dim == 64 ? 3 : 4, least = 8 - (shift < 6 ? shift : 6);
+  return least < most ? least : most;
+}
+
+template <typename T, int D>
+__global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int waves, int tokens) {
+  __shared__ uint32_t s_max[4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int bs = a.block_size, shift = __builtin_ctz(bs);
+  const auto block_of = [&](int slot) {
+    return slot < 0 || (slot >> shift) >= a.num_blocks ? -1 : slot >> shift;
   };
-  const int b = block_of(t);
-  if (b < 0 || (t > 0 && block_of(t - 1) == b)) return;
-  const CachePart c = a.part[part];
-  const T* x = (const T*)a.x[part] + (int64_t)h * dim;
-  uint8_t* codes = c.codes + (int64_t)b * c.stride + (int64_t)h * bs * dim;
-  float* scale = c.scale + (int64_t)b * a.heads + h;
-  // element i of the token at offset o
-  const auto at = [&](int o, int i) { return part ? i * bs + o : o * dim + i; };
-  float amax = 0.0f;
-  bool fresh = false, broken = false;
-  int end = t;
-  for (; end < a.T && block_of(end) == b; ++end) {
-    fresh |= a.slots[end] % bs == 0;
-    for (int i = lane; i < dim; i += 64) {
-      const float f = (float)x[end * a.ld[part] + i];
-      broken |= !(f - f == 0.0f);
-      amax = fmaxf(amax, fabsf(f));
+  const int per = 4 / waves, items = a.heads * 2;
+  const int t0 = blockIdx.y * tokens;
+  // the slots from the workgroup's first on, and which of its tokens begin a run
+  const int mine = t0 + lane < a.T ? a.slots[t0 + lane] : -1;
+  int prior = __shfl_up(mine, 1);        // by all lanes: one that is not there gives nothing
+  if (lane == 0 && t0 > 0) prior = a.slots[t0 - 1];
+  const int my_block = block_of(mine);
+  uint64_t begins = __ballot(lane < tokens && my_block >= 0 &&
+                             (t0 + lane == 0 || my_block != block_of(prior)));
+  for (; begins; begins &= begins - 1) {
+    const int i0 = __builtin_ctzll(begins), t = t0 + i0;
+    const int slot0 = __builtin_amdgcn_readlane(mine, i0), b = block_of(slot0);
+    // the run: how long, and whether slots follow each other
+    uint64_t out = ~__ballot(my_block == b) >> i0;
+    int n = out ? __builtin_ctzll(out) : 64;
+    if (n > 64 - i0) n = 64 - i0;
+    const bool in = lane >= i0 && lane < i0 + n;
+    bool follows = __all(!in || mine == slot0 + lane - i0);
+    bool zero = __any(in && (mine & (bs - 1)) == 0);     // the block's first slot is written
+    for (int more = i0 + n == 64 ? 64 : 0; more == 64; n += more) {
+      const int i = t + n + lane, slot = i < a.T ? a.slots[i] : -1;
+      out = ~__ballot(block_of(slot) == b);
+      more = out ? __builtin_ctzll(out) : 64;
+      follows &= __all(lane >= more || slot == slot0 + n + lane);
+      zero |= __any(lane < more && (slot & (bs - 1)) == 0);
+    }
+    const int o0 = slot0 & (bs - 1);
+    for (int item0 = blockIdx.x * per; item0 < items; item0 += gridDim.x * per) {
+      // the same number of rounds for every wave: they meet below
+      const int item = item0 + wave / waves;
+      const bool works = item < items;
+      const int h = works ? item >> 1 : 0, part = item & 1, w = wave & (waves - 1);
+      const CachePart c = a.part[part];
+      const T* x = (const T*)a.x[part] + (int64_t)h * D;
+      uint8_t* codes = c.codes + (int64_t)b * c.stride + (int64_t)h * bs * D;
+      float* scale = c.scale + (int64_t)b * a.heads + h;
+      const int64_t ld = a.ld[part];
+      // lanes of a tile side by side in dims, 8 each; tokens and dims of the lane
+      const int side = part ? append_side(D, shift) : __builtin_ctz(D / 8);   // log2
+      const int wide = __builtin_ctz(D / 8) - side, length = 8 - side;        // dims, tokens
+      const int q = (lane >> side) * 4, d0 = (lane & ((1 << side) - 1)) * 8;
+      const int first = o0 >> length;
+      const int end = works && follows ? (((o0 + n - 1) >> length) + 1 - first) << wide : 0;
+      Quad<T> v;
+      const auto token_of = [&](int tile) { return ((first + (tile >> wide)) << length) + q; };
+      const auto dim_of = [&](int tile) { return d0 + ((tile & ((1 << wide) - 1)) << (side + 3)); };
+      // whether all of a tile's tokens are the run's
+      const auto inside = [&](int tile) {
+        const int o = (first + (tile >> wide)) << length;
+        return o >= o0 && o + (1 << length) <= o0 + n;
+      };
+      const auto load = [&](int tile) {
+        const int i = token_of(tile) - o0;
+        const T* p = x + (t + i) * ld + dim_of(tile);
+        if (inside(tile)) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < Quad<T>::W; ++j) v.raw[k][j] = *((const u32x4*)(p + k * ld) + j);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < Quad<T>::W; ++j) {
+              v.raw[k][j] = u32x4{0, 0, 0, 0};
+              if (i + k >= 0 && i + k < n) v.raw[k][j] = *((const u32x4*)(p + k * ld) + j);
+            }
+        }
+      };
+      uint32_t top = 0;
+      const float was = works ? *scale : 1.0f;
+      int here = w - waves;              // the tile in registers; none yet
+      for (int tile = w; tile < end; tile += waves) {
+        load(here = tile);
+        const uint32_t m = v.largest();
+        top = m > top ? m : top;
+      }
+      if (works && !follows)             // tokens in any order
+        for (int i = w * 64 + lane; i < n * D; i += waves * 64) {
+          const float f = (float)x[(int64_t)(t + i / D) * a.ld[part] + i % D];
+          const uint32_t m = __float_as_uint(f) & 0x7fffffffu;
+          top = m > top ? m : top;
+        }
+      top = wave_max_u32(top);
+      if (waves > 1) {
+        if (lane == 0) s_max[wave] = top;
+        __syncthreads();
+        for (int i = wave & ~(waves - 1), end = i + waves; i < end; ++i)
+          top = s_max[i] > top ? s_max[i] : top;
+      }
+      const bool bad = top >= 0x7f800000u;
+      float now = scale_of(bad ? 0.0f : __uint_as_float(top));
+      if (!zero) now = grown_scale(was, now);
+      if (bad) now = __builtin_nanf("");
+      const bool none = now != now;      // all codes are 0 then
+      // in any order, or beyond the largest scale: number by number
+      const bool single = !follows || now >= kScaleMax;
+      if (works && !zero && now != was && !none) {
+        const float k = clamp_scale(was) / now;
+        u32x4* p = (u32x4*)codes;
+        for (int i = w * 64 + lane; i < bs * D / 16; i += waves * 64) {
+          u32x4 u = p[i];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) u[j] = recode(u[j], k);
+          p[i] = u;
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // before others' codes go there
+      }
+      // the scale has been read, and what stood there is written, by all of the group
+      if (waves > 1) __syncthreads();
+      if (!works) continue;
+      if (w == 0 && lane == 0) *scale = now;
+      for (int tile = here; tile >= 0 && !single; tile -= waves) {   // the last is there
+        if (tile != here) load(tile);
+        if (none)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < Quad<T>::W; ++j) v.raw[k][j] = u32x4{0, 0, 0, 0};
+        const float by = none ? 1.0f : now;
+        const int o = token_of(tile), d = dim_of(tile);
+        const uint32_t at = part ? d * bs + o : o * D + d;
+        if (inside(tile)) {
+          if (part == 0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *(u32x2*)(codes + k * D + at) = u32x2{v.dims4(k, 0, by), v.dims4(k, 1, by)};
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) *(uint32_t*)(codes + i * bs + at) = v.tokens4(i, by);
+          }
+          continue;
+        }
+        // the run ends inside the tile
+        if (part == 0) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (o + k >= o0 && o + k < o0 + n)
+              *(u32x2*)(codes + k * D + at) = u32x2{v.dims4(k, 0, by), v.dims4(k, 1, by)};
+        } else {
+          const bool whole = o >= o0 && o + 3 < o0 + n;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t u = v.tokens4(i, by);
+            uint8_t* p = codes + i * bs + at;
+            if (whole) *(uint32_t*)p = u;
+            else
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (o + k >= o0 && o + k < o0 + n) p[k] = (uint8_t)(u >> (8 * k));
+          }
+        }
+      }
+      if (!single) continue;
+      const float inv = none ? 1.0f : 1.0f / now;
+      for (int j = 0; j < n; ++j) {      // one after the other: the later one stays
+        const int o = a.slots[t + j] & (bs - 1);
+        for (int i = w * 64 + lane; i < D; i += waves * 64) {
+          const float f = (float)x[(t + j) * ld + i];
+          codes[part ? i * bs + o : o * D + i] = to_code(none ? 0.0f : f * inv);
+        }
+      }
     }
   }
-  amax = cache_wave_max(amax);
-  broken = __any(broken);
-  const float was = *scale;
-  float now = scale_of(amax);
-  if (!fresh) now = grown_scale(was, now);
-  if (broken) now = __builtin_nanf("");
-  if (!fresh && now != was && now == now) {
-    const float k = clamp_scale(was) / now;
-    for (int i = lane; i < bs * dim; i += 64) codes[i] = to_code(from_code(codes[i]) * k);
-  }
-  __syncthreads();
-  const float inv = now == now ? 1.0f / now : 0.0f;
-  for (int j = t; j < end; ++j)
-    for (int i = lane; i < dim; i += 64) {
-      const float f = (float)x[j * a.ld[part] + i];
-      codes[at(a.slots[j] % bs, i)] = to_code(f - f == 0.0f && inv > 0.0f ? f * inv : 0.0f);
-    }
-  if (lane == 0) *scale = now;
 }
 
 }  // namespace
@@ -306,12 +556,31 @@ hipError_t run_tables(const TablesArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename T>
+hipError_t append_t(const AppendArgs& a, hipStream_t s) {
+  // a wave a tile of 256 x 8 numbers, at most four a run
+  const int tiles = a.block_size * a.dim / 2048;
+  const int waves = tiles > 2 ? 4 : (tiles > 1 ? 2 : 1);
+  // Many tokens: most do not begin a run, and a workgroup looks at 64 of them (18400
+  // tokens, blocks of 64: 16 of them 105 us, 64 51 us).
+  const int tokens = a.T > 2048 ? 64 : 1;
+  const int items = a.heads * 2, per = 4 / waves;
+  const int64_t y = ((int64_t)a.T + tokens - 1) / tokens;
+  const int x = (items + per - 1) / per;
+  const auto launch = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    hipLaunchKernelGGL((append_kernel<T, D>), dim3(x, (unsigned)y), dim3(256), 0, s, a, waves, tokens);
+    return hipGetLastError();
+  };
+  if (a.dim == 64) return launch(std::integral_constant<int, 64>());
+  if (a.dim == 128) return launch(std::integral_constant<int, 128>());
+  return launch(std::integral_constant<int, 256>());
+}
+
 hipError_t run_append(const AppendArgs& a, hipStream_t s) {
-  const dim3 grid(a.T, a.heads, 2);
-  if (a.dtype == LIK_F16) hipLaunchKernelGGL(append_kernel<_Float16>, grid, dim3(64), 0, s, a);
-  else if (a.dtype == LIK_BF16) hipLaunchKernelGGL(append_kernel<__bf16>, grid, dim3(64), 0, s, a);
-  else hipLaunchKernelGGL(append_kernel<float>, grid, dim3(64), 0, s, a);
-  return hipGetLastError();
+  if (a.dtype == LIK_F16) return append_t<_Float16>(a, s);
+  if (a.dtype == LIK_BF16) return append_t<__bf16>(a, s);
+  return append_t<float>(a, s);
 }
 
 }  // namespace lik

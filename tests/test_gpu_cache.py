@@ -276,6 +276,33 @@ def test_append_many_tokens():
     c.append(k, v, slots)
 
 
+@pytest.mark.parametrize("heads,bs,dim,T,dtype", [(2, 16, 64, 5003, BF16), (1, 64, 128, 4500, F16), (1, 128, 64, 3100, F32),
+                                                  (3, 32, 64, 2049, F16), (1, 256, 256, 2600, BF16)])
+def test_append_prompts(heads, bs, dim, T, dtype):
+    """More tokens than one wave looks at, requests and blocks beginning anywhere among
+    them, some without a slot, some in no order."""
+    rng = np.random.default_rng(T)
+    N = 2 * (T // bs) + 8
+    c = Cache(N, heads, bs, dim, T, gap=1)
+    ids, slots = list(rng.permutation(N)), []
+    while len(slots) < T:
+        at, n = int(rng.integers(0, 2 * bs)) * (rng.random() < 0.6), int(rng.integers(1, 6 * bs))
+        blocks = [ids.pop() for _ in range((at + n - 1) // bs - at // bs + 1)] if len(ids) > 14 else []
+        if not blocks:
+            slots += [-1] * (T - len(slots))
+            break
+        mine = [blocks[(at + i) // bs - at // bs] * bs + (at + i) % bs for i in range(n)]
+        if rng.random() < 0.2:             # within its blocks in another order
+            mine = sorted(mine, key=lambda s: (blocks.index(s // bs), -s))
+        slots += mine + [-1] * int(rng.integers(0, 4))
+    slots = slots[:T]
+    assert sum(s >= 0 for s in slots) > T // 2
+    k, v = tokens(T, heads, dim, dtype, T)
+    c.append(k, v, slots)
+    k, v = tokens(T, heads, dim, dtype, T + 1)
+    c.append(k, v, slots)
+
+
 # ---------------------------------------------------------------------------
 # attention
 # ---------------------------------------------------------------------------
