@@ -39,60 +39,64 @@ __device__ __forceinline__ Change change_of(const TablesArgs& a, int s, int shif
 
 constexpr int kTablesThreads = 256;
 
-// Three running sums over a workgroup: before this thread, and of all.
+// Sums of blocks and tokens are unsigned and stay at the largest number: what a pool or
+// a slot map can hold is far below, and beyond it nothing is granted or stored.
+__device__ __forceinline__ uint32_t add(uint32_t a, uint32_t b) {
+  return __builtin_elementwise_add_sat(a, b);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_add(uint32_t v) {
+  return add(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false));
+}
+// Sum over the lanes up to this one.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v = dpp_add<0x111, 0xf>(v);            // row_shr 1, 2, 4, 8
+  v = dpp_add<0x112, 0xf>(v);
+  v = dpp_add<0x114, 0xf>(v);
+  v = dpp_add<0x118, 0xf>(v);
+  v = dpp_add<0x142, 0xa>(v);            // the last of a row to the next
+  return dpp_add<0x143, 0xc>(v);         // of the lower half to the upper
+}
+
+// Three running sums over a workgroup: before this thread, and of all.  Two places in
+// LDS in turn: one meeting a call.
 struct Sums {
-  int64_t ask, give, grown;
+  uint32_t x, y, z;
 };
-struct ScanLds {
-  Sums wave[kTablesThreads / 64];
-};
-__device__ __forceinline__ int64_t wave_scan(int64_t v) {
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) {
-    const int64_t y = __shfl_up(v, o);
-    if ((threadIdx.x & 63) >= (unsigned)o) v += y;
-  }
-  return v;
-}
-__device__ __forceinline__ Sums scan3(Sums v, ScanLds& lds, Sums* all) {
+typedef Sums ScanLds[2][kTablesThreads / 64];
+__device__ __forceinline__ Sums scan3(Sums v, ScanLds& lds, int& turn, Sums* all) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  Sums x{wave_scan(v.ask), wave_scan(v.give), wave_scan(v.grown)};
+  const Sums upto{wave_scan(v.x), wave_scan(v.y), wave_scan(v.z)};
+  turn ^= 1;
+  if (lane == 63) lds[turn][wave] = upto;
   __syncthreads();
-  if (lane == 63) lds.wave[wave] = x;
-  __syncthreads();
-  x.ask -= v.ask;
-  x.give -= v.give;
-  x.grown -= v.grown;
-  *all = Sums{0, 0, 0};
+  Sums r{0, 0, 0}, sum{0, 0, 0};
+#pragma unroll
   for (int w = 0; w < kTablesThreads / 64; ++w) {
-    const Sums y = lds.wave[w];
-    if (w < wave) {
-      x.ask += y.ask;
-      x.give += y.give;
-      x.grown += y.grown;
-    }
-    all->ask += y.ask;
-    all->give += y.give;
-    all->grown += y.grown;
+    if (w == wave) r = sum;
+    const Sums o = lds[turn][w];
+    sum = Sums{add(sum.x, o.x), add(sum.y, o.y), add(sum.z, o.z)};
   }
-  return x;
+  *all = sum;
+  // the lanes before this one
+  const int before = lane == 0 ? 64 : lane - 1;
+  const uint32_t x = __shfl(upto.x, before), y = __shfl(upto.y, before), z = __shfl(upto.z, before);
+  if (lane == 0) return r;
+  return Sums{add(r.x, x), add(r.y, y), add(r.z, z)};
 }
 
-__device__ __forceinline__ int clamp_int(int64_t x) { return x < INT32_MAX ? (int)x : INT32_MAX; }
-
-// The last of n entries of a rising array that is at most x; the first is.
-__device__ __forceinline__ int last_at_most(const int64_t* v, int64_t x) {
+// The last entry of a rising array that is at most x; the first is.
+__device__ __forceinline__ int last_at_most(const uint32_t* v, uint32_t x) {
   int b = 0;
 #pragma unroll
   for (int step = kTablesThreads / 2; step > 0; step /= 2)
     if (v[b + step] <= x) b += step;
   return b;
 }
-
 // A place in the ring; a consistent pool goes round its end once at most.
-__device__ __forceinline__ int ring_at(int64_t i, int N) {
-  if (i >= N) i -= N;
-  return (int)(i < N ? i : i % N);
+__device__ __forceinline__ int ring_at(uint32_t i, int N) {
+  if (i >= (uint32_t)N) i -= N;
+  return (int)(i < (uint32_t)N ? i : i % N);
 }
 
 // One launch.  Workgroup (x, y) takes the requests 256 x .. 256 x + 255 (and further
@@ -102,15 +106,16 @@ __device__ __forceinline__ int ring_at(int64_t i, int N) {
 // wait for another.  The workgroup that is last to have read the pool's state
 // (counted in ring_state[2], which it sets back) moves it.  Blocks to take and room
 // for blocks given back lie apart in the ring, so entries are independent.
-// 64 requests, 100000 slots: see the table of cases.
 __global__ __launch_bounds__(kTablesThreads) void tables_kernel(TablesArgs a) {
   __shared__ ScanLds lds;
-  __shared__ int64_t entry0[kTablesThreads], token0[kTablesThreads];
+  __shared__ uint32_t entry0[kTablesThreads], token0[kTablesThreads];
   __shared__ int s_old[kTablesThreads], s_have[kTablesThreads], s_need[kTablesThreads];
-  __shared__ int64_t s_ring[kTablesThreads];     // where its blocks come from or go to; -1: not granted
+  __shared__ uint32_t s_ring[kTablesThreads];    // where its blocks come from or go to
   __shared__ int is_last, s_state[2];
+  constexpr uint32_t kNotGranted = ~0u;
   const int tid = threadIdx.x, bs = a.block_size, N = a.num_blocks;
   const int shift = __builtin_ctz(bs);
+  int turn = 0;
   // one thread reads the state, and counts once it has it
   if (tid == 0) {
     const int h = a.state[0], f = a.state[1], n = (int)(gridDim.x * gridDim.y);
@@ -119,125 +124,137 @@ __global__ __launch_bounds__(kTablesThreads) void tables_kernel(TablesArgs a) {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
     is_last = n == 1 || atomicAdd(&a.state[2], 1) == n - 1;
   }
-  __syncthreads();
-  const int head = s_state[0], free_blocks = s_state[1];
-
-  Sums upto{0, 0, 0};                            // of all requests before s0
-  int64_t tokens = 0, taken = 0, back = 0;
-  bool whole = false;                            // taken and back are those of all
-  const auto ok_of = [&](const Change& c, int64_t before) {
-    return c.fits && (c.ask() == 0 || before + c.ask() <= free_blocks);
-  };
-  int done = 0;
-  for (int s0 = blockIdx.x * kTablesThreads; s0 < a.S || done == 0;
-       s0 += gridDim.x * kTablesThreads) {
-    // sums of the requests between
-    Sums mine{0, 0, 0}, all;
-    for (int s = done + tid; s < s0 && s < a.S; s += kTablesThreads) {
-      const Change c = change_of(a, s, shift);
-      mine.ask += c.ask();
-      mine.give += c.give();
-      mine.grown += c.grown();
-    }
-    scan3(mine, lds, &all);
-    upto.ask += all.ask;
-    upto.give += all.give;
-    upto.grown += all.grown;
-    if (s0 >= a.S) break;
-
-    const int s = s0 + tid;
+  const auto change = [&](int s) {
     Change c{0, 0, 0, 0, false};
     if (s < a.S) c = change_of(a, s, shift);
-    const Sums before = scan3(Sums{c.ask(), c.give(), c.grown()}, lds, &all);
-    const int64_t start = upto.ask + before.ask, rel = upto.give + before.give;
-    const bool ok = ok_of(c, start);
-    const int64_t first = upto.grown + before.grown;
-    const int moves = ok ? c.ask() + c.give() : 0;
+    return c;
+  };
+  const auto granted = [&](const Change& c, uint32_t before) {
+    const uint32_t ask = c.ask();
+    return c.fits && (ask == 0 || add(before, ask) <= (uint32_t)s_state[1]);
+  };
+
+  Sums upto{0, 0, 0};                            // asked, given, grown before s0
+  uint32_t taken = 0, back = 0;                  // of all, where one workgroup sees all
+  int done = 0;
+  for (int s0 = blockIdx.x * kTablesThreads; s0 < a.S; s0 += gridDim.x * kTablesThreads) {
+    Sums all;
+    Change c = change(s0 + tid);
+    if (s0 > done) {                             // sums of the requests between
+      Sums mine{0, 0, 0};
+      for (int s = done + tid; s < s0; s += kTablesThreads) {
+        const Change o = change_of(a, s, shift);
+        mine = Sums{add(mine.x, o.ask()), add(mine.y, o.give()), add(mine.z, o.grown())};
+      }
+      scan3(mine, lds, turn, &all);
+      upto = Sums{add(upto.x, all.x), add(upto.y, all.y), add(upto.z, all.z)};
+    }
+    const int s = s0 + tid;
+    const Sums before = scan3(Sums{(uint32_t)c.ask(), (uint32_t)c.give(), (uint32_t)c.grown()}, lds,
+                              turn, &all);       // s_state is there too now
+    const int head = s_state[0], free_blocks = s_state[1];
+    const uint32_t start = add(upto.x, before.x), rel = add(upto.y, before.y);
+    const bool ok = granted(c, start);
+    const uint32_t ask = ok ? c.ask() : 0, give = ok ? c.give() : 0;
     Sums moved;
-    const Sums entry = scan3(Sums{moves, 0, 0}, lds, &moved);
-    entry0[tid] = entry.ask;
-    token0[tid] = before.grown;
+    const Sums entry = scan3(Sums{ask + give, ask, give}, lds, turn, &moved);
+    taken = add(taken, moved.y);
+    back = add(back, moved.z);
+    entry0[tid] = entry.x;
+    token0[tid] = before.z;
     s_old[tid] = c.old_len;
     s_have[tid] = c.have;
     s_need[tid] = c.need;
-    s_ring[tid] = !ok ? -1 : (c.ask() ? head + start : (int64_t)head + free_blocks + rel);
+    s_ring[tid] = !ok ? kNotGranted : (ask ? head + start : add(head + free_blocks, rel));
     if (s < a.S && blockIdx.y == 0) {
+      const uint32_t first = add(upto.z, before.z);
       a.granted[s] = ok ? c.new_len : c.old_len;
-      a.offsets[s] = clamp_int(first);
+      a.offsets[s] = first < INT32_MAX ? (int)first : INT32_MAX;
     }
     __syncthreads();
     // table entries
-    const int64_t step = (int64_t)gridDim.y * kTablesThreads;
-    for (int64_t e = (int64_t)blockIdx.y * kTablesThreads + tid; e < moved.ask; e += step) {
-      const int i = last_at_most(entry0, e);
-      const int k = (int)(e - entry0[i]);
+    for (uint32_t e = blockIdx.y * kTablesThreads + tid; e < moved.x;
+         e += gridDim.y * kTablesThreads) {
+      const int i = last_at_most(entry0, e), k = (int)(e - entry0[i]);
       int32_t* row = a.table + (s0 + i) * a.table_ld;
-      // a request without blocks granted has no ring to look at: N > 0 where it takes some
+      int32_t* ring = a.ring + ring_at(s_ring[i] + k, N);
       if (s_need[i] > s_have[i]) {
-        row[s_have[i] + k] = a.ring[ring_at(s_ring[i] + k, N)];
+        row[s_have[i] + k] = *ring;
       } else {
-        if (N > 0) a.ring[ring_at(s_ring[i] + k, N)] = row[s_need[i] + k];
+        *ring = row[s_need[i] + k];
         row[s_need[i] + k] = -1;
       }
     }
-    // slots
-    const int64_t most = a.T - upto.grown, here = all.grown < most ? all.grown : most;
-    for (int64_t e = (int64_t)blockIdx.y * kTablesThreads + tid; e < here; e += step) {
-      const int i = last_at_most(token0, e);
-      const int p = s_old[i] + (int)(e - token0[i]);
-      int b = -1;
-      if (s_ring[i] >= 0) {
-        const int at = p >> shift;
-        b = at < s_have[i] ? a.table[(s0 + i) * a.table_ld + at]
-                           : a.ring[ring_at(s_ring[i] + at - s_have[i], N)];
+    // slots, four neighbours a thread
+    const uint32_t most = upto.z < (uint32_t)a.T ? a.T - upto.z : 0;
+    const uint32_t here = all.z < most ? all.z : most;
+    for (uint32_t e = (blockIdx.y * kTablesThreads + tid) * 4; e < here;
+         e += gridDim.y * kTablesThreads * 4) {
+      typedef int32_t i32x4 __attribute__((ext_vector_type(4), aligned(4)));
+      i32x4 slot;
+      int i = last_at_most(token0, e), from = -1, which = -1, b = -1;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        while (i + 1 < kTablesThreads && token0[i + 1] <= e + j) ++i;
+        const int p = s_old[i] + (int)(e + j - token0[i]), at = p >> shift;
+        if (from != i || which != at) {          // another block than the last
+          from = i;
+          which = at;
+          b = -1;
+          if (e + j < here && s_ring[i] != kNotGranted)
+            b = at < s_have[i] ? a.table[(s0 + i) * a.table_ld + at]
+                               : a.ring[ring_at(s_ring[i] + at - s_have[i], N)];
+        }
+        slot[j] = (unsigned)b < (unsigned)N ? (b << shift) + (p & (bs - 1)) : -1;
       }
-      a.slots[upto.grown + e] = (unsigned)b < (unsigned)N ? (b << shift) + (p & (bs - 1)) : -1;
+      int32_t* out = a.slots + upto.z + e;
+      if (e + 3 < here) *(i32x4*)out = slot;
+      else
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (e + j < here) out[j] = slot[j];
     }
-    upto.ask += all.ask;
-    upto.give += all.give;
-    upto.grown += all.grown;
+    upto = Sums{add(upto.x, all.x), add(upto.y, all.y), add(upto.z, all.z)};
     done = s0 + kTablesThreads;
-    if (gridDim.x == 1) {
-      Sums x;
-      scan3(Sums{ok ? c.ask() : 0, ok ? c.give() : 0, 0}, lds, &x);
-      taken += x.ask;
-      back += x.give;
-      whole = true;
-    }
-    __syncthreads();
+    if (done + (int)(gridDim.x - 1) * kTablesThreads < a.S) __syncthreads();   // the arrays again
   }
+  __syncthreads();
   // tokens of the requests behind, then what no request has
-  {
+  uint32_t tokens = upto.z;
+  if (done < a.S) {
     Sums mine{0, 0, 0}, all;
-    for (int s = done + tid; s < a.S; s += kTablesThreads) mine.grown += change_of(a, s, shift).grown();
-    scan3(mine, lds, &all);
-    tokens = upto.grown + all.grown;
+    for (int s = done + tid; s < a.S; s += kTablesThreads)
+      mine.x = add(mine.x, change_of(a, s, shift).grown());
+    scan3(mine, lds, turn, &all);
+    tokens = add(tokens, all.x);
   }
   const int64_t linear = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
   const int64_t threads = (int64_t)gridDim.x * gridDim.y * kTablesThreads;
   for (int64_t i = tokens + linear * kTablesThreads + tid; i < a.T; i += threads) a.slots[i] = -1;
-  if (linear == 0 && tid == 0) a.offsets[a.S] = clamp_int(tokens);
+  if (linear == 0 && tid == 0) a.offsets[a.S] = tokens < INT32_MAX ? (int)tokens : INT32_MAX;
   if (!is_last) return;
-  if (!whole) {
-    Sums sum{0, 0, 0};
+  if (gridDim.x > 1) {                           // what all took and gave back
+    Sums all, x;
+    uint32_t asked = 0;
+    taken = back = 0;
     for (int s0 = 0; s0 < a.S; s0 += kTablesThreads) {
-      Change c{0, 0, 0, 0, false};
-      if (s0 + tid < a.S) c = change_of(a, s0 + tid, shift);
-      Sums all, x;
-      const Sums before = scan3(Sums{c.ask(), 0, 0}, lds, &all);
-      const bool ok = ok_of(c, sum.ask + before.ask);
-      scan3(Sums{ok ? c.ask() : 0, ok ? c.give() : 0, 0}, lds, &x);
-      sum.ask += all.ask;
-      taken += x.ask;
-      back += x.give;
+      const Change c = change(s0 + tid);
+      const Sums before = scan3(Sums{(uint32_t)c.ask(), 0, 0}, lds, turn, &all);
+      const bool ok = granted(c, add(asked, before.x));
+      scan3(Sums{0, ok ? (uint32_t)c.ask() : 0, ok ? (uint32_t)c.give() : 0}, lds, turn, &x);
+      asked = add(asked, all.x);
+      taken = add(taken, x.y);
+      back = add(back, x.z);
     }
   }
-  if (tid == 0 && N > 0) {
-    const int64_t now = free_blocks - taken + back;
-    a.state[0] = (int)((head + taken) % N);
-    a.state[1] = (int)(now > N ? N : now);
+  if (tid == 0) {
+    if (N > 0) {
+      const uint32_t now = add(s_state[1] - taken, back);
+      a.state[0] = ring_at(s_state[0] + taken, N);
+      a.state[1] = (int)(now > (uint32_t)N ? N : now);
+    }
+    a.state[2] = 0;
   }
-  if (tid == 0) a.state[2] = 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -544,12 +561,15 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int waves, in
 }  // namespace
 
 hipError_t run_tables(const TablesArgs& a, hipStream_t s) {
-  // workgroups for the requests, and so many times them that a thread has about 16
-  // slots or, where few are asked for, table entries
+  // workgroups for the requests, and so many times them that a thread has four slots
+  // and four entries, up to two a CU (1000 requests, a million slots: 128 in all 24 us,
+  // 256 17; their blocks given back by 4 29 us, by 128 9 us)
+  constexpr int64_t kMost = 512;
   const int64_t x = a.S < 256 * kTablesThreads ? (a.S + kTablesThreads - 1) / kTablesThreads : 256;
-  const int64_t groups = x > 0 ? x : 1;
-  int64_t y = ((int64_t)a.T + groups * 4096 - 1) / (groups * 4096);
-  const int64_t most = 1024 / groups > 1 ? 1024 / groups : 1;
+  const int64_t groups = x > 0 ? x : 1, each = 4 * kTablesThreads;
+  const int64_t entries = (int64_t)a.S * a.max_blocks, work = a.T > entries ? a.T : entries;
+  int64_t y = (work + groups * each - 1) / (groups * each);
+  const int64_t most = kMost / groups > 1 ? kMost / groups : 1;
   y = y < 1 ? 1 : (y > most ? most : y);
   hipLaunchKernelGGL(tables_kernel, dim3((unsigned)groups, (unsigned)y), dim3(kTablesThreads), 0, s,
                      a);

@@ -377,6 +377,12 @@ struct RowTile {
       return (unsigned)block < (unsigned)a.num_blocks;
     }
   };
+  // One row tile a request: nothing reads its blocks again, and they need not stay in
+  // the caches.
+  static __device__ __forceinline__ u32x4 load16(const uint8_t* p) {
+    if constexpr (MT == 1) return __builtin_nontemporal_load((const u32x4*)p);
+    return *(const u32x4*)p;
+  }
   __device__ __forceinline__ void load_keys(const Cursor& c, const Blocks& b, int kt) {
     const int key = c.there(b.key) ? b.key : 0, own = c.there(b.own) ? b.own : 0;
     const int o = (c.key(kt) & (c.a.block_size - 1)) + (c.lane & 3);
@@ -384,7 +390,7 @@ struct RowTile {
 #pragma unroll
     for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-      for (int i = 0; i < NI; ++i) kr[tt][i] = *(const u32x4*)(p + tt * 4 * D + i * 64);
+      for (int i = 0; i < NI; ++i) kr[tt][i] = load16(p + tt * 4 * D + i * 64);
     ks = c.a.k.scale[(int64_t)own * c.a.kv_heads + c.head];
     vs = c.a.v.scale[(int64_t)own * c.a.kv_heads + c.head];
   }
@@ -393,7 +399,7 @@ struct RowTile {
     const uint8_t* p =
         c.vb + (int64_t)own * c.a.v.stride + (c.own(kt) & (c.a.block_size - 1));
 #pragma unroll
-    for (int d = 0; d < ND; ++d) vr[d] = *(const u32x4*)(p + d * 16 * c.a.block_size);
+    for (int d = 0; d < ND; ++d) vr[d] = load16(p + d * 16 * c.a.block_size);
   }
 
   // Tiles kt0 .. kt1 - 1.  `now` and `next`: the blocks of kt0, whose keys and values
