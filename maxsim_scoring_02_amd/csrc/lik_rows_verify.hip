@@ -103,9 +103,6 @@ struct Weights {
     if (drow) return fmaxf(pc - row_exp(q, d) * iq, 0.0f);
     return c == x ? fmaxf(pc - 1.0f, 0.0f) : pc;
   }
-  __device__ __forceinline__ float at(int c) const {
-    return of((float)row[c], drow ? (float)drow[c] : 0.0f, c);
-  }
 };
 
 constexpr int kVerifyPieces = 4;
@@ -153,13 +150,27 @@ struct PartWeights {
 };
 
 // Sum over the lanes up to this one.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+  return v + __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
 __device__ __forceinline__ double lane_scan(double v) {
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) {
-    const double y = __shfl_up(v, o);
-    if ((threadIdx.x & 63) >= (unsigned)o) v += y;
-  }
-  return v;
+  v = dpp_add<0x111, 0xf>(v);            // row_shr 1, 2, 4, 8
+  v = dpp_add<0x112, 0xf>(v);
+  v = dpp_add<0x114, 0xf>(v);
+  v = dpp_add<0x118, 0xf>(v);
+  v = dpp_add<0x142, 0xa>(v);            // the last of a row to the next
+  return dpp_add<0x143, 0xc>(v);         // of the lower half to the upper
+}
+// v of lane k, the same for all lanes
+__device__ __forceinline__ double lane_of(double v, int k) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, k);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), k);
+  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
 }
 
 // The column of a part at which the running sum passes `goal`; the last with a
@@ -196,9 +207,13 @@ __device__ int pick(const Weights<T>& w, int lo, int cols, double goal, double* 
   if (wave == at % 4) {
     const int k = at / 4;
     double mine = 0.0;
+    float f[P::N] = {};
 #pragma unroll
     for (int i = 0; i < P::kSlots; ++i)
-      if (i == k) mine = v[i];
+      if (i == k) {
+        mine = v[i];
+        if (i > 0 && i < P::kSlots - 1) part.piece_of(w, lo, i - 1, f);
+      }
     const double upto = at_before + lane_scan(mine);
     const uint64_t over = beyond ? 0 : __ballot(upto > goal), some = __ballot(mine > 0.0);
     const int who = over ? __builtin_ctzll(over) : 63 - __builtin_clzll(some | 1);
@@ -208,10 +223,10 @@ __device__ int pick(const Weights<T>& w, int lo, int cols, double goal, double* 
         double run = upto - mine;
         hit = -1;
         int positive = c;
+#pragma unroll
         for (int j = 0; j < P::N; ++j) {
-          const float x = w.at(c + j);
-          run += (double)x;
-          if (x > 0.0f) positive = c + j;
+          run += (double)f[j];
+          if (f[j] > 0.0f) positive = c + j;
           if (over && hit < 0 && run > goal) hit = c + j;
         }
         if (hit < 0) hit = positive;
@@ -345,7 +360,7 @@ __global__ __launch_bounds__(256) void verify_draw_kernel(VerifyArgs a, int look
                  ? __hip_atomic_load(&sums[p], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
                  : 0.0;
     };
-    for (int p0 = 0; p0 < parts.n; p0 += 64) total += __shfl(lane_scan(sum_at(p0 + lane)), 63);
+    for (int p0 = 0; p0 < parts.n; p0 += 64) total += lane_of(lane_scan(sum_at(p0 + lane)), 63);
     if (!(total > 0.0)) continue;
     if (u < 0.0) {
       token = 0;
@@ -356,20 +371,19 @@ __global__ __launch_bounds__(256) void verify_draw_kernel(VerifyArgs a, int look
     int at = -1, some = -1;
     for (int p0 = 0; p0 < parts.n && at < 0; p0 += 64) {
       const double mine = sum_at(p0 + lane), upto = before + lane_scan(mine);
-      const double up = __shfl_up(upto, 1), start = lane == 0 ? before : up;
       const uint64_t over = __ballot(upto > goal && p0 + lane < parts.n);
       const uint64_t any = __ballot(mine > 0.0);
       if (any) {
         const int k = 63 - __builtin_clzll(any);
         some = p0 + k;
-        last_before = __shfl(start, k);
+        last_before = k ? lane_of(upto, k - 1) : before;
       }
       if (over) {
         const int k = __builtin_ctzll(over);
         at = p0 + k;
-        at_before = __shfl(start, k);
+        at_before = k ? lane_of(upto, k - 1) : before;
       }
-      before = __shfl(upto, 63);
+      before = lane_of(upto, 63);
     }
     if (at < 0) {
       at = some;
