@@ -72,8 +72,8 @@ extern "C" {
  *   slots [T]          the slot of every new token in that order; -1 for
  *                      those of requests that were not granted, and from
  *                      token_offsets[S] on.  Tokens beyond T have none.
- * S up to 2^20 and max_blocks * block_size < 2^31 (LIK_ERR_UNSUPPORTED
- * beyond).  The outputs must not overlap the inputs, or each other.  A ring that
+ * Calls on one pool or table must not overlap.  S up to 2^20 and max_blocks *
+ * block_size < 2^31 (LIK_ERR_UNSUPPORTED beyond).  The outputs must not overlap the inputs, or each other.  A ring that
  * is not consistent gives wrong blocks, but nothing outside the arrays is read or
  * written.  No workspace; S == 0 sets slots to -1 and token_offsets[0] to 0.
  */

@@ -177,11 +177,10 @@ __global__ __launch_bounds__(kTablesThreads) void tables_kernel(TablesArgs a) {
          e += gridDim.y * kTablesThreads) {
       const int i = last_at_most(entry0, e), k = (int)(e - entry0[i]);
       int32_t* row = a.table + (s0 + i) * a.table_ld;
-      int32_t* ring = a.ring + ring_at(s_ring[i] + k, N);
       if (s_need[i] > s_have[i]) {
-        row[s_have[i] + k] = *ring;
+        row[s_have[i] + k] = a.ring[ring_at(s_ring[i] + k, N)];
       } else {
-        *ring = row[s_need[i] + k];
+        if (N > 0) a.ring[ring_at(s_ring[i] + k, N)] = row[s_need[i] + k];
         row[s_need[i] + k] = -1;
       }
     }
@@ -393,165 +392,167 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, int waves, in
     return slot < 0 || (slot >> shift) >= a.num_blocks ? -1 : slot >> shift;
   };
   const int per = 4 / waves, items = a.heads * 2;
-  const int t0 = blockIdx.y * tokens;
-  // the slots from the workgroup's first on, and which of its tokens begin a run
-  const int mine = t0 + lane < a.T ? a.slots[t0 + lane] : -1;
-  int prior = __shfl_up(mine, 1);        // by all lanes: one that is not there gives nothing
-  if (lane == 0 && t0 > 0) prior = a.slots[t0 - 1];
-  const int my_block = block_of(mine);
-  uint64_t begins = __ballot(lane < tokens && my_block >= 0 &&
-                             (t0 + lane == 0 || my_block != block_of(prior)));
-  for (; begins; begins &= begins - 1) {
-    const int i0 = __builtin_ctzll(begins), t = t0 + i0;
-    const int slot0 = __builtin_amdgcn_readlane(mine, i0), b = block_of(slot0);
-    // the run: how long, and whether slots follow each other
-    uint64_t out = ~__ballot(my_block == b) >> i0;
-    int n = out ? __builtin_ctzll(out) : 64;
-    if (n > 64 - i0) n = 64 - i0;
-    const bool in = lane >= i0 && lane < i0 + n;
-    bool follows = __all(!in || mine == slot0 + lane - i0);
-    bool zero = __any(in && (mine & (bs - 1)) == 0);     // the block's first slot is written
-    for (int more = i0 + n == 64 ? 64 : 0; more == 64; n += more) {
-      const int i = t + n + lane, slot = i < a.T ? a.slots[i] : -1;
-      out = ~__ballot(block_of(slot) == b);
-      more = out ? __builtin_ctzll(out) : 64;
-      follows &= __all(lane >= more || slot == slot0 + n + lane);
-      zero |= __any(lane < more && (slot & (bs - 1)) == 0);
-    }
-    const int o0 = slot0 & (bs - 1);
-    for (int item0 = blockIdx.x * per; item0 < items; item0 += gridDim.x * per) {
-      // the same number of rounds for every wave: they meet below
-      const int item = item0 + wave / waves;
-      const bool works = item < items;
-      const int h = works ? item >> 1 : 0, part = item & 1, w = wave & (waves - 1);
-      const CachePart c = a.part[part];
-      const T* x = (const T*)a.x[part] + (int64_t)h * D;
-      uint8_t* codes = c.codes + (int64_t)b * c.stride + (int64_t)h * bs * D;
-      float* scale = c.scale + (int64_t)b * a.heads + h;
-      const int64_t ld = a.ld[part];
-      // lanes of a tile side by side in dims, 8 each; tokens and dims of the lane
-      const int side = part ? append_side(D, shift) : __builtin_ctz(D / 8);   // log2
-      const int wide = __builtin_ctz(D / 8) - side, length = 8 - side;        // dims, tokens
-      const int q = (lane >> side) * 4, d0 = (lane & ((1 << side) - 1)) * 8;
-      const int first = o0 >> length;
-      const int end = works && follows ? (((o0 + n - 1) >> length) + 1 - first) << wide : 0;
-      Quad<T> v;
-      const auto token_of = [&](int tile) { return ((first + (tile >> wide)) << length) + q; };
-      const auto dim_of = [&](int tile) { return d0 + ((tile & ((1 << wide) - 1)) << (side + 3)); };
-      // whether all of a tile's tokens are the run's
-      const auto inside = [&](int tile) {
-        const int o = (first + (tile >> wide)) << length;
-        return o >= o0 && o + (1 << length) <= o0 + n;
-      };
-      const auto load = [&](int tile) {
-        const int i = token_of(tile) - o0;
-        const T* p = x + (t + i) * ld + dim_of(tile);
-        if (inside(tile)) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int j = 0; j < Quad<T>::W; ++j) v.raw[k][j] = *((const u32x4*)(p + k * ld) + j);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int j = 0; j < Quad<T>::W; ++j) {
-              v.raw[k][j] = u32x4{0, 0, 0, 0};
-              if (i + k >= 0 && i + k < n) v.raw[k][j] = *((const u32x4*)(p + k * ld) + j);
-            }
-        }
-      };
-      uint32_t top = 0;
-      const float was = works ? *scale : 1.0f;
-      int here = w - waves;              // the tile in registers; none yet
-      for (int tile = w; tile < end; tile += waves) {
-        load(here = tile);
-        const uint32_t m = v.largest();
-        top = m > top ? m : top;
+  for (int64_t at0 = (int64_t)blockIdx.y * tokens; at0 < a.T; at0 += (int64_t)gridDim.y * tokens) {
+    const int t0 = (int)at0;
+    // the slots from the workgroup's first on, and which of its tokens begin a run
+    const int mine = t0 + lane < a.T ? a.slots[t0 + lane] : -1;
+    int prior = __shfl_up(mine, 1);        // by all lanes: one that is not there gives nothing
+    if (lane == 0 && t0 > 0) prior = a.slots[t0 - 1];
+    const int my_block = block_of(mine);
+    uint64_t begins = __ballot(lane < tokens && my_block >= 0 &&
+                               (t0 + lane == 0 || my_block != block_of(prior)));
+    for (; begins; begins &= begins - 1) {
+      const int i0 = __builtin_ctzll(begins), t = t0 + i0;
+      const int slot0 = __builtin_amdgcn_readlane(mine, i0), b = block_of(slot0);
+      // the run: how long, and whether slots follow each other
+      uint64_t out = ~__ballot(my_block == b) >> i0;
+      int n = out ? __builtin_ctzll(out) : 64;
+      if (n > 64 - i0) n = 64 - i0;
+      const bool in = lane >= i0 && lane < i0 + n;
+      bool follows = __all(!in || mine == slot0 + lane - i0);
+      bool zero = __any(in && (mine & (bs - 1)) == 0);     // the block's first slot is written
+      for (int more = i0 + n == 64 ? 64 : 0; more == 64; n += more) {
+        const int i = t + n + lane, slot = i < a.T ? a.slots[i] : -1;
+        out = ~__ballot(block_of(slot) == b);
+        more = out ? __builtin_ctzll(out) : 64;
+        follows &= __all(lane >= more || slot == slot0 + n + lane);
+        zero |= __any(lane < more && (slot & (bs - 1)) == 0);
       }
-      if (works && !follows)             // tokens in any order
-        for (int i = w * 64 + lane; i < n * D; i += waves * 64) {
-          const float f = (float)x[(int64_t)(t + i / D) * a.ld[part] + i % D];
-          const uint32_t m = __float_as_uint(f) & 0x7fffffffu;
+      const int o0 = slot0 & (bs - 1);
+      for (int item0 = blockIdx.x * per; item0 < items; item0 += gridDim.x * per) {
+        // the same number of rounds for every wave: they meet below
+        const int item = item0 + wave / waves;
+        const bool works = item < items;
+        const int h = works ? item >> 1 : 0, part = item & 1, w = wave & (waves - 1);
+        const CachePart c = a.part[part];
+        const T* x = (const T*)a.x[part] + (int64_t)h * D;
+        uint8_t* codes = c.codes + (int64_t)b * c.stride + (int64_t)h * bs * D;
+        float* scale = c.scale + (int64_t)b * a.heads + h;
+        const int64_t ld = a.ld[part];
+        // lanes of a tile side by side in dims, 8 each; tokens and dims of the lane
+        const int side = part ? append_side(D, shift) : __builtin_ctz(D / 8);   // log2
+        const int wide = __builtin_ctz(D / 8) - side, length = 8 - side;        // dims, tokens
+        const int q = (lane >> side) * 4, d0 = (lane & ((1 << side) - 1)) * 8;
+        const int first = o0 >> length;
+        const int end = works && follows ? (((o0 + n - 1) >> length) + 1 - first) << wide : 0;
+        Quad<T> v;
+        const auto token_of = [&](int tile) { return ((first + (tile >> wide)) << length) + q; };
+        const auto dim_of = [&](int tile) { return d0 + ((tile & ((1 << wide) - 1)) << (side + 3)); };
+        // whether all of a tile's tokens are the run's
+        const auto inside = [&](int tile) {
+          const int o = (first + (tile >> wide)) << length;
+          return o >= o0 && o + (1 << length) <= o0 + n;
+        };
+        const auto load = [&](int tile) {
+          const int i = token_of(tile) - o0;
+          const T* p = x + (t + i) * ld + dim_of(tile);
+          if (inside(tile)) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int j = 0; j < Quad<T>::W; ++j) v.raw[k][j] = *((const u32x4*)(p + k * ld) + j);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int j = 0; j < Quad<T>::W; ++j) {
+                v.raw[k][j] = u32x4{0, 0, 0, 0};
+                if (i + k >= 0 && i + k < n) v.raw[k][j] = *((const u32x4*)(p + k * ld) + j);
+              }
+          }
+        };
+        uint32_t top = 0;
+        const float was = works ? *scale : 1.0f;
+        int here = w - waves;              // the tile in registers; none yet
+        for (int tile = w; tile < end; tile += waves) {
+          load(here = tile);
+          const uint32_t m = v.largest();
           top = m > top ? m : top;
         }
-      top = wave_max_u32(top);
-      if (waves > 1) {
-        if (lane == 0) s_max[wave] = top;
-        __syncthreads();
-        for (int i = wave & ~(waves - 1), end = i + waves; i < end; ++i)
-          top = s_max[i] > top ? s_max[i] : top;
-      }
-      const bool bad = top >= 0x7f800000u;
-      float now = scale_of(bad ? 0.0f : __uint_as_float(top));
-      if (!zero) now = grown_scale(was, now);
-      if (bad) now = __builtin_nanf("");
-      const bool none = now != now;      // all codes are 0 then
-      // in any order, or beyond the largest scale: number by number
-      const bool single = !follows || now >= kScaleMax;
-      if (works && !zero && now != was && !none) {
-        const float k = clamp_scale(was) / now;
-        u32x4* p = (u32x4*)codes;
-        for (int i = w * 64 + lane; i < bs * D / 16; i += waves * 64) {
-          u32x4 u = p[i];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) u[j] = recode(u[j], k);
-          p[i] = u;
+        if (works && !follows)             // tokens in any order
+          for (int i = w * 64 + lane; i < n * D; i += waves * 64) {
+            const float f = (float)x[(int64_t)(t + i / D) * a.ld[part] + i % D];
+            const uint32_t m = __float_as_uint(f) & 0x7fffffffu;
+            top = m > top ? m : top;
+          }
+        top = wave_max_u32(top);
+        if (waves > 1) {
+          if (lane == 0) s_max[wave] = top;
+          __syncthreads();
+          for (int i = wave & ~(waves - 1), end = i + waves; i < end; ++i)
+            top = s_max[i] > top ? s_max[i] : top;
         }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // before others' codes go there
-      }
-      // the scale has been read, and what stood there is written, by all of the group
-      if (waves > 1) __syncthreads();
-      if (!works) continue;
-      if (w == 0 && lane == 0) *scale = now;
-      for (int tile = here; tile >= 0 && !single; tile -= waves) {   // the last is there
-        if (tile != here) load(tile);
-        if (none)
+        const bool bad = top >= 0x7f800000u;
+        float now = scale_of(bad ? 0.0f : __uint_as_float(top));
+        if (!zero) now = grown_scale(was, now);
+        if (bad) now = __builtin_nanf("");
+        const bool none = now != now;      // all codes are 0 then
+        // in any order, or beyond the largest scale: number by number
+        const bool single = !follows || now >= kScaleMax;
+        if (works && !zero && now != was && !none) {
+          const float k = clamp_scale(was) / now;
+          u32x4* p = (u32x4*)codes;
+          for (int i = w * 64 + lane; i < bs * D / 16; i += waves * 64) {
+            u32x4 u = p[i];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+            for (int j = 0; j < 4; ++j) u[j] = recode(u[j], k);
+            p[i] = u;
+          }
+          asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // before others' codes go there
+        }
+        // the scale has been read, and what stood there is written, by all of the group
+        if (waves > 1) __syncthreads();
+        if (!works) continue;
+        if (w == 0 && lane == 0) *scale = now;
+        for (int tile = here; tile >= 0 && !single; tile -= waves) {   // the last is there
+          if (tile != here) load(tile);
+          if (none)
 #pragma unroll
-            for (int j = 0; j < Quad<T>::W; ++j) v.raw[k][j] = u32x4{0, 0, 0, 0};
-        const float by = none ? 1.0f : now;
-        const int o = token_of(tile), d = dim_of(tile);
-        const uint32_t at = part ? d * bs + o : o * D + d;
-        if (inside(tile)) {
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int j = 0; j < Quad<T>::W; ++j) v.raw[k][j] = u32x4{0, 0, 0, 0};
+          const float by = none ? 1.0f : now;
+          const int o = token_of(tile), d = dim_of(tile);
+          const uint32_t at = part ? d * bs + o : o * D + d;
+          if (inside(tile)) {
+            if (part == 0) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                *(u32x2*)(codes + k * D + at) = u32x2{v.dims4(k, 0, by), v.dims4(k, 1, by)};
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) *(uint32_t*)(codes + i * bs + at) = v.tokens4(i, by);
+            }
+            continue;
+          }
+          // the run ends inside the tile
           if (part == 0) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              *(u32x2*)(codes + k * D + at) = u32x2{v.dims4(k, 0, by), v.dims4(k, 1, by)};
+              if (o + k >= o0 && o + k < o0 + n)
+                *(u32x2*)(codes + k * D + at) = u32x2{v.dims4(k, 0, by), v.dims4(k, 1, by)};
           } else {
+            const bool whole = o >= o0 && o + 3 < o0 + n;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) *(uint32_t*)(codes + i * bs + at) = v.tokens4(i, by);
-          }
-          continue;
-        }
-        // the run ends inside the tile
-        if (part == 0) {
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t u = v.tokens4(i, by);
+              uint8_t* p = codes + i * bs + at;
+              if (whole) *(uint32_t*)p = u;
+              else
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (o + k >= o0 && o + k < o0 + n)
-              *(u32x2*)(codes + k * D + at) = u32x2{v.dims4(k, 0, by), v.dims4(k, 1, by)};
-        } else {
-          const bool whole = o >= o0 && o + 3 < o0 + n;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t u = v.tokens4(i, by);
-            uint8_t* p = codes + i * bs + at;
-            if (whole) *(uint32_t*)p = u;
-            else
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (o + k >= o0 && o + k < o0 + n) p[k] = (uint8_t)(u >> (8 * k));
+                for (int k = 0; k < 4; ++k)
+                  if (o + k >= o0 && o + k < o0 + n) p[k] = (uint8_t)(u >> (8 * k));
+            }
           }
         }
-      }
-      if (!single) continue;
-      const float inv = none ? 1.0f : 1.0f / now;
-      for (int j = 0; j < n; ++j) {      // one after the other: the later one stays
-        const int o = a.slots[t + j] & (bs - 1);
-        for (int i = w * 64 + lane; i < D; i += waves * 64) {
-          const float f = (float)x[(t + j) * ld + i];
-          codes[part ? i * bs + o : o * D + i] = to_code(none ? 0.0f : f * inv);
+        if (!single) continue;
+        const float inv = none ? 1.0f : 1.0f / now;
+        for (int j = 0; j < n; ++j) {      // one after the other: the later one stays
+          const int o = a.slots[t + j] & (bs - 1);
+          for (int i = w * 64 + lane; i < D; i += waves * 64) {
+            const float f = (float)x[(t + j) * ld + i];
+            codes[part ? i * bs + o : o * D + i] = to_code(none ? 0.0f : f * inv);
+          }
         }
       }
     }
@@ -585,7 +586,8 @@ hipError_t append_t(const AppendArgs& a, hipStream_t s) {
   // tokens, blocks of 64: 16 of them 105 us, 64 51 us).
   const int tokens = a.T > 2048 ? 64 : 1;
   const int items = a.heads * 2, per = 4 / waves;
-  const int64_t y = ((int64_t)a.T + tokens - 1) / tokens;
+  int64_t y = ((int64_t)a.T + tokens - 1) / tokens;
+  if (y > 65535) y = 65535;
   const int x = (items + per - 1) / per;
   const auto launch = [&](auto d) {
     constexpr int D = decltype(d)::value;

@@ -668,7 +668,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_kernel(AttendArg
                                                : last / plan.chunk) -
                                           worker);
         const int rows = r.rows - t * M < M ? r.rows - t * M : M;
-        *space.piece(head, at.tile0 + t) =
+        // more row tiles than there is room for have offsets that decrease
+        if (at.tile0 + t < sp.tiles)
+          *space.piece(head, at.tile0 + t) =
             Piece{r.q0, t * M, rows, (int)(worker * 2 + (u > u0)), n, 0};
       }
     }
@@ -685,65 +687,70 @@ __global__ __launch_bounds__(NT) void merge_kernel(AttendArgs a, Split sp, char*
   __shared__ f32x4 sums[NT];
   __shared__ float2 mls[NT / L];
   const Space<M, D> space(ws, a.kv_heads, sp);
-  const int head = blockIdx.y, tile = blockIdx.x;
-  if (tile >= *space.count()) return;
-  const Piece x = *space.piece(head, tile);
-  const int i0 = blockIdx.z * R;
-  if (x.n == 0 || i0 >= x.rows) return;
-  const int here = x.rows - i0 < R ? x.rows - i0 : R;
-  // fewer rows: more groups, each with every G-th part
-  int G = G0, span = R;
-  while (span / 2 >= here) {
-    span /= 2;
-    G *= 2;
-  }
-  const int lanes = threadIdx.x / L, i = i0 + lanes % span, g = lanes / span;
-  const int d = threadIdx.x % L * 4;
-  float m = kNegInf, l = 0.0f;
-  f32x4 o = {0, 0, 0, 0};
-  if (i < x.rows) {
-    const int first = x.at / 2;
-    // a part's place: its worker's slot 0, but for the first
-    const auto part = [&](int k) { return space.part(sp, head, k == 0 ? x.at : (first + k) * 2); };
-#pragma unroll 4
-    for (int k = g; k <= x.n; k += G) m = fmaxf(m, part(k).ml[i].x);
-    const float ref = m == kNegInf ? 0.0f : m;
-#pragma unroll 4
-    for (int k = g; k <= x.n; k += G) {
-      const Partial p = part(k);
-      const float2 ml = p.ml[i];
-      const float f = exp2_fast(ml.x - ref);
-      l = fmaf(ml.y, f, l);
-      o += *(const f32x4*)(p.o + i * D + d) * f;
+  const int head = blockIdx.y, i0 = blockIdx.z * R, group = a.q_heads / a.kv_heads;
+  const int64_t tiles = *space.count() < sp.tiles ? *space.count() : sp.tiles;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const Piece x = *space.piece(head, tile);
+    if (x.n == 0 || i0 >= x.rows) continue;
+    const int here = x.rows - i0 < R ? x.rows - i0 : R;
+    // fewer rows: more groups, each with every G-th part
+    int G = G0, span = R;
+    while (span / 2 >= here) {
+      span /= 2;
+      G *= 2;
     }
-  }
-  if (G > 1) {
-    sums[threadIdx.x] = o;
-    if (d == 0) mls[lanes] = make_float2(m, l);
-    __syncthreads();
-    if (g > 0) return;
-    float top = m;
-    for (int k = 1; k < G; ++k) top = fmaxf(top, mls[lanes + k * span].x);
-    const float ref = top == kNegInf ? 0.0f : top, f0 = exp2_fast(m - ref);
-    o = o * f0;
-    l *= f0;
-    for (int k = 1; k < G; ++k) {
-      const float2 ml = mls[lanes + k * span];
-      const float f = exp2_fast(ml.x - ref);
-      l = fmaf(ml.y, f, l);
-      o += sums[threadIdx.x + k * span * L] * f;
+    const int lanes = threadIdx.x / L, i = i0 + lanes % span, g = lanes / span;
+    const int d = threadIdx.x % L * 4;
+    float m = kNegInf, l = 0.0f;
+    f32x4 o = {0, 0, 0, 0};
+    if (i < x.rows) {
+      const int first = x.at / 2;
+      // a part's place: its worker's slot 0, but for the first
+      const auto part = [&](int k) {
+        return space.part(sp, head, k == 0 ? x.at : (first + k) * 2);
+      };
+#pragma unroll 4
+      for (int k = g; k <= x.n; k += G) m = fmaxf(m, part(k).ml[i].x);
+      const float ref = m == kNegInf ? 0.0f : m;
+#pragma unroll 4
+      for (int k = g; k <= x.n; k += G) {
+        const Partial p = part(k);
+        const float2 ml = p.ml[i];
+        const float f = exp2_fast(ml.x - ref);
+        l = fmaf(ml.y, f, l);
+        o += *(const f32x4*)(p.o + i * D + d) * f;
+      }
     }
-    m = top;
+    if (G > 1) {
+      __syncthreads();                   // the sums of the tile before are used
+      sums[threadIdx.x] = o;
+      if (d == 0) mls[lanes] = make_float2(m, l);
+      __syncthreads();
+      if (g == 0) {
+        float top = m;
+        for (int k = 1; k < G; ++k) top = fmaxf(top, mls[lanes + k * span].x);
+        const float ref = top == kNegInf ? 0.0f : top, f0 = exp2_fast(m - ref);
+        o = o * f0;
+        l *= f0;
+        for (int k = 1; k < G; ++k) {
+          const float2 ml = mls[lanes + k * span];
+          const float f = exp2_fast(ml.x - ref);
+          l = fmaf(ml.y, f, l);
+          o += sums[threadIdx.x + k * span * L] * f;
+        }
+        m = top;
+      }
+    }
+    if (g > 0 || i >= x.rows) continue;
+    const int row = x.row0 + i, token = row / group;
+    const int h = head * group + row - token * group;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    store4((T*)a.out + (int64_t)(x.q0 + token) * a.out_ld + (int64_t)h * D + d, o[0] * inv,
+           o[1] * inv, o[2] * inv, o[3] * inv);
+    if (a.lse && d == 0)
+      a.lse[(int64_t)(x.q0 + token) * a.q_heads + h] =
+          l == 0.0f ? kNegInf : (float)(kLn2 * ((double)m + log2((double)l)));
   }
-  if (g > 0 || i >= x.rows) return;
-  const int group = a.q_heads / a.kv_heads, row = x.row0 + i, token = row / group;
-  const int h = head * group + row - token * group;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  store4((T*)a.out + (int64_t)(x.q0 + token) * a.out_ld + (int64_t)h * D + d, o[0] * inv,
-         o[1] * inv, o[2] * inv, o[3] * inv);
-  if (a.lse && d == 0)
-    a.lse[(int64_t)(x.q0 + token) * a.q_heads + h] =
-        l == 0.0f ? kNegInf : (float)(kLn2 * ((double)m + log2((double)l)));
 }
 
 int row_tiles_of(int64_t T, int64_t S, int64_t group) {
@@ -766,7 +773,8 @@ hipError_t attend_t(const AttendArgs& a, char* ws, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.S == 0) return e;
   // few row tiles leave room for more threads on each
-  const dim3 grid((unsigned)sp.tiles, a.kv_heads, 16 * MT * D / kMergeRows);
+  const dim3 grid((unsigned)(sp.tiles < 65536 ? sp.tiles : 65536), a.kv_heads,
+                  16 * MT * D / kMergeRows);
   if (sp.tiles * a.kv_heads <= 512)
     hipLaunchKernelGGL((merge_kernel<T, D, MT, 1024>), grid, dim3(1024), 0, s, a, sp, ws);
   else

@@ -22,16 +22,20 @@ __device__ __forceinline__ void rows_of(const VerifyArgs& a, int64_t s, int64_t*
   *hi = y > a.R ? a.R : y;
 }
 
-// Whether a sequence ends behind row r, or r lies in none: by the threads of a group.
-template <int GT>
+// Whether a sequence ends behind row r, or r lies in none.  Every wave looks for the
+// first offset beyond r, in 64 places at a time.
 __device__ __forceinline__ bool drafts_end(const VerifyArgs& a, int64_t r) {
-  bool end = false;
-  for (int64_t s = group_tid<GT>(); s <= a.S; s += GT) {
-    const int64_t x = a.offsets[s];
-    end |= x == r + 1 || (s == 0 && r < x) || (s == a.S && r >= x);
+  const int lane = threadIdx.x & 63;
+  int64_t lo = 0, n = a.S + 1;           // it is among offsets[lo .. lo + n]
+  while (n > 0) {
+    const int64_t step = (n + 63) / 64, i = lane * step;
+    const int before = __popcll(__ballot(i < n && a.offsets[lo + (i < n ? i : 0)] <= r));
+    if (before == 0) break;
+    lo += (before - 1) * step + 1;
+    n -= (before - 1) * step + 1;
+    if (n > step - 1) n = step - 1;
   }
-  if constexpr (GT == 64) return __any(end);
-  return __syncthreads_or(end);
+  return lo == 0 || lo > a.S || a.offsets[lo] == r + 1;
 }
 
 // Group b: a part of row b of the targets, then of the drafters.
@@ -48,7 +52,7 @@ __global__ __launch_bounds__(256) void verify_look_kernel(VerifyArgs a, Parts pa
   const int64_t r = drafter ? at.r - a.R : at.r;
   if (r >= a.R || (drafter && !a.d)) return;
   if (drafter) {
-    if (a.drafts[r] < 0 || drafts_end<GT>(a, r)) return;
+    if (a.drafts[r] < 0 || drafts_end(a, r)) return;
   } else if (at.p == 0 && tid == 0) {
     a.tokens[r] = -1;
     a.logp[r] = 0.0f;

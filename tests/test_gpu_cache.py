@@ -109,6 +109,9 @@ def test_tables_without_requests_or_blocks():
                                           e, state, 16, 5)
     assert g.tolist() == [0, 3] and off.tolist() == [0, 4, 4] and slots.tolist() == [-1] * 5
     assert state.tolist() == [0, 0, 0, 0]
+    table = torch.full((2, 3), 5, dtype=torch.int32, device="cuda")    # blocks given back to a pool without room
+    g, _, _ = _lib.lik_cache_tables(i32([40, 3]), i32([1, 0]), table, e, state, 16, 0)
+    assert g.tolist() == [1, 0] and table.tolist() == [[5, -1, -1], [-1, 5, 5]] and state.tolist() == [0, 0, 0, 0]
 
 
 def test_tables_with_a_broken_pool_stay_inside():
@@ -530,6 +533,39 @@ def test_results_do_not_change():
     for _ in range(3):
         b = _lib.lik_cache_attention(q, i32(off), i32(lens), i32(table), *c.parts, want_lse=True)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_offsets_that_decrease_stay_inside():
+    """Requests that claim the same rows again and again: more row tiles than rows give."""
+    c, q, off, lens, table = setup([3] * 70, [90] * 70, 4, 2, 64, 16, BF16, 31)
+    T, S = q.shape[0], 70
+    clean = _lib.lik_cache_attention(q, i32(off), i32(lens), i32(table), *c.parts)[0]
+    bad = np.where(np.arange(S + 1) % 2 == 0, 0, T)
+    need = _lib.lib().lik_cache_workspace_bytes(T, S, 4, 2, 64, _lib.LIK_BF16)
+    ws = torch.full((need + 4096,), 0x77, dtype=torch.uint8, device="cuda")
+    out = torch.zeros_like(q)
+    st = _lib.lib().lik_cache_attention(
+        q.data_ptr(), _lib.LIK_BF16, T, 4, 256, i32(bad).data_ptr(), i32(lens).data_ptr(), S,
+        i32(table).data_ptr(), table.shape[1], table.shape[1], *_lib._blocks(*c.parts, q.device), 0.1,
+        out.data_ptr(), 256, None, ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == 0 and (ws[need:] == 0x77).all()
+    again = _lib.lik_cache_attention(q, i32(off), i32(lens), i32(table), *c.parts)[0]
+    assert torch.equal(clean, again)
+
+
+def test_append_millions_of_tokens():
+    """More than a grid has rows for; all but the last few without a slot."""
+    T, n = 65535 * 64 + 900, 700
+    x = torch.zeros((T, 1, 64), dtype=F16, device="cuda")
+    x[-n:] = torch.randn((n, 1, 64), device="cuda")
+    slots = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    at = [16 * (3 * (i // 16) % 59) + i % 16 for i in range(n)]
+    slots[-n:] = i32(at)
+    a, b = Cache(60, 1, 16, 64, 1), Cache(60, 1, 16, 64, 1)
+    _lib.lik_cache_append(x, x, slots, *a.parts)
+    _lib.lik_cache_append(x[-n:], x[-n:], i32(at), *b.parts)
+    assert torch.equal(a.buf, b.buf) and torch.equal(a.gks, b.gks) and torch.equal(a.gvs, b.gvs)
 
 
 def test_binding_on_the_gpu():

@@ -267,6 +267,25 @@ def test_tokens_have_the_targets_distribution():
     assert 0 < a.sum() < S
 
 
+@pytest.mark.parametrize("S", [1, 63, 64, 65, 4095, 4097, 70001])
+def test_last_rows_of_many_sequences(S):
+    """Drafters' rows behind the last draft are anything, whatever their number and the
+    sequences': the offsets are searched in steps of 64."""
+    rng = np.random.default_rng(S)
+    counts = rng.integers(0, 4, S)
+    off = np.concatenate([[0], np.cumsum(counts)])
+    R, C = int(off[-1]) + 1, 4
+    z = torch.randn(R, C, device="cuda")
+    d = z.clone()
+    ends = torch.as_tensor(off[1:][counts > 0] - 1).cuda()
+    d[ends] = float("nan")
+    drafts = torch.zeros(R, dtype=torch.int32, device="cuda")
+    t, a, lp = _lib.lik_verify_rows(z, drafts, i32(off), torch.full((R,), 0.99, device="cuda"),
+                                    torch.full((S,), 0.5, device="cuda"), draft_logits=d)
+    assert a.tolist() == np.maximum(counts - 1, 0).tolist()
+    assert not torch.isnan(lp).any() and (t[ends] >= 0).all() and (t[:-1] >= 0).sum() == int(off[-1])
+
+
 def test_offsets_past_32_bits():
     C = 2 ** 20
     R = 2 ** 32 // (2 * C) + 3
