@@ -236,8 +236,9 @@ lik_status lik_preference_rows(const void* logits, lik_dtype dtype, int64_t R,
  *     a sequence without rows.
  *   logp [R] float32: log p of the emitted token, 0 where tokens has none.
  * A row whose logits, or whose draft's, have no softmax (all -inf, a NaN, +inf)
- * ends its sequence with the token -1 and logp NaN.  Probabilities are float32,
- * sums of them and comparisons float64; the outputs must not overlap the inputs.
+ * ends its sequence with the token -1 and logp NaN.  Probabilities are float32, and
+ * sums of up to 8 neighbouring ones; all further sums and the comparisons are
+ * float64.  The outputs must not overlap the inputs.
  */
 lik_status lik_verify_rows(const void* logits, lik_dtype dtype, int64_t R,
                            int64_t C, int64_t ld, const void* draft_logits,

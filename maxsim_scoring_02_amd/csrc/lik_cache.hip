@@ -586,8 +586,7 @@ hipError_t append_t(const AppendArgs& a, hipStream_t s) {
   // a wave a tile of 256 x 8 numbers, at most four a run
   const int tiles = a.block_size * a.dim / 2048;
   const int waves = tiles > 2 ? 4 : (tiles > 1 ? 2 : 1);
-  // Many tokens: most do not begin a run, and a workgroup looks at 64 of them (18400
-  // tokens, blocks of 64: 16 of them 105 us, 64 51 us).
+  // Many tokens: most do not begin a run, and a workgroup looks at 64 of them.
   const int tokens = a.T > 2048 ? 64 : 1;
   const int items = a.heads * 2, per = 4 / waves;
   int64_t y = ((int64_t)a.T + tokens - 1) / tokens;

@@ -225,15 +225,21 @@ inline Parts verify_draw(int64_t S, int64_t C, lik_dtype dtype) {
   p.gt = 256;
   return p;
 }
+// Beyond so many workgroups that draw, the rows that sequences end at are found by a launch
+// of their own and not by each of them (16-bit drafts, 5 rows: 1000 sequences of 131072
+// 540 us against 589, 256 of 131072 145 against 153; 256 of 32768, 1024 workgroups, 52
+// against 49).
+constexpr int64_t kVerifyEnds = 1024;
 struct VerifyLayout {
-  size_t sums, done, bytes;              // behind the parts' [rows][n] float2
+  size_t sums, done, ends, bytes;        // behind the parts' [rows][n] float2
 };
 inline VerifyLayout verify_layout(int64_t R, int64_t C, int64_t S, lik_dtype dtype, bool drafter) {
   const int64_t rows = drafter ? 2 * R : R;
   VerifyLayout w;
   w.sums = rows_up((size_t)rows * verify_look(R, C, dtype, drafter).n * 8);
   w.done = rows_up(w.sums + (size_t)S * verify_draw(S, C, dtype).n * 8);
-  w.bytes = rows_up(w.done + (size_t)S * 4);
+  w.ends = rows_up(w.done + (size_t)S * 4);
+  w.bytes = rows_up(w.ends + (size_t)S * 64);
   return w;
 }
 hipError_t run_verify(const VerifyArgs& a, char* ws, hipStream_t s);

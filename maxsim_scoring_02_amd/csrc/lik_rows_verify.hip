@@ -1,15 +1,16 @@
 // Verification of drafted tokens (include/lik_rows.h, lik_verify_rows), in two
 // launches.  The first looks at every row of target and drafter once and leaves the
 // (m, Z) of its parts.  In the second a workgroup has a part of the row that its
-// sequence ends at: it finds that row (every workgroup by itself, from the parts), sums
-// the weights w of its columns, and the last of a sequence's workgroups to be done
-// finds the part, and in it the column, that the random number points at.
-// Weights are float32, sums of them float64: a token of a vocabulary of 10^5
+// sequence ends at: it finds that row from the parts (every workgroup by itself, or a
+// launch in between where they are many), sums the weights w of its columns, and the
+// last of a sequence's workgroups to be done finds the part, and in it the column, that
+// the random number points at.
+// Weights are float32, sums of their pieces float64: a token of a vocabulary of 10^5
 // has an interval of 10^-5 and less, which float32 sums would blur.
 //
 // 256 x 5 rows of 131072 bf16 (604 MB): the first launch is bound by reads, 6.9 TB/s, 87
-// us; the second reads the two rows a sequence ends at again (134 MB) and takes two
-// exponentials a column, 66 to 73 us.  One sequence of 5 rows of 32768: 3.8 and 10.5
+// us; the rows of the ends take 6 us; the second reads the two rows a sequence ends at
+// again (134 MB) and takes two exponentials a column, 44 to 51 us.  One sequence of 5 rows of 32768: 3.8 and 10.5
 // us, latency: the second goes from offsets to drafts, to their logits, to the row's
 // parts, to the sums and back into one part.
 #include <hip/hip_runtime.h>
@@ -118,11 +119,13 @@ struct Weights {
 constexpr int kVerifyPieces = 4;
 
 // A part's weights by 256 threads, as 16-byte pieces of the row: sums a piece, the
-// columns before the first and behind the last whole piece first and last.
-template <typename T>
+// columns before the first and behind the last whole piece first and last.  The 4 or 8
+// weights of a piece are added in float32: what that rounds is of the size of the weights'
+// own error.
+template <typename T, bool Once>
 struct PartWeights {
   static constexpr int NV = kVerifyPieces, N = PieceOf<T>::N, kSlots = NV + 2;
-  HeldRow<T, 256, NV, false> z, d;
+  HeldRow<T, 256, NV, Once> z, d;
 
   __device__ __forceinline__ void load(const Weights<T>& w, int lo, int cols) {
     z.load(w.row + lo, cols, threadIdx.x, nullptr);
@@ -149,10 +152,7 @@ struct PartWeights {
     if (!z.deal.has(k - 1)) return 0.0;
     float f[N];
     piece_of(w, lo, k - 1, f);
-    double sum = 0.0;
-#pragma unroll
-    for (int j = 0; j < N; ++j) sum += (double)f[j];
-    return sum;
+    return (double)piece_total<N>(f);
   }
   __device__ __forceinline__ int column_of(int k) const {
     return k == 0 || k == kSlots - 1 ? z.deal.edge() : z.deal.column(k - 1);
@@ -187,7 +187,7 @@ __device__ __forceinline__ double lane_of(double v, int k) {
 // weight where rounding, or a goal beyond the part, leaves none.
 template <typename T>
 __device__ int pick(const Weights<T>& w, int lo, int cols, double goal, double* tmp, int* found) {
-  typedef PartWeights<T> P;
+  typedef PartWeights<T, false> P;
   P part;
   part.load(w, lo, cols);
   const int lane = threadIdx.x & 63, wave = wave_id();
@@ -248,87 +248,112 @@ __device__ int pick(const Weights<T>& w, int lo, int cols, double goal, double* 
   return *found;
 }
 
+// Where a sequence ends: the row a token is drawn from.
+struct VerifyEnd {
+  int64_t r;                             // -1: it has no rows
+  double ln_sum;
+  RowSoft p, q;
+  int more, broken;
+};
+
 struct VerifySpace {
   float2* mz;                            // [2 R][parts of a row]
   double* sums;                          // [S][parts of a drawn row]
   int* done;                             // [S]
+  VerifyEnd* ends;                       // [S], where they are found by a launch of their own
 };
 
+// The end of sequence s, by 256 threads: four rows at a time, a wave each, until one
+// does not accept.  With `write` the outputs up to there too.
 template <typename T>
-__global__ __launch_bounds__(256) void verify_draw_kernel(VerifyArgs a, int look, Parts parts,
-                                                          VerifySpace ws) {
-  __shared__ double tmp[PartWeights<T>::kSlots * 4];
-  __shared__ RowSoft soft[2][4];
-  __shared__ double ln_sums[4];
-  __shared__ int flags[4], last, found;
-  const int64_t s = linear_block() / parts.n;
-  if (s >= a.S) return;
-  const int part = (int)(linear_block() - s * parts.n);
+__device__ __forceinline__ VerifyEnd find_end(const VerifyArgs& a, const float2* mz, int look,
+                                              int64_t s, bool write) {
+  __shared__ VerifyEnd rows[4];
+  __shared__ int taken[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
+  VerifyEnd e;
   int64_t lo, hi;
   rows_of(a, s, &lo, &hi);
   if (hi <= lo) {
-    if (part == 0 && tid == 0) a.accepted[s] = 0;
-    return;
+    if (write && tid == 0) a.accepted[s] = 0;
+    e.r = -1;
+    return e;
   }
-  // four rows at a time, a wave each, until one does not accept
-  int64_t r = lo;
-  int how = 0;
   for (int64_t r0 = lo;; r0 += 4) {
     Verdict v;
     v.taken = false;
-    const bool there = r0 + wave < hi;
-    if (there) v = judge<T>(a, ws.mz, look, r0 + wave, hi);
+    const int64_t r = r0 + wave;
+    if (r < hi) v = judge<T>(a, mz, look, r, hi);
     if (lane == 0) {
-      flags[wave] = there ? (v.taken ? 4 : 0) | (v.more ? 1 : 0) | (v.broken ? 2 : 0) : 0;
-      soft[0][wave] = v.p;
-      soft[1][wave] = v.q;
-      ln_sums[wave] = v.ln_sum;
+      taken[wave] = r < hi && v.taken;
+      if (r < hi) rows[wave] = VerifyEnd{r, v.ln_sum, v.p, v.q, v.more, v.broken};
     }
     __syncthreads();
     int w = 0;
-    while (w < 4 && (flags[w] & 4)) ++w;
-    if (part == 0 && lane == 0 && wave < w) {
-      const int x = a.drafts[r0 + wave];
-      a.tokens[r0 + wave] = x;
-      a.logp[r0 + wave] = (float)row_logp(v.p, (float)((const T*)a.z)[(r0 + wave) * a.ld + x],
-                                          a.scale, v.ln_sum);
+    while (w < 4 && taken[w]) ++w;
+    if (write && lane == 0 && wave < w) {
+      const int x = a.drafts[r];
+      a.tokens[r] = x;
+      a.logp[r] = (float)row_logp(v.p, (float)((const T*)a.z)[r * a.ld + x], a.scale, v.ln_sum);
     }
     if (w < 4) {
-      r = r0 + w;
-      how = w;
+      e = rows[w];
       break;
     }
     __syncthreads();
   }
-  const int flag = flags[how];
-  const bool more = flag & 1, broken = flag & 2;
-  const double u = (double)a.sample_u[s];
-  if (part == 0 && tid == 0) {
-    a.accepted[s] = (int)(r - lo);
-    if (broken) a.logp[r] = __builtin_nanf("");
+  if (write && tid == 0) {
+    a.accepted[s] = (int)(e.r - lo);
+    if (e.broken) a.logp[e.r] = __builtin_nanf("");
   }
+  return e;
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void verify_end_kernel(VerifyArgs a, int look, VerifySpace ws) {
+  const int64_t s = linear_block();
+  if (s >= a.S) return;
+  const VerifyEnd e = find_end<T>(a, ws.mz, look, s, true);
+  if (threadIdx.x == 0) ws.ends[s] = e;
+}
+
+// Once: the rows are not in the cache behind the L2s, and go past it again.
+// Found: by verify_end_kernel.
+template <typename T, bool Once, bool Found>
+__global__ __launch_bounds__(256) void verify_draw_kernel(VerifyArgs a, int look, Parts parts,
+                                                          VerifySpace ws) {
+  __shared__ double tmp[PartWeights<T, Once>::kSlots * 4];
+  __shared__ int last, found;
+  const int64_t s = linear_block() / parts.n;
+  if (s >= a.S) return;
+  const int part = (int)(linear_block() - s * parts.n);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const VerifyEnd e = Found ? ws.ends[s] : find_end<T>(a, ws.mz, look, s, part == 0);
+  const int64_t r = e.r;
+  if (r < 0) return;
+  const bool more = e.more, broken = e.broken;
+  const double u = (double)a.sample_u[s];
   if (broken || u != u) return;
   Weights<T> w;
   w.row = (const T*)a.z + r * a.ld;
   w.drow = a.d && more ? (const T*)a.d + r * a.draft_ld : nullptr;
-  w.p = soft[0][how];
-  w.q = soft[1][how];
+  w.p = e.p;
+  w.q = e.q;
   w.ip = 1.0f / w.p.Z;
   w.iq = 1.0f / w.q.Z;
   w.x = !a.d && more ? a.drafts[r] : -1;
-  const double ln_sum = ln_sums[how];
+  const double ln_sum = e.ln_sum;
   const auto columns = [&](int p) {
     const int left = a.C - p * parts.cols;
     return left < parts.cols ? left : parts.cols;
   };
   double* sums = ws.sums + s * parts.n;
   if (parts.n > 1) {
-    PartWeights<T> mine;
+    PartWeights<T, Once> mine;
     mine.load(w, part * parts.cols, columns(part));
     double sum = 0.0;
 #pragma unroll
-    for (int k = 0; k < PartWeights<T>::kSlots; ++k) sum += mine.slot(w, part * parts.cols, k);
+    for (int k = 0; k < PartWeights<T, Once>::kSlots; ++k) sum += mine.slot(w, part * parts.cols, k);
     sum = block_sum(sum, tmp);
     if (tid == 0) {
       // The sum goes past the caches by itself, and has arrived when the count moves: no
@@ -353,11 +378,11 @@ __global__ __launch_bounds__(256) void verify_draw_kernel(VerifyArgs a, int look
     if (pass == 1 || parts.n == 1) {
       // a part after the other, into the parts' places
       for (int p = 0; p < parts.n; ++p) {
-        PartWeights<T> x;
+        PartWeights<T, false> x;
         x.load(w, p * parts.cols, columns(p));
         double sum = 0.0;
 #pragma unroll
-        for (int k = 0; k < PartWeights<T>::kSlots; ++k) sum += x.slot(w, p * parts.cols, k);
+        for (int k = 0; k < PartWeights<T, false>::kSlots; ++k) sum += x.slot(w, p * parts.cols, k);
         sum = block_sum(sum, tmp);
         if (tid == 0) __hip_atomic_store(&sums[p], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
@@ -414,7 +439,8 @@ hipError_t verify_t(const VerifyArgs& a, char* ws, hipStream_t s) {
   const int64_t rows = a.d ? 2 * a.R : a.R;
   const Parts look = verify_look(a.R, a.C, a.dtype, a.d), draw = verify_draw(a.S, a.C, a.dtype);
   const VerifyLayout at = verify_layout(a.R, a.C, a.S, a.dtype, a.d);
-  const VerifySpace space{(float2*)ws, (double*)(ws + at.sums), (int*)(ws + at.done)};
+  const VerifySpace space{(float2*)ws, (double*)(ws + at.sums), (int*)(ws + at.done),
+                          (VerifyEnd*)(ws + at.ends)};
   const bool once = rows * a.C * elem_bytes_of(a.dtype) > kFarBytes;
   hipError_t e = parts_dispatch(look, [&](auto gt) {
     constexpr int GT = decltype(gt)::value;
@@ -424,8 +450,18 @@ hipError_t verify_t(const VerifyArgs& a, char* ws, hipStream_t s) {
     return hipGetLastError();
   });
   if (e != hipSuccess || a.S == 0) return e;
-  hipLaunchKernelGGL(verify_draw_kernel<T>, linear_grid(a.S * draw.n), dim3(256), 0, s, a, look.n,
-                     draw, space);
+  const auto draws = [&](auto found) {
+    constexpr bool F = decltype(found)::value;
+    const auto kernel = once ? verify_draw_kernel<T, true, F> : verify_draw_kernel<T, false, F>;
+    hipLaunchKernelGGL(kernel, linear_grid(a.S * draw.n), dim3(256), 0, s, a, look.n, draw, space);
+  };
+  if (a.S * draw.n > kVerifyEnds) {
+    hipLaunchKernelGGL(verify_end_kernel<T>, linear_grid(a.S), dim3(256), 0, s, a, look.n, space);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    draws(std::true_type());
+  } else {
+    draws(std::false_type());
+  }
   return hipGetLastError();
 }
 

@@ -149,6 +149,36 @@ def test_many_and_long(S, K, C, dtype):
     run(*make([K + 1] * S, C, S + C), dtype)
 
 
+@pytest.mark.parametrize("drafter", [True, False])
+@pytest.mark.parametrize("S,top,C,dtype", [(170, 4, 33001, F16), (160, 3, 32768, BF16), (165, 3, 16411, F32),
+                                           (161, 2, 140001, BF16), (159, 3, 33000, F16)])
+def test_many_sequences_of_long_rows(S, top, C, dtype, drafter):
+    """Rows of more than one part, beyond what the caches keep: every kind of end and of
+    row among them."""
+    say(f"[verify] {S} sequences of up to {top} rows of {C} {dtype}, drafter {drafter}")
+    rng = np.random.default_rng(C)
+    counts = rng.integers(0, top + 1, S)
+    counts[:24] = top
+    z, d, drafts, off, u, su = make(counts, C, C, drafter, lead=3, pad=2)
+    z[:3], z[-2:] = np.nan, np.inf
+    for r in (off[0], off[1] + 1):
+        z[r] = -np.inf
+    z[off[2] + 1, 77], z[off[3], C - 1] = np.nan, np.inf
+    z[off[4] + 1, rng.random(C) < 0.99] = -np.inf
+    z[off[5]], z[off[5], 5] = -np.inf, 1.0           # one column left
+    z[off[6]:off[7]] = np.float32(-6e4 if dtype == F16 else -1e9)
+    drafts[off[7]], drafts[off[8] + 1], drafts[off[9]] = -1, -7, C
+    su[10:16] = [0.0, np.nextafter(np.float32(1), np.float32(0)), 1.0, 5.0, -0.25, math.nan]
+    u[off[0]:off[10]] = 0.0
+    u[off[16]], u[off[17] + 1] = math.nan, 2.0
+    if drafter:
+        d[:3] = np.nan
+        d[off[18]], d[off[19] + 1, 9] = -np.inf, np.nan
+        d[off[20] + top - 1] = np.nan                # a last row's draft is not read
+        d[off[21]:off[22]] = z[off[21]:off[22]]
+    run(z, d, drafts, off, u, su, dtype, scale=0.9, dscale=1.2, pad=C % 2, shift=C % 3)
+
+
 def test_random_numbers_at_their_ends():
     z, d, drafts, off, u, su = make([4] * 7, 501, 3)
     u[:] = [0.0, np.nextafter(np.float32(1), np.float32(0))] * 14
