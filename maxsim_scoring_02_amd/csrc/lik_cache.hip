@@ -586,15 +586,20 @@ hipError_t append_t(const AppendArgs& a, hipStream_t s) {
   // a wave a tile of 256 x 8 numbers, at most four a run
   const int tiles = a.block_size * a.dim / 2048;
   const int waves = tiles > 2 ? 4 : (tiles > 1 ? 2 : 1);
-  // Many tokens: most do not begin a run, and a workgroup looks at 64 of them.
-  const int tokens = a.T > 2048 ? 64 : 1;
-  const int items = a.heads * 2, per = 4 / waves;
-  int64_t y = ((int64_t)a.T + tokens - 1) / tokens;
+  const int items = a.heads * 2, per = 4 / waves, x = (items + per - 1) / per;
+  // A workgroup looks at as many tokens as leave kAppendGroups workgroups, 64 at most: of
+  // a prompt's tokens most do not begin a run, of single ones all do, one after the other
+  // (8 heads of 128; one token a workgroup, this, 64 tokens: 2000 single tokens 31, 30 and
+  // 173 us; 4004 tokens of 4 prompts 32, 10 and 13 us).
+  constexpr int64_t kAppendGroups = 2048;
+  int64_t tokens = (int64_t)a.T * x / kAppendGroups;
+  tokens = tokens < 1 ? 1 : (tokens > 64 ? 64 : tokens);
+  int64_t y = (a.T + tokens - 1) / tokens;
   if (y > 65535) y = 65535;
-  const int x = (items + per - 1) / per;
   const auto launch = [&](auto d) {
     constexpr int D = decltype(d)::value;
-    hipLaunchKernelGGL((append_kernel<T, D>), dim3(x, (unsigned)y), dim3(256), 0, s, a, waves, tokens);
+    hipLaunchKernelGGL((append_kernel<T, D>), dim3(x, (unsigned)y), dim3(256), 0, s, a, waves,
+                       (int)tokens);
     return hipGetLastError();
   };
   if (a.dim == 64) return launch(std::integral_constant<int, 64>());
