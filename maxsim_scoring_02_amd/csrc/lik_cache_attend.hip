@@ -696,10 +696,11 @@ __global__ __launch_bounds__(NT) void merge_kernel(AttendArgs a, Split sp, char*
   __shared__ float2 mls[NT / L];
   const Space<M, D> space(ws, a.kv_heads, sp);
   const int head = blockIdx.y, i0 = blockIdx.z * R, group = a.q_heads / a.kv_heads;
-  const int64_t tiles = *space.count() < sp.tiles ? *space.count() : sp.tiles;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+  const int all = *space.count();
+  for (int64_t tile = blockIdx.x; tile < sp.tiles; tile += gridDim.x) {
+    // (read before it is known whether there is one: its place is there)
     const Piece x = *space.piece(head, tile);
-    if (x.n == 0 || i0 >= x.rows) continue;
+    if (tile >= all || x.n == 0 || i0 >= x.rows) continue;
     const int here = x.rows - i0 < R ? x.rows - i0 : R;
     // fewer rows: more groups, each with every G-th part
     int G = G0, span = R;
@@ -718,15 +719,15 @@ __global__ __launch_bounds__(NT) void merge_kernel(AttendArgs a, Split sp, char*
         return space.part(sp, head, k == 0 ? x.at : (first + k) * 2);
       };
 #pragma unroll 4
-      for (int k = g; k <= x.n; k += G) m = fmaxf(m, part(k).ml[i].x);
-      const float ref = m == kNegInf ? 0.0f : m;
-#pragma unroll 4
       for (int k = g; k <= x.n; k += G) {
         const Partial p = part(k);
         const float2 ml = p.ml[i];
-        const float f = exp2_fast(ml.x - ref);
-        l = fmaf(ml.y, f, l);
-        o += *(const f32x4*)(p.o + i * D + d) * f;
+        const f32x4 v = *(const f32x4*)(p.o + i * D + d);
+        const float top = fmaxf(m, ml.x), ref = top == kNegInf ? 0.0f : top;
+        const float keep = exp2_fast(m - ref), f = exp2_fast(ml.x - ref);
+        l = fmaf(ml.y, f, l * keep);
+        o = o * keep + v * f;
+        m = top;
       }
     }
     if (G > 1) {
