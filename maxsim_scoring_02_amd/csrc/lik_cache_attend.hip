@@ -385,8 +385,8 @@ struct RowTile {
       return (unsigned)block < (unsigned)a.num_blocks;
     }
   };
-  // One row tile a request: nothing reads its blocks again, and they need not stay in
-  // the caches.
+  // Mostly one row tile a request: nothing reads its blocks again, and they need not stay
+  // in the caches (64 requests of up to 8192: 126 us, through them 133).
   static __device__ __forceinline__ u32x4 load16(const uint8_t* p) {
     if constexpr (MT == 1) return __builtin_nontemporal_load((const u32x4*)p);
     return *(const u32x4*)p;
@@ -762,12 +762,19 @@ __global__ __launch_bounds__(NT) void merge_kernel(AttendArgs a, Split sp, char*
   }
 }
 
-int row_tiles_of(int64_t T, int64_t S, int64_t group) {
-  return S > 0 && T * group <= 16 * S ? 1 : 2;
+// Row tiles of 16 or 32 rows, by the mean rows of a request: 32 share what a tile of
+// tokens costs (3 prompts of up to 2048 over 8192, 32 / 8 heads of 128 bf16: 439 us, by
+// 16 1308).  Float32 of dim 128 and 256 spills registers with 32, and takes them from
+// three 16s on only (16 x 5 over 8192, 32 / 8 heads of 128: by 16 75 us, by 32 92; 7 x
+// 3 over 4000, 8 / 1 of 256: 26 and 33; 3 prompts of up to 1024, 8 / 2 of 256: 400 and 320).
+int row_tiles_of(int64_t T, int64_t S, int64_t group, int64_t dim, lik_dtype dtype) {
+  const int64_t most = dtype == LIK_F32 && dim > 64 ? 32 : 16;
+  return S > 0 && T * group <= most * S ? 1 : 2;
 }
-Split split_of(int64_t T, int64_t S, int64_t q_heads, int64_t kv_heads) {
+Split split_of(int64_t T, int64_t S, int64_t q_heads, int64_t kv_heads, int64_t dim,
+               lik_dtype dtype) {
   constexpr int kWaves = 2048;           // eight a CU
-  const int64_t group = q_heads / kv_heads, M = 16 * row_tiles_of(T, S, group);
+  const int64_t group = q_heads / kv_heads, M = 16 * row_tiles_of(T, S, group, dim, dtype);
   const int64_t w = (kWaves / 4 + kv_heads - 1) / kv_heads * 4;
   // every request has a row tile that is not full at most
   const int64_t tiles = T * group / M + (S < T ? S : T);
@@ -776,7 +783,7 @@ Split split_of(int64_t T, int64_t S, int64_t q_heads, int64_t kv_heads) {
 
 template <typename T, int D, int MT>
 hipError_t attend_t(const AttendArgs& a, char* ws, hipStream_t s) {
-  const Split sp = split_of(a.T, a.S, a.q_heads, a.kv_heads);
+  const Split sp = split_of(a.T, a.S, a.q_heads, a.kv_heads, a.dim, a.dtype);
   hipLaunchKernelGGL((attend_kernel<T, D, MT>), dim3(sp.workers / 4 * a.kv_heads), dim3(256), 0, s,
                      a, sp, ws);
   hipError_t e = hipGetLastError();
@@ -793,7 +800,8 @@ hipError_t attend_t(const AttendArgs& a, char* ws, hipStream_t s) {
 
 template <typename T, int D>
 hipError_t attend_d(const AttendArgs& a, char* ws, hipStream_t s) {
-  if (row_tiles_of(a.T, a.S, a.q_heads / a.kv_heads) == 1) return attend_t<T, D, 1>(a, ws, s);
+  if (row_tiles_of(a.T, a.S, a.q_heads / a.kv_heads, a.dim, a.dtype) == 1)
+    return attend_t<T, D, 1>(a, ws, s);
   return attend_t<T, D, 2>(a, ws, s);
 }
 
@@ -809,8 +817,8 @@ hipError_t attend_type(const AttendArgs& a, char* ws, hipStream_t s) {
 size_t attend_workspace(int64_t T, int64_t S, int64_t q_heads, int64_t kv_heads, int64_t dim,
                         lik_dtype dtype) {
   if (S == 0) return 0;
-  const Split sp = split_of(T, S, q_heads, kv_heads);
-  const bool one = row_tiles_of(T, S, q_heads / kv_heads) == 1;
+  const Split sp = split_of(T, S, q_heads, kv_heads, dim, dtype);
+  const bool one = row_tiles_of(T, S, q_heads / kv_heads, dim, dtype) == 1;
   const auto bytes = [&](auto d) -> int64_t {
     constexpr int D = decltype(d)::value;
     return one ? Space<16, D>(nullptr, kv_heads, sp).bytes(kv_heads)

@@ -72,15 +72,15 @@ __global__ __launch_bounds__(256) void verify_look_kernel(VerifyArgs a, Parts pa
 }
 
 // A row against its draft.
-struct Verdict {
+struct Outcome {
   RowSoft p, q;
   double ln_sum;
   bool more, broken, taken;
 };
 template <typename T>
-__device__ __forceinline__ Verdict judge(const VerifyArgs& a, const float2* mz, int n, int64_t r,
+__device__ __forceinline__ Outcome weigh(const VerifyArgs& a, const float2* mz, int n, int64_t r,
                                          int64_t hi) {
-  Verdict v;
+  Outcome v;
   const int x = a.drafts[r];
   v.more = r + 1 < hi && x >= 0;
   const bool in = v.more && x < a.C;
@@ -280,10 +280,10 @@ __device__ __forceinline__ VerifyEnd find_end(const VerifyArgs& a, const float2*
     return e;
   }
   for (int64_t r0 = lo;; r0 += 4) {
-    Verdict v;
+    Outcome v;
     v.taken = false;
     const int64_t r = r0 + wave;
-    if (r < hi) v = judge<T>(a, mz, look, r, hi);
+    if (r < hi) v = weigh<T>(a, mz, look, r, hi);
     if (lane == 0) {
       taken[wave] = r < hi && v.taken;
       if (r < hi) rows[wave] = VerifyEnd{r, v.ln_sum, v.p, v.q, v.more, v.broken};
