@@ -685,6 +685,16 @@ def lik_cache_tables(old_len, new_len, block_table, ring, ring_state, block_size
     return granted, offsets, slots
 
 
+def _block_stride(x, name: str) -> int:
+    """Bytes from block to block of one that is dense within a block."""
+    N, heads, rows, last = x.shape
+    a, b, c, d = x.stride()
+    inner = rows * last
+    if d != 1 or c != last or (heads > 1 and b != inner) or (N > 1 and a < heads * inner):
+        raise ValueError(f"{name} must be dense within a block")
+    return a if N > 1 else heads * inner
+
+
 def _blocks(k_cache, v_cache, k_scale, v_scale, device) -> Tuple:
     """What the C ABI takes of a cache: addresses, sizes and block strides."""
     if k_cache.dim() != 4 or k_cache.dtype != _F8 or v_cache.dtype != _F8:
@@ -693,21 +703,18 @@ def _blocks(k_cache, v_cache, k_scale, v_scale, device) -> Tuple:
     N, heads, bs, dim = k_cache.shape
     if v_cache.shape != (N, heads, dim, bs):
         raise ValueError(f"v_cache must have shape {(N, heads, dim, bs)}, not {tuple(v_cache.shape)}")
-    size = heads * bs * dim
-    strides = []
-    for x, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        a, b, c, d = x.stride()
-        inner, last = x.shape[2:]
-        if d != 1 or c != last or (heads > 1 and b != inner * last) or (N > 1 and a < size):
-            raise ValueError(f"{name} must be dense within a block")
-        strides.append(a if N > 1 else size)
+    inner = bs * dim
+    size = heads * inner
+    k_stride = v_stride = size
+    if k_cache.stride() != (size, inner, dim, 1) or v_cache.stride() != (size, inner, bs, 1):
+        k_stride, v_stride = _block_stride(k_cache, "k_cache"), _block_stride(v_cache, "v_cache")
     for x, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
         if x.shape != (N, heads) or x.dtype != torch.float32 or not x.is_contiguous():
             raise ValueError(f"{name} must be contiguous float32 of shape {(N, heads)}")
     if not (device == k_cache.device == v_cache.device == k_scale.device == v_scale.device):
         raise ValueError(f"the cache must be on {device}")
     return (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), N,
-            heads, bs, dim, *strides)
+            heads, bs, dim, k_stride, v_stride)
 
 
 def _token_stride(x, heads: int, dim: int, name: str) -> int:
