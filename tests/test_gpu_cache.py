@@ -403,6 +403,15 @@ def test_prompts(hq, hkv, n, lens, dtype):
     check_attention(c, q, off, lens, table)
 
 
+@pytest.mark.parametrize("dim", [128, 256])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_many_rows_a_request(dim, dtype):
+    """Row tiles of 32, full and not, over parts of the cache and all of it."""
+    for hq, hkv, n, lens in ((8, 2, [40, 1, 33], [40, 700, 130]), (4, 1, [90, 9], [91, 400]), (2, 2, [65, 0, 40], [1300, 5, 40])):
+        c, q, off, lens, table = setup(n, lens, hq, hkv, dim, 32, dtype, dim + hq, pad=1)
+        check_attention(c, q, off, lens, table)
+
+
 @pytest.mark.parametrize("dtype,lens", [(BF16, [9000]), (F16, [5000, 13, 4097]), (F32, [3001, 6000])])
 def test_long_caches(dtype, lens):
     c, q, off, lens, table = setup([1] * len(lens), lens, 8, 2, 128, 16, dtype, 77)
