@@ -256,6 +256,11 @@ struct VerifyEnd {
   int more, broken;
 };
 
+// Waits until this wave's stores have arrived; what follows stays behind them.
+__device__ __forceinline__ void wait_stores() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
 struct VerifySpace {
   float2* mz;                            // [2 R][parts of a row]
   double* sums;                          // [S][parts of a drawn row]
@@ -356,11 +361,12 @@ __global__ __launch_bounds__(256) void verify_draw_kernel(VerifyArgs a, int look
     for (int k = 0; k < PartWeights<T, Once>::kSlots; ++k) sum += mine.slot(w, part * parts.cols, k);
     sum = block_sum(sum, tmp);
     if (tid == 0) {
-      // The sum goes past the caches by itself, and has arrived when the count moves: no
-      // cache is written back or dropped for it (with a fence of the whole chip in each
-      // workgroup this launch took 435 us over 256 x 5 rows of 131072).
+      // The sum goes past the caches by itself and has arrived when the count moves, for
+      // which the wave waits: no cache is written back or dropped for it (with a fence of
+      // the whole chip in each workgroup this launch took 435 us over 256 x 5 rows of
+      // 131072).
       __hip_atomic_store(&sums[part], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+      wait_stores();
       last = __hip_atomic_fetch_add(&ws.done[s], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
              parts.n - 1;
     }
@@ -386,7 +392,7 @@ __global__ __launch_bounds__(256) void verify_draw_kernel(VerifyArgs a, int look
         sum = block_sum(sum, tmp);
         if (tid == 0) __hip_atomic_store(&sums[p], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+      wait_stores();                     // the other waves read them behind the meeting
       __syncthreads();
     }
     // every wave: a lane a part, 64 at a time
