@@ -13,13 +13,13 @@
 //   which lie in one block: its scale is one number a lane.  The key's goes into the
 //   factor of the score, the value's into the exponent:
 //     w' = 2^(score log2(e) + log2(v_scale) - m),   P = w',   sum w = sum w' / v_scale
-//   so that P is at most 2^8 and float16 whatever the scales are, and neither costs
-//   an instruction per score.
+//   so that P is float16 with the largest of a row near float16's end whatever the scales
+//   are, and neither costs an instruction per score.
 // * The tokens of a score tile are chosen so that its output registers are the
 //   next product's operand: no weight crosses a lane.
 // * Values lie dim by dim in the cache, so 16 tokens of one dim are a 16-byte load
 //   and the operand of two products.
-// * The maximum m moves only when a score passes it by 2^8.
+// * The reference m moves only when a weight would leave float16's range (RowTile).
 //
 // The work of a head is numbered (request, row tile, 64 tokens) and cut into
 // equal ranges, one a wave, whatever the lengths are.  A row tile that lies in
@@ -78,13 +78,13 @@ __device__ __forceinline__ float row_sum4(float x) {
   return a + b;
 }
 
-// Eight codes (two words) as float16.
-__device__ __forceinline__ half8 widen(uint32_t lo, uint32_t hi) {
+// Eight codes (two words) times a power of two as float16.
+__device__ __forceinline__ half8 widen(uint32_t lo, uint32_t hi, float by = 1.0f) {
   half8 h;
-  const half2v a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
-  const half2v b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
-  const half2v c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
-  const half2v d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+  const half2v a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, by, false);
+  const half2v b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, by, true);
+  const half2v c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, by, false);
+  const half2v d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, by, true);
   h[0] = a[0]; h[1] = a[1]; h[2] = b[0]; h[3] = b[1];
   h[4] = c[0]; h[5] = c[1]; h[6] = d[0]; h[7] = d[1];
   return h;
@@ -300,8 +300,16 @@ struct RowTile {
   static constexpr bool kTwo = std::is_same<T, float>::value;   // float32: two float16 parts
   static constexpr int kParts = kTwo ? 2 : 1;
   static constexpr int M = 16 * MT, NC = D / 32, NI = D / 64, ND = D / 16;
-  // how far a score may pass the maximum before it moves (float32's parts: not at all)
-  static constexpr float kSlack = kTwo ? 0.0f : 8.0f;
+  // Weights use float16 up to its end: a row's reference m lies 2^kBelow below the largest
+  // when it moves, and moves where a weight would pass 2^kTop (with what is rounded,
+  // 2^15.7 at most).  Float16 keeps 11 bits down to 2^-14, so of 16-bit types' weights those
+  // above 2^-25 of the row's largest, and is off by 2^-25 below, 2^-36 of the largest.
+  // A kBelow of 15 moves every row whose largest grows: prompts 431 us with 7, 433 with
+  // 11, 438 with 13, 455 with 15 (3 of up to 2048 over 8192, 32 / 8 heads of 128).
+  // Float32 does, and its low part is kept times kLow, against values over kLow, so that it
+  // is never short of digits before the high one: 22 bits down to 2^-29, off by 2^-51 below.
+  static constexpr float kTop = 15.25f, kBelow = kTwo ? 15.0f : 11.0f;
+  static constexpr float kLow = 0x1p11f;
 
   half8 q[kParts][MT][NC];
   float factor[MT];                      // scale log2(e) 2^-k of the lane's query row
@@ -497,12 +505,15 @@ struct RowTile {
         float cf = factor[mt] * kf;
         if (cf < 0x1p-126f) cf = 0x1p-126f;          // -inf * 0 would be NaN
         want[mt] = row_max4(fmaf(top, cf, lv));
-        moves |= want[mt] > m[mt] + kSlack;
+        moves |= want[mt] - m[mt] > kTop;
       }
       if (__any(moves)) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const float now = fmaxf(m[mt], want[mt]);
+          // (far from 0 the difference may be rounded to more)
+          float low = want[mt] - kBelow;
+          if (!(want[mt] - low <= kTop)) low = want[mt];
+          const float now = fmaxf(m[mt], low);
           const float keep = m[mt] == kNegInf ? 0.0f : exp2_fast(m[mt] - now);
           m[mt] = now;
           l[mt] *= keep;
@@ -518,8 +529,9 @@ struct RowTile {
         if (cf < 0x1p-126f) cf = 0x1p-126f;
         float shiftv = lv - (m[mt] == kNegInf ? 0.0f : m[mt]);
         // The product below is exact and m is rounded: they are apart by up to 2^-24 |m|.
-        // Where that is much the scores are rounded first, as m was.
-        if (__any(fabsf(m[mt]) > 0x1p26f && m[mt] != kNegInf)) {
+        // Where that is much (a quarter: weights stay below 2^16) the scores are rounded first,
+        // as m was.
+        if (__any(fabsf(m[mt]) > 0x1p22f && m[mt] != kNegInf)) {
 #pragma unroll
           for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
@@ -538,7 +550,7 @@ struct RowTile {
             sum += w;
             p[0][mt][tt >> 1][(tt & 1) * 4 + e] = (_Float16)w;
             if constexpr (kTwo)
-              p[kParts - 1][mt][tt >> 1][(tt & 1) * 4 + e] = (_Float16)(w - (float)(_Float16)w);
+              p[kParts - 1][mt][tt >> 1][(tt & 1) * 4 + e] = (_Float16)((w - (float)(_Float16)w) * kLow);
           }
         }
         l[mt] = fmaf(sum, iv, l[mt]);
@@ -547,11 +559,13 @@ struct RowTile {
       for (int d = 0; d < ND; ++d) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const half8 v8 = widen(vr[d][half * 2], vr[d][half * 2 + 1]);
 #pragma unroll
-          for (int part = 0; part < kParts; ++part)
+          for (int part = 0; part < kParts; ++part) {
+            const half8 v8 =
+                widen(vr[d][half * 2], vr[d][half * 2 + 1], part == 0 ? 1.0f : 1.0f / kLow);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) o[mt][d] = mma(v8, p[part][mt][half], o[mt][d]);
+          }
         }
       }
       __builtin_amdgcn_sched_barrier(0);
