@@ -129,7 +129,8 @@ size_t lik_cache_workspace_bytes(int64_t T, int64_t S, int64_t q_heads,
  *   lse[t, h] = log sum_j w_j                (float32 [T][q_heads], or NULL)
  * in q's type with a token stride of out_ld, rounded once.  A row that attends to
  * nothing (a length of 0, no block in its table), and one outside every request, is 0
- * with lse -inf.  kv_len beyond max_blocks * block_size counts as that.
+ * with lse -inf, whatever its query holds; a query that is not finite is NaN, with its
+ * lse, where it attends to anything.  kv_len beyond max_blocks * block_size counts as that.
  * Scores and sums are float32.  A query's numbers are off by up to 2^-39 of the
  * row's largest (LIK_F32: or 2^-22 of themselves).  A weight w_j is rounded before its
  * product with the values, which sums in float32: to 11 bits (22 with LIK_F32) where

@@ -312,7 +312,7 @@ struct RowTile {
   static constexpr float kLow = 0x1p11f;
 
   half8 q[kParts][MT][NC];
-  float factor[MT];                      // scale log2(e) 2^-k of the lane's query row
+  float factor[MT];                      // scale log2(e) 2^-k of the lane's query row, or < 0
   int seen[MT];
   float m[MT], l[MT];
   f32x4 o[MT][ND];
@@ -345,7 +345,8 @@ struct RowTile {
       broken = row_max4(broken ? 1.0f : 0.0f) > 0.0f;
       // the row's largest number to [2^14, 2^15): exact, and small ones keep their digits
       const int k = top > 0.0f && !broken ? 14 - ilogbf(top) : 0;
-      factor[mt] = broken ? __builtin_nanf("") : ldexpf(a.scale * kLog2e, -k);
+      // a row that is not finite: equal scores, and NaN at the end where it has any
+      factor[mt] = broken ? -1.0f : ldexpf(a.scale * kLog2e, -k);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
 #pragma unroll
@@ -503,7 +504,7 @@ struct RowTile {
           top = fmaxf(top, fmaxf(fmaxf(sc[mt][tt][0], sc[mt][tt][1]),
                                  fmaxf(sc[mt][tt][2], sc[mt][tt][3])));
         float cf = factor[mt] * kf;
-        if (cf < 0x1p-126f) cf = 0x1p-126f;          // -inf * 0 would be NaN
+        if (cf < 0x1p-126f) cf = 0x1p-126f;          // -inf * 0 would be NaN; a broken row
         want[mt] = row_max4(fmaf(top, cf, lv));
         moves |= want[mt] - m[mt] > kTop;
       }
@@ -575,7 +576,10 @@ struct RowTile {
       next = after;
     }
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) l[mt] = row_sum4(l[mt]);
+    for (int mt = 0; mt < MT; ++mt) {
+      l[mt] = row_sum4(l[mt]);
+      if (factor[mt] < 0.0f && l[mt] != 0.0f) l[mt] = __builtin_nanf("");
+    }
   }
 
   __device__ __forceinline__ void finish(const AttendArgs& a, const Request& r, int t, int head,

@@ -493,6 +493,32 @@ def test_rows_that_see_nothing():
         assert out.shape == q.shape
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("dim", [64, 256])
+@pytest.mark.parametrize("n,lens", [([5, 2, 3, 1], [3, 40, 64, 0]), ([90, 70], [30, 700])])
+def test_rows_that_are_not_finite(n, lens, dim, dtype):
+    """Queries with NaN and infinities: NaN where they attend to something, 0 and -inf where
+    they do not (more rows than tokens, tables of holes), others as they were."""
+    c, q, off, lens, table = setup(n, lens, 4, 2, dim, 16, dtype, 17, pad=2, lead=1)
+    if len(n) > 2:
+        table[2] = -1                      # nothing but holes
+        table[1, 1] = c.sizes[0]           # and one among blocks
+    clean, clean_lse = _lib.lik_cache_attention(q, i32(off), i32(lens), i32(table), *c.parts, want_lse=True)
+    T = q.shape[0]
+    bad = torch.zeros((T, 4), dtype=torch.bool, device="cuda")
+    bad[::2, 0], bad[1::3, 3], bad[0], bad[-1], bad[off[1] - 1] = True, True, True, True, True
+    x = q.clone()
+    for i, (t, h) in enumerate(bad.nonzero().tolist()):
+        x[t, h, (7 * i) % dim] = (math.nan, math.inf, -math.inf)[i % 3]
+    got = check_attention(c, x, off, lens, table)
+    lse = _lib.lik_cache_attention(x, i32(off), i32(lens), i32(table), *c.parts, want_lse=True)[1]
+    assert torch.equal(got[~bad], clean[~bad]) and torch.equal(lse[~bad], clean_lse[~bad])
+    sees = ~torch.isneginf(clean_lse)
+    assert (bad & ~sees).any() and (bad & sees).any()
+    assert torch.isnan(got[bad & sees]).all() and torch.isnan(lse[bad & sees]).all()
+    assert not got[bad & ~sees].any() and torch.isneginf(lse[bad & ~sees]).all()
+
+
 def test_strided_queries_and_outputs():
     c, q, off, lens, table = setup([1, 4], [50, 80], 4, 2, 64, 16, BF16, 4)
     T = q.shape[0]
