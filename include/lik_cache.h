@@ -12,7 +12,10 @@
  * lengths grow by the drafts, tables give the slots and the offsets of every
  * request's rows, keys and values are appended, attention runs over them, the
  * drafts are verified over the same offsets, and lengths shrink to what was
- * accepted.
+ * accepted.  A request that the pool has no blocks for is not granted its drafts: it
+ * keeps its length, while its rows go through the step with the others'.  Nothing of
+ * them is appended, what attention and verification give for them means nothing, and
+ * what was accepted must not change its length.
  *
  * The conventions of lik.h hold (memory, stream, errors, determinism,
  * reentrancy), and for every operator here:
