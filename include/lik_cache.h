@@ -106,6 +106,7 @@ lik_status lik_cache_tables(const int32_t* old_len, const int32_t* new_len,
  *
  * Tokens of one block must follow each other in the call (what
  * lik_cache_tables gives does); of two with the same slot the later one stays.
+ * T below 2^31 - 2^8 (LIK_ERR_UNSUPPORTED beyond).
  */
 lik_status lik_cache_append(const void* k, const void* v, lik_dtype dtype,
                             int64_t T, int64_t k_ld, int64_t v_ld,

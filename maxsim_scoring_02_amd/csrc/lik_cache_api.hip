@@ -188,7 +188,9 @@ lik_status lik_cache_append(const void* k, const void* v, lik_dtype dtype, int64
   LIK_TRY(check_cache(k_cache, v_cache, k_scale, v_scale, num_blocks, kv_heads, block_size, dim,
                       k_stride, v_stride));
   if (T == 0 || num_blocks == 0) return ok();
-  if (T > INT32_MAX) return fail(LIK_ERR_UNSUPPORTED, "T must be below 2^31");
+  // the kernel looks 127 tokens beyond the one that a run begins with
+  if (T >= INT32_MAX - 255)
+    return fail(LIK_ERR_UNSUPPORTED, "T must be below 2^31 - 2^8 (got %lld)", (long long)T);
   const int64_t width = kv_heads * dim;
   LIK_TRY(check_tokens(k, "k", T, width, k_ld, size));
   LIK_TRY(check_tokens(v, "v", T, width, v_ld, size));

@@ -136,6 +136,14 @@ def test_what_is_not_supported(L, name, kw, msg):
     assert msg in L.lik_last_error().decode()
 
 
+def test_appends_whose_tokens_pass_32_bits(L):
+    """The kernel's numbers of tokens are 32 bits, with a look at what follows them."""
+    for T in (2 ** 31 - 2 ** 8, 2 ** 31 - 127, 2 ** 31 - 1):
+        assert call(L, "lik_cache_append", T=T, k_ld=128, v_ld=128, v=P(1 << 44), slots=P(1 << 45),
+                    k=P(1 << 46)) == LIK_ERR_UNSUPPORTED
+        assert "T must be below 2^31 - 2^8" in L.lik_last_error().decode()
+
+
 @pytest.mark.parametrize("name,fields", [
     ("lik_cache_tables", ["old_len", "new_len", "block_table", "ring", "ring_state", "granted",
                           "token_offsets", "slots"]),
