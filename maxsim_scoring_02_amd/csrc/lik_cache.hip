@@ -175,9 +175,10 @@ __global__ __launch_bounds__(kTablesThreads) void tables_kernel(TablesArgs a) {
       a.offsets[s] = first < INT32_MAX ? (int)first : INT32_MAX;
     }
     __syncthreads();
-    // table entries
-    for (uint32_t e = blockIdx.y * kTablesThreads + tid; e < moved.x;
-         e += gridDim.y * kTablesThreads) {
+    // table entries (their number may be next to 2^32, where a step further is not)
+    for (uint64_t at = blockIdx.y * kTablesThreads + tid; at < moved.x;
+         at += gridDim.y * kTablesThreads) {
+      const uint32_t e = (uint32_t)at;
       const int i = last_at_most(entry0, e), k = (int)(e - entry0[i]);
       int32_t* row = a.table + (s0 + i) * a.table_ld;
       if (s_need[i] > s_have[i]) {

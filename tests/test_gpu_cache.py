@@ -129,6 +129,24 @@ def test_tables_with_a_broken_pool_stay_inside():
         assert (guard[1, :20] == 7).all() and (guard[1, 20 + N:] == 7).all()
 
 
+def test_tables_that_give_back_nearly_two_to_the_32_entries():
+    """Lengths that no pool holds: every entry becomes -1, and the loop over them ends."""
+    S, width, bs, N = 64, 1 << 26, 16, 5
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs a table of 16 GiB")
+    table = torch.zeros((S, width), dtype=torch.int32, device="cuda")
+    old = torch.full((S,), width * bs, dtype=torch.int32, device="cuda")
+    old[S - 1] -= 1000 * bs                # 2^32 - 1000 entries
+    guard = torch.full((3, N), 7, dtype=torch.int32, device="cuda")
+    guard[1] = i32(range(N))
+    state = i32([0, 0, 0, 0])
+    g, off, _ = _lib.lik_cache_tables(old, torch.zeros_like(old), table, guard[1], state, bs, 0)
+    assert not g.any() and not off.any()
+    assert (table[:S - 1] == -1).all() and (table[S - 1, :-1000] == -1).all() and not table[S - 1, -1000:].any()
+    assert (guard[0] == 7).all() and (guard[2] == 7).all() and not guard[1].any()
+    assert state.tolist() == [0, N, 0, 0]
+
+
 # ---------------------------------------------------------------------------
 # appends
 # ---------------------------------------------------------------------------
