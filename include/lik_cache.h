@@ -134,10 +134,13 @@ size_t lik_cache_workspace_bytes(int64_t T, int64_t S, int64_t q_heads,
  * in q's type with a token stride of out_ld, rounded once.  A row that attends to
  * nothing (a length of 0, no block in its table), and one outside every request, is 0
  * with lse -inf, whatever its query holds; a query that is not finite is NaN, with its
- * lse, where it attends to anything.  kv_len beyond max_blocks * block_size counts as that.
- * Scores and sums are float32.  A query's numbers are off by up to 2^-39 of the
- * row's largest (LIK_F32: or 2^-22 of themselves).  A weight w_j is rounded before its
- * product with the values, which sums in float32: to 11 bits (22 with LIK_F32) where
+ * lse, where it attends to anything.  kv_len beyond max_blocks * block_size
+ * counts as that.
+ * Scores, with log2 of their block's v_scale added, and sums are float32; where
+ * scale times a query's largest number times a k_scale passes 2^128 the row may be
+ * NaN.  A query's numbers are off by up to 2^-39 of its largest (LIK_F32: or 2^-22 of
+ * themselves).  A weight w_j is rounded before its product with the values,
+ * which sums in float32: to 11 bits (22 with LIK_F32) where
  * w_j times its block's v_scale is above 2^-25 (2^-29) of the largest such product of
  * the row, and by up to 2^-36 (2^-51) of that largest below; scores beyond 2^22, whose
  * differences float32 holds to a quarter, leave 2^-14 and 2^-25 (2^-36) in their place.

@@ -380,7 +380,8 @@ struct Quad {
 // number, then the scale, then the codes; a wave with one tile keeps it in registers
 // meanwhile, one with more reads them again from the cache.  A scale is a power of
 // two, so one instruction scales, rounds and packs two codes.  18437 tokens of 8 heads of
-// 128, f16, blocks of 64 (113 MB): 25 us, 4.5 TB/s; 64 single tokens 5.5 us, latency.
+// 128, f16, blocks of 64 (113 MB): 25 us, 4.5 TB/s, f32 (189 MB) 43 us, 4.4 TB/s; 64 single
+// tokens 5.5 us, latency (one more where scales grow and blocks of 64 are coded again).
 // log2 of the lanes side by side in a tile of values: as few as there are dims for, so
 // that a tile is as long as 64 tokens or the block.
 __device__ __forceinline__ int append_side(int dim, int shift) {

@@ -21,17 +21,21 @@
 //   and the operand of two products.
 // * The reference m moves only when a weight would leave float16's range (RowTile).
 //
-// The work of a head is numbered (request, row tile, 64 tokens) and cut into
-// equal ranges, one a wave, whatever the lengths are.  A row tile that lies in
-// several ranges leaves its sums in the workspace, and a second kernel merges them.
+// The work of a head is numbered (request, row tile, 64 tokens of the request's length)
+// and cut into equal ranges, one a wave.  What lies behind a row tile's own positions is
+// numbered too and not done: nothing of it in single tokens and drafts, an eighth in
+// prompts behind long caches, half where nothing was cached before, where the busiest
+// waves have twice the mean.  A row tile that lies in several ranges leaves its sums
+// in the workspace, and a second kernel merges them.
 //
 // 64 requests of 2100 to 8100 tokens, 32 / 8 heads of 128, blocks of 16 (673 MB): 125 us,
 // 5.4 TB/s, bound by reads with 8 waves a CU and 16 KB of each on their way (3 waves a
 // SIMD, 44 registers spilled, 147 us).  Prompts of 600 to 1800 tokens over 2700 to 6800:
-// 431 to 457 us, 650 TFLOP/s: 440 vector instructions beside 64 matrix instructions a
+// 431 to 464 us, 650 TFLOP/s: 440 vector instructions beside 64 matrix instructions a
 // tile of 64 tokens x 32 rows (128 of them widen codes, 32 are exponentials), the matrix
-// cores busy a quarter of the time.  One request of 1030 tokens: 8 us and 5 us for the merge,
-// latency.
+// cores busy a quarter of the time.  Prompts with nothing cached before them: one of 2048
+// tokens 358 TFLOP/s, of 8192 506, 32 of 1024 329.  One request of 1030 tokens: 8 us and 4.5
+// us for the merge, latency.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -784,14 +788,17 @@ __global__ __launch_bounds__(NT) void merge_kernel(AttendArgs a, Split sp, char*
 // tokens costs (3 prompts of up to 2048 over 8192, 32 / 8 heads of 128 bf16: 439 us, by
 // 16 1308).  Float32 of dim 128 and 256 spills registers with 32, and takes them from
 // three 16s on only (16 x 5 over 8192, 32 / 8 heads of 128: by 16 75 us, by 32 92; 7 x
-// 3 over 4000, 8 / 1 of 256: 26 and 33; 3 prompts of up to 1024, 8 / 2 of 256: 400 and 320).
+// 3 over 4000, 8 / 1 of 256: 26 and 33; 3 prompts of up to 1024, 8 / 2 of 256: 400 and 320,
+// all with float32's low weights at the high ones' scale; the last is 291 now).
 int row_tiles_of(int64_t T, int64_t S, int64_t group, int64_t dim, lik_dtype dtype) {
   const int64_t most = dtype == LIK_F32 && dim > 64 ? 32 : 16;
   return S > 0 && T * group <= most * S ? 1 : 2;
 }
 Split split_of(int64_t T, int64_t S, int64_t q_heads, int64_t kv_heads, int64_t dim,
                lik_dtype dtype) {
-  constexpr int kWaves = 2048;           // eight a CU
+  // Eight a CU, as many as are resident at dims 64 and 128.  At 256 four are, and the others
+  // follow them: fewer would halve the workspace and the merge there (not tried).
+  constexpr int kWaves = 2048;
   const int64_t group = q_heads / kv_heads, M = 16 * row_tiles_of(T, S, group, dim, dtype);
   const int64_t w = (kWaves / 4 + kv_heads - 1) / kv_heads * 4;
   // every request has a row tile that is not full at most

@@ -9,10 +9,12 @@
 // has an interval of 10^-5 and less, which float32 sums would blur.
 //
 // 256 x 5 rows of 131072 bf16 (604 MB): the first launch is bound by reads, 6.9 TB/s, 87
-// us; the rows of the ends take 6 us; the second reads the two rows a sequence ends at
-// again (134 MB) and takes two exponentials a column, 44 to 51 us.  One sequence of 5 rows of 32768: 3.8 and 10.5
-// us, latency: the second goes from offsets to drafts, to their logits, to the row's
-// parts, to the sums and back into one part.
+// us; the rows of the ends take 6 us; the second reads the one or two rows that a sequence
+// ends at again (134 MB at the most), 45 to 52 us.  Neither the reads (20 us at the first launch's
+// rate) nor the exponentials (two a column, 7 us) explain that: its waves wait during
+// 54% of their cycles, a part's sum, count and end one after the other.  One sequence of
+// 5 rows of 32768: 3.8 and 11 us, latency: the second goes from offsets to drafts, to their
+// logits, to the row's parts, to the sums and back into one part.
 #include <hip/hip_runtime.h>
 
 #include "lik_rows_device.h"
@@ -121,7 +123,8 @@ constexpr int kVerifyPieces = 4;
 // A part's weights by 256 threads, as 16-byte pieces of the row: sums a piece, the
 // columns before the first and behind the last whole piece first and last.  The 4 or 8
 // weights of a piece are added in float32: what that rounds is of the size of the weights'
-// own error.
+// own error (in float64 1000 x 5 rows of 131072 553 us against 540, 256 x 5 149 against
+// 147).
 template <typename T, bool Once>
 struct PartWeights {
   static constexpr int NV = kVerifyPieces, N = PieceOf<T>::N, kSlots = NV + 2;

@@ -1,4 +1,4 @@
-"""The step of generation that README.md shows, run as it stands there: on the CPU over
+"""The step of generation that the readme shows, run as it stands there: on the CPU over
 the oracle, and on the GPU over the library, with a pool that cannot serve every request.
 A request that got no blocks keeps its length, its blocks and its tokens."""
 
